@@ -288,6 +288,90 @@ int gdn_bwd_vg(const gdn_dims* d, const void* q, const void* k, const void* v, c
                void* db, float* dstate, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * Linear attention with a decay for each head: the recurrence without the
+ * delta correction, with a gate that is a constant of the value head.
+ *   valid step:  S <- g S + k v^T;   every step:  o = scale S^T q
+ * with g = exp(lg[h]); a masked step leaves S unchanged (its k and v are not
+ * read into anything, NaN or not) and still reads o.  Value head h reads
+ * query/key head h / G, the state is [B,Hv,Dk,Dv] fp32 and is carried, as in
+ * gdn_fwd.  q and k are taken as they are (no normalisation).
+ *   d         Dk, Dv: multiples of 8 from 8 to 256 (else GDN_ERR_UNSUPPORTED);
+ *             save is ignored; algo:
+ *               SCAN        the per-step recurrence (forward only)
+ *               CHUNK       64-step chunks on the matrix cores (32-step for
+ *                           fp32), one pass over the sequence
+ *               CHUNK_TPAR  the same with the sequence cut into segments that
+ *                           run in parallel: their state sums, a chain over
+ *                           them, then their outputs (one pass where one
+ *                           segment is best)
+ *               AUTO        SCAN for single steps, else CHUNK_TPAR
+ *             bf16 tensors are multiplied by bf16 matrix products with fp32
+ *             sums (the state keeps fp32 precision), fp32 ones by fp32
+ *             products.
+ *   lg        [Hv] fp32, the log of the decay.  Meant for lg <= 0; -inf (g = 0)
+ *             is allowed.  No quotient of decays is formed, so nothing
+ *             overflows for any lg <= 0, and growth (lg > 0) overflows only
+ *             where g^64 does.
+ *   q, k, v, state0, mask, o, state_out: as gdn_fwd; state_out may alias state0
+ *             exactly
+ * Alignment: q, k, v, o, dO, dq, dk, dv and the states 16 bytes (else
+ * GDN_ERR_INVALID_ARG).  A NaN or Inf in a valid step reaches the outputs of
+ * its whole chunk in the chunk forms, those of earlier steps included.
+ */
+int gdn_decay_fwd_workspace_bytes(const gdn_dims* d, size_t* out);
+int gdn_decay_bwd_workspace_bytes(const gdn_dims* d, size_t* out);
+int gdn_decay_fwd(const gdn_dims* d, const void* q, const void* k, const void* v, const float* lg,
+                  float scale, const float* state0, const uint8_t* mask, void* o, float* state_out,
+                  void* ws, size_t ws_bytes, void* stream);
+/* VJP of gdn_decay_fwd.  dO, dS_final (NULL = zeros), dq, dk, dv, dstate as
+ * gdn_bwd (grouped heads summed; masked steps get dk = dv = 0), and
+ *   dlg       [Hv] fp32 (out), summed over the batch
+ * algo SCAN gives GDN_ERR_UNSUPPORTED.  No checkpoints: the states are
+ * recomputed. */
+int gdn_decay_bwd(const gdn_dims* d, const void* q, const void* k, const void* v, const float* lg,
+                  float scale, const float* state0, const uint8_t* mask, const void* dO,
+                  const float* dS_final, void* dq, void* dk, void* dv, float* dlg, float* dstate,
+                  void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * RMS norm of every query and key head and rotation by position, in one pass:
+ *   u = x (mean(x^2) + eps)^-1/2 (w + w_offset)      over the D channels
+ *   y = u with the pairs of its first R channels turned: for pair i at position p
+ *       (y1, y2) = (u1 c - u2 s, u2 c + u1 s), c = rope[p][i], s = rope[p][R/2 + i]
+ * where pair i is channels (i, i + R/2), or (2i, 2i + 1) when interleaved.
+ */
+typedef struct gdn_norm_dims {
+  int64_t B, T, Hq, Hk, D;     /* D a multiple of 8 from 8 to 512            */
+  int64_t R;                   /* turned channels: a multiple of 16, 0 .. D  */
+  int64_t P;                   /* rows of the table                          */
+  int64_t q_stride, k_stride;  /* elements from one token's q (k) rows to the
+                                  next one's, in q, k only; 0 = dense; at least
+                                  Hq D (Hk D), a multiple of 16 bytes        */
+  int32_t dtype;               /* enum gdn_dtype                             */
+  int32_t interleaved;
+  float eps, w_offset;         /* eps >= 0                                   */
+} gdn_norm_dims;
+/*
+ *   q [B,T,Hq,D], k [B,T,Hk,D] dtype, tokens q_stride / k_stride apart (rows of
+ *   a packed projection, for instance); wq, wk [D] fp32; rope [P,R] fp32 (R/2
+ *   cosines, then R/2 sines; NULL only with R = 0); pos [B,T] int32, NULL =
+ *   0 .. T-1 in every sequence.  A position outside 0 .. P-1 turns its token's
+ *   first R channels to NaN (and the weights' gradients with them).
+ *   oq, ok, dyq, dyk, dq, dk: dense, as q and k.  No output may overlap an input.
+ * The VJP takes the inputs again and recomputes the norms; dwq, dwk [D] fp32
+ * are sums over all rows, in a fixed order.  Alignment: all but pos 16 bytes
+ * (else GDN_ERR_INVALID_ARG).
+ */
+int gdn_norm_rope_fwd(const gdn_norm_dims* d, const void* q, const void* k, const float* wq,
+                      const float* wk, const float* rope, const int32_t* pos, void* oq, void* ok,
+                      void* stream);
+int gdn_norm_rope_bwd_workspace_bytes(const gdn_norm_dims* d, size_t* out);
+int gdn_norm_rope_bwd(const gdn_norm_dims* d, const void* q, const void* k, const float* wq,
+                      const float* wk, const float* rope, const int32_t* pos, const void* dyq,
+                      const void* dyk, void* dq, void* dk, float* dwq, float* dwk, void* ws,
+                      size_t ws_bytes, void* stream);
+
+/*
  * Optional per-kernel timing, for benchmarks and profilers.  While `events`
  * is non-NULL, each kernel that the following gdn_fwd / gdn_bwd calls launch
  * (in launch order, i = 0, 1, ...) records events[2i] on the call's stream

@@ -26,7 +26,10 @@ STATUS = {0: "GDN_OK", 1: "GDN_ERR_INVALID_ARG", 2: "GDN_ERR_UNSUPPORTED",
 EXPORTS = ("gdn_ckpt_elems", "gdn_ckpt_bytes", "gdn_workspace_bytes", "gdn_fwd_workspace_bytes", "gdn_bwd_workspace_bytes",
            "gdn_fwd", "gdn_fwd_noalloc", "gdn_bwd", "gdn_decode_conv", "gdn_vg_ckpt_elems", "gdn_vg_ckpt_bytes",
            "gdn_fwd_vg_workspace_bytes",
-           "gdn_bwd_vg_workspace_bytes", "gdn_fwd_vg", "gdn_bwd_vg", "gdn_set_kernel_events",
+           "gdn_bwd_vg_workspace_bytes", "gdn_fwd_vg", "gdn_bwd_vg",
+           "gdn_decay_fwd_workspace_bytes", "gdn_decay_bwd_workspace_bytes", "gdn_decay_fwd", "gdn_decay_bwd",
+           "gdn_norm_rope_fwd", "gdn_norm_rope_bwd_workspace_bytes", "gdn_norm_rope_bwd",
+           "gdn_set_kernel_events",
            "gdn_status_string", "gdn_version")
 
 
@@ -34,6 +37,14 @@ class Dims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("Hk", ctypes.c_int64),
                 ("Hv", ctypes.c_int64), ("Dk", ctypes.c_int64), ("Dv", ctypes.c_int64),
                 ("dtype", ctypes.c_int32), ("algo", ctypes.c_int32), ("save", ctypes.c_int32)]
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("Hq", ctypes.c_int64),
+                ("Hk", ctypes.c_int64), ("D", ctypes.c_int64), ("R", ctypes.c_int64),
+                ("P", ctypes.c_int64), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("w_offset", ctypes.c_float)]
 
 
 class GdnError(RuntimeError):
@@ -56,7 +67,8 @@ def lib():
         P, S = ctypes.c_void_p, ctypes.c_size_t
         PD = ctypes.POINTER(Dims)
         for n in ("gdn_ckpt_elems", "gdn_fwd_workspace_bytes", "gdn_bwd_workspace_bytes", "gdn_vg_ckpt_elems",
-                  "gdn_vg_ckpt_bytes", "gdn_fwd_vg_workspace_bytes", "gdn_bwd_vg_workspace_bytes"):
+                  "gdn_vg_ckpt_bytes", "gdn_fwd_vg_workspace_bytes", "gdn_bwd_vg_workspace_bytes",
+                  "gdn_decay_fwd_workspace_bytes", "gdn_decay_bwd_workspace_bytes"):
             getattr(L, n).argtypes = [PD, ctypes.POINTER(S)]
             getattr(L, n).restype = ctypes.c_int
         L.gdn_ckpt_bytes.argtypes = [PD, ctypes.POINTER(S)]
@@ -75,6 +87,17 @@ def lib():
         L.gdn_fwd_vg.restype = ctypes.c_int
         L.gdn_bwd_vg.argtypes = [PD] + [P] * 17 + [S, P]
         L.gdn_bwd_vg.restype = ctypes.c_int
+        L.gdn_decay_fwd.argtypes = [PD] + [P] * 4 + [ctypes.c_float] + [P] * 5 + [S, P]
+        L.gdn_decay_fwd.restype = ctypes.c_int
+        L.gdn_decay_bwd.argtypes = [PD] + [P] * 4 + [ctypes.c_float] + [P] * 10 + [S, P]
+        L.gdn_decay_bwd.restype = ctypes.c_int
+        PN = ctypes.POINTER(NormDims)
+        L.gdn_norm_rope_fwd.argtypes = [PN] + [P] * 9
+        L.gdn_norm_rope_fwd.restype = ctypes.c_int
+        L.gdn_norm_rope_bwd_workspace_bytes.argtypes = [PN, ctypes.POINTER(S)]
+        L.gdn_norm_rope_bwd_workspace_bytes.restype = ctypes.c_int
+        L.gdn_norm_rope_bwd.argtypes = [PN] + [P] * 13 + [S, P]
+        L.gdn_norm_rope_bwd.restype = ctypes.c_int
         L.gdn_set_kernel_events.argtypes = [ctypes.POINTER(ctypes.c_void_p), ctypes.c_int]
         L.gdn_set_kernel_events.restype = ctypes.c_int
         L.gdn_status_string.argtypes = [ctypes.c_int]
@@ -500,3 +523,183 @@ def decode_conv(x, conv_w, conv_state, a, b, A_log, dt_bias, Hk, Dk, Hv, Dv, sta
     if rc:
         raise GdnError("gdn_decode_conv", rc)
     return o, state_out, conv_state_out
+
+
+# ---- linear attention with a decay for each head (gdn_decay_fwd / gdn_decay_bwd)
+
+def _check_decay(d, q, k, v, lg, state0, mask):
+    dev, dt = q.device, q.dtype
+    if dev.type != "cuda":
+        raise ValueError("gdn runs on the GPU; got device %s" % dev)
+    _check(q, "q", (d.B, d.T, d.Hk, d.Dk), dt, dev)
+    _check(k, "k", (d.B, d.T, d.Hk, d.Dk), dt, dev)
+    _check(v, "v", (d.B, d.T, d.Hv, d.Dv), dt, dev)
+    _check(lg, "lg", (d.Hv,), torch.float32, dev)
+    if state0 is not None:
+        _check(state0, "state0", (d.B, d.Hv, d.Dk, d.Dv), torch.float32, dev)
+    if mask is not None:
+        _check(mask, "mask", (d.B, d.T), torch.uint8, dev)
+
+
+def decay_fwd(q, k, v, lg, state0=None, mask=None, *, scale=None, state_out=None, algo=ALGO_AUTO):
+    """Linear attention with a decay for each head (gdn_decay_fwd): S <- e^lg S
+    + k v^T, o = scale S^T q (scale: Dk^-1/2 by default), T = 1 for a single
+    token.  Returns (o, state_out).  Pass state_out=state0 to update the state
+    in place."""
+    d = _dims_of(q, v, algo)
+    _check_decay(d, q, k, v, lg, state0, mask)
+    dev = q.device
+    if state_out is None:
+        state_out = torch.empty((d.B, d.Hv, d.Dk, d.Dv), dtype=torch.float32, device=dev)
+    else:
+        _check(state_out, "state_out", (d.B, d.Hv, d.Dk, d.Dv), torch.float32, dev)
+    wsb = _query("gdn_decay_fwd_workspace_bytes", d)
+    o = torch.empty((d.B, d.T, d.Hv, d.Dv), dtype=q.dtype, device=dev)
+    ws = torch.empty((wsb,), dtype=torch.uint8, device=dev) if wsb else None
+    with torch.cuda.device(dev):
+        rc = lib().gdn_decay_fwd(ctypes.byref(d), _p(q), _p(k), _p(v), _p(lg),
+                                 d.Dk ** -0.5 if scale is None else scale, _p(state0), _p(mask), _p(o),
+                                 _p(state_out), _p(ws), wsb, _stream(dev))
+    if rc:
+        raise GdnError("gdn_decay_fwd", rc)
+    return o, state_out
+
+
+def decay_bwd(q, k, v, lg, state0, mask, dO, dS_final=None, *, scale=None, algo=ALGO_AUTO):
+    """VJP of decay_fwd.  Returns dict(dq, dk, dv, dlg, dstate)."""
+    d = _dims_of(q, v, algo)
+    _check_decay(d, q, k, v, lg, state0, mask)
+    dev = q.device
+    _check(dO, "dO", (d.B, d.T, d.Hv, d.Dv), q.dtype, dev)
+    if dS_final is not None:
+        _check(dS_final, "dS_final", (d.B, d.Hv, d.Dk, d.Dv), torch.float32, dev)
+    wsb = _query("gdn_decay_bwd_workspace_bytes", d)
+    out = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
+               dlg=torch.empty_like(lg),
+               dstate=torch.empty((d.B, d.Hv, d.Dk, d.Dv), dtype=torch.float32, device=dev))
+    ws = torch.empty((wsb,), dtype=torch.uint8, device=dev) if wsb else None
+    with torch.cuda.device(dev):
+        rc = lib().gdn_decay_bwd(ctypes.byref(d), _p(q), _p(k), _p(v), _p(lg),
+                                 d.Dk ** -0.5 if scale is None else scale, _p(state0), _p(mask), _p(dO),
+                                 _p(dS_final), *[_p(out[n]) for n in ("dq", "dk", "dv", "dlg", "dstate")],
+                                 _p(ws), wsb, _stream(dev))
+    if rc:
+        raise GdnError("gdn_decay_bwd", rc)
+    return out
+
+
+class DecayAttention(torch.autograd.Function):
+    """Autograd wrapper of decay_fwd / decay_bwd: forward(q, k, v, lg, state0,
+    mask, scale) returns (o, state_out)."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, lg, state0=None, mask=None, scale=None):
+        o, st = decay_fwd(q, k, v, lg, state0, mask, scale=scale)
+        ctx.save_for_backward(q, k, v, lg, state0, mask)
+        ctx.scale = scale
+        return o, st
+
+    @staticmethod
+    def backward(ctx, dO, dS):
+        q, k, v, lg, state0, mask = ctx.saved_tensors
+        g = decay_bwd(q, k, v, lg, state0, mask, dO.contiguous(), None if dS is None else dS.contiguous(),
+                      scale=ctx.scale)
+        return (g["dq"], g["dk"], g["dv"], g["dlg"], g["dstate"] if state0 is not None else None, None, None)
+
+
+# ---- norm of queries and keys with rotation (gdn_norm_rope_fwd / gdn_norm_rope_bwd)
+
+def rope_table(P, R, base=10000.0, device="cuda"):
+    """The table of norm_rope: cos and sin of position * base^(-2i/R), computed
+    in 64 bits, as [P, R] fp32 (R/2 cosines, then R/2 sines)."""
+    f = base ** (-torch.arange(0, R, 2, dtype=torch.float64, device=device) / max(R, 1))
+    a = torch.arange(P, dtype=torch.float64, device=device)[:, None] * f[None]
+    return torch.cat([a.cos(), a.sin()], 1).float().contiguous()
+
+
+def _token_stride(x, name):
+    """Elements between the rows of consecutive tokens of [B, T, H, D]; the
+    heads of a token are dense, the tokens evenly spaced over batch and time."""
+    B, T, H, D = x.shape
+    if (D > 1 and x.stride(3) != 1) or (H > 1 and x.stride(2) != D):
+        raise ValueError("%s: the heads of a token must be contiguous" % name)
+    st = x.stride(1) if T > 1 else x.stride(0) if B > 1 else H * D
+    if B > 1 and T > 1 and x.stride(0) != T * st:
+        raise ValueError("%s: tokens must be evenly spaced over batch and time" % name)
+    return st
+
+
+def _norm_dims(q, k, wq, wk, rope, pos, eps, w_offset, interleaved):
+    dev, dt = q.device, q.dtype
+    if dev.type != "cuda":
+        raise ValueError("gdn runs on the GPU; got device %s" % dev)
+    if dt not in (torch.float32, torch.bfloat16):
+        raise TypeError("q: expected float32 or bfloat16, got %s" % dt)
+    B, T, Hq, D = q.shape
+    Hk = k.shape[2]
+    if k.dtype != dt:
+        raise TypeError("k: expected %s, got %s" % (dt, k.dtype))
+    if tuple(k.shape) != (B, T, Hk, D) or k.device != dev:
+        raise ValueError("k: expected shape %s on %s, got %s on %s" % ((B, T, Hk, D), dev, tuple(k.shape), k.device))
+    _check(wq, "wq", (D,), torch.float32, dev)
+    _check(wk, "wk", (D,), torch.float32, dev)
+    P, R = 0, 0
+    if rope is not None:
+        P, R = rope.shape
+        _check(rope, "rope", (P, R), torch.float32, dev)
+    if pos is not None:
+        _check(pos, "pos", (B, T), torch.int32, dev)
+    return NormDims(B, T, Hq, Hk, D, R, P, _token_stride(q, "q"), _token_stride(k, "k"),
+                    GDN_F32 if dt == torch.float32 else GDN_BF16, 1 if interleaved else 0, eps, w_offset)
+
+
+def norm_rope(q, k, wq, wk, rope=None, pos=None, *, eps=1e-6, w_offset=0.0, interleaved=False):
+    """RMS norm of every head of q [B,T,Hq,D] and k [B,T,Hk,D] with weights wq,
+    wk [D] fp32 (plus w_offset) and rotation of their first R channels by the
+    table rope [P,R] at positions pos [B,T] int32 (0 .. T-1 by default), in one
+    pass.  q and k may be slices of a packed projection.  Returns dense (q, k)."""
+    d = _norm_dims(q, k, wq, wk, rope, pos, eps, w_offset, interleaved)
+    oq = torch.empty((d.B, d.T, d.Hq, d.D), dtype=q.dtype, device=q.device)
+    ok = torch.empty((d.B, d.T, d.Hk, d.D), dtype=q.dtype, device=q.device)
+    with torch.cuda.device(q.device):
+        rc = lib().gdn_norm_rope_fwd(ctypes.byref(d), _p(q), _p(k), _p(wq), _p(wk), _p(rope), _p(pos), _p(oq),
+                                     _p(ok), _stream(q.device))
+    if rc:
+        raise GdnError("gdn_norm_rope_fwd", rc)
+    return oq, ok
+
+
+def norm_rope_bwd(q, k, wq, wk, rope, pos, dyq, dyk, *, eps=1e-6, w_offset=0.0, interleaved=False):
+    """VJP of norm_rope.  Returns dict(dq, dk, dwq, dwk), dq and dk dense."""
+    d = _norm_dims(q, k, wq, wk, rope, pos, eps, w_offset, interleaved)
+    dev = q.device
+    _check(dyq, "dyq", (d.B, d.T, d.Hq, d.D), q.dtype, dev)
+    _check(dyk, "dyk", (d.B, d.T, d.Hk, d.D), q.dtype, dev)
+    out = dict(dq=torch.empty_like(dyq), dk=torch.empty_like(dyk), dwq=torch.empty_like(wq),
+               dwk=torch.empty_like(wk))
+    wsb = _query("gdn_norm_rope_bwd_workspace_bytes", d)
+    ws = torch.empty((wsb,), dtype=torch.uint8, device=dev) if wsb else None
+    with torch.cuda.device(dev):
+        rc = lib().gdn_norm_rope_bwd(ctypes.byref(d), _p(q), _p(k), _p(wq), _p(wk), _p(rope), _p(pos), _p(dyq),
+                                     _p(dyk), *[_p(out[n]) for n in ("dq", "dk", "dwq", "dwk")], _p(ws), wsb,
+                                     _stream(dev))
+    if rc:
+        raise GdnError("gdn_norm_rope_bwd", rc)
+    return out
+
+
+class NormRope(torch.autograd.Function):
+    """Autograd wrapper of norm_rope / norm_rope_bwd: forward(q, k, wq, wk, rope,
+    pos, eps, w_offset, interleaved) returns (q, k)."""
+
+    @staticmethod
+    def forward(ctx, q, k, wq, wk, rope=None, pos=None, eps=1e-6, w_offset=0.0, interleaved=False):
+        ctx.save_for_backward(q, k, wq, wk, rope, pos)
+        ctx.kw = dict(eps=eps, w_offset=w_offset, interleaved=interleaved)
+        return norm_rope(q, k, wq, wk, rope, pos, **ctx.kw)
+
+    @staticmethod
+    def backward(ctx, dyq, dyk):
+        q, k, wq, wk, rope, pos = ctx.saved_tensors
+        g = norm_rope_bwd(q, k, wq, wk, rope, pos, dyq.contiguous(), dyk.contiguous(), **ctx.kw)
+        return (g["dq"], g["dk"], g["dwq"], g["dwk"]) + (None,) * 5

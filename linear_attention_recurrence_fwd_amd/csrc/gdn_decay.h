@@ -1,0 +1,139 @@
+// Host-side interfaces of the decay operator (linear attention with a decay
+// for each head) and of the query/key norm with rotation: between their entry
+// points (gdn_decay_api.hip) and their kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace gdn {
+
+constexpr int kDecayChunk = 64;   // steps per chunk; segments are whole chunks
+constexpr int kDecayMaxSeg = 512; // segments of one sequence
+
+struct DecayDims {
+  int B, T, Hk, Hv, Dk, Dv;
+  __host__ __device__ int G() const { return Hv / Hk; }
+  __host__ __device__ int nchunk() const { return (T + kDecayChunk - 1) / kDecayChunk; }
+};
+
+// One [B, T, H, D] tensor as a walk reads it: the head of value head h is
+// h / group.
+struct DecayRows {
+  const void* p;
+  int H, D, group;
+};
+
+// A walk over the chunks of one segment for each (b, value head): with a state
+// S [KD, N] (KD channels of x and y, N columns of z and w),
+//   w_i = rs (S_i^T x_i) with S_i = sum_j<=i decay y_j z_j^T + decay S_start.
+// The four sums of the operator and its backward are walks:
+//   o : x = q,  y = k,  z = v,  forward in time, start state0
+//   dq: x = dO, y = v,  z = k,  forward in time, start state0 transposed
+//   dk: x = v,  y = dO, z = q,  backward in time, start dS_final transposed
+//   dv: x = k,  y = q,  z = dO, backward in time, start dS_final
+struct DecayWalk {
+  DecayRows x, y, z, e;   // e: what the outputs are dotted with (dlg), [.., N]
+  void* w;                // [B, T, Hv, N]
+  int w32;                // w holds fp32 (partial rows of grouped heads)
+  int KD, N;              // channels and columns
+  int reverse;            // backward in time
+  float scale_p;          // on the products x . y
+  float scale_i;          // on the products with the state
+  float scale_u;          // on the state update
+  // states [Dk, Dv] fp32 per (b, h): element (channel, column) at
+  // channel * sr + column * sc
+  int sr, sc;
+  const float* start;       // [B*Hv] states the first segment walked starts from (null: zeros)
+  const float* seg_start;   // [nseg, B*Hv] start states (null: one segment)
+  float* end;               // state after the last segment walked (null: not written)
+  float* seg_sum;           // the walk only sums its segment's update into [nseg, B*Hv] (else null)
+  float* dots;              // sums for dlg (else null); see DecayStats
+  const float* cross;       // [B*Hv] states, dotted with the end state of every segment (dlg):
+  const float* seg_cross;   //   first segment's, and [nseg, B*Hv]
+};
+
+struct DecayWalkArgs {
+  DecayDims d;
+  const float* lg;          // [Hv]
+  const uint8_t* mask;      // may be null
+  int nseg, seg;            // segments, chunks per segment
+  int nwalk;
+  DecayWalk walk[2];        // walks of one launch, with the same KD, N class
+};
+
+// What the backward's walks hand to the reduction for dlg, fp32:
+//   dq walk: per (b, h, chunk, wave) the sums a0, a1 and the in-chunk sum
+//   dk walk: per (b, h, chunk, wave) the sums b0, b1, and the chunk's valid steps
+//   dv walk: per (b, h, segment, wave) the dot of the states at its start
+struct DecayReduceArgs {
+  DecayDims d;
+  const float* lg;
+  int nseg, seg, sub;       // sub: steps per stats chunk (64 bf16, 32 fp32)
+  const float *qa, *kb, *vx;
+  int nwk, nwv;             // waves of the dq / dk walks, and of the dv walk
+  float* dlg;               // [Hv]
+};
+constexpr int kDecayQStats = 3, kDecayKStats = 3;
+
+struct DecayChainArgs {
+  DecayDims d;
+  const float* lg;
+  const uint8_t* mask;
+  int nseg, seg;
+  float* states;            // [nseg, B*Hv, Dk*Dv]: segment sums in, start states out
+  const float* start;       // may be null
+  int reverse;
+};
+
+// dq / dk of a key head: the sum of its value heads' rows, rounded once.
+struct DecayGroupArgs {
+  DecayDims d;
+  const float *pq, *pk;     // [B, T, Hv, Dk] fp32
+  void *dq, *dk;            // [B, T, Hk, Dk]
+};
+
+struct DecayStepArgs {
+  DecayDims d;
+  const void *q, *k, *v;
+  const float* lg;
+  float scale;
+  const float* state0;
+  const uint8_t* mask;
+  void* o;
+  float* state_out;
+};
+
+int decay_waves(int N);     // waves of a walk with N columns
+
+hipError_t launch_decay_walk(const DecayWalkArgs& a, bool bf16, hipStream_t st);
+hipError_t launch_decay_chain(const DecayChainArgs* a, int n, hipStream_t st);
+hipError_t launch_decay_reduce(const DecayReduceArgs& a, hipStream_t st);
+hipError_t launch_decay_group(const DecayGroupArgs& a, bool bf16, hipStream_t st);
+hipError_t launch_decay_step(const DecayStepArgs& a, bool bf16, hipStream_t st);
+
+// ---- norm of queries and keys with rotation
+
+struct NormRopeArgs {
+  int64_t BT;               // tokens
+  int Hq, Hk, D, R, P;
+  int64_t qs, ks;           // elements from one token's rows to the next one's
+  int T;                    // positions when pos is null: token % T
+  int interleaved;
+  float eps, w_offset;
+  const void *q, *k;
+  const float *wq, *wk;     // [D]
+  const float* rope;        // [P, R]
+  const int32_t* pos;       // [BT], may be null
+  void *oq, *ok;            // forward: outputs
+  const void *dyq, *dyk;    // backward: cotangents
+  float* part;              // backward: [blocks, 2, D]
+  float *dwq, *dwk;
+  int blocks;
+};
+int norm_rope_blocks(int64_t BT, int Hq, int Hk, int D, bool bf16);
+hipError_t launch_norm_rope_fwd(const NormRopeArgs& a, bool bf16, hipStream_t st);
+hipError_t launch_norm_rope_bwd(const NormRopeArgs& a, bool bf16, hipStream_t st);
+
+}  // namespace gdn

@@ -1,0 +1,271 @@
+// Kernels of the decay operator beside the walks (gdn_decay_walk.h): the chain
+// over segment states, the reductions of the backward, and the single steps.
+#include "gdn_decay_walk.h"
+
+#include <limits.h>
+
+namespace gdn {
+
+int decay_waves(int N) { return N <= 64 ? 2 : N <= 128 ? 4 : N <= 192 ? 6 : 8; }
+
+hipError_t launch_decay_walk(const DecayWalkArgs& a, bool bf, hipStream_t st) {
+  const int KD = a.walk[0].KD;
+  if (KD <= 64) return bf ? decay_walk_bf16_64(a, st) : decay_walk_f32_64(a, st);
+  if (KD <= 128) return bf ? decay_walk_bf16_128(a, st) : decay_walk_f32_128(a, st);
+  if (KD <= 192) return bf ? decay_walk_bf16_192(a, st) : decay_walk_f32_192(a, st);
+  return bf ? decay_walk_bf16_256(a, st) : decay_walk_f32_256(a, st);
+}
+
+namespace {
+
+using decay::exp2_fast;
+using decay::log2_decay;
+
+// ---- chain: the segment sums U_s of one direction become the states before
+// each segment, start_{s+1} = g^{N_s} start_s + U_s with N_s the segment's valid
+// steps.  One thread per four elements of one (b, h) goes through the segments
+// (in walk order); the loads of eight segments are in flight together.
+struct ChainArgs {
+  DecayChainArgs c[2];
+};
+
+__global__ void __launch_bounds__(256) chain_kernel(ChainArgs aa) {
+  const DecayChainArgs& a = aa.c[blockIdx.z];
+  const DecayDims& d = a.d;
+  const int bh = blockIdx.x, b = bh / d.Hv, h = bh % d.Hv, BH = d.B * d.Hv;
+  const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
+  const int len = a.seg * kDecayChunk;
+  __shared__ float dec[kDecayMaxSeg];  // g^{N_s}
+  const float lg2 = log2_decay(a.lg[h]);
+  for (int s = w; s < a.nseg; s += 4) {
+    const int t0 = s * len, t1 = min(d.T, t0 + len);
+    int n = 0;
+    if (a.mask == nullptr) {
+      n = t1 - t0;
+    } else {
+      const uint8_t* m = a.mask + static_cast<size_t>(b) * d.T;
+      for (int t = t0 + l; t - l < t1; t += 64) n += __popcll(__ballot(t < t1 && m[t] != 0));
+    }
+    if (l == 0) dec[s] = exp2_fast(lg2 * static_cast<float>(n));
+  }
+  __syncthreads();
+  const size_t hs = static_cast<size_t>(d.Dk) * d.Dv;
+  const size_t e = (static_cast<size_t>(blockIdx.y) * 256 + threadIdx.x) * 4;
+  if (e >= hs) return;
+  float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (a.start) run = *reinterpret_cast<const float4*>(a.start + bh * hs + e);
+  const size_t step = static_cast<size_t>(BH) * hs;
+  float* p = a.states + bh * hs + e;
+  for (int s0 = 0; s0 < a.nseg; s0 += 8) {
+    float4 u[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int s = min(s0 + k, a.nseg - 1);
+      u[k] = *reinterpret_cast<const float4*>(p + (a.reverse ? a.nseg - 1 - s : s) * step);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (s0 + k >= a.nseg) break;
+      const int s = a.reverse ? a.nseg - 1 - (s0 + k) : s0 + k;
+      *reinterpret_cast<float4*>(p + s * step) = run;
+      const float f = dec[s];
+      run.x = fmaf(f, run.x, u[k].x);
+      run.y = fmaf(f, run.y, u[k].y);
+      run.z = fmaf(f, run.z, u[k].z);
+      run.w = fmaf(f, run.w, u[k].w);
+    }
+  }
+}
+
+// ---- dlg of one head.  A pair of a source step j and a later step i that reads
+// it weighs (valid steps after j up to i) times its share of the loss,
+//   f_ij = scale g^(n_i - n_j) (q_i . k_j)(dO_i . v_j),
+// likewise with the initial state for a source and dS_final for a reader.  Per
+// chunk: pairs inside it are summed in the dq walk; of pairs that enter, a1
+// holds the part of their steps inside the chunk (a0: the pairs' plain sum);
+// of pairs that leave, b1 (b0); pairs that pass through it cross all of its L
+// steps.  What crosses a boundary, X, follows from a0 and b0 chunk by chunk,
+// starting at each segment from the dot of the two states there, so that
+// rounding does not build up over a long sequence.  Where g^L is below 2^-24
+// nothing that counts passes through.
+__global__ void __launch_bounds__(256) reduce_kernel(DecayReduceArgs a) {
+  const DecayDims& d = a.d;
+  const int h = blockIdx.x, n = d.B * a.nseg;
+  const int nstat = (d.T + a.sub - 1) / a.sub, per = a.seg * kDecayChunk / a.sub;
+  const float lg2 = log2_decay(a.lg[h]);
+  double total = 0.0;
+  for (int i = threadIdx.x; i < n; i += 256) {
+    const int b = i / a.nseg, s = i % a.nseg;
+    const size_t bh = static_cast<size_t>(b) * d.Hv + h;
+    double X = 0.0;
+    for (int w = 0; w < a.nwv; ++w) X += a.vx[(bh * a.nseg + s) * a.nwv + w];
+    const int c1 = min(nstat, (s + 1) * per);
+    for (int c = s * per; c < c1; ++c) {
+      double a0 = 0, a1 = 0, in = 0, b0 = 0, b1 = 0;
+      const float* q = a.qa + (bh * nstat + c) * a.nwk * kDecayQStats;
+      const float* k = a.kb + (bh * nstat + c) * a.nwk * kDecayKStats;
+      const float L = k[2];
+      for (int w = 0; w < a.nwk; ++w) {
+        a0 += q[w * kDecayQStats];
+        a1 += q[w * kDecayQStats + 1];
+        in += q[w * kDecayQStats + 2];
+        b0 += k[w * kDecayKStats];
+        b1 += k[w * kDecayKStats + 1];
+      }
+      total += in + a1 + b1;
+      const double through = lg2 * L < -24.f ? 0.0 : X - a0;
+      total += L * through;
+      X = through + b0;
+    }
+  }
+  __shared__ double part[256];
+  part[threadIdx.x] = total;
+  __syncthreads();
+  for (int m = 128; m >= 1; m >>= 1) {
+    if (threadIdx.x < m) part[threadIdx.x] += part[threadIdx.x + m];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) a.dlg[h] = static_cast<float>(part[0]);
+}
+
+// ---- dq / dk of the key heads: their value heads' rows summed in fp32, in
+// head order, and rounded once.
+template <typename T>
+__global__ void __launch_bounds__(256) group_kernel(DecayGroupArgs a, size_t n) {
+  const DecayDims& d = a.d;
+  const int G = d.G();
+  const float* src = blockIdx.y ? a.pk : a.pq;
+  T* dst = static_cast<T*>(blockIdx.y ? a.dk : a.dq);
+  for (size_t i = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < n;
+       i += static_cast<size_t>(gridDim.x) * 1024) {
+    const size_t row = i / d.Dk, c = i % d.Dk;  // (token, key head), channel
+    const float* p = src + row * G * d.Dk + c;
+    float4 s = *reinterpret_cast<const float4*>(p);
+    for (int g = 1; g < G; ++g) {
+      const float4 v = *reinterpret_cast<const float4*>(p + static_cast<size_t>(g) * d.Dk);
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+    if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(dst + i) = pack4_bf16(s.x, s.y, s.z, s.w);
+    else *reinterpret_cast<float4*>(dst + i) = s;
+  }
+}
+
+// ---- single steps, S <- g S + k v^T, o = scale S^T q, T of them in turn.  The
+// state is the whole traffic of a single step, read and written once.  One
+// wave per 32 columns of one (b, h): lane 8 rg + cq holds rows rg RL .. + RL - 1 of
+// columns 4 cq .. + 3, so eight lanes cover 128 contiguous bytes of a row.
+template <typename T, int DK>
+__global__ void __launch_bounds__(64) step_kernel(DecayStepArgs p, int slices) {
+  constexpr int RL = DK / 8;
+  const DecayDims& d = p.d;
+  const int bh = blockIdx.x / slices, w = blockIdx.x % slices, b = bh / d.Hv, h = bh % d.Hv, j = h / d.G();
+  const int l = threadIdx.x, rg = l >> 3, cq = l & 7, col = 32 * w + 4 * cq;
+  const size_t hs = static_cast<size_t>(d.Dk) * d.Dv;
+  const uint32_t bytes = static_cast<uint32_t>(hs * 4);
+  // rows past Dk lie past the descriptor's size; columns past Dv are sent there
+  uint32_t off[RL];
+#pragma unroll
+  for (int r = 0; r < RL; ++r)
+    off[r] = col < d.Dv && rg * RL + r < d.Dk ? 4u * ((rg * RL + r) * d.Dv + col) : 0xfffffff0u;
+  const rsrc_t rs0 = make_rsrc(p.state0 ? static_cast<const void*>(p.state0 + bh * hs) : p.state_out, p.state0 ? bytes : 0);
+  float4 s[RL];
+#pragma unroll
+  for (int r = 0; r < RL; ++r) s[r] = buf_f4(rs0, off[r]);
+  const float gate = exp2_fast(log2_decay(p.lg[h]));
+  for (int t = 0; t < d.T; ++t) {
+    const size_t bt = static_cast<size_t>(b) * d.T + t;
+    const T* qr = static_cast<const T*>(p.q) + (bt * d.Hk + j) * d.Dk;
+    const T* kr = static_cast<const T*>(p.k) + (bt * d.Hk + j) * d.Dk;
+    const T* vr = static_cast<const T*>(p.v) + (bt * d.Hv + h) * d.Dv + col;
+    const bool on = col < d.Dv;
+    float q[RL], k[RL], v[4];
+#pragma unroll
+    for (int r = 0; r < RL; ++r) {
+      const bool in = rg * RL + r < d.Dk;
+      q[r] = in ? to_f32(qr[rg * RL + r]) * p.scale : 0.f;
+      k[r] = in ? to_f32(kr[rg * RL + r]) : 0.f;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = on ? to_f32(vr[c]) : 0.f;
+    if (p.mask == nullptr || p.mask[bt] != 0) {
+#pragma unroll
+      for (int r = 0; r < RL; ++r) {
+        s[r].x = fmaf(k[r], v[0], gate * s[r].x);
+        s[r].y = fmaf(k[r], v[1], gate * s[r].y);
+        s[r].z = fmaf(k[r], v[2], gate * s[r].z);
+        s[r].w = fmaf(k[r], v[3], gate * s[r].w);
+      }
+    }
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < RL; ++r) {
+      o.x = fmaf(q[r], s[r].x, o.x);
+      o.y = fmaf(q[r], s[r].y, o.y);
+      o.z = fmaf(q[r], s[r].z, o.z);
+      o.w = fmaf(q[r], s[r].w, o.w);
+    }
+#pragma unroll
+    for (int m = 8; m <= 32; m <<= 1) {
+      o.x += __shfl_xor(o.x, m);
+      o.y += __shfl_xor(o.y, m);
+      o.z += __shfl_xor(o.z, m);
+      o.w += __shfl_xor(o.w, m);
+    }
+    if (rg == 0 && on) {
+      T* orow = static_cast<T*>(p.o) + (bt * d.Hv + h) * d.Dv + col;
+      if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(orow) = pack4_bf16(o.x, o.y, o.z, o.w);
+      else *reinterpret_cast<float4*>(orow) = o;
+    }
+  }
+  const rsrc_t rs1 = make_rsrc(p.state_out + bh * hs, bytes);
+#pragma unroll
+  for (int r = 0; r < RL; ++r)
+    buf_store_u4(rs1, off[r], make_uint4(__float_as_uint(s[r].x), __float_as_uint(s[r].y), __float_as_uint(s[r].z),
+                                         __float_as_uint(s[r].w)));
+}
+
+template <typename T>
+hipError_t launch_step(const DecayStepArgs& a, hipStream_t st) {
+  const int slices = (a.d.Dv + 31) / 32, n = a.d.B * a.d.Hv * slices;
+  if (a.d.Dk <= 16) step_kernel<T, 16><<<n, 64, 0, st>>>(a, slices);
+  else if (a.d.Dk <= 32) step_kernel<T, 32><<<n, 64, 0, st>>>(a, slices);
+  else if (a.d.Dk <= 64) step_kernel<T, 64><<<n, 64, 0, st>>>(a, slices);
+  else if (a.d.Dk <= 128) step_kernel<T, 128><<<n, 64, 0, st>>>(a, slices);
+  else if (a.d.Dk <= 192) step_kernel<T, 192><<<n, 64, 0, st>>>(a, slices);
+  else step_kernel<T, 256><<<n, 64, 0, st>>>(a, slices);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_decay_chain(const DecayChainArgs* a, int n, hipStream_t st) {
+  ChainArgs c;
+  for (int i = 0; i < 2; ++i) c.c[i] = a[i < n ? i : 0];
+  const DecayDims& d = a[0].d;
+  const size_t hs = static_cast<size_t>(d.Dk) * d.Dv;
+  chain_kernel<<<dim3(d.B * d.Hv, static_cast<unsigned>((hs + 1023) / 1024), n), 256, 0, st>>>(c);
+  return hipGetLastError();
+}
+
+hipError_t launch_decay_reduce(const DecayReduceArgs& a, hipStream_t st) {
+  reduce_kernel<<<a.d.Hv, 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_decay_group(const DecayGroupArgs& a, bool bf, hipStream_t st) {
+  const size_t n = static_cast<size_t>(a.d.B) * a.d.T * a.d.Hk * a.d.Dk;
+  const size_t blocks = (n + 1023) / 1024;
+  const dim3 grid(static_cast<unsigned>(blocks < 4096 ? blocks : 4096), 2);
+  if (bf) group_kernel<gdn::bf16><<<grid, 256, 0, st>>>(a, n);
+  else group_kernel<float><<<grid, 256, 0, st>>>(a, n);
+  return hipGetLastError();
+}
+
+hipError_t launch_decay_step(const DecayStepArgs& a, bool bf, hipStream_t st) {
+  return bf ? launch_step<gdn::bf16>(a, st) : launch_step<float>(a, st);
+}
+
+}  // namespace gdn

@@ -1,0 +1,367 @@
+// C ABI of the decay operator and of the query/key norm with rotation (declared
+// in include/gdn.h): argument validation, workspace layout and launch order.
+// No allocation, no host sync.
+#include "../../include/gdn.h"
+#include "gdn_decay.h"
+
+#include <limits.h>
+
+namespace {
+
+using gdn::DecayDims;
+
+size_t align_up(size_t n) { return (n + 255) / 256 * 256; }
+bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+template <typename... P> bool all_aligned(P... p) { return (aligned(p) && ...); }
+template <typename... P> bool all_given(P... p) { return (... && (p != nullptr)); }
+
+int check_dims(const gdn_dims* p, bool bwd, DecayDims* out) {
+  if (!p) return GDN_ERR_INVALID_ARG;
+  if (p->B < 1 || p->T < 0 || p->Hk < 1 || p->Hv < 1 || p->Dk < 1 || p->Dv < 1) return GDN_ERR_INVALID_ARG;
+  if (p->Hv % p->Hk != 0) return GDN_ERR_INVALID_ARG;
+  if (p->dtype != GDN_F32 && p->dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
+  if (p->algo != GDN_ALGO_AUTO && p->algo != GDN_ALGO_SCAN && p->algo != GDN_ALGO_CHUNK &&
+      p->algo != GDN_ALGO_CHUNK_TPAR)
+    return GDN_ERR_INVALID_ARG;
+  if (bwd && p->algo == GDN_ALGO_SCAN) return GDN_ERR_UNSUPPORTED;
+  if (p->Dk % 8 || p->Dv % 8 || p->Dk > 256 || p->Dv > 256) return GDN_ERR_UNSUPPORTED;
+  // counts that the kernels hold in 32 bits: steps, heads, (b, h) pairs times
+  // their slices or segments (the tensors themselves are addressed in 64)
+  if (p->T > INT_MAX / 2 || p->Hv > INT_MAX / 1024 || p->B > INT_MAX / 1024 ||
+      static_cast<double>(p->B) * p->Hv * gdn::kDecayMaxSeg * 2 > INT_MAX ||
+      static_cast<double>(p->B) * p->T * p->Hv > 9.0e12)
+    return GDN_ERR_UNSUPPORTED;
+  *out = DecayDims{static_cast<int>(p->B),  static_cast<int>(p->T),  static_cast<int>(p->Hk),
+                   static_cast<int>(p->Hv), static_cast<int>(p->Dk), static_cast<int>(p->Dv)};
+  return GDN_OK;
+}
+
+bool use_step(const gdn_dims* p) { return p->algo == GDN_ALGO_SCAN || (p->algo == GDN_ALGO_AUTO && p->T == 1); }
+
+// Chunks per segment and segments.
+struct Cut {
+  int seg, n;
+};
+Cut cut(const gdn_dims* p, const DecayDims& d, bool bwd) {
+  const int nc = d.nchunk();
+  int n = 1;
+  if (p->algo != GDN_ALGO_CHUNK && nc > 1) {
+    const int want = 512, bh = d.B * d.Hv;
+    n = (want + bh - 1) / bh;
+  }
+  // the backward's sums for dlg follow the boundaries chunk by chunk from the
+  // start of a segment: short segments keep their rounding down
+  if (bwd && n < (nc + 15) / 16) n = (nc + 15) / 16;
+  if (n > gdn::kDecayMaxSeg) n = gdn::kDecayMaxSeg;
+  if (n > nc) n = nc;
+  if (n < 1) n = 1;
+  Cut c;
+  c.seg = nc ? (nc + n - 1) / n : 1;
+  c.n = nc ? (nc + c.seg - 1) / c.seg : 1;
+  return c;
+}
+
+struct Layout {
+  size_t S, R;            // segment states, forward and backward in time
+  size_t qa, kb, vx;      // sums for dlg
+  size_t pq, pk;          // rows of grouped heads
+  size_t total;
+};
+
+Layout layout(const gdn_dims* p, const DecayDims& d, bool bwd) {
+  Layout L{};
+  size_t off = 0;
+  auto take = [&](size_t nfloat) {
+    const size_t o = off;
+    off += align_up(nfloat * sizeof(float));
+    return o;
+  };
+  const Cut c = cut(p, d, bwd);
+  const size_t bh = static_cast<size_t>(d.B) * d.Hv;
+  const size_t states = static_cast<size_t>(c.n) * bh * d.Dk * d.Dv;
+  if (c.n > 1) L.S = take(states);
+  if (bwd) {
+    if (c.n > 1) L.R = take(states);
+    const int sub = p->dtype == GDN_BF16 ? 64 : 32;
+    const size_t nstat = (static_cast<size_t>(d.T) + sub - 1) / sub, nwk = gdn::decay_waves(d.Dk);
+    L.qa = take(bh * nstat * nwk * gdn::kDecayQStats);
+    L.kb = take(bh * nstat * nwk * gdn::kDecayKStats);
+    L.vx = take(bh * c.n * gdn::decay_waves(d.Dv));
+    if (d.G() > 1) {
+      const size_t rows = static_cast<size_t>(d.B) * d.T * d.Hv * d.Dk;
+      L.pq = take(rows);
+      L.pk = take(rows);
+    }
+  }
+  L.total = off;
+  return L;
+}
+
+template <typename P> P* at(void* ws, size_t off) { return reinterpret_cast<P*>(static_cast<char*>(ws) + off); }
+
+struct Rows {
+  gdn::DecayRows key, val;
+};
+gdn::DecayRows key_rows(const DecayDims& d, const void* p) { return gdn::DecayRows{p, d.Hk, d.Dk, d.G()}; }
+gdn::DecayRows val_rows(const DecayDims& d, const void* p) { return gdn::DecayRows{p, d.Hv, d.Dv, 1}; }
+
+// Walks whose state is [Dk, Dv] as stored (o, dv), and transposed (dq, dk).
+gdn::DecayWalk walk_kv(const DecayDims& d) {
+  gdn::DecayWalk w{};
+  w.KD = d.Dk;
+  w.N = d.Dv;
+  w.sr = d.Dv;
+  w.sc = 1;
+  return w;
+}
+gdn::DecayWalk walk_vk(const DecayDims& d) {
+  gdn::DecayWalk w{};
+  w.KD = d.Dv;
+  w.N = d.Dk;
+  w.sr = 1;
+  w.sc = d.Dv;
+  return w;
+}
+
+int check_norm(const gdn_norm_dims* p, gdn::NormRopeArgs* a) {
+  if (!p) return GDN_ERR_INVALID_ARG;
+  if (p->B < 1 || p->T < 0 || p->Hq < 1 || p->Hk < 1 || p->D < 1 || p->R < 0 || p->P < 0) return GDN_ERR_INVALID_ARG;
+  if (p->dtype != GDN_F32 && p->dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
+  if (p->D % 8 || p->D > 512) return GDN_ERR_UNSUPPORTED;
+  if (p->R > p->D) return GDN_ERR_INVALID_ARG;
+  if (p->R % 16) return GDN_ERR_UNSUPPORTED;
+  if (!(p->eps >= 0.f)) return GDN_ERR_INVALID_ARG;
+  if (p->Hq > INT_MAX / 1024 || p->Hk > INT_MAX / 1024 || p->P > INT_MAX || p->B > INT_MAX || p->T > INT_MAX ||
+      static_cast<double>(p->B) * p->T > INT_MAX / 2)
+    return GDN_ERR_UNSUPPORTED;
+  const int64_t qs = p->q_stride ? p->q_stride : p->Hq * p->D, ks = p->k_stride ? p->k_stride : p->Hk * p->D;
+  const int64_t unit = p->dtype == GDN_BF16 ? 8 : 4;
+  if (qs < p->Hq * p->D || ks < p->Hk * p->D || qs % unit || ks % unit || qs > INT_MAX || ks > INT_MAX)
+    return GDN_ERR_INVALID_ARG;
+  *a = gdn::NormRopeArgs{};
+  a->BT = p->B * p->T;
+  a->Hq = static_cast<int>(p->Hq);
+  a->Hk = static_cast<int>(p->Hk);
+  a->D = static_cast<int>(p->D);
+  a->R = static_cast<int>(p->R);
+  a->P = static_cast<int>(p->P);
+  a->qs = qs;
+  a->ks = ks;
+  a->T = static_cast<int>(p->T);
+  a->interleaved = p->interleaved != 0;
+  a->eps = p->eps;
+  a->w_offset = p->w_offset;
+  a->blocks = gdn::norm_rope_blocks(a->BT, a->Hq, a->Hk, a->D, p->dtype == GDN_BF16);
+  return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gdn_decay_fwd_workspace_bytes(const gdn_dims* d, size_t* out) {
+  DecayDims dd;
+  const int rc = check_dims(d, false, &dd);
+  if (rc) return rc;
+  if (!out) return GDN_ERR_INVALID_ARG;
+  *out = use_step(d) ? 0 : layout(d, dd, false).total;
+  return GDN_OK;
+}
+
+int gdn_decay_bwd_workspace_bytes(const gdn_dims* d, size_t* out) {
+  DecayDims dd;
+  const int rc = check_dims(d, true, &dd);
+  if (rc) return rc;
+  if (!out) return GDN_ERR_INVALID_ARG;
+  *out = layout(d, dd, true).total;
+  return GDN_OK;
+}
+
+int gdn_decay_fwd(const gdn_dims* d, const void* q, const void* k, const void* v, const float* lg,
+                  float scale, const float* state0, const uint8_t* mask, void* o, float* state_out,
+                  void* ws, size_t ws_bytes, void* stream) {
+  DecayDims dd;
+  const int rc = check_dims(d, false, &dd);
+  if (rc) return rc;
+  if (!all_given(lg, state_out)) return GDN_ERR_INVALID_ARG;
+  if (dd.T > 0 && !all_given(q, k, v, o)) return GDN_ERR_INVALID_ARG;
+  if (!all_aligned(q, k, v, state0, o, state_out)) return GDN_ERR_INVALID_ARG;
+  const bool bf = d->dtype == GDN_BF16;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (use_step(d)) {
+    const gdn::DecayStepArgs a{dd, q, k, v, lg, scale, state0, mask, o, state_out};
+    return gdn::launch_decay_step(a, bf, st) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+  }
+  const Layout L = layout(d, dd, false);
+  if (L.total > ws_bytes || (L.total > 0 && !ws)) return GDN_ERR_WORKSPACE;
+  if (L.total > 0 && !aligned(ws)) return GDN_ERR_INVALID_ARG;
+  const Cut c = cut(d, dd, false);
+  gdn::DecayWalk w = walk_kv(dd);
+  w.x = key_rows(dd, q);
+  w.y = key_rows(dd, k);
+  w.z = val_rows(dd, v);
+  w.w = o;
+  w.scale_p = w.scale_i = scale;
+  w.scale_u = 1.f;
+  w.start = state0;
+  w.end = state_out;
+  gdn::DecayWalkArgs a{dd, lg, mask, c.n, c.seg, 1, {w, w}};
+  if (c.n > 1) {
+    float* S = at<float>(ws, L.S);
+    gdn::DecayWalkArgs sum = a;
+    sum.walk[0].seg_sum = S;
+    if (gdn::launch_decay_walk(sum, bf, st) != hipSuccess) return GDN_ERR_HIP;
+    const gdn::DecayChainArgs ch{dd, lg, mask, c.n, c.seg, S, state0, 0};
+    if (gdn::launch_decay_chain(&ch, 1, st) != hipSuccess) return GDN_ERR_HIP;
+    a.walk[0].seg_start = S;
+  }
+  return gdn::launch_decay_walk(a, bf, st) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+int gdn_decay_bwd(const gdn_dims* d, const void* q, const void* k, const void* v, const float* lg,
+                  float scale, const float* state0, const uint8_t* mask, const void* dO,
+                  const float* dS_final, void* dq, void* dk, void* dv, float* dlg, float* dstate,
+                  void* ws, size_t ws_bytes, void* stream) {
+  DecayDims dd;
+  const int rc = check_dims(d, true, &dd);
+  if (rc) return rc;
+  if (!all_given(lg, dlg, dstate)) return GDN_ERR_INVALID_ARG;
+  if (dd.T > 0 && !all_given(q, k, v, dO, dq, dk, dv)) return GDN_ERR_INVALID_ARG;
+  if (!all_aligned(q, k, v, state0, dO, dS_final, dq, dk, dv, dstate)) return GDN_ERR_INVALID_ARG;
+  const Layout L = layout(d, dd, true);
+  if (L.total > ws_bytes || (L.total > 0 && !ws)) return GDN_ERR_WORKSPACE;
+  if (L.total > 0 && !aligned(ws)) return GDN_ERR_INVALID_ARG;
+  const bool bf = d->dtype == GDN_BF16;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const Cut c = cut(d, dd, true);
+  const bool grouped = dd.G() > 1;
+
+  gdn::DecayWalk wq = walk_vk(dd);  // dq
+  wq.x = val_rows(dd, dO);
+  wq.y = val_rows(dd, v);
+  wq.z = key_rows(dd, k);
+  wq.e = key_rows(dd, q);
+  wq.w = grouped ? at<void>(ws, L.pq) : dq;
+  wq.w32 = grouped;
+  wq.scale_p = wq.scale_i = scale;
+  wq.scale_u = 1.f;
+  wq.start = state0;
+  wq.dots = at<float>(ws, L.qa);
+
+  gdn::DecayWalk wk = walk_vk(dd);  // dk
+  wk.x = val_rows(dd, v);
+  wk.y = val_rows(dd, dO);
+  wk.z = key_rows(dd, q);
+  wk.e = key_rows(dd, k);
+  wk.w = grouped ? at<void>(ws, L.pk) : dk;
+  wk.w32 = grouped;
+  wk.reverse = 1;
+  wk.scale_p = wk.scale_u = scale;
+  wk.scale_i = 1.f;
+  wk.start = dS_final;
+  wk.dots = at<float>(ws, L.kb);
+
+  gdn::DecayWalk wv = walk_kv(dd);  // dv, dstate
+  wv.x = key_rows(dd, k);
+  wv.y = key_rows(dd, q);
+  wv.z = val_rows(dd, dO);
+  wv.w = dv;
+  wv.reverse = 1;
+  wv.scale_p = wv.scale_u = scale;
+  wv.scale_i = 1.f;
+  wv.start = dS_final;
+  wv.end = dstate;
+  wv.dots = at<float>(ws, L.vx);
+  wv.cross = state0;
+
+  if (c.n > 1) {
+    float *S = at<float>(ws, L.S), *R = at<float>(ws, L.R);
+    gdn::DecayWalk ws_ = walk_kv(dd), wr = wv;
+    ws_.y = key_rows(dd, k);
+    ws_.z = val_rows(dd, v);
+    ws_.scale_u = 1.f;
+    ws_.seg_sum = S;
+    wr.seg_sum = R;
+    const gdn::DecayWalkArgs sum{dd, lg, mask, c.n, c.seg, 2, {ws_, wr}};
+    if (gdn::launch_decay_walk(sum, bf, st) != hipSuccess) return GDN_ERR_HIP;
+    const gdn::DecayChainArgs ch[2] = {{dd, lg, mask, c.n, c.seg, S, state0, 0},
+                                       {dd, lg, mask, c.n, c.seg, R, dS_final, 1}};
+    if (gdn::launch_decay_chain(ch, 2, st) != hipSuccess) return GDN_ERR_HIP;
+    wq.seg_start = S;
+    wk.seg_start = R;
+    wv.seg_start = R;
+    wv.seg_cross = S;
+  }
+  const gdn::DecayWalkArgs av{dd, lg, mask, c.n, c.seg, 1, {wv, wv}};
+  if (gdn::launch_decay_walk(av, bf, st) != hipSuccess) return GDN_ERR_HIP;
+  const gdn::DecayWalkArgs aqk{dd, lg, mask, c.n, c.seg, 2, {wq, wk}};
+  if (gdn::launch_decay_walk(aqk, bf, st) != hipSuccess) return GDN_ERR_HIP;
+  if (grouped && dd.T > 0) {
+    const gdn::DecayGroupArgs ga{dd, at<float>(ws, L.pq), at<float>(ws, L.pk), dq, dk};
+    if (gdn::launch_decay_group(ga, bf, st) != hipSuccess) return GDN_ERR_HIP;
+  }
+  const gdn::DecayReduceArgs ra{dd, lg, c.n, c.seg, bf ? 64 : 32, wq.dots, wk.dots, wv.dots,
+                                gdn::decay_waves(dd.Dk), gdn::decay_waves(dd.Dv), dlg};
+  return gdn::launch_decay_reduce(ra, st) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+int gdn_norm_rope_fwd(const gdn_norm_dims* d, const void* q, const void* k, const float* wq,
+                      const float* wk, const float* rope, const int32_t* pos, void* oq, void* ok,
+                      void* stream) {
+  gdn::NormRopeArgs a;
+  const int rc = check_norm(d, &a);
+  if (rc) return rc;
+  if (!all_given(wq, wk) || (a.R > 0 && !rope)) return GDN_ERR_INVALID_ARG;
+  if (a.BT > 0 && !all_given(q, k, oq, ok)) return GDN_ERR_INVALID_ARG;
+  if (!all_aligned(q, k, wq, wk, rope, oq, ok)) return GDN_ERR_INVALID_ARG;
+  a.q = q;
+  a.k = k;
+  a.wq = wq;
+  a.wk = wk;
+  a.rope = rope;
+  a.pos = pos;
+  a.oq = oq;
+  a.ok = ok;
+  return gdn::launch_norm_rope_fwd(a, d->dtype == GDN_BF16, static_cast<hipStream_t>(stream)) == hipSuccess
+             ? GDN_OK : GDN_ERR_HIP;
+}
+
+int gdn_norm_rope_bwd_workspace_bytes(const gdn_norm_dims* d, size_t* out) {
+  gdn::NormRopeArgs a;
+  const int rc = check_norm(d, &a);
+  if (rc) return rc;
+  if (!out) return GDN_ERR_INVALID_ARG;
+  *out = align_up(static_cast<size_t>(a.blocks) * 2 * a.D * sizeof(float));
+  return GDN_OK;
+}
+
+int gdn_norm_rope_bwd(const gdn_norm_dims* d, const void* q, const void* k, const float* wq,
+                      const float* wk, const float* rope, const int32_t* pos, const void* dyq,
+                      const void* dyk, void* dq, void* dk, float* dwq, float* dwk, void* ws,
+                      size_t ws_bytes, void* stream) {
+  gdn::NormRopeArgs a;
+  const int rc = check_norm(d, &a);
+  if (rc) return rc;
+  if (!all_given(wq, wk, dwq, dwk) || (a.R > 0 && !rope)) return GDN_ERR_INVALID_ARG;
+  if (a.BT > 0 && !all_given(q, k, dyq, dyk, dq, dk)) return GDN_ERR_INVALID_ARG;
+  if (!all_aligned(q, k, wq, wk, rope, dyq, dyk, dq, dk, dwq, dwk)) return GDN_ERR_INVALID_ARG;
+  const size_t need = align_up(static_cast<size_t>(a.blocks) * 2 * a.D * sizeof(float));
+  if (need > ws_bytes || (need > 0 && !ws)) return GDN_ERR_WORKSPACE;
+  a.q = q;
+  a.k = k;
+  a.wq = wq;
+  a.wk = wk;
+  a.rope = rope;
+  a.pos = pos;
+  a.dyq = dyq;
+  a.dyk = dyk;
+  a.oq = dq;
+  a.ok = dk;
+  a.part = static_cast<float*>(ws);
+  a.dwq = dwq;
+  a.dwk = dwk;
+  return gdn::launch_norm_rope_bwd(a, d->dtype == GDN_BF16, static_cast<hipStream_t>(stream)) == hipSuccess
+             ? GDN_OK : GDN_ERR_HIP;
+}
+
+}  // extern "C"

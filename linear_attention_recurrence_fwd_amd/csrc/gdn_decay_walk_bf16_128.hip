@@ -1,0 +1,6 @@
+// Walks of the decay operator over up to 128 channels, bf16 tensors.
+#include "gdn_decay_walk.h"
+
+namespace gdn {
+hipError_t decay_walk_bf16_128(const DecayWalkArgs& a, hipStream_t st) { return decay::launch_kd<bf16, 128>(a, st); }
+}  // namespace gdn

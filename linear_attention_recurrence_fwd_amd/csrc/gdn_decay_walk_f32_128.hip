@@ -1,0 +1,6 @@
+// Walks of the decay operator over up to 128 channels, f32 tensors.
+#include "gdn_decay_walk.h"
+
+namespace gdn {
+hipError_t decay_walk_f32_128(const DecayWalkArgs& a, hipStream_t st) { return decay::launch_kd<float, 128>(a, st); }
+}  // namespace gdn

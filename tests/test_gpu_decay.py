@@ -1,0 +1,199 @@
+"""The decay operator (gdn_decay_fwd, gdn_decay_bwd, through the binding)
+against a 64-bit reference that goes one step after the other, with the bounds
+derived in decay_reference.py."""
+import pytest
+import torch
+
+import decay_reference as R
+from helpers import say
+from linear_attention_recurrence_fwd_amd import binding
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    binding.lib()
+
+
+def make(B, T, Hk, Hv, Dk, Dv, dtype, seed, mask="none", state=True, lg=None):
+    g = torch.Generator().manual_seed(seed)
+
+    def rnd(*s, dt=dtype):
+        return torch.randn(s, generator=g).to(dt)
+    t = dict(q=rnd(B, T, Hk, Dk), k=rnd(B, T, Hk, Dk), v=rnd(B, T, Hv, Dv), dO=rnd(B, T, Hv, Dv),
+             lg=-torch.exp2(-8.0 * torch.rand((Hv,), generator=g)),
+             state0=rnd(B, Hv, Dk, Dv, dt=F32) if state else None, dS=rnd(B, Hv, Dk, Dv, dt=F32) if state else None)
+    if lg is not None:
+        t["lg"] = torch.full((Hv,), float(lg)) if not isinstance(lg, (list, tuple)) else torch.tensor(lg)
+    m = None
+    if mask != "none":
+        m = torch.ones((B, T), dtype=torch.uint8)
+        n = torch.randint(0, T + 1, (B,), generator=g)
+        n[0] = 0  # one row without a valid step
+        for b in range(B):
+            if mask == "behind":
+                m[b, int(n[b]):] = 0
+            elif mask == "before":
+                m[b, : T - int(n[b])] = 0
+        if mask == "some":
+            m = (torch.rand((B, T), generator=g) < 0.6).to(torch.uint8)
+            m[0] = 0
+        bad = m == 0
+        for x in ("k", "v"):  # what stands at masked steps is not read
+            t[x][bad] = float("nan")
+        t["k"][bad.nonzero()[::2].unbind(1)] = float("inf")
+    t["mask"] = m
+    return t
+
+
+def up(t):
+    return {n: None if x is None else x.cuda() for n, x in t.items()}
+
+
+def f64(x):
+    return None if x is None else x.double()
+
+
+def run_both(t, algo=binding.ALGO_AUTO, bwd=True, scale=None, tag=""):
+    dtype = t["q"].dtype
+    rounded = dtype == BF
+    c = up(t)
+    o, st = binding.decay_fwd(c["q"], c["k"], c["v"], c["lg"], c["state0"], c["mask"], algo=algo, scale=scale)
+    torch.cuda.synchronize()
+    k, v = R.clean(f64(t["k"]), f64(t["v"]), t["mask"])
+    q, lg, s0 = f64(t["q"]), f64(t["lg"]), f64(t["state0"])
+    B, T, Hk, Dk = q.shape
+    Dv = v.shape[3]
+    sc = None if scale is None else abs(scale)
+    ro, rst = R.decay(q, k, v, lg, s0, t["mask"], scale)
+    mo, mst = R.decay(q.abs(), k.abs(), v.abs(), lg, None if s0 is None else s0.abs(), t["mask"], sc)
+    terms = Dk + Dv + 128 + T
+    errs = {"o": R.check("o", o, ro, mo, dtype, terms, rounded),
+            "state": R.check("state", st, rst, mst, dtype, terms, False)}
+    norm = {"o": R.NORM[rounded], "state": R.NORM[False]}
+    if bwd:
+        # the VJP knows one algo less
+        balgo = binding.ALGO_AUTO if algo == binding.ALGO_SCAN else algo
+        g = binding.decay_bwd(c["q"], c["k"], c["v"], c["lg"], c["state0"], c["mask"], c["dO"], c["dS"], algo=balgo,
+                              scale=scale)
+        torch.cuda.synchronize()
+        dO, dS = f64(t["dO"]), f64(t["dS"])
+        rg = R.decay_grads(q, k, v, lg, s0, t["mask"], dO, dS, scale)
+        ab = lambda x: None if x is None else x.abs()  # noqa: E731
+        mg = R.decay_grads(q.abs(), k.abs(), v.abs(), lg, ab(s0), t["mask"], dO.abs(), ab(dS), sc)
+        # dlg: sums over pairs weighted with distances of up to 64 a chunk on top of their own
+        like = R.decay_grads(q.abs(), k.abs(), v.abs(), lg, ab(s0), t["mask"], dO.abs(), ab(dS), sc)
+        flow = (ro.new_tensor(0.0) + (mo * dO.abs()).sum((0, 1, 3)))
+        if dS is not None:
+            flow = flow + (mst * dS.abs()).sum((0, 2, 3))
+        mg["dlg"] = like["dlg"].abs() + 64 * flow
+        for n in ("dq", "dk", "dv"):
+            errs[n] = R.check(n, g[n], rg[n], mg[n], dtype, terms + Hk, rounded)
+            norm[n] = R.NORM[rounded]
+        errs["dstate"] = R.check("dstate", g["dstate"], rg["dstate"], mg["dstate"], dtype, terms, False)
+        errs["dlg"] = R.check("dlg", g["dlg"], rg["dlg"], mg["dlg"], dtype, terms, False)
+        norm["dstate"] = norm["dlg"] = R.NORM[False]
+        if t["mask"] is not None:
+            bad = (t["mask"] == 0).cuda()
+            assert (g["dv"][bad] == 0).all() and (g["dk"][bad] == 0).all()
+    say("[decay %s] %s" % (tag, " ".join("%s=%.1e" % kv for kv in errs.items())))
+    for n, e in errs.items():
+        assert e <= norm[n], (n, e, norm[n])
+    return o, st
+
+
+SIZES = [  # B, T, Hk, Hv, Dk, Dv
+    (1, 2, 1, 1, 8, 8), (2, 31, 1, 2, 16, 8), (2, 33, 2, 2, 64, 32), (1, 64, 2, 4, 64, 64), (3, 65, 1, 1, 40, 72),
+    (2, 130, 2, 4, 128, 128), (1, 200, 1, 2, 192, 128), (1, 96, 1, 1, 256, 256), (2, 191, 3, 3, 96, 200),
+    (1, 257, 1, 3, 128, 8), (1, 129, 1, 1, 8, 256),
+]
+
+
+@pytest.mark.parametrize("mask", ["none", "behind", "before", "some"])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("size", SIZES, ids=lambda s: "x".join(map(str, s)))
+def test_parity(size, dtype, mask):
+    say("[decay] size=%s dtype=%s mask=%s" % (size, dtype, mask))
+    run_both(make(*size, dtype, 100 + sum(size), mask), tag="%s %s" % (size, mask))
+
+
+@pytest.mark.parametrize("algo", [binding.ALGO_SCAN, binding.ALGO_CHUNK, binding.ALGO_CHUNK_TPAR])
+@pytest.mark.parametrize("T", [1, 3, 64, 300, 777])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_every_form(dtype, T, algo):
+    """The per-step form, one pass and parallel segments, each against the reference."""
+    say("[decay form] dtype=%s T=%d algo=%d" % (dtype, T, algo))
+    run_both(make(2, T, 2, 4, 64, 48, dtype, 7 + T, "some"), algo, tag="algo %d T %d" % (algo, T))
+
+
+@pytest.mark.parametrize("lg", [0.0, -1e-4, -3.0, -40.0, -1e30, float("-inf"), 0.01])
+def test_decays(lg):
+    """No decay, slow and fast ones, a state dropped at every step, growth."""
+    t = make(2, 150, 1, 2, 64, 64, F32, 11, "some", lg=lg)
+    if lg < -1e3:  # the reference's derivative is 0 * inf there: exp(lg) = 0 exactly, so dlg = 0
+        c = up(t)
+        g = binding.decay_bwd(c["q"], c["k"], c["v"], c["lg"], c["state0"], c["mask"], c["dO"], c["dS"])
+        assert (g["dlg"] == 0).all()
+        run_both(dict(t, lg=torch.full_like(t["lg"], -800.0)), tag="lg -800")
+        o, st = binding.decay_fwd(c["q"], c["k"], c["v"], c["lg"], c["state0"], c["mask"])
+        d = torch.full_like(c["lg"], -800.0)
+        o2, st2 = binding.decay_fwd(c["q"], c["k"], c["v"], d, c["state0"], c["mask"])
+        assert torch.equal(o, o2) and torch.equal(st, st2)
+        return
+    run_both(t, tag="lg %g" % lg)
+
+
+def test_no_state_and_scale():
+    run_both(make(2, 100, 2, 2, 64, 64, BF, 5, state=False), tag="no state")
+    run_both(make(1, 100, 1, 2, 64, 64, F32, 6), scale=-2.5, tag="scale")
+    run_both(make(1, 100, 1, 2, 64, 64, F32, 6), scale=0.0, tag="scale 0")
+
+
+@pytest.mark.parametrize("algo", [binding.ALGO_AUTO, binding.ALGO_SCAN, binding.ALGO_CHUNK])
+def test_empty(algo):
+    t = up(make(2, 0, 1, 2, 64, 32, BF, 3))
+    o, st = binding.decay_fwd(t["q"], t["k"], t["v"], t["lg"], t["state0"], None, algo=algo)
+    assert o.shape == (2, 0, 2, 32) and torch.equal(st, t["state0"])
+    g = binding.decay_bwd(t["q"], t["k"], t["v"], t["lg"], t["state0"], None, t["dO"], t["dS"])
+    assert torch.equal(g["dstate"], t["dS"]) and (g["dlg"] == 0).all()
+
+
+def bits(x):
+    return x.view(torch.uint8) if x.dtype == BF else x
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_carry_in_place_and_repeats(dtype):
+    """Segments carried through the state equal one call; in-place updates and
+    repeated calls give the same bits."""
+    t = make(2, 260, 1, 2, 64, 96, dtype, 21, "some")
+    c = up(t)
+    o, st = binding.decay_fwd(c["q"], c["k"], c["v"], c["lg"], c["state0"], c["mask"])
+    o2, st2 = binding.decay_fwd(c["q"], c["k"], c["v"], c["lg"], c["state0"], c["mask"])
+    assert torch.equal(bits(o), bits(o2)) and torch.equal(st, st2)
+    s = c["state0"].clone()
+    o3, s3 = binding.decay_fwd(c["q"], c["k"], c["v"], c["lg"], s, c["mask"], state_out=s)
+    assert s3.data_ptr() == s.data_ptr() and torch.equal(s, st) and torch.equal(bits(o3), bits(o))
+    a = binding.decay_bwd(c["q"], c["k"], c["v"], c["lg"], c["state0"], c["mask"], c["dO"], c["dS"])
+    b = binding.decay_bwd(c["q"], c["k"], c["v"], c["lg"], c["state0"], c["mask"], c["dO"], c["dS"])
+    for n in a:
+        assert torch.equal(bits(a[n]), bits(b[n])), n
+    # prompt, then single tokens in place
+    q, k, v = (f64(t[n]) for n in ("q", "k", "v"))
+    k, v = R.clean(k, v, t["mask"])
+    ro, rst = R.decay(q, k, v, f64(t["lg"]), f64(t["state0"]), t["mask"])
+    P = 255
+    cut = lambda x, i, j: x[:, i:j].contiguous()  # noqa: E731
+    s = c["state0"].clone()
+    outs = [binding.decay_fwd(cut(c["q"], 0, P), cut(c["k"], 0, P), cut(c["v"], 0, P), c["lg"], s, cut(c["mask"], 0, P),
+                              state_out=s)[0]]
+    for i in range(P, 260):
+        outs.append(binding.decay_fwd(cut(c["q"], i, i + 1), cut(c["k"], i, i + 1), cut(c["v"], i, i + 1), c["lg"], s,
+                                      cut(c["mask"], i, i + 1), state_out=s)[0])
+    got = torch.cat(outs, 1).double().cpu()
+    assert (got - ro).norm() <= R.NORM[dtype == BF] * ro.norm()
+    assert (s.double().cpu() - rst).norm() <= R.NORM[False] * rst.norm()
