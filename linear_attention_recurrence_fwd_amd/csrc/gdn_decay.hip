@@ -6,7 +6,7 @@
 
 namespace gdn {
 
-int decay_waves(int N) { return N <= 64 ? 2 : N <= 128 ? 4 : N <= 192 ? 6 : 8; }
+int decay_waves(int N) { return N <= 64 ? 4 : N <= 128 ? 8 : N <= 192 ? 12 : 8; }
 
 hipError_t launch_decay_walk(const DecayWalkArgs& a, bool bf, hipStream_t st) {
   const int KD = a.walk[0].KD;

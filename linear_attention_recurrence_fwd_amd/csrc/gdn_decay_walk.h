@@ -2,10 +2,10 @@
 //
 // A workgroup owns one segment of one (batch, value head) and goes through its
 // chunks of CH steps with the whole state in registers: wave w holds columns
-// 32 w .. 32 w + 31 of all KD channels, fp32, in the accumulator layout of the
-// matrix cores.  With c_i the valid steps of the chunk up to step i (counted in
-// walk order; up to and with i forward in time, before i backward), L its valid
-// steps, and g = e^lg:
+// 16 NTL w .. of all KD channels, fp32, in the accumulator layout of the matrix
+// cores.  With c_i the valid steps of the chunk up to step i (counted in walk
+// order; up to and with i forward in time, before i backward), L its valid steps,
+// and g = e^lg:
 //   P_ij = [j <= i] g^(c_i - c_j) (x_i . y_j)
 //   w_i  = g^c_i S^T x_i + sum_j P_ij z_j
 //   S   <- g^L S + sum_j y_j (g^(L - c_j) z_j)^T
@@ -21,6 +21,10 @@
 //     relative error of at most 2^-8 for each product, independent between the
 //     products); three parts where the result also enters the fp32 sums for dlg;
 //   - P: one bf16 part, as the result is rounded to bf16.
+//
+// Tiles go to LDS by direct loads, a chunk ahead where two sets of them fit.  The
+// descriptors end behind the sequence's last row of the chunk and masked or
+// padding pieces get an offset past them, so all of these read as zeros.
 #pragma once
 
 #include "gdn_dev.h"
@@ -66,6 +70,12 @@ __device__ __forceinline__ int xcd_order(int blk, int n) {
   return (blk & 7) * per + (blk >> 3);
 }
 
+__device__ __forceinline__ float wave_sum(float v) {
+  v = row_sum16(v);
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
 template <typename T> struct Cfg;
 template <> struct Cfg<bf16> {
   static constexpr int CH = 64, EPP = 8;
@@ -74,201 +84,301 @@ template <> struct Cfg<float> {
   static constexpr int CH = 32, EPP = 4;
 };
 
-template <typename T, int KD, int NW, bool OUT, bool DOTS>
-struct Smem {
+constexpr uint32_t kOff = 0x80000000u;  // an offset past every descriptor here
+
+// LDS, in bytes: one or two sets of tiles, then P and the chunk's per-step
+// factors (two sets of these).  Tiles are row-major 16-byte pieces, piece p of
+// row r at place p ^ (r & 7).
+template <typename T, int KD, int NW, int NTL, bool OUT, bool DOTS>
+struct Lds {
   static constexpr int CH = Cfg<T>::CH, EPP = Cfg<T>::EPP;
-  static constexpr int PX = KD / EPP, PZ = 32 * NW / EPP;
-  uint4 x[OUT ? CH * PX : 1];
-  uint4 y[CH * PX];
-  uint4 z[CH * PZ];
-  uint4 e[DOTS ? CH * PZ : 1];
-  uint4 p[OUT ? CH * CH / EPP : 1];
-  float c[CH], rf[CH], sw[CH];
+  static constexpr int COLS = 16 * NW * NTL;
+  static constexpr int PX = KD / EPP, PZ = COLS / EPP, PP = CH / EPP;  // pieces per row
+  static constexpr int Y = 0, Z = Y + CH * PX * 16, X = Z + CH * PZ * 16, E = X + (OUT ? CH * PX * 16 : 0);
+  static constexpr int SET = E + (DOTS ? CH * PZ * 16 : 0);
+  static constexpr int PBYTES = OUT ? CH * PP * 16 : 0, FBYTES = 2 * 3 * CH * 4;
+  static constexpr int SLOTS = 2 * SET + PBYTES + FBYTES <= 160 * 1024 ? 2 : 1;
+  static constexpr int P = SLOTS * SET, F = P + PBYTES, TOTAL = F + FBYTES;
 };
 
-// Tiles in LDS: row-major 16-byte pieces, piece p of row r at p ^ (r & 7).
-template <int PPR> __device__ __forceinline__ int piece(int r, int p) { return r * PPR + (p ^ (r & 7)); }
-// 8-byte unit u of row r.
-template <int PPR> __device__ __forceinline__ const uint2* unit(const uint4* t, int r, int u) {
-  return reinterpret_cast<const uint2*>(t + piece<PPR>(r, u >> 1)) + (u & 1);
-}
-
-template <typename T, int PPR, int NT>
-__device__ __forceinline__ void load_tile(uint4* dst, const DecayRows& s, size_t bT, int Tn, int h, int t0, bool rev,
-                                          const uint8_t* zero_at) {
-  constexpr int CH = Cfg<T>::CH, EPP = Cfg<T>::EPP;
-  const T* base = static_cast<const T*>(s.p) + static_cast<size_t>(h / s.group) * s.D;
-  const size_t rs = static_cast<size_t>(s.H) * s.D;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < CH * PPR; i += NT) {
-    const int r = i / PPR, p = i % PPR, t = rev ? t0 + CH - 1 - r : t0 + r;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (t < Tn && p * EPP < s.D && (zero_at == nullptr || zero_at[t] != 0))
-      v = *reinterpret_cast<const uint4*>(base + (bT + t) * rs + p * EPP);
-    dst[piece<PPR>(r, p)] = v;
+// Loads of one tile by this wave: 64 pieces at a time.
+template <int CH, int PPR, int EPP, int NW> struct Loader {
+  static constexpr int N = CH * PPR / 64, PER = (N + NW - 1) / NW;
+  uint32_t off[PER];
+  // row_bytes: from one step's row to the next; D: channels in a row
+  __device__ __forceinline__ void init(int w, int l, uint32_t row_bytes, int D, bool rev) {
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int s = (k * NW + w) * 64 + l, r = s / PPR, p = (s % PPR) ^ (r & 7);
+      off[k] = p * EPP < D ? (rev ? CH - 1 - r : r) * row_bytes + p * 16 : kOff;
+    }
   }
-}
-
-__device__ __forceinline__ float wave_sum(float v) {
-  v = row_sum16(v);
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
-}
+  __device__ __forceinline__ void load(const i32x4& desc, char* dst, int w, int l) const {
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+      if (N % NW == 0 || k * NW + w < N) dma16(desc, dst + (k * NW + w) * 1024, off[k]);
+  }
+  // rows whose bit in live is clear read as zeros
+  __device__ __forceinline__ void load_live(const i32x4& desc, char* dst, int w, int l, unsigned long long live) const {
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+      if (N % NW == 0 || k * NW + w < N) {
+        const int r = ((k * NW + w) * 64 + l) / PPR;
+        dma16(desc, dst + (k * NW + w) * 1024, (live >> r) & 1 ? off[k] : kOff);
+      }
+  }
+};
 
 // SPS: bf16 parts of the state in the products with x.
-template <typename T, int KD, int NW, bool OUT, bool DOTS, int SPS>
+template <typename T, int KD, int NW, int NTL, bool OUT, bool DOTS, int SPS>
 __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
-  using M = Smem<T, KD, NW, OUT, DOTS>;
+  using M = Lds<T, KD, NW, NTL, OUT, DOTS>;
   constexpr bool BF = sizeof(T) == 2;
-  constexpr int CH = M::CH, EPP = M::EPP, PX = M::PX, PZ = M::PZ, PP = CH / EPP, MT = CH / 16, KT = KD / 16;
-  constexpr int NT = 64 * NW;
-  __shared__ M sm;
-  const DecayDims& d = a.d;
-  const int BH = d.B * d.Hv, per_walk = BH * a.nseg;
-  const int id = xcd_order(blockIdx.x, per_walk * a.nwalk);
-  if (id >= per_walk * a.nwalk) return;
-  const DecayWalk& wk = a.walk[id / per_walk];
+  constexpr int CH = M::CH, EPP = M::EPP, PX = M::PX, PZ = M::PZ, PP = M::PP, MT = CH / 16, KT = KD / 16;
+  __shared__ __attribute__((aligned(16))) char sm[M::TOTAL];
+  const int Hv = a.d.Hv, Tn = a.d.T, BH = a.d.B * Hv, nseg = a.nseg, n_items = BH * nseg;
+  const int it = xcd_order(blockIdx.x, n_items);
+  if (it >= n_items) return;
+  const DecayWalk& wk = a.walk[blockIdx.y];
   // value heads fastest: the heads of a group run side by side
-  const int it = id % per_walk, h = it % d.Hv, sg = (it / d.Hv) % a.nseg, b = it / (d.Hv * a.nseg);
-  const int bh = b * d.Hv + h;
+  const int h = it % Hv, sg = (it / Hv) % nseg, b = it / (Hv * nseg), bh = b * Hv + h;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, lr = l & 15, g = l >> 4;
   const bool rev = wk.reverse != 0;
-  const size_t bT = static_cast<size_t>(b) * d.T;
+  const int N = wk.N, KDr = wk.KD;
+  const size_t bT = static_cast<size_t>(b) * Tn;
   const uint8_t* mrow = a.mask ? a.mask + bT : nullptr;
   const float lg2 = log2_decay(a.lg[h]);
+  const float scale_p = wk.scale_p, scale_i = wk.scale_i, scale_u = wk.scale_u;
 
-  // state tile i, register r of lane (lr, g): channel 32 (i/2) + 8 g + 4 (i%2)
-  // + r for bf16 (two tiles together then are the B operand of a 32-deep
-  // product as they stand), 16 i + 4 g + r for fp32; column 32 w + 16 n + lr
-  auto chan = [&](int i, int r) { return BF ? 32 * (i / 2) + 8 * g + 4 * (i % 2) + r : 16 * i + 4 * g + r; };
-  f32x4 S[KT][2];
+  // state tile (i, n), register r of lane (lr, g): channel 32 (i/2) + 8 g + 4
+  // (i%2) + r for bf16 (two tiles together then are an operand of a 32-deep
+  // product as they stand), 16 i + 4 g + r for fp32.  Column of place idx of
+  // tile n: two tiles together hold runs of eight columns for each g.
+  auto chan = [&](int i) { return BF ? 32 * (i / 2) + 8 * g + 4 * (i % 2) : 16 * i + 4 * g; };
+  const int col0 = 16 * NTL * w;
+  auto column = [&](int n, int idx) {
+    return n < NTL / 2 * 2 ? col0 + 32 * (n / 2) + 8 * (idx >> 2) + 4 * (n & 1) + (idx & 3) : col0 + 16 * n + idx;
+  };
+  const size_t hs = static_cast<size_t>(a.d.Dk) * a.d.Dv;
+  const uint32_t hbytes = static_cast<uint32_t>(hs * 4);
+  const int sr = wk.sr, sc = wk.sc;
+  auto state_off = [&](int i, int n) {
+    const int ch = chan(i), col = column(n, lr);
+    return ch < KDr && col < N ? 4u * static_cast<uint32_t>(ch * sr + col * sc) : kOff;
+  };
+
+  f32x4 S[KT][NTL];
+  const float* src = nullptr;
+  if (OUT) {
+    if (wk.seg_start) src = wk.seg_start + (static_cast<size_t>(sg) * BH + bh) * hs;
+    else if (wk.start) src = wk.start + bh * hs;  // (one segment)
+  }
   {
-    const bool first = rev ? sg == a.nseg - 1 : sg == 0;
-    const size_t hs = static_cast<size_t>(d.Dk) * d.Dv;
-    const float* src = nullptr;
-    if (OUT) {
-      if (wk.seg_start) src = wk.seg_start + (static_cast<size_t>(sg) * BH + bh) * hs;
-      else if (first && wk.start) src = wk.start + bh * hs;
-    }
+    const rsrc_t rs = make_rsrc(src, src ? hbytes : 0);
 #pragma unroll
     for (int i = 0; i < KT; ++i)
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int ch = chan(i, r), col = 32 * w + 16 * n + lr;
-          S[i][n][r] = src && ch < wk.KD && col < wk.N
-                           ? src[static_cast<size_t>(ch) * wk.sr + static_cast<size_t>(col) * wk.sc] : 0.f;
-        }
-  }
-
-  const int t_lo = sg * a.seg * kDecayChunk;
-  const int t_hi = min(d.T, t_lo + a.seg * kDecayChunk);
-  const int nch = t_hi > t_lo ? (t_hi - t_lo + CH - 1) / CH : 0;
-  const size_t nstat = (static_cast<size_t>(d.T) + CH - 1) / CH;
-  for (int ci = 0; ci < nch; ++ci) {
-    const int cc = rev ? nch - 1 - ci : ci;
-    const int t0 = t_lo + cc * CH;
-    __syncthreads();  // the tiles of the chunk before are read
-    if constexpr (OUT) load_tile<T, PX, NT>(sm.x, wk.x, bT, d.T, h, t0, rev, rev ? mrow : nullptr);
-    load_tile<T, PX, NT>(sm.y, wk.y, bT, d.T, h, t0, rev, rev ? nullptr : mrow);
-    load_tile<T, PZ, NT>(sm.z, wk.z, bT, d.T, h, t0, rev, rev ? nullptr : mrow);
-    if constexpr (DOTS) load_tile<T, PZ, NT>(sm.e, wk.e, bT, d.T, h, t0, rev, rev ? mrow : nullptr);
-    // the valid steps, in walk order
-    const int tl = rev ? t0 + CH - 1 - l : t0 + l;
-    const bool live = l < CH && tl < d.T && (mrow == nullptr || mrow[tl] != 0);
-    const unsigned long long bal = __ballot(live);
-    const int L = __popcll(bal);
-    if (w == 0 && l < CH) {
-      const float c = static_cast<float>(__popcll(bal & ((rev ? 1ull : 2ull) << l) - 1ull));
-      sm.c[l] = c;
-      sm.rf[l] = wk.scale_i * exp2_fast(lg2 * c);
-      sm.sw[l] = wk.scale_u * exp2_fast(lg2 * (static_cast<float>(L) - c));
-    }
-    __syncthreads();
-
-    f32x4 acc[MT][2];
-    if constexpr (OUT) {
-      // ---- P, transposed tiles (rows j, columns i): lower ones, and zeros
-      // where a 32-deep product reaches past the diagonal
-      float intra = 0.f;
-      // (BF: MT (MT + 1) / 2 lower tiles, then tiles (0, 1) and (2, 3))
-      constexpr int LOW = MT * (MT + 1) / 2, TILES = LOW + (BF ? MT / 2 : 0);
-      for (int tile = w; tile < TILES; tile += NW) {
-        int mt, nt;
-        if (tile >= LOW) {
-          mt = 2 * (tile - LOW);
-          nt = mt + 1;
+      for (int n = 0; n < NTL; ++n) {
+        if constexpr (!OUT) {
+          S[i][n] = f4zero();
         } else {
-          mt = tile >= 6 ? 3 : tile >= 3 ? 2 : tile >= 1 ? 1 : 0;
-          nt = tile - mt * (mt + 1) / 2;
-        }
-        {
-          f32x4 t = f4zero();
-          if (nt <= mt) {
-            f32x4 u = f4zero();
-            if constexpr (BF) {
+          const uint32_t o = state_off(i, n);
+          if (sr == 1) {
+            const float4 v = buf_f4(rs, o);
+            S[i][n] = f32x4{v.x, v.y, v.z, v.w};
+          } else {
 #pragma unroll
-              for (int ks = 0; ks < KD / 32; ++ks)
-                t = mfma16(load_bf16x8(&sm.y[piece<PX>(16 * nt + lr, 4 * ks + g)]),
-                           load_bf16x8(&sm.x[piece<PX>(16 * mt + lr, 4 * ks + g)]), t);
-              if constexpr (DOTS) {
-#pragma unroll
-                for (int ks = 0; ks < NW; ++ks)
-                  u = mfma16(load_bf16x8(&sm.z[piece<PZ>(16 * nt + lr, 4 * ks + g)]),
-                             load_bf16x8(&sm.e[piece<PZ>(16 * mt + lr, 4 * ks + g)]), u);
-              }
-            } else {
-#pragma unroll
-              for (int ks = 0; ks < KD / 16; ++ks) {
-                const float4 yv = *reinterpret_cast<const float4*>(&sm.y[piece<PX>(16 * nt + lr, 4 * ks + g)]);
-                const float4 xv = *reinterpret_cast<const float4*>(&sm.x[piece<PX>(16 * mt + lr, 4 * ks + g)]);
-                t = mfma16f(yv.x, xv.x, t);
-                t = mfma16f(yv.y, xv.y, t);
-                t = mfma16f(yv.z, xv.z, t);
-                t = mfma16f(yv.w, xv.w, t);
-              }
-              if constexpr (DOTS) {
-#pragma unroll
-                for (int ks = 0; ks < 2 * NW; ++ks) {
-                  const float4 zv = *reinterpret_cast<const float4*>(&sm.z[piece<PZ>(16 * nt + lr, 4 * ks + g)]);
-                  const float4 ev = *reinterpret_cast<const float4*>(&sm.e[piece<PZ>(16 * mt + lr, 4 * ks + g)]);
-                  u = mfma16f(zv.x, ev.x, u);
-                  u = mfma16f(zv.y, ev.y, u);
-                  u = mfma16f(zv.z, ev.z, u);
-                  u = mfma16f(zv.w, ev.w, u);
-                }
-              }
-            }
-            const float ci_ = sm.c[16 * mt + lr];
-            const float4 cj = *reinterpret_cast<const float4*>(&sm.c[16 * nt + 4 * g]);
-            const float cjs[4] = {cj.x, cj.y, cj.z, cj.w};
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float dn = ci_ - cjs[r];
-              const bool in = 16 * nt + 4 * g + r <= 16 * mt + lr;
-              t[r] = in ? t[r] * exp2_fast(lg2 * dn) * wk.scale_p : 0.f;
-              if constexpr (DOTS) intra += in ? dn * t[r] * u[r] : 0.f;
-            }
+            for (int r = 0; r < 4; ++r) S[i][n][r] = buf_f1(rs, o + 4u * static_cast<uint32_t>(r * sr));
           }
-          if constexpr (BF)
-            reinterpret_cast<uint2*>(&sm.p[piece<PP>(16 * mt + lr, 2 * nt + (g >> 1))])[g & 1] =
-                pack4_bf16(t[0], t[1], t[2], t[3]);
-          else
-            *reinterpret_cast<f32x4*>(&sm.p[piece<PP>(16 * mt + lr, 4 * nt + g)]) = t;
         }
       }
-      // ---- S^T x
+  }
+
+  const int t_lo = sg * a.seg * kDecayChunk, t_hi = min(Tn, t_lo + a.seg * kDecayChunk);
+  const int nch = t_hi > t_lo ? (t_hi - t_lo + CH - 1) / CH : 0;
+  auto chunk_start = [&](int ci) { return t_lo + (rev ? nch - 1 - ci : ci) * CH; };
+  // the mask byte of this lane's step of a chunk (walk order), and the live steps
+  auto live_of = [&](int ci) -> unsigned long long {
+    const int t = chunk_start(ci) + (rev ? CH - 1 - l : l);
+    bool v = l < CH && t < Tn;
+    if (mrow != nullptr && v) v = mrow[t] != 0;
+    return __ballot(v);
+  };
+
+  const int xH = wk.x.H, xg = wk.x.group, yH = wk.y.H, yg = wk.y.group, zH = wk.z.H, zg = wk.z.group;
+  Loader<CH, PX, EPP, NW> ly;
+  Loader<CH, PZ, EPP, NW> lz;
+  ly.init(w, l, static_cast<uint32_t>(yH) * KDr * sizeof(T), KDr, rev);
+  lz.init(w, l, static_cast<uint32_t>(zH) * N * sizeof(T), N, rev);
+  // a chunk's rows of one head: from its first step to the sequence's end
+  auto rows = [&](const void* p, int H, int group, int D, int t0) {
+    const int n = min(Tn - t0, CH);
+    return raw_desc(static_cast<const T*>(p) + ((bT + t0) * H + h / group) * D,
+                    (static_cast<size_t>(n - 1) * H * D + D) * sizeof(T));
+  };
+  auto issue = [&](int ci, int slot, unsigned long long live) {
+    char* s = sm + slot * M::SET;
+    const int t0 = chunk_start(ci);
+    const i32x4 dy = rows(wk.y.p, yH, yg, KDr, t0), dz = rows(wk.z.p, zH, zg, N, t0);
+    const bool m = mrow != nullptr;
+    if (m && !rev) {
+      ly.load_live(dy, s + M::Y, w, l, live);
+      lz.load_live(dz, s + M::Z, w, l, live);
+    } else {
+      ly.load(dy, s + M::Y, w, l);
+      lz.load(dz, s + M::Z, w, l);
+    }
+    if constexpr (OUT) {  // x has y's row length, e has z's
+      const i32x4 dx = rows(wk.x.p, xH, xg, KDr, t0);
+      if (m && rev) ly.load_live(dx, s + M::X, w, l, live);
+      else ly.load(dx, s + M::X, w, l);
+    }
+    if constexpr (DOTS) {
+      const i32x4 de = rows(wk.e.p, zH, zg, N, t0);
+      if (m && rev) lz.load_live(de, s + M::E, w, l, live);
+      else lz.load(de, s + M::E, w, l);
+    }
+  };
+
+  // byte offsets of this lane's operand pieces in a tile: row lr (a 16-row
+  // tile further is a constant further), piece 4 ks + g for even and odd ks
+  const uint32_t rx[2] = {static_cast<uint32_t>(lr * PX + (g ^ (lr & 7))) * 16u,
+                          static_cast<uint32_t>(lr * PX + ((4 + g) ^ (lr & 7))) * 16u};
+  const uint32_t rz[2] = {static_cast<uint32_t>(lr * PZ + (g ^ (lr & 7))) * 16u,
+                          static_cast<uint32_t>(lr * PZ + ((4 + g) ^ (lr & 7))) * 16u};
+  auto at_x = [&](int tile, int ks) { return rx[ks & 1] + tile * 16 * PX * 16 + (ks >> 1) * 128; };
+  auto at_z = [&](int tile, int ks) { return rz[ks & 1] + tile * 16 * PZ * 16 + (ks >> 1) * 128; };
+  // transposing reads (bf16): lane (lr, g) addresses row 8 g + lr/4 (+ 4 for the
+  // second half), and of two 16-channel tiles together piece lr%4, half i%2
+  const int tr = 8 * g + (lr >> 2);
+  uint32_t ty[2][2], tz[NTL][2];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) acc[mt][0] = acc[mt][1] = f4zero();
+  for (int q = 0; q < 2; ++q) {
+    const int row = tr + 4 * q;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      ty[e][q] = static_cast<uint32_t>(row * PX + ((4 * e + (lr & 3)) ^ (row & 7))) * 16u;
+#pragma unroll
+    for (int n = 0; n < NTL; ++n) {
+      const int c = column(n, 4 * (lr & 3));  // four columns from here
+      tz[n][q] = static_cast<uint32_t>(row * PZ + ((c >> 3) ^ (row & 7))) * 16u + (c & 4) * 2;
+    }
+  }
+
+  unsigned long long live = 0, live_next = 0;
+  if (nch > 0) {
+    live = live_of(0);
+    if constexpr (M::SLOTS == 2) issue(0, 0, live);
+  }
+  const size_t nstat = (static_cast<size_t>(Tn) + CH - 1) / CH;
+  for (int ci = 0; ci < nch; ++ci) {
+    const int t0 = chunk_start(ci), slot = M::SLOTS == 2 ? ci & 1 : 0;
+    char* tile = sm + slot * M::SET;
+    float* fc = reinterpret_cast<float*>(sm + M::F) + (ci & 1) * 3 * CH;  // c, row factors, source weights
+    float *frf = fc + CH, *fsw = fc + 2 * CH;
+    if constexpr (M::SLOTS == 1) {
+      lds_barrier();  // the chunk before is read
+      issue(ci, 0, live);
+    }
+    const int L = __popcll(live);
+    if (w == 0 && l < CH) {
+      const float c = static_cast<float>(__popcll(live & (((rev ? 1ull : 2ull) << l) - 1ull)));
+      fc[l] = c;
+      frf[l] = scale_i * exp2_fast(lg2 * c);
+      fsw[l] = scale_u * exp2_fast(lg2 * (static_cast<float>(L) - c));
+    }
+    // this wave's part of the tiles has arrived (what it stored after asking for
+    // them, MT stores at least, may be on the way still)
+    if (OUT && M::SLOTS == 2 && ci > 0) wait_vm<MT>();
+    else wait_vm<0>();
+    lds_barrier();
+    if (ci + 1 < nch) {
+      live_next = live_of(ci + 1);
+      if constexpr (M::SLOTS == 2) issue(ci + 1, slot ^ 1, live_next);
+    }
+
+    f32x4 acc[MT][NTL];
+    if constexpr (OUT) {
+      // ---- P, transposed tiles (rows j, columns i): the MT (MT + 1) / 2 lower
+      // ones, and zeros where a 32-deep product reaches past the diagonal
+      // (tiles (0, 1) and (2, 3))
+      float intra = 0.f;
+      constexpr int LOW = MT * (MT + 1) / 2, TILES = LOW + (BF ? MT / 2 : 0);
+      for (int tl = w; tl < TILES; tl += NW) {
+        int mt, nt;
+        if (tl >= LOW) {
+          mt = 2 * (tl - LOW);
+          nt = mt + 1;
+        } else {
+          mt = tl >= 6 ? 3 : tl >= 3 ? 2 : tl >= 1 ? 1 : 0;
+          nt = tl - mt * (mt + 1) / 2;
+        }
+        f32x4 t = f4zero();
+        if (nt <= mt) {
+          f32x4 u = f4zero();
+          const char *py = tile + M::Y + nt * 16 * PX * 16, *px = tile + M::X + mt * 16 * PX * 16;
+          const char *pz = tile + M::Z + nt * 16 * PZ * 16, *pe = tile + M::E + mt * 16 * PZ * 16;
+          if constexpr (BF) {
+#pragma unroll
+            for (int ks = 0; ks < KD / 32; ++ks)
+              t = mfma16(load_bf16x8(py + at_x(0, ks)), load_bf16x8(px + at_x(0, ks)), t);
+            if constexpr (DOTS) {
+#pragma unroll
+              for (int ks = 0; ks < M::COLS / 32; ++ks)
+                u = mfma16(load_bf16x8(pz + at_z(0, ks)), load_bf16x8(pe + at_z(0, ks)), u);
+            }
+          } else {
+#pragma unroll
+            for (int ks = 0; ks < KD / 16; ++ks) {
+              const float4 yv = *reinterpret_cast<const float4*>(py + at_x(0, ks));
+              const float4 xv = *reinterpret_cast<const float4*>(px + at_x(0, ks));
+              t = mfma16f(yv.x, xv.x, t);
+              t = mfma16f(yv.y, xv.y, t);
+              t = mfma16f(yv.z, xv.z, t);
+              t = mfma16f(yv.w, xv.w, t);
+            }
+            if constexpr (DOTS) {
+#pragma unroll
+              for (int ks = 0; ks < M::COLS / 16; ++ks) {
+                const float4 zv = *reinterpret_cast<const float4*>(pz + at_z(0, ks));
+                const float4 ev = *reinterpret_cast<const float4*>(pe + at_z(0, ks));
+                u = mfma16f(zv.x, ev.x, u);
+                u = mfma16f(zv.y, ev.y, u);
+                u = mfma16f(zv.z, ev.z, u);
+                u = mfma16f(zv.w, ev.w, u);
+              }
+            }
+          }
+          const float c_i = fc[16 * mt + lr];
+          const f32x4 c_j = *reinterpret_cast<const f32x4*>(fc + 16 * nt + 4 * g);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float dn = c_i - c_j[r];
+            const bool in = 16 * nt + 4 * g + r <= 16 * mt + lr;
+            t[r] = in ? t[r] * exp2_fast(lg2 * dn) * scale_p : 0.f;
+            if constexpr (DOTS) intra += in ? dn * t[r] * u[r] : 0.f;
+          }
+        }
+        char* pp = sm + M::P + (16 * mt + lr) * PP * 16;
+        if constexpr (BF)
+          *reinterpret_cast<uint2*>(pp + (((2 * nt + (g >> 1)) ^ (lr & 7)) * 16 + (g & 1) * 8)) =
+              pack4_bf16(t[0], t[1], t[2], t[3]);
+        else
+          *reinterpret_cast<f32x4*>(pp + ((4 * nt + g) ^ (lr & 7)) * 16) = t;
+      }
+      // ---- S^T x, transposed tiles (rows are columns of w, columns are steps)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < NTL; ++n) acc[mt][n] = f4zero();
       if constexpr (BF) {
 #pragma unroll
         for (int ks = 0; ks < KD / 32; ++ks) {
           bf16x8 xa[MT];
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) xa[mt] = load_bf16x8(&sm.x[piece<PX>(16 * mt + lr, 4 * ks + g)]);
+          for (int mt = 0; mt < MT; ++mt) xa[mt] = load_bf16x8(tile + M::X + at_x(mt, ks));
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
+          for (int n = 0; n < NTL; ++n) {
             float v[8];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -280,7 +390,7 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
 #pragma unroll
             for (int s = 0; s < SPS; ++s)
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt) acc[mt][n] = mfma16(xa[mt], part[s], acc[mt][n]);
+              for (int mt = 0; mt < MT; ++mt) acc[mt][n] = mfma16(part[s], xa[mt], acc[mt][n]);
           }
         }
       } else {
@@ -288,49 +398,40 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
         for (int i = 0; i < KT; ++i)
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            const float4 xv = *reinterpret_cast<const float4*>(&sm.x[piece<PX>(16 * mt + lr, 4 * i + g)]);
-            const float xs[4] = {xv.x, xv.y, xv.z, xv.w};
+            const f32x4 xv = *reinterpret_cast<const f32x4*>(tile + M::X + at_x(mt, i));
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
-              for (int n = 0; n < 2; ++n) acc[mt][n] = mfma16f(xs[r], S[i][n][r], acc[mt][n]);
+              for (int n = 0; n < NTL; ++n) acc[mt][n] = mfma16f(S[i][n][r], xv[r], acc[mt][n]);
           }
       }
       float s0 = 0.f, s1 = 0.f;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const float4 rf = *reinterpret_cast<const float4*>(&sm.rf[16 * mt + 4 * g]);
-        const float rfs[4] = {rf.x, rf.y, rf.z, rf.w};
-        float ct[4];
-        if constexpr (DOTS) {
-          const float4 c4 = *reinterpret_cast<const float4*>(&sm.c[16 * mt + 4 * g]);
-          ct[0] = c4.x; ct[1] = c4.y; ct[2] = c4.z; ct[3] = c4.w;
-        }
+        const float rf = frf[16 * mt + lr], ct = fc[16 * mt + lr];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          float ev[4];
+        for (int n = 0; n < NTL; ++n) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[mt][n][r] *= rf;
           if constexpr (DOTS) {
+            const int c = column(n, 4 * g), row = 16 * mt + lr;  // four columns from here
+            float ev[4];
             if constexpr (BF) {
-              const uint2 u = lds_read_tr16(unit<PZ>(sm.e, 16 * mt + 4 * g + (lr >> 2), 4 * (2 * w + n) + (lr & 3)));
+              const uint2 u = *reinterpret_cast<const uint2*>(
+                  tile + M::E + (row * PZ + ((c >> 3) ^ (lr & 7))) * 16 + (c & 4) * 2);
               ev[0] = __uint_as_float(u.x << 16);
               ev[1] = __uint_as_float(u.x & 0xffff0000u);
               ev[2] = __uint_as_float(u.y << 16);
               ev[3] = __uint_as_float(u.y & 0xffff0000u);
             } else {
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-                ev[r] = reinterpret_cast<const float*>(
-                    &sm.e[piece<PZ>(16 * mt + 4 * g + r, 4 * (2 * w + n) + (lr >> 2))])[lr & 3];
+              *reinterpret_cast<f32x4*>(ev) =
+                  *reinterpret_cast<const f32x4*>(tile + M::E + (row * PZ + ((c >> 2) ^ (lr & 7))) * 16);
             }
-          }
+            float f = 0.f;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            acc[mt][n][r] *= rfs[r];
-            if constexpr (DOTS) {
-              const float f = acc[mt][n][r] * ev[r];
-              s0 += f;
-              s1 = fmaf(ct[r], f, s1);
-            }
+            for (int r = 0; r < 4; ++r) f = fmaf(acc[mt][n][r], ev[r], f);
+            s0 += f;
+            s1 = fmaf(ct, f, s1);
           }
         }
       }
@@ -339,19 +440,13 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
         s1 = wave_sum(s1);
         intra = wave_sum(intra);
         if (l == 0) {
-          const size_t at = (static_cast<size_t>(bh) * nstat + t0 / CH) * NW + w;
-          if (rev) {
-            wk.dots[at * kDecayKStats] = s0;
-            wk.dots[at * kDecayKStats + 1] = s1;
-            wk.dots[at * kDecayKStats + 2] = static_cast<float>(L);
-          } else {
-            wk.dots[at * kDecayQStats] = s0;
-            wk.dots[at * kDecayQStats + 1] = s1;
-            wk.dots[at * kDecayQStats + 2] = intra;
-          }
+          float* o = wk.dots + ((static_cast<size_t>(bh) * nstat + t0 / CH) * NW + w) * 3;
+          o[0] = s0;
+          o[1] = s1;
+          o[2] = rev ? static_cast<float>(L) : intra;
         }
       }
-      __syncthreads();  // P is whole
+      lds_barrier();  // P is whole
     }
 
     // ---- products with z: P z, and the state's update
@@ -359,27 +454,27 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
 #pragma unroll
     for (int i = 0; i < KT; ++i)
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < NTL; ++n)
 #pragma unroll
         for (int r = 0; r < 4; ++r) S[i][n][r] *= gL;
     if constexpr (BF) {
 #pragma unroll
       for (int kt = 0; kt < CH / 32; ++kt) {
-        const int r0 = 32 * kt + 8 * g + (lr >> 2);
         float sw[8];
-        *reinterpret_cast<float4*>(sw) = *reinterpret_cast<const float4*>(&sm.sw[32 * kt + 8 * g]);
-        *reinterpret_cast<float4*>(sw + 4) = *reinterpret_cast<const float4*>(&sm.sw[32 * kt + 8 * g + 4]);
-        bf16x8 zp[2][3];
+        *reinterpret_cast<f32x4*>(sw) = *reinterpret_cast<const f32x4*>(fsw + 32 * kt + 8 * g);
+        *reinterpret_cast<f32x4*>(sw + 4) = *reinterpret_cast<const f32x4*>(fsw + 32 * kt + 8 * g + 4);
+        bf16x8 zp[NTL][3];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const int u = 4 * (2 * w + n) + (lr & 3);
-          const uint2 z0 = lds_read_tr16(unit<PZ>(sm.z, r0, u)), z1 = lds_read_tr16(unit<PZ>(sm.z, r0 + 4, u));
+        for (int n = 0; n < NTL; ++n) {
+          const char* zt = tile + M::Z + kt * 32 * PZ * 16;
+          const uint2 z0 = lds_read_tr16(zt + tz[n][0]), z1 = lds_read_tr16(zt + tz[n][1]);
           const uint4 zu = make_uint4(z0.x, z0.y, z1.x, z1.y);
           if constexpr (OUT) {
             const bf16x8 zf = as_bf16x8(zu);
 #pragma unroll
             for (int mt = 2 * kt; mt < MT; ++mt)
-              acc[mt][n] = mfma16(load_bf16x8(&sm.p[piece<PP>(16 * mt + lr, 4 * kt + g)]), zf, acc[mt][n]);
+              acc[mt][n] = mfma16(zf, load_bf16x8(sm + M::P + ((16 * mt + lr) * PP + ((4 * kt + g) ^ (lr & 7))) * 16),
+                                  acc[mt][n]);
           }
           float v[8];
           Vec16<bf16>::unpack(zu, v);
@@ -389,119 +484,141 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
         }
 #pragma unroll
         for (int i = 0; i < KT; ++i) {
-          const int u = 8 * (i / 2) + 2 * (lr & 3) + (i & 1);
-          const uint2 y0 = lds_read_tr16(unit<PX>(sm.y, r0, u)), y1 = lds_read_tr16(unit<PX>(sm.y, r0 + 4, u));
+          const char* yt = tile + M::Y + kt * 32 * PX * 16 + (i / 4) * 128 + (i & 1) * 8;
+          const uint2 y0 = lds_read_tr16(yt + ty[(i / 2) & 1][0]), y1 = lds_read_tr16(yt + ty[(i / 2) & 1][1]);
           const bf16x8 ya = as_bf16x8(make_uint4(y0.x, y0.y, y1.x, y1.y));
 #pragma unroll
           for (int s = 2; s >= 0; --s)
 #pragma unroll
-            for (int n = 0; n < 2; ++n) S[i][n] = mfma16(ya, zp[n][s], S[i][n]);
+            for (int n = 0; n < NTL; ++n) S[i][n] = mfma16(ya, zp[n][s], S[i][n]);
         }
       }
     } else {
 #pragma unroll
       for (int bq = 0; bq < CH / 16; ++bq) {
-        float zv[2][4], sw[4];
-        *reinterpret_cast<float4*>(sw) = *reinterpret_cast<const float4*>(&sm.sw[16 * bq + 4 * g]);
+        float zv[NTL][4];
+        const f32x4 sw = *reinterpret_cast<const f32x4*>(fsw + 16 * bq + 4 * g);
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NTL; ++n) {
+          const int c = column(n, lr);
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            zv[n][r] = reinterpret_cast<const float*>(
-                &sm.z[piece<PZ>(16 * bq + 4 * g + r, 4 * (2 * w + n) + (lr >> 2))])[lr & 3];
+          for (int r = 0; r < 4; ++r) {
+            const int row = 16 * bq + 4 * g + r;
+            zv[n][r] = *reinterpret_cast<const float*>(tile + M::Z + (row * PZ + ((c >> 2) ^ (row & 7))) * 16 + (c & 3) * 4);
+          }
+        }
         if constexpr (OUT) {
 #pragma unroll
           for (int mt = bq; mt < MT; ++mt) {
-            const float4 pv = *reinterpret_cast<const float4*>(&sm.p[piece<PP>(16 * mt + lr, 4 * bq + g)]);
-            const float ps[4] = {pv.x, pv.y, pv.z, pv.w};
+            const f32x4 pv = *reinterpret_cast<const f32x4*>(sm + M::P + ((16 * mt + lr) * PP + ((4 * bq + g) ^ (lr & 7))) * 16);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
-              for (int n = 0; n < 2; ++n) acc[mt][n] = mfma16f(ps[r], zv[n][r], acc[mt][n]);
+              for (int n = 0; n < NTL; ++n) acc[mt][n] = mfma16f(zv[n][r], pv[r], acc[mt][n]);
           }
         }
 #pragma unroll
         for (int i = 0; i < KT; ++i)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float yv = reinterpret_cast<const float*>(
-                &sm.y[piece<PX>(16 * bq + 4 * g + r, 4 * i + (lr >> 2))])[lr & 3];
+            const int row = 16 * bq + 4 * g + r;
+            const float yv = *reinterpret_cast<const float*>(
+                tile + M::Y + (row * PX + ((4 * i + (lr >> 2)) ^ (row & 7))) * 16 + (lr & 3) * 4);
 #pragma unroll
-            for (int n = 0; n < 2; ++n) S[i][n] = mfma16f(yv, zv[n][r] * sw[r], S[i][n]);
+            for (int n = 0; n < NTL; ++n) S[i][n] = mfma16f(yv, zv[n][r] * sw[r], S[i][n]);
           }
       }
     }
 
     if constexpr (OUT) {
+      // rows behind the sequence and columns past N lie past the descriptor
+      const int es = wk.w32 || !BF ? 4 : 2, steps = min(Tn - t0, CH);
+      const rsrc_t rw = make_rsrc(static_cast<char*>(wk.w) + ((bT + t0) * Hv + h) * N * es,
+                                  (static_cast<size_t>(steps - 1) * Hv * N + N) * es);
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int mt = 0; mt < MT; ++mt) {
+        const int row = 16 * mt + lr;
+        const uint32_t ro = static_cast<uint32_t>(rev ? CH - 1 - row : row) * static_cast<uint32_t>(Hv * N);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 16 * mt + 4 * g + r, t = rev ? t0 + CH - 1 - row : t0 + row;
-          if (t >= d.T) continue;
-          const size_t at = ((bT + t) * d.Hv + h) * wk.N;
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int col = 32 * w + 16 * n + lr;
-            if (col >= wk.N) continue;
-            if (wk.w32) static_cast<float*>(wk.w)[at + col] = acc[mt][n][r];
-            else static_cast<T*>(wk.w)[at + col] = from_f32<T>(acc[mt][n][r]);
+        for (int n = 0; n < NTL; ++n) {
+          const int c = column(n, 4 * g);
+          const uint32_t o = c < N ? (ro + c) * es : kOff;
+          if (es == 4) {
+            buf_store_u4(rw, o, __builtin_bit_cast(uint4, acc[mt][n]));
+          } else if (n < NTL / 2 * 2) {  // eight columns of two tiles
+            if (n & 1) continue;
+            const uint2 p = pack4_bf16(acc[mt][n][0], acc[mt][n][1], acc[mt][n][2], acc[mt][n][3]);
+            const f32x4 q = acc[mt][n + 1 < NTL ? n + 1 : n];
+            const uint2 s = pack4_bf16(q[0], q[1], q[2], q[3]);
+            buf_store_u4(rw, o, make_uint4(p.x, p.y, s.x, s.y));
+          } else {
+            buf_store_u2(rw, o, pack4_bf16(acc[mt][n][0], acc[mt][n][1], acc[mt][n][2], acc[mt][n][3]));
           }
         }
+      }
     }
+    live = live_next;
   }
 
   // ---- the state behind the segment
-  const size_t hs = static_cast<size_t>(d.Dk) * d.Dv;
   float* dst = nullptr;
   const float* crs = nullptr;
   if constexpr (OUT) {
-    if (sg == (rev ? 0 : a.nseg - 1) && wk.end) dst = wk.end + bh * hs;
+    if (sg == (rev ? 0 : nseg - 1) && wk.end) dst = wk.end + bh * hs;
     if (wk.seg_cross) crs = wk.seg_cross + (static_cast<size_t>(sg) * BH + bh) * hs;
     else if (wk.cross) crs = wk.cross + bh * hs;
   } else {
     dst = wk.seg_sum + (static_cast<size_t>(sg) * BH + bh) * hs;
   }
   float dot = 0.f;
-  if (dst || crs) {
+  if (crs) {
+    const rsrc_t rc = make_rsrc(crs, hbytes);
 #pragma unroll
     for (int i = 0; i < KT; ++i)
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < NTL; ++n) {
+        const uint32_t o = state_off(i, n);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int ch = chan(i, r), col = 32 * w + 16 * n + lr;
-          if (ch >= wk.KD || col >= wk.N) continue;
-          const size_t at = static_cast<size_t>(ch) * wk.sr + static_cast<size_t>(col) * wk.sc;
-          if (dst) dst[at] = S[i][n][r];
-          if (crs) dot = fmaf(S[i][n][r], crs[at], dot);
-        }
+        for (int r = 0; r < 4; ++r) dot = fmaf(S[i][n][r], buf_f1(rc, o + 4u * static_cast<uint32_t>(r * sr)), dot);
+      }
+  }
+  if (dst) {
+    const rsrc_t rd = make_rsrc(dst, hbytes);
+#pragma unroll
+    for (int i = 0; i < KT; ++i)
+#pragma unroll
+      for (int n = 0; n < NTL; ++n) {
+        const uint32_t o = state_off(i, n);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[i][n][r]), rd, o + 4u * static_cast<uint32_t>(r * sr), 0, 0);
+      }
   }
   if constexpr (OUT && !DOTS) {
     if (wk.dots) {
       dot = wave_sum(dot);
-      if (l == 0) wk.dots[(static_cast<size_t>(bh) * a.nseg + sg) * NW + w] = dot;
+      if (l == 0) wk.dots[(static_cast<size_t>(bh) * nseg + sg) * NW + w] = dot;
     }
   }
 }
 
-template <typename T, int KD, int NW>
+template <typename T, int KD, int NW, int NTL>
 hipError_t launch_nw(const DecayWalkArgs& a, hipStream_t st) {
-  const int n = a.d.B * a.d.Hv * a.nseg * a.nwalk, grid = (n + 7) / 8 * 8;
+  const int n = a.d.B * a.d.Hv * a.nseg;
+  const dim3 grid((n + 7) / 8 * 8, a.nwalk);
   const DecayWalk& w = a.walk[0];
-  if (w.seg_sum) walk_kernel<T, KD, NW, false, false, 1><<<grid, 64 * NW, 0, st>>>(a);
-  else if (w.e.p) walk_kernel<T, KD, NW, true, true, 3><<<grid, 64 * NW, 0, st>>>(a);
-  else walk_kernel<T, KD, NW, true, false, 1><<<grid, 64 * NW, 0, st>>>(a);
+  if (w.seg_sum) walk_kernel<T, KD, NW, NTL, false, false, 1><<<grid, 64 * NW, 0, st>>>(a);
+  else if (w.e.p) walk_kernel<T, KD, NW, NTL, true, true, 3><<<grid, 64 * NW, 0, st>>>(a);
+  else walk_kernel<T, KD, NW, NTL, true, false, 1><<<grid, 64 * NW, 0, st>>>(a);
   return hipGetLastError();
 }
 
 template <typename T, int KD> hipError_t launch_kd(const DecayWalkArgs& a, hipStream_t st) {
-  switch (decay_waves(a.walk[0].N)) {
-    case 2: return launch_nw<T, KD, 2>(a, st);
-    case 4: return launch_nw<T, KD, 4>(a, st);
-    case 6: return launch_nw<T, KD, 6>(a, st);
-    default: return launch_nw<T, KD, 8>(a, st);
-  }
+  const int N = a.walk[0].N;
+  if (N <= 64) return launch_nw<T, KD, 4, 1>(a, st);
+  if (N <= 128) return launch_nw<T, KD, 8, 1>(a, st);
+  if (N <= 192) return launch_nw<T, KD, 12, 1>(a, st);
+  return launch_nw<T, KD, 8, 2>(a, st);
 }
 
 }  // namespace decay
