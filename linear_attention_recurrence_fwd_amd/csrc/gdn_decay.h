@@ -45,10 +45,11 @@ struct DecayWalk {
   // states [Dk, Dv] fp32 per (b, h): element (channel, column) at
   // channel * sr + column * sc
   int sr, sc;
-  const float* start;       // [B*Hv] states the first segment walked starts from (null: zeros)
+  const float* start;       // [B*Hv] states the walk starts from, with one segment (null: zeros)
   const float* seg_start;   // [nseg, B*Hv] start states (null: one segment)
-  float* end;               // state after the last segment walked (null: not written)
+  float* end;               // state behind the sequence, with one segment (else null)
   float* seg_sum;           // the walk only sums its segment's update into [nseg, B*Hv] (else null)
+  float* seg_steps;         //   and writes its valid steps into [B, nseg] (may be null)
   float* dots;              // sums for dlg (else null); see DecayStats
   const float* cross;       // [B*Hv] states, dotted with the end state of every segment (dlg):
   const float* seg_cross;   //   first segment's, and [nseg, B*Hv]
@@ -80,10 +81,11 @@ constexpr int kDecayQStats = 3, kDecayKStats = 3;
 struct DecayChainArgs {
   DecayDims d;
   const float* lg;
-  const uint8_t* mask;
-  int nseg, seg;
+  const float* seg_steps;   // [B, nseg] valid steps of the segments
+  int nseg;
   float* states;            // [nseg, B*Hv, Dk*Dv]: segment sums in, start states out
   const float* start;       // may be null
+  float* end;               // state behind the last segment walked (may alias start)
   int reverse;
 };
 

@@ -24,57 +24,57 @@ using decay::log2_decay;
 // ---- chain: the segment sums U_s of one direction become the states before
 // each segment, start_{s+1} = g^{N_s} start_s + U_s with N_s the segment's valid
 // steps.  One thread per four elements of one (b, h) goes through the segments
-// (in walk order); the loads of eight segments are in flight together.
+// (in walk order), a wave to a workgroup so that few heads still reach every
+// compute unit; the loads of the next eight segments are in flight while the last
+// eight are summed.
 struct ChainArgs {
   DecayChainArgs c[2];
 };
 
-__global__ void __launch_bounds__(256) chain_kernel(ChainArgs aa) {
+__global__ void __launch_bounds__(64) chain_kernel(ChainArgs aa) {
   const DecayChainArgs& a = aa.c[blockIdx.z];
   const DecayDims& d = a.d;
-  const int bh = blockIdx.x, b = bh / d.Hv, h = bh % d.Hv, BH = d.B * d.Hv;
-  const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
-  const int len = a.seg * kDecayChunk;
-  __shared__ float dec[kDecayMaxSeg];  // g^{N_s}
+  const int bh = blockIdx.x, b = bh / d.Hv, h = bh % d.Hv, BH = d.B * d.Hv, l = threadIdx.x, nseg = a.nseg;
+  __shared__ float dec[kDecayMaxSeg];  // g^{N_s}, in walk order
   const float lg2 = log2_decay(a.lg[h]);
-  for (int s = w; s < a.nseg; s += 4) {
-    const int t0 = s * len, t1 = min(d.T, t0 + len);
-    int n = 0;
-    if (a.mask == nullptr) {
-      n = t1 - t0;
-    } else {
-      const uint8_t* m = a.mask + static_cast<size_t>(b) * d.T;
-      for (int t = t0 + l; t - l < t1; t += 64) n += __popcll(__ballot(t < t1 && m[t] != 0));
-    }
-    if (l == 0) dec[s] = exp2_fast(lg2 * static_cast<float>(n));
-  }
+  for (int s = l; s < nseg; s += 64)
+    dec[s] = exp2_fast(lg2 * a.seg_steps[static_cast<size_t>(b) * nseg + (a.reverse ? nseg - 1 - s : s)]);
   __syncthreads();
   const size_t hs = static_cast<size_t>(d.Dk) * d.Dv;
-  const size_t e = (static_cast<size_t>(blockIdx.y) * 256 + threadIdx.x) * 4;
+  const size_t e = (static_cast<size_t>(blockIdx.y) * 64 + l) * 4;
   if (e >= hs) return;
   float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
   if (a.start) run = *reinterpret_cast<const float4*>(a.start + bh * hs + e);
   const size_t step = static_cast<size_t>(BH) * hs;
   float* p = a.states + bh * hs + e;
-  for (int s0 = 0; s0 < a.nseg; s0 += 8) {
-    float4 u[8];
+  auto at = [&](int s) { return reinterpret_cast<float4*>(p + (a.reverse ? nseg - 1 - s : s) * step); };
+  constexpr int N = 8;
+  float4 u[2][N];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int s = min(s0 + k, a.nseg - 1);
-      u[k] = *reinterpret_cast<const float4*>(p + (a.reverse ? a.nseg - 1 - s : s) * step);
-    }
+  for (int k = 0; k < N; ++k) u[0][k] = *at(min(k, nseg - 1));
+  for (int s0 = 0; s0 < nseg; s0 += 2 * N) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (s0 + k >= a.nseg) break;
-      const int s = a.reverse ? a.nseg - 1 - (s0 + k) : s0 + k;
-      *reinterpret_cast<float4*>(p + s * step) = run;
-      const float f = dec[s];
-      run.x = fmaf(f, run.x, u[k].x);
-      run.y = fmaf(f, run.y, u[k].y);
-      run.z = fmaf(f, run.z, u[k].z);
-      run.w = fmaf(f, run.w, u[k].w);
+    for (int half = 0; half < 2; ++half) {
+      const int s1 = s0 + half * N;
+      if (s1 >= nseg) break;
+      if (s1 + N < nseg) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) u[half ^ 1][k] = *at(min(s1 + N + k, nseg - 1));
+      }
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        if (s1 + k >= nseg) break;
+        *at(s1 + k) = run;
+        const float f = dec[s1 + k];
+        const float4 v = u[half][k];
+        run.x = fmaf(f, run.x, v.x);
+        run.y = fmaf(f, run.y, v.y);
+        run.z = fmaf(f, run.z, v.z);
+        run.w = fmaf(f, run.w, v.w);
+      }
     }
   }
+  *reinterpret_cast<float4*>(a.end + bh * hs + e) = run;
 }
 
 // ---- dlg of one head.  A pair of a source step j and a later step i that reads
@@ -246,7 +246,7 @@ hipError_t launch_decay_chain(const DecayChainArgs* a, int n, hipStream_t st) {
   for (int i = 0; i < 2; ++i) c.c[i] = a[i < n ? i : 0];
   const DecayDims& d = a[0].d;
   const size_t hs = static_cast<size_t>(d.Dk) * d.Dv;
-  chain_kernel<<<dim3(d.B * d.Hv, static_cast<unsigned>((hs + 1023) / 1024), n), 256, 0, st>>>(c);
+  chain_kernel<<<dim3(d.B * d.Hv, static_cast<unsigned>((hs + 255) / 256), n), 64, 0, st>>>(c);
   return hipGetLastError();
 }
 

@@ -63,6 +63,8 @@ Cut cut(const gdn_dims* p, const DecayDims& d, bool bwd) {
 
 struct Layout {
   size_t S, R;            // segment states, forward and backward in time
+  size_t steps;           // valid steps of the segments
+  size_t end;             // the backward's recomputed final state
   size_t qa, kb, vx;      // sums for dlg
   size_t pq, pk;          // rows of grouped heads
   size_t total;
@@ -79,9 +81,15 @@ Layout layout(const gdn_dims* p, const DecayDims& d, bool bwd) {
   const Cut c = cut(p, d, bwd);
   const size_t bh = static_cast<size_t>(d.B) * d.Hv;
   const size_t states = static_cast<size_t>(c.n) * bh * d.Dk * d.Dv;
-  if (c.n > 1) L.S = take(states);
+  if (c.n > 1) {
+    L.S = take(states);
+    L.steps = take(static_cast<size_t>(d.B) * c.n);
+  }
   if (bwd) {
-    if (c.n > 1) L.R = take(states);
+    if (c.n > 1) {
+      L.R = take(states);
+      L.end = take(bh * d.Dk * d.Dv);
+    }
     const int sub = p->dtype == GDN_BF16 ? 64 : 32;
     const size_t nstat = (static_cast<size_t>(d.T) + sub - 1) / sub, nwk = gdn::decay_waves(d.Dk);
     L.qa = take(bh * nstat * nwk * gdn::kDecayQStats);
@@ -210,10 +218,12 @@ int gdn_decay_fwd(const gdn_dims* d, const void* q, const void* k, const void* v
     float* S = at<float>(ws, L.S);
     gdn::DecayWalkArgs sum = a;
     sum.walk[0].seg_sum = S;
+    sum.walk[0].seg_steps = at<float>(ws, L.steps);
     if (gdn::launch_decay_walk(sum, bf, st) != hipSuccess) return GDN_ERR_HIP;
-    const gdn::DecayChainArgs ch{dd, lg, mask, c.n, c.seg, S, state0, 0};
+    const gdn::DecayChainArgs ch{dd, lg, at<float>(ws, L.steps), c.n, S, state0, state_out, 0};
     if (gdn::launch_decay_chain(&ch, 1, st) != hipSuccess) return GDN_ERR_HIP;
     a.walk[0].seg_start = S;
+    a.walk[0].end = nullptr;
   }
   return gdn::launch_decay_walk(a, bf, st) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
 }
@@ -282,15 +292,17 @@ int gdn_decay_bwd(const gdn_dims* d, const void* q, const void* k, const void* v
     ws_.scale_u = 1.f;
     ws_.seg_sum = S;
     wr.seg_sum = R;
+    ws_.seg_steps = at<float>(ws, L.steps);
     const gdn::DecayWalkArgs sum{dd, lg, mask, c.n, c.seg, 2, {ws_, wr}};
     if (gdn::launch_decay_walk(sum, bf, st) != hipSuccess) return GDN_ERR_HIP;
-    const gdn::DecayChainArgs ch[2] = {{dd, lg, mask, c.n, c.seg, S, state0, 0},
-                                       {dd, lg, mask, c.n, c.seg, R, dS_final, 1}};
+    const gdn::DecayChainArgs ch[2] = {{dd, lg, at<float>(ws, L.steps), c.n, S, state0, at<float>(ws, L.end), 0},
+                                       {dd, lg, at<float>(ws, L.steps), c.n, R, dS_final, dstate, 1}};
     if (gdn::launch_decay_chain(ch, 2, st) != hipSuccess) return GDN_ERR_HIP;
     wq.seg_start = S;
     wk.seg_start = R;
     wv.seg_start = R;
     wv.seg_cross = S;
+    wv.end = nullptr;
   }
   const gdn::DecayWalkArgs av{dd, lg, mask, c.n, c.seg, 1, {wv, wv}};
   if (gdn::launch_decay_walk(av, bf, st) != hipSuccess) return GDN_ERR_HIP;

@@ -16,15 +16,21 @@
 // the fp32 ones for fp32 tensors.  Where bf16 operands are not tensors as they
 // were given, they are rounded as follows:
 //   - g^(L - c_j) z_j, which the state sums: as three bf16 parts (24 bits), so
-//     the state keeps fp32 precision over any number of steps;
+//     the state keeps fp32 precision over any number of steps; two parts (16
+//     bits) where only bf16 results are read from this state;
 //   - the state against x: one bf16 part, as the result is rounded to bf16 (a
 //     relative error of at most 2^-8 for each product, independent between the
 //     products); three parts where the result also enters the fp32 sums for dlg;
 //   - P: one bf16 part, as the result is rounded to bf16.
 //
-// Tiles go to LDS by direct loads, a chunk ahead where two sets of them fit.  The
-// descriptors end behind the sequence's last row of the chunk and masked or
-// padding pieces get an offset past them, so all of these read as zeros.
+// Tiles go to LDS by direct loads.  y and z have two sets of tiles where these fit,
+// and the next chunk's are asked for as soon as the chunk's own have come; x and
+// e are last read before the barrier that completes P, and asked for again behind
+// it.  The descriptors end behind the sequence's last row of the chunk and masked
+// or padding pieces get an offset past them, so all of these read as zeros.
+// Results in bf16 go to LDS and from there to memory a chunk later, as whole
+// rows: a wave's own columns would be 32 bytes of a row at a time, which costs the
+// memory pipeline four times the cycles.
 #pragma once
 
 #include "gdn_dev.h"
@@ -86,19 +92,22 @@ template <> struct Cfg<float> {
 
 constexpr uint32_t kOff = 0x80000000u;  // an offset past every descriptor here
 
-// LDS, in bytes: one or two sets of tiles, then P and the chunk's per-step
-// factors (two sets of these).  Tiles are row-major 16-byte pieces, piece p of
-// row r at place p ^ (r & 7).
+// LDS, in bytes: tiles of y and z (one or two sets), of x and e, P, the results
+// to store, and the chunk's per-step factors (two sets).  Tiles are row-major
+// 16-byte pieces, piece p of row r at place p ^ (r & 7).
 template <typename T, int KD, int NW, int NTL, bool OUT, bool DOTS>
 struct Lds {
-  static constexpr int CH = Cfg<T>::CH, EPP = Cfg<T>::EPP;
+  static constexpr int CH = Cfg<T>::CH, EPP = Cfg<T>::EPP, MAX = 160 * 1024;
   static constexpr int COLS = 16 * NW * NTL;
   static constexpr int PX = KD / EPP, PZ = COLS / EPP, PP = CH / EPP;  // pieces per row
-  static constexpr int Y = 0, Z = Y + CH * PX * 16, X = Z + CH * PZ * 16, E = X + (OUT ? CH * PX * 16 : 0);
-  static constexpr int SET = E + (DOTS ? CH * PZ * 16 : 0);
-  static constexpr int PBYTES = OUT ? CH * PP * 16 : 0, FBYTES = 2 * 3 * CH * 4;
-  static constexpr int SLOTS = 2 * SET + PBYTES + FBYTES <= 160 * 1024 ? 2 : 1;
-  static constexpr int P = SLOTS * SET, F = P + PBYTES, TOTAL = F + FBYTES;
+  static constexpr int XB = CH * PX * 16, ZB = CH * PZ * 16;
+  static constexpr int SET = XB + ZB, Y = 0, Z = XB;
+  static constexpr int XE = (OUT ? XB : 0) + (DOTS ? ZB : 0);
+  static constexpr int REST = XE + (OUT ? CH * PP * 16 : 0) + 2 * 3 * CH * 4;
+  static constexpr int SLOTS = 2 * SET + REST <= MAX ? 2 : 1;
+  static constexpr bool STAGE = OUT && sizeof(T) == 2 && SLOTS * SET + REST + ZB <= MAX;
+  static constexpr int X = SLOTS * SET, E = X + XB, P = X + XE, O = P + (OUT ? CH * PP * 16 : 0);
+  static constexpr int F = O + (STAGE ? ZB : 0), TOTAL = F + 2 * 3 * CH * 4;
 };
 
 // Loads of one tile by this wave: 64 pieces at a time.
@@ -129,8 +138,9 @@ template <int CH, int PPR, int EPP, int NW> struct Loader {
   }
 };
 
-// SPS: bf16 parts of the state in the products with x.
-template <typename T, int KD, int NW, int NTL, bool OUT, bool DOTS, int SPS>
+// SPS: bf16 parts of the state in the products with x; SPU: of the weighted z
+// that the state sums.
+template <typename T, int KD, int NW, int NTL, bool OUT, bool DOTS, int SPS, int SPU>
 __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
   using M = Lds<T, KD, NW, NTL, OUT, DOTS>;
   constexpr bool BF = sizeof(T) == 2;
@@ -211,32 +221,58 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
   ly.init(w, l, static_cast<uint32_t>(yH) * KDr * sizeof(T), KDr, rev);
   lz.init(w, l, static_cast<uint32_t>(zH) * N * sizeof(T), N, rev);
   // a chunk's rows of one head: from its first step to the sequence's end
-  auto rows = [&](const void* p, int H, int group, int D, int t0) {
+  // (all of this is the same in every lane, so the words stay in scalar registers)
+  auto rows = [&](const void* p, int H, int head, int D, int t0) {
     const int n = min(Tn - t0, CH);
-    return raw_desc(static_cast<const T*>(p) + ((bT + t0) * H + h / group) * D,
-                    (static_cast<size_t>(n - 1) * H * D + D) * sizeof(T));
+    const uint64_t at = reinterpret_cast<uint64_t>(static_cast<const T*>(p) + ((bT + t0) * H + head) * D);
+    return i32x4{static_cast<int>(at), static_cast<int>(at >> 32) & 0xffff,
+                 ((n - 1) * H * D + D) * static_cast<int>(sizeof(T)), 0x00020000};
   };
-  auto issue = [&](int ci, int slot, unsigned long long live) {
+  const int xh = h / xg, yh = h / yg, zh = h / zg;
+  const bool masked = mrow != nullptr;
+  auto issue_yz = [&](int ci, int slot, unsigned long long live) {
     char* s = sm + slot * M::SET;
     const int t0 = chunk_start(ci);
-    const i32x4 dy = rows(wk.y.p, yH, yg, KDr, t0), dz = rows(wk.z.p, zH, zg, N, t0);
-    const bool m = mrow != nullptr;
-    if (m && !rev) {
+    const i32x4 dy = rows(wk.y.p, yH, yh, KDr, t0), dz = rows(wk.z.p, zH, zh, N, t0);
+    if (masked && !rev) {
       ly.load_live(dy, s + M::Y, w, l, live);
       lz.load_live(dz, s + M::Z, w, l, live);
     } else {
       ly.load(dy, s + M::Y, w, l);
       lz.load(dz, s + M::Z, w, l);
     }
-    if constexpr (OUT) {  // x has y's row length, e has z's
-      const i32x4 dx = rows(wk.x.p, xH, xg, KDr, t0);
-      if (m && rev) ly.load_live(dx, s + M::X, w, l, live);
-      else ly.load(dx, s + M::X, w, l);
+  };
+  auto issue_xe = [&](int ci, unsigned long long live) {  // x has y's row length, e has z's
+    const int t0 = chunk_start(ci);
+    if constexpr (OUT) {
+      const i32x4 dx = rows(wk.x.p, xH, xh, KDr, t0);
+      if (masked && rev) ly.load_live(dx, sm + M::X, w, l, live);
+      else ly.load(dx, sm + M::X, w, l);
     }
     if constexpr (DOTS) {
-      const i32x4 de = rows(wk.e.p, zH, zg, N, t0);
-      if (m && rev) lz.load_live(de, s + M::E, w, l, live);
-      else lz.load(de, s + M::E, w, l);
+      const i32x4 de = rows(wk.e.p, zH, zh, N, t0);
+      if (masked && rev) lz.load_live(de, sm + M::E, w, l, live);
+      else lz.load(de, sm + M::E, w, l);
+    }
+  };
+  // results of a chunk: rows behind the sequence and columns past N lie past the
+  // descriptor
+  auto out_rows = [&](int t0, int es) {
+    return make_rsrc(static_cast<char*>(wk.w) + ((bT + t0) * Hv + h) * N * es,
+                     (static_cast<size_t>(min(Tn - t0, CH) - 1) * Hv * N + N) * es);
+  };
+  const bool staged = M::STAGE && !wk.w32;
+  auto store_staged = [&](int ci) {
+    if constexpr (M::STAGE) {
+      const rsrc_t rw = out_rows(chunk_start(ci), 2);
+      constexpr int NS = CH * PZ / 64;
+#pragma unroll
+      for (int k = 0; k < (NS + NW - 1) / NW; ++k) {
+        if (NS % NW != 0 && k * NW + w >= NS) continue;
+        const int s = (k * NW + w) * 64 + l, r = s / PZ, p = s % PZ;
+        const uint4 v = *reinterpret_cast<const uint4*>(sm + M::O + (r * PZ + (p ^ (r & 7))) * 16);
+        buf_store_u4(rw, p * 8 < N ? (static_cast<uint32_t>(rev ? CH - 1 - r : r) * Hv * N + p * 8) * 2u : kOff, v);
+      }
     }
   };
 
@@ -266,9 +302,11 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
   }
 
   unsigned long long live = 0, live_next = 0;
+  int counted = 0;  // valid steps of the segment
   if (nch > 0) {
     live = live_of(0);
-    if constexpr (M::SLOTS == 2) issue(0, 0, live);
+    if constexpr (M::SLOTS == 2) issue_yz(0, 0, live);
+    issue_xe(0, live);
   }
   const size_t nstat = (static_cast<size_t>(Tn) + CH - 1) / CH;
   for (int ci = 0; ci < nch; ++ci) {
@@ -278,9 +316,10 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
     float *frf = fc + CH, *fsw = fc + 2 * CH;
     if constexpr (M::SLOTS == 1) {
       lds_barrier();  // the chunk before is read
-      issue(ci, 0, live);
+      issue_yz(ci, 0, live);
     }
     const int L = __popcll(live);
+    counted += L;
     if (w == 0 && l < CH) {
       const float c = static_cast<float>(__popcll(live & (((rev ? 1ull : 2ull) << l) - 1ull)));
       fc[l] = c;
@@ -289,82 +328,91 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
     }
     // this wave's part of the tiles has arrived (what it stored after asking for
     // them, MT stores at least, may be on the way still)
-    if (OUT && M::SLOTS == 2 && ci > 0) wait_vm<MT>();
+    if (OUT && M::SLOTS == 2 && !staged && ci > 0) wait_vm<MT>();
     else wait_vm<0>();
     lds_barrier();
     if (ci + 1 < nch) {
       live_next = live_of(ci + 1);
-      if constexpr (M::SLOTS == 2) issue(ci + 1, slot ^ 1, live_next);
+      if constexpr (M::SLOTS == 2) issue_yz(ci + 1, slot ^ 1, live_next);
     }
+    if (staged && ci > 0) store_staged(ci - 1);
 
     f32x4 acc[MT][NTL];
     if constexpr (OUT) {
-      // ---- P, transposed tiles (rows j, columns i): the MT (MT + 1) / 2 lower
-      // ones, and zeros where a 32-deep product reaches past the diagonal
-      // (tiles (0, 1) and (2, 3))
+      // ---- P, transposed tiles (rows j, columns i).  Needed are the lower ones
+      // and, for 32-deep products with z, those up to the next even tile: runs of
+      // TW tiles of one row, one run to a wave at a time
       float intra = 0.f;
-      constexpr int LOW = MT * (MT + 1) / 2, TILES = LOW + (BF ? MT / 2 : 0);
-      for (int tl = w; tl < TILES; tl += NW) {
-        int mt, nt;
-        if (tl >= LOW) {
-          mt = 2 * (tl - LOW);
-          nt = mt + 1;
+      constexpr int TW = BF && NW < 12 ? 2 : 1, RUNS = BF ? 12 / TW : 3;
+      for (int run = w; run < RUNS; run += NW) {
+        int mt, nt0;
+        if constexpr (!BF) {
+          mt = run > 0;
+          nt0 = run - mt;
+        } else if constexpr (TW == 2) {
+          mt = run < 2 ? run : 1 + run / 2;
+          nt0 = run < 2 ? 0 : 2 * (run & 1);
         } else {
-          mt = tl >= 6 ? 3 : tl >= 3 ? 2 : tl >= 1 ? 1 : 0;
-          nt = tl - mt * (mt + 1) / 2;
+          mt = run < 4 ? run >> 1 : 2 + ((run - 4) >> 2);
+          nt0 = run < 4 ? run & 1 : (run - 4) & 3;
         }
-        f32x4 t = f4zero();
-        if (nt <= mt) {
-          f32x4 u = f4zero();
-          const char *py = tile + M::Y + nt * 16 * PX * 16, *px = tile + M::X + mt * 16 * PX * 16;
-          const char *pz = tile + M::Z + nt * 16 * PZ * 16, *pe = tile + M::E + mt * 16 * PZ * 16;
-          if constexpr (BF) {
+        f32x4 t[TW], u[TW];
 #pragma unroll
-            for (int ks = 0; ks < KD / 32; ++ks)
-              t = mfma16(load_bf16x8(py + at_x(0, ks)), load_bf16x8(px + at_x(0, ks)), t);
-            if constexpr (DOTS) {
+        for (int q = 0; q < TW; ++q) t[q] = u[q] = f4zero();
+        const char *py = tile + M::Y + nt0 * 16 * PX * 16, *px = sm + M::X + mt * 16 * PX * 16;
+        const char *pz = tile + M::Z + nt0 * 16 * PZ * 16, *pe = sm + M::E + mt * 16 * PZ * 16;
+        if constexpr (BF) {
 #pragma unroll
-              for (int ks = 0; ks < M::COLS / 32; ++ks)
-                u = mfma16(load_bf16x8(pz + at_z(0, ks)), load_bf16x8(pe + at_z(0, ks)), u);
-            }
-          } else {
+          for (int ks = 0; ks < KD / 32; ++ks) {
+            const bf16x8 xa = load_bf16x8(px + at_x(0, ks));
 #pragma unroll
-            for (int ks = 0; ks < KD / 16; ++ks) {
-              const float4 yv = *reinterpret_cast<const float4*>(py + at_x(0, ks));
-              const float4 xv = *reinterpret_cast<const float4*>(px + at_x(0, ks));
-              t = mfma16f(yv.x, xv.x, t);
-              t = mfma16f(yv.y, xv.y, t);
-              t = mfma16f(yv.z, xv.z, t);
-              t = mfma16f(yv.w, xv.w, t);
-            }
-            if constexpr (DOTS) {
+            for (int q = 0; q < TW; ++q) t[q] = mfma16(load_bf16x8(py + at_x(q, ks)), xa, t[q]);
+          }
+          if constexpr (DOTS) {
 #pragma unroll
-              for (int ks = 0; ks < M::COLS / 16; ++ks) {
-                const float4 zv = *reinterpret_cast<const float4*>(pz + at_z(0, ks));
-                const float4 ev = *reinterpret_cast<const float4*>(pe + at_z(0, ks));
-                u = mfma16f(zv.x, ev.x, u);
-                u = mfma16f(zv.y, ev.y, u);
-                u = mfma16f(zv.z, ev.z, u);
-                u = mfma16f(zv.w, ev.w, u);
-              }
+            for (int ks = 0; ks < M::COLS / 32; ++ks) {
+              const bf16x8 ea = load_bf16x8(pe + at_z(0, ks));
+#pragma unroll
+              for (int q = 0; q < TW; ++q) u[q] = mfma16(load_bf16x8(pz + at_z(q, ks)), ea, u[q]);
             }
           }
-          const float c_i = fc[16 * mt + lr];
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < KD / 16; ++ks) {
+            const f32x4 yv = *reinterpret_cast<const f32x4*>(py + at_x(0, ks));
+            const f32x4 xv = *reinterpret_cast<const f32x4*>(px + at_x(0, ks));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) t[0] = mfma16f(yv[r], xv[r], t[0]);
+          }
+          if constexpr (DOTS) {
+#pragma unroll
+            for (int ks = 0; ks < M::COLS / 16; ++ks) {
+              const f32x4 zv = *reinterpret_cast<const f32x4*>(pz + at_z(0, ks));
+              const f32x4 ev = *reinterpret_cast<const f32x4*>(pe + at_z(0, ks));
+#pragma unroll
+              for (int r = 0; r < 4; ++r) u[0] = mfma16f(zv[r], ev[r], u[0]);
+            }
+          }
+        }
+        const float c_i = fc[16 * mt + lr];
+        char* pp = sm + M::P + (16 * mt + lr) * PP * 16;
+#pragma unroll
+        for (int q = 0; q < TW; ++q) {
+          const int nt = nt0 + q;
           const f32x4 c_j = *reinterpret_cast<const f32x4*>(fc + 16 * nt + 4 * g);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const float dn = c_i - c_j[r];
             const bool in = 16 * nt + 4 * g + r <= 16 * mt + lr;
-            t[r] = in ? t[r] * exp2_fast(lg2 * dn) * scale_p : 0.f;
-            if constexpr (DOTS) intra += in ? dn * t[r] * u[r] : 0.f;
+            t[q][r] = in ? t[q][r] * exp2_fast(lg2 * dn) * scale_p : 0.f;
+            if constexpr (DOTS) intra += in ? dn * t[q][r] * u[q][r] : 0.f;
           }
+          if constexpr (BF)
+            *reinterpret_cast<uint2*>(pp + (((2 * nt + (g >> 1)) ^ (lr & 7)) * 16 + (g & 1) * 8)) =
+                pack4_bf16(t[q][0], t[q][1], t[q][2], t[q][3]);
+          else
+            *reinterpret_cast<f32x4*>(pp + ((4 * nt + g) ^ (lr & 7)) * 16) = t[q];
         }
-        char* pp = sm + M::P + (16 * mt + lr) * PP * 16;
-        if constexpr (BF)
-          *reinterpret_cast<uint2*>(pp + (((2 * nt + (g >> 1)) ^ (lr & 7)) * 16 + (g & 1) * 8)) =
-              pack4_bf16(t[0], t[1], t[2], t[3]);
-        else
-          *reinterpret_cast<f32x4*>(pp + ((4 * nt + g) ^ (lr & 7)) * 16) = t;
       }
       // ---- S^T x, transposed tiles (rows are columns of w, columns are steps)
 #pragma unroll
@@ -376,7 +424,7 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
         for (int ks = 0; ks < KD / 32; ++ks) {
           bf16x8 xa[MT];
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) xa[mt] = load_bf16x8(tile + M::X + at_x(mt, ks));
+          for (int mt = 0; mt < MT; ++mt) xa[mt] = load_bf16x8(sm + M::X + at_x(mt, ks));
 #pragma unroll
           for (int n = 0; n < NTL; ++n) {
             float v[8];
@@ -398,7 +446,7 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
         for (int i = 0; i < KT; ++i)
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            const f32x4 xv = *reinterpret_cast<const f32x4*>(tile + M::X + at_x(mt, i));
+            const f32x4 xv = *reinterpret_cast<const f32x4*>(sm + M::X + at_x(mt, i));
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -418,14 +466,14 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
             float ev[4];
             if constexpr (BF) {
               const uint2 u = *reinterpret_cast<const uint2*>(
-                  tile + M::E + (row * PZ + ((c >> 3) ^ (lr & 7))) * 16 + (c & 4) * 2);
+                  sm + M::E + (row * PZ + ((c >> 3) ^ (lr & 7))) * 16 + (c & 4) * 2);
               ev[0] = __uint_as_float(u.x << 16);
               ev[1] = __uint_as_float(u.x & 0xffff0000u);
               ev[2] = __uint_as_float(u.y << 16);
               ev[3] = __uint_as_float(u.y & 0xffff0000u);
             } else {
               *reinterpret_cast<f32x4*>(ev) =
-                  *reinterpret_cast<const f32x4*>(tile + M::E + (row * PZ + ((c >> 2) ^ (lr & 7))) * 16);
+                  *reinterpret_cast<const f32x4*>(sm + M::E + (row * PZ + ((c >> 2) ^ (lr & 7))) * 16);
             }
             float f = 0.f;
 #pragma unroll
@@ -446,9 +494,7 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
           o[2] = rev ? static_cast<float>(L) : intra;
         }
       }
-      lds_barrier();  // P is whole
     }
-
     // ---- products with z: P z, and the state's update
     const float gL = exp2_fast(lg2 * static_cast<float>(L));
 #pragma unroll
@@ -457,41 +503,56 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
       for (int n = 0; n < NTL; ++n)
 #pragma unroll
         for (int r = 0; r < 4; ++r) S[i][n][r] *= gL;
+    if constexpr (OUT) {
+      lds_barrier();  // P is whole, x and e are read
+      if (ci + 1 < nch) issue_xe(ci + 1, live_next);
+    }
+
     if constexpr (BF) {
 #pragma unroll
       for (int kt = 0; kt < CH / 32; ++kt) {
         float sw[8];
         *reinterpret_cast<f32x4*>(sw) = *reinterpret_cast<const f32x4*>(fsw + 32 * kt + 8 * g);
         *reinterpret_cast<f32x4*>(sw + 4) = *reinterpret_cast<const f32x4*>(fsw + 32 * kt + 8 * g + 4);
-        bf16x8 zp[NTL][3];
+        // reads first, so that the products with P and the splitting of z run
+        // while y's arrive; then products on different state tiles in turn
+        uint4 zu[NTL];
+        bf16x8 zp[NTL][SPU], pa[MT], ya[KT];
 #pragma unroll
         for (int n = 0; n < NTL; ++n) {
           const char* zt = tile + M::Z + kt * 32 * PZ * 16;
           const uint2 z0 = lds_read_tr16(zt + tz[n][0]), z1 = lds_read_tr16(zt + tz[n][1]);
-          const uint4 zu = make_uint4(z0.x, z0.y, z1.x, z1.y);
-          if constexpr (OUT) {
-            const bf16x8 zf = as_bf16x8(zu);
+          zu[n] = make_uint4(z0.x, z0.y, z1.x, z1.y);
+        }
+        if constexpr (OUT) {
 #pragma unroll
-            for (int mt = 2 * kt; mt < MT; ++mt)
-              acc[mt][n] = mfma16(zf, load_bf16x8(sm + M::P + ((16 * mt + lr) * PP + ((4 * kt + g) ^ (lr & 7))) * 16),
-                                  acc[mt][n]);
-          }
-          float v[8];
-          Vec16<bf16>::unpack(zu, v);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] *= sw[k];
-          split8<3>(v, zp[n]);
+          for (int mt = 2 * kt; mt < MT; ++mt)
+            pa[mt] = load_bf16x8(sm + M::P + ((16 * mt + lr) * PP + ((4 * kt + g) ^ (lr & 7))) * 16);
         }
 #pragma unroll
         for (int i = 0; i < KT; ++i) {
           const char* yt = tile + M::Y + kt * 32 * PX * 16 + (i / 4) * 128 + (i & 1) * 8;
           const uint2 y0 = lds_read_tr16(yt + ty[(i / 2) & 1][0]), y1 = lds_read_tr16(yt + ty[(i / 2) & 1][1]);
-          const bf16x8 ya = as_bf16x8(make_uint4(y0.x, y0.y, y1.x, y1.y));
-#pragma unroll
-          for (int s = 2; s >= 0; --s)
-#pragma unroll
-            for (int n = 0; n < NTL; ++n) S[i][n] = mfma16(ya, zp[n][s], S[i][n]);
+          ya[i] = as_bf16x8(make_uint4(y0.x, y0.y, y1.x, y1.y));
         }
+#pragma unroll
+        for (int n = 0; n < NTL; ++n) {
+          if constexpr (OUT) {
+#pragma unroll
+            for (int mt = 2 * kt; mt < MT; ++mt) acc[mt][n] = mfma16(as_bf16x8(zu[n]), pa[mt], acc[mt][n]);
+          }
+          float v[8];
+          Vec16<bf16>::unpack(zu[n], v);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] *= sw[k];
+          split8<SPU>(v, zp[n]);
+        }
+#pragma unroll
+        for (int s = 0; s < SPU; ++s)
+#pragma unroll
+          for (int i = 0; i < KT; ++i)
+#pragma unroll
+            for (int n = 0; n < NTL; ++n) S[i][n] = mfma16(ya[i], zp[n][s], S[i][n]);
       }
     } else {
 #pragma unroll
@@ -531,28 +592,31 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
     }
 
     if constexpr (OUT) {
-      // rows behind the sequence and columns past N lie past the descriptor
-      const int es = wk.w32 || !BF ? 4 : 2, steps = min(Tn - t0, CH);
-      const rsrc_t rw = make_rsrc(static_cast<char*>(wk.w) + ((bT + t0) * Hv + h) * N * es,
-                                  (static_cast<size_t>(steps - 1) * Hv * N + N) * es);
+      if (staged) {
+        if constexpr (M::STAGE) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const int row = 16 * mt + lr;
-        const uint32_t ro = static_cast<uint32_t>(rev ? CH - 1 - row : row) * static_cast<uint32_t>(Hv * N);
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int n = 0; n < NTL; ++n) {
-          const int c = column(n, 4 * g);
-          const uint32_t o = c < N ? (ro + c) * es : kOff;
-          if (es == 4) {
-            buf_store_u4(rw, o, __builtin_bit_cast(uint4, acc[mt][n]));
-          } else if (n < NTL / 2 * 2) {  // eight columns of two tiles
-            if (n & 1) continue;
-            const uint2 p = pack4_bf16(acc[mt][n][0], acc[mt][n][1], acc[mt][n][2], acc[mt][n][3]);
-            const f32x4 q = acc[mt][n + 1 < NTL ? n + 1 : n];
-            const uint2 s = pack4_bf16(q[0], q[1], q[2], q[3]);
-            buf_store_u4(rw, o, make_uint4(p.x, p.y, s.x, s.y));
-          } else {
-            buf_store_u2(rw, o, pack4_bf16(acc[mt][n][0], acc[mt][n][1], acc[mt][n][2], acc[mt][n][3]));
+            for (int n = 0; n < NTL; ++n) {
+              const int c = column(n, 4 * g), row = 16 * mt + lr;
+              *reinterpret_cast<uint2*>(sm + M::O + (row * PZ + ((c >> 3) ^ (lr & 7))) * 16 + (c & 4) * 2) =
+                  pack4_bf16(acc[mt][n][0], acc[mt][n][1], acc[mt][n][2], acc[mt][n][3]);
+            }
+        }
+      } else {
+        const bool wide = !BF || wk.w32;
+        const rsrc_t rw = out_rows(t0, wide ? 4 : 2);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const int row = 16 * mt + lr;
+          const uint32_t ro = static_cast<uint32_t>(rev ? CH - 1 - row : row) * static_cast<uint32_t>(Hv * N);
+#pragma unroll
+          for (int n = 0; n < NTL; ++n) {
+            const int c = column(n, 4 * g);
+            if (wide) buf_store_u4(rw, c < N ? (ro + c) * 4u : kOff, __builtin_bit_cast(uint4, acc[mt][n]));
+            else
+              buf_store_u2(rw, c < N ? (ro + c) * 2u : kOff,
+                           pack4_bf16(acc[mt][n][0], acc[mt][n][1], acc[mt][n][2], acc[mt][n][3]));
           }
         }
       }
@@ -560,15 +624,21 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
     live = live_next;
   }
 
+  if (staged && nch > 0) {
+    lds_barrier();
+    store_staged(nch - 1);
+  }
+
   // ---- the state behind the segment
   float* dst = nullptr;
   const float* crs = nullptr;
   if constexpr (OUT) {
-    if (sg == (rev ? 0 : nseg - 1) && wk.end) dst = wk.end + bh * hs;
+    if (wk.end) dst = wk.end + bh * hs;  // (one segment)
     if (wk.seg_cross) crs = wk.seg_cross + (static_cast<size_t>(sg) * BH + bh) * hs;
     else if (wk.cross) crs = wk.cross + bh * hs;
   } else {
     dst = wk.seg_sum + (static_cast<size_t>(sg) * BH + bh) * hs;
+    if (wk.seg_steps && h == 0 && threadIdx.x == 0) wk.seg_steps[b * nseg + sg] = static_cast<float>(counted);
   }
   float dot = 0.f;
   if (crs) {
@@ -607,9 +677,10 @@ hipError_t launch_nw(const DecayWalkArgs& a, hipStream_t st) {
   const int n = a.d.B * a.d.Hv * a.nseg;
   const dim3 grid((n + 7) / 8 * 8, a.nwalk);
   const DecayWalk& w = a.walk[0];
-  if (w.seg_sum) walk_kernel<T, KD, NW, NTL, false, false, 1><<<grid, 64 * NW, 0, st>>>(a);
-  else if (w.e.p) walk_kernel<T, KD, NW, NTL, true, true, 3><<<grid, 64 * NW, 0, st>>>(a);
-  else walk_kernel<T, KD, NW, NTL, true, false, 1><<<grid, 64 * NW, 0, st>>>(a);
+  if (w.seg_sum) walk_kernel<T, KD, NW, NTL, false, false, 1, 3><<<grid, 64 * NW, 0, st>>>(a);
+  else if (w.e.p) walk_kernel<T, KD, NW, NTL, true, true, 3, 3><<<grid, 64 * NW, 0, st>>>(a);
+  else if (w.end || w.dots) walk_kernel<T, KD, NW, NTL, true, false, 1, 3><<<grid, 64 * NW, 0, st>>>(a);
+  else walk_kernel<T, KD, NW, NTL, true, false, 1, 2><<<grid, 64 * NW, 0, st>>>(a);
   return hipGetLastError();
 }
 
