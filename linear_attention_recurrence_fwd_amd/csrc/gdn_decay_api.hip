@@ -46,7 +46,7 @@ Cut cut(const gdn_dims* p, const DecayDims& d, bool bwd) {
   const int nc = d.nchunk();
   int n = 1;
   if (p->algo != GDN_ALGO_CHUNK && nc > 1) {
-    const int want = 512, bh = d.B * d.Hv;
+    const int want = 256, bh = d.B * d.Hv;
     n = (want + bh - 1) / bh;
   }
   // the backward's sums for dlg follow the boundaries chunk by chunk from the

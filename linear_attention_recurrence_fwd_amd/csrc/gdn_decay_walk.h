@@ -90,11 +90,18 @@ template <> struct Cfg<float> {
   static constexpr int CH = 32, EPP = 4;
 };
 
+// Place of piece p of row r in a tile's row: p ^ key(r).  Eight rows in turn get
+// eight keys, so a read of one piece of eight rows meets no bank twice, and four
+// rows from a multiple of four get keys two apart, so that a transposing read (four
+// rows, four neighbouring pieces, half of each) meets each bank twice, which is
+// the least that half pieces allow.
+__device__ __forceinline__ int key(int r) { return ((r & 3) << 1) | ((r >> 2) & 1); }
+
 constexpr uint32_t kOff = 0x80000000u;  // an offset past every descriptor here
 
 // LDS, in bytes: tiles of y and z (one or two sets), of x and e, P, the results
 // to store, and the chunk's per-step factors (two sets).  Tiles are row-major
-// 16-byte pieces, piece p of row r at place p ^ (r & 7).
+// 16-byte pieces, piece p of row r at place p ^ key(r).
 template <typename T, int KD, int NW, int NTL, bool OUT, bool DOTS>
 struct Lds {
   static constexpr int CH = Cfg<T>::CH, EPP = Cfg<T>::EPP, MAX = 160 * 1024;
@@ -118,7 +125,7 @@ template <int CH, int PPR, int EPP, int NW> struct Loader {
   __device__ __forceinline__ void init(int w, int l, uint32_t row_bytes, int D, bool rev) {
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-      const int s = (k * NW + w) * 64 + l, r = s / PPR, p = (s % PPR) ^ (r & 7);
+      const int s = (k * NW + w) * 64 + l, r = s / PPR, p = (s % PPR) ^ key(r);
       off[k] = p * EPP < D ? (rev ? CH - 1 - r : r) * row_bytes + p * 16 : kOff;
     }
   }
@@ -270,7 +277,7 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
       for (int k = 0; k < (NS + NW - 1) / NW; ++k) {
         if (NS % NW != 0 && k * NW + w >= NS) continue;
         const int s = (k * NW + w) * 64 + l, r = s / PZ, p = s % PZ;
-        const uint4 v = *reinterpret_cast<const uint4*>(sm + M::O + (r * PZ + (p ^ (r & 7))) * 16);
+        const uint4 v = *reinterpret_cast<const uint4*>(sm + M::O + (r * PZ + (p ^ key(r))) * 16);
         buf_store_u4(rw, p * 8 < N ? (static_cast<uint32_t>(rev ? CH - 1 - r : r) * Hv * N + p * 8) * 2u : kOff, v);
       }
     }
@@ -278,10 +285,10 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
 
   // byte offsets of this lane's operand pieces in a tile: row lr (a 16-row
   // tile further is a constant further), piece 4 ks + g for even and odd ks
-  const uint32_t rx[2] = {static_cast<uint32_t>(lr * PX + (g ^ (lr & 7))) * 16u,
-                          static_cast<uint32_t>(lr * PX + ((4 + g) ^ (lr & 7))) * 16u};
-  const uint32_t rz[2] = {static_cast<uint32_t>(lr * PZ + (g ^ (lr & 7))) * 16u,
-                          static_cast<uint32_t>(lr * PZ + ((4 + g) ^ (lr & 7))) * 16u};
+  const uint32_t rx[2] = {static_cast<uint32_t>(lr * PX + (g ^ key(lr))) * 16u,
+                          static_cast<uint32_t>(lr * PX + ((4 + g) ^ key(lr))) * 16u};
+  const uint32_t rz[2] = {static_cast<uint32_t>(lr * PZ + (g ^ key(lr))) * 16u,
+                          static_cast<uint32_t>(lr * PZ + ((4 + g) ^ key(lr))) * 16u};
   auto at_x = [&](int tile, int ks) { return rx[ks & 1] + tile * 16 * PX * 16 + (ks >> 1) * 128; };
   auto at_z = [&](int tile, int ks) { return rz[ks & 1] + tile * 16 * PZ * 16 + (ks >> 1) * 128; };
   // transposing reads (bf16): lane (lr, g) addresses row 8 g + lr/4 (+ 4 for the
@@ -293,11 +300,11 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
     const int row = tr + 4 * q;
 #pragma unroll
     for (int e = 0; e < 2; ++e)
-      ty[e][q] = static_cast<uint32_t>(row * PX + ((4 * e + (lr & 3)) ^ (row & 7))) * 16u;
+      ty[e][q] = static_cast<uint32_t>(row * PX + ((4 * e + (lr & 3)) ^ key(row))) * 16u;
 #pragma unroll
     for (int n = 0; n < NTL; ++n) {
       const int c = column(n, 4 * (lr & 3));  // four columns from here
-      tz[n][q] = static_cast<uint32_t>(row * PZ + ((c >> 3) ^ (row & 7))) * 16u + (c & 4) * 2;
+      tz[n][q] = static_cast<uint32_t>(row * PZ + ((c >> 3) ^ key(row))) * 16u + (c & 4) * 2;
     }
   }
 
@@ -408,10 +415,10 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
             if constexpr (DOTS) intra += in ? dn * t[q][r] * u[q][r] : 0.f;
           }
           if constexpr (BF)
-            *reinterpret_cast<uint2*>(pp + (((2 * nt + (g >> 1)) ^ (lr & 7)) * 16 + (g & 1) * 8)) =
+            *reinterpret_cast<uint2*>(pp + (((2 * nt + (g >> 1)) ^ key(lr)) * 16 + (g & 1) * 8)) =
                 pack4_bf16(t[q][0], t[q][1], t[q][2], t[q][3]);
           else
-            *reinterpret_cast<f32x4*>(pp + ((4 * nt + g) ^ (lr & 7)) * 16) = t[q];
+            *reinterpret_cast<f32x4*>(pp + ((4 * nt + g) ^ key(lr)) * 16) = t[q];
         }
       }
       // ---- S^T x, transposed tiles (rows are columns of w, columns are steps)
@@ -466,14 +473,14 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
             float ev[4];
             if constexpr (BF) {
               const uint2 u = *reinterpret_cast<const uint2*>(
-                  sm + M::E + (row * PZ + ((c >> 3) ^ (lr & 7))) * 16 + (c & 4) * 2);
+                  sm + M::E + (row * PZ + ((c >> 3) ^ key(lr))) * 16 + (c & 4) * 2);
               ev[0] = __uint_as_float(u.x << 16);
               ev[1] = __uint_as_float(u.x & 0xffff0000u);
               ev[2] = __uint_as_float(u.y << 16);
               ev[3] = __uint_as_float(u.y & 0xffff0000u);
             } else {
               *reinterpret_cast<f32x4*>(ev) =
-                  *reinterpret_cast<const f32x4*>(sm + M::E + (row * PZ + ((c >> 2) ^ (lr & 7))) * 16);
+                  *reinterpret_cast<const f32x4*>(sm + M::E + (row * PZ + ((c >> 2) ^ key(lr))) * 16);
             }
             float f = 0.f;
 #pragma unroll
@@ -517,7 +524,13 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
         // reads first, so that the products with P and the splitting of z run
         // while y's arrive; then products on different state tiles in turn
         uint4 zu[NTL];
-        bf16x8 zp[NTL][SPU], pa[MT], ya[KT];
+        constexpr int YH = KT > 8 ? KT / 2 : KT;  // y tiles held at a time
+        bf16x8 zp[NTL][SPU], pa[MT], ya[YH];
+        auto load_y = [&](int i) {
+          const char* yt = tile + M::Y + kt * 32 * PX * 16 + (i / 4) * 128 + (i & 1) * 8;
+          const uint2 y0 = lds_read_tr16(yt + ty[(i / 2) & 1][0]), y1 = lds_read_tr16(yt + ty[(i / 2) & 1][1]);
+          return as_bf16x8(make_uint4(y0.x, y0.y, y1.x, y1.y));
+        };
 #pragma unroll
         for (int n = 0; n < NTL; ++n) {
           const char* zt = tile + M::Z + kt * 32 * PZ * 16;
@@ -527,14 +540,10 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
         if constexpr (OUT) {
 #pragma unroll
           for (int mt = 2 * kt; mt < MT; ++mt)
-            pa[mt] = load_bf16x8(sm + M::P + ((16 * mt + lr) * PP + ((4 * kt + g) ^ (lr & 7))) * 16);
+            pa[mt] = load_bf16x8(sm + M::P + ((16 * mt + lr) * PP + ((4 * kt + g) ^ key(lr))) * 16);
         }
 #pragma unroll
-        for (int i = 0; i < KT; ++i) {
-          const char* yt = tile + M::Y + kt * 32 * PX * 16 + (i / 4) * 128 + (i & 1) * 8;
-          const uint2 y0 = lds_read_tr16(yt + ty[(i / 2) & 1][0]), y1 = lds_read_tr16(yt + ty[(i / 2) & 1][1]);
-          ya[i] = as_bf16x8(make_uint4(y0.x, y0.y, y1.x, y1.y));
-        }
+        for (int i = 0; i < YH; ++i) ya[i] = load_y(i);
 #pragma unroll
         for (int n = 0; n < NTL; ++n) {
           if constexpr (OUT) {
@@ -548,11 +557,18 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
           split8<SPU>(v, zp[n]);
         }
 #pragma unroll
-        for (int s = 0; s < SPU; ++s)
+        for (int i0 = 0; i0 < KT; i0 += YH) {
+          if (i0 > 0) {
 #pragma unroll
-          for (int i = 0; i < KT; ++i)
+            for (int i = 0; i < YH; ++i) ya[i] = load_y(i0 + i);
+          }
 #pragma unroll
-            for (int n = 0; n < NTL; ++n) S[i][n] = mfma16(ya[i], zp[n][s], S[i][n]);
+          for (int s = 0; s < SPU; ++s)
+#pragma unroll
+            for (int i = 0; i < YH; ++i)
+#pragma unroll
+              for (int n = 0; n < NTL; ++n) S[i0 + i][n] = mfma16(ya[i], zp[n][s], S[i0 + i][n]);
+        }
       }
     } else {
 #pragma unroll
@@ -565,13 +581,13 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int row = 16 * bq + 4 * g + r;
-            zv[n][r] = *reinterpret_cast<const float*>(tile + M::Z + (row * PZ + ((c >> 2) ^ (row & 7))) * 16 + (c & 3) * 4);
+            zv[n][r] = *reinterpret_cast<const float*>(tile + M::Z + (row * PZ + ((c >> 2) ^ key(row))) * 16 + (c & 3) * 4);
           }
         }
         if constexpr (OUT) {
 #pragma unroll
           for (int mt = bq; mt < MT; ++mt) {
-            const f32x4 pv = *reinterpret_cast<const f32x4*>(sm + M::P + ((16 * mt + lr) * PP + ((4 * bq + g) ^ (lr & 7))) * 16);
+            const f32x4 pv = *reinterpret_cast<const f32x4*>(sm + M::P + ((16 * mt + lr) * PP + ((4 * bq + g) ^ key(lr))) * 16);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -584,7 +600,7 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
           for (int r = 0; r < 4; ++r) {
             const int row = 16 * bq + 4 * g + r;
             const float yv = *reinterpret_cast<const float*>(
-                tile + M::Y + (row * PX + ((4 * i + (lr >> 2)) ^ (row & 7))) * 16 + (lr & 3) * 4);
+                tile + M::Y + (row * PX + ((4 * i + (lr >> 2)) ^ key(row))) * 16 + (lr & 3) * 4);
 #pragma unroll
             for (int n = 0; n < NTL; ++n) S[i][n] = mfma16f(yv, zv[n][r] * sw[r], S[i][n]);
           }
@@ -599,7 +615,7 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
 #pragma unroll
             for (int n = 0; n < NTL; ++n) {
               const int c = column(n, 4 * g), row = 16 * mt + lr;
-              *reinterpret_cast<uint2*>(sm + M::O + (row * PZ + ((c >> 3) ^ (lr & 7))) * 16 + (c & 4) * 2) =
+              *reinterpret_cast<uint2*>(sm + M::O + (row * PZ + ((c >> 3) ^ key(lr))) * 16 + (c & 4) * 2) =
                   pack4_bf16(acc[mt][n][0], acc[mt][n][1], acc[mt][n][2], acc[mt][n][3]);
             }
         }
