@@ -23,10 +23,12 @@
 //     products); three parts where the result also enters the fp32 sums for dlg;
 //   - P: one bf16 part, as the result is rounded to bf16.
 //
-// Tiles go to LDS by direct loads.  y and z have two sets of tiles where these fit,
-// and the next chunk's are asked for as soon as the chunk's own have come; x and
-// e are last read before the barrier that completes P, and asked for again behind
-// it.  The descriptors end behind the sequence's last row of the chunk and masked
+// Tiles go to LDS by direct loads into a second set, where two sets fit, while the
+// chunk's own are used; x and e, which are read first, into their only set otherwise
+// as soon as they are.  With two sets of all, loads stand between the products one
+// at a time: asked for in a row they hold up every wave, as a compute unit takes
+// one (1 KB) in about 25 cycles; and the only product that needs the other waves'
+// P comes last, behind the state's update.  The descriptors end behind the sequence's last row of the chunk and masked
 // or padding pieces get an offset past them, so all of these read as zeros.
 // Results in bf16 go to LDS and from there to memory a chunk later, as whole
 // rows: a wave's own columns would be 32 bytes of a row at a time, which costs the
@@ -90,17 +92,23 @@ template <> struct Cfg<float> {
   static constexpr int CH = 32, EPP = 4;
 };
 
-// Place of piece p of row r in a tile's row: p ^ key(r).  Eight rows in turn get
-// eight keys, so a read of one piece of eight rows meets no bank twice, and four
-// rows from a multiple of four get keys two apart, so that a transposing read (four
-// rows, four neighbouring pieces, half of each) meets each bank twice, which is
-// the least that half pieces allow.
-__device__ __forceinline__ int key(int r) { return ((r & 3) << 1) | ((r >> 2) & 1); }
+// Place of piece p of row r in a tile's row of PPR pieces: p ^ key(r).  LDS serves
+// 256 bytes (16 pieces) a cycle from 64 banks, over all 64 lanes of a read (measured:
+// a read takes as many cycles as distinct rows meet on its busiest bank).  With
+// these keys 16 rows' pieces of one number lie on all 16 places: a 16-byte read of 16
+// rows by 4 pieces takes 4 cycles, the least.  (Rows of 8 or 24 pieces start on the
+// other half of the places in turn, which stands for the key's fourth bit.)  A
+// transposing read of four neighbouring half pieces of 16 rows takes 4 cycles (2 if
+// it took lower and upper halves in turn, but then x had to be read in the same
+// order, eight bytes at a time, and put together again).
+template <int PPR> __device__ __forceinline__ int key(int r) {
+  return PPR % 16 == 0 ? ((r & 1) << 3) | ((r >> 1) & 7) : (r >> 1) & 7;
+}
 
 constexpr uint32_t kOff = 0x80000000u;  // an offset past every descriptor here
 
-// LDS, in bytes: tiles of y and z (one or two sets), of x and e, P, the results
-// to store, and the chunk's per-step factors (two sets).  Tiles are row-major
+// LDS, in bytes: tiles of y and z and of x and e (one or two sets each), P, the
+// results to store, and the chunk's per-step factors (two sets).  Tiles are row-major
 // 16-byte pieces, piece p of row r at place p ^ key(r).
 template <typename T, int KD, int NW, int NTL, bool OUT, bool DOTS>
 struct Lds {
@@ -110,10 +118,11 @@ struct Lds {
   static constexpr int XB = CH * PX * 16, ZB = CH * PZ * 16;
   static constexpr int SET = XB + ZB, Y = 0, Z = XB;
   static constexpr int XE = (OUT ? XB : 0) + (DOTS ? ZB : 0);
-  static constexpr int REST = XE + (OUT ? CH * PP * 16 : 0) + 2 * 3 * CH * 4;
-  static constexpr int SLOTS = 2 * SET + REST <= MAX ? 2 : 1;
-  static constexpr bool STAGE = OUT && sizeof(T) == 2 && SLOTS * SET + REST + ZB <= MAX;
-  static constexpr int X = SLOTS * SET, E = X + XB, P = X + XE, O = P + (OUT ? CH * PP * 16 : 0);
+  static constexpr int REST = (OUT ? CH * PP * 16 : 0) + 2 * 3 * CH * 4;
+  static constexpr int SLOTS = 2 * SET + XE + REST <= MAX ? 2 : 1;
+  static constexpr bool STAGE = OUT && sizeof(T) == 2 && SLOTS * SET + XE + REST + ZB <= MAX;
+  static constexpr bool XE2 = OUT && SLOTS == 2 && 2 * (SET + XE) + REST + (STAGE ? ZB : 0) <= MAX;
+  static constexpr int X = SLOTS * SET, E = X + XB, P = X + (XE2 ? 2 : 1) * XE, O = P + (OUT ? CH * PP * 16 : 0);
   static constexpr int F = O + (STAGE ? ZB : 0), TOTAL = F + 2 * 3 * CH * 4;
 };
 
@@ -125,25 +134,32 @@ template <int CH, int PPR, int EPP, int NW> struct Loader {
   __device__ __forceinline__ void init(int w, int l, uint32_t row_bytes, int D, bool rev) {
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-      const int s = (k * NW + w) * 64 + l, r = s / PPR, p = (s % PPR) ^ key(r);
+      const int s = (k * NW + w) * 64 + l, r = s / PPR, p = (s % PPR) ^ key<PPR>(r);
       off[k] = p * EPP < D ? (rev ? CH - 1 - r : r) * row_bytes + p * 16 : kOff;
     }
+  }
+  // where rows whose bit in live is clear read as zeros
+  __device__ __forceinline__ uint32_t live_off(int k, int w, int l, unsigned long long live) const {
+    const int r = ((k * NW + w) * 64 + l) / PPR;
+    return (live >> r) & 1 ? off[k] : kOff;
   }
   __device__ __forceinline__ void load(const i32x4& desc, char* dst, int w, int l) const {
 #pragma unroll
     for (int k = 0; k < PER; ++k)
       if (N % NW == 0 || k * NW + w < N) dma16(desc, dst + (k * NW + w) * 1024, off[k]);
   }
-  // rows whose bit in live is clear read as zeros
   __device__ __forceinline__ void load_live(const i32x4& desc, char* dst, int w, int l, unsigned long long live) const {
 #pragma unroll
     for (int k = 0; k < PER; ++k)
-      if (N % NW == 0 || k * NW + w < N) {
-        const int r = ((k * NW + w) * 64 + l) / PPR;
-        dma16(desc, dst + (k * NW + w) * 1024, (live >> r) & 1 ? off[k] : kOff);
-      }
+      if (N % NW == 0 || k * NW + w < N) dma16(desc, dst + (k * NW + w) * 1024, live_off(k, w, l, live));
   }
 };
+
+// dma16 for a place that nothing reads before the next barrier: without the clobber
+// that would keep LDS reads from moving past it.
+__device__ __forceinline__ void dma16_ahead(const i32x4& r, const void* lds, uint32_t off) {
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(r), "{m0}"(lds_addr(lds)));
+}
 
 // SPS: bf16 parts of the state in the products with x; SPU: of the weighted z
 // that the state sums.
@@ -214,12 +230,16 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
   const int t_lo = sg * a.seg * kDecayChunk, t_hi = min(Tn, t_lo + a.seg * kDecayChunk);
   const int nch = t_hi > t_lo ? (t_hi - t_lo + CH - 1) / CH : 0;
   auto chunk_start = [&](int ci) { return t_lo + (rev ? nch - 1 - ci : ci) * CH; };
-  // the mask byte of this lane's step of a chunk (walk order), and the live steps
-  auto live_of = [&](int ci) -> unsigned long long {
+  // the mask byte of this lane's step of a chunk (walk order; any where there is
+  // no such step), and the live steps
+  auto mask_byte = [&](int ci) -> int {
+    if (mrow == nullptr || ci >= nch) return 1;
     const int t = chunk_start(ci) + (rev ? CH - 1 - l : l);
-    bool v = l < CH && t < Tn;
-    if (mrow != nullptr && v) v = mrow[t] != 0;
-    return __ballot(v);
+    return mrow[max(0, min(t, Tn - 1))];
+  };
+  auto live_of = [&](int ci, int byte) -> unsigned long long {
+    const int t = chunk_start(ci) + (rev ? CH - 1 - l : l);
+    return __ballot(l < CH && t < Tn && byte != 0);
   };
 
   const int xH = wk.x.H, xg = wk.x.group, yH = wk.y.H, yg = wk.y.group, zH = wk.z.H, zg = wk.z.group;
@@ -249,17 +269,18 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
       lz.load(dz, s + M::Z, w, l);
     }
   };
-  auto issue_xe = [&](int ci, unsigned long long live) {  // x has y's row length, e has z's
+  auto issue_xe = [&](int ci, int slot, unsigned long long live) {  // x has y's row length, e has z's
+    char* s = sm + (M::XE2 ? slot * M::XE : 0);
     const int t0 = chunk_start(ci);
     if constexpr (OUT) {
       const i32x4 dx = rows(wk.x.p, xH, xh, KDr, t0);
-      if (masked && rev) ly.load_live(dx, sm + M::X, w, l, live);
-      else ly.load(dx, sm + M::X, w, l);
+      if (masked && rev) ly.load_live(dx, s + M::X, w, l, live);
+      else ly.load(dx, s + M::X, w, l);
     }
     if constexpr (DOTS) {
       const i32x4 de = rows(wk.e.p, zH, zh, N, t0);
-      if (masked && rev) lz.load_live(de, sm + M::E, w, l, live);
-      else lz.load(de, sm + M::E, w, l);
+      if (masked && rev) lz.load_live(de, s + M::E, w, l, live);
+      else lz.load(de, s + M::E, w, l);
     }
   };
   // results of a chunk: rows behind the sequence and columns past N lie past the
@@ -277,82 +298,137 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
       for (int k = 0; k < (NS + NW - 1) / NW; ++k) {
         if (NS % NW != 0 && k * NW + w >= NS) continue;
         const int s = (k * NW + w) * 64 + l, r = s / PZ, p = s % PZ;
-        const uint4 v = *reinterpret_cast<const uint4*>(sm + M::O + (r * PZ + (p ^ key(r))) * 16);
+        const uint4 v = *reinterpret_cast<const uint4*>(sm + M::O + (r * PZ + (p ^ key<PZ>(r))) * 16);
         buf_store_u4(rw, p * 8 < N ? (static_cast<uint32_t>(rev ? CH - 1 - r : r) * Hv * N + p * 8) * 2u : kOff, v);
       }
     }
   };
 
-  // byte offsets of this lane's operand pieces in a tile: row lr (a 16-row
-  // tile further is a constant further), piece 4 ks + g for even and odd ks
-  const uint32_t rx[2] = {static_cast<uint32_t>(lr * PX + (g ^ key(lr))) * 16u,
-                          static_cast<uint32_t>(lr * PX + ((4 + g) ^ key(lr))) * 16u};
-  const uint32_t rz[2] = {static_cast<uint32_t>(lr * PZ + (g ^ key(lr))) * 16u,
-                          static_cast<uint32_t>(lr * PZ + ((4 + g) ^ key(lr))) * 16u};
-  auto at_x = [&](int tile, int ks) { return rx[ks & 1] + tile * 16 * PX * 16 + (ks >> 1) * 128; };
-  auto at_z = [&](int tile, int ks) { return rz[ks & 1] + tile * 16 * PZ * 16 + (ks >> 1) * 128; };
+  // byte offsets of this lane's operand pieces in a tile: row lr (a 16-row tile
+  // further is a constant further), piece 4 ks + g for ks = 0 .. 3 (0, 1 where
+  // keys have three bits; further ks are a constant further)
+  constexpr int QX = PX % 16 == 0 ? 4 : 2, QZ = PZ % 16 == 0 ? 4 : 2;
+  uint32_t rx[QX], rz[QZ];
+#pragma unroll
+  for (int q = 0; q < QX; ++q) rx[q] = static_cast<uint32_t>(lr * PX + ((4 * q + g) ^ key<PX>(lr))) * 16u;
+#pragma unroll
+  for (int q = 0; q < QZ; ++q) rz[q] = static_cast<uint32_t>(lr * PZ + ((4 * q + g) ^ key<PZ>(lr))) * 16u;
+  auto at_x = [&](int tile, int ks) { return rx[ks % QX] + tile * 16 * PX * 16 + (ks / QX) * QX * 64; };
+  auto at_z = [&](int tile, int ks) { return rz[ks % QZ] + tile * 16 * PZ * 16 + (ks / QZ) * QZ * 64; };
   // transposing reads (bf16): lane (lr, g) addresses row 8 g + lr/4 (+ 4 for the
   // second half), and of two 16-channel tiles together piece lr%4, half i%2
   const int tr = 8 * g + (lr >> 2);
-  uint32_t ty[2][2], tz[NTL][2];
+  uint32_t ty[QX][2], tz[NTL][2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const int row = tr + 4 * q;
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      ty[e][q] = static_cast<uint32_t>(row * PX + ((4 * e + (lr & 3)) ^ key(row))) * 16u;
+    for (int e = 0; e < QX; ++e)
+      ty[e][q] = static_cast<uint32_t>(row * PX + ((4 * e + (lr & 3)) ^ key<PX>(row))) * 16u;
 #pragma unroll
     for (int n = 0; n < NTL; ++n) {
       const int c = column(n, 4 * (lr & 3));  // four columns from here
-      tz[n][q] = static_cast<uint32_t>(row * PZ + ((c >> 3) ^ key(row))) * 16u + (c & 4) * 2;
+      tz[n][q] = static_cast<uint32_t>(row * PZ + ((c >> 3) ^ key<PZ>(row))) * 16u + (c & 4) * 2;
     }
   }
 
   unsigned long long live = 0, live_next = 0;
   int counted = 0;  // valid steps of the segment
+  // a chunk's c, row factors and source weights
+  auto factors = [&](int ci, unsigned long long live) {
+    if (l >= CH) return;
+    float* f = reinterpret_cast<float*>(sm + M::F) + (ci & 1) * 3 * CH + l;
+    const float c = static_cast<float>(__popcll(live & (((rev ? 1ull : 2ull) << l) - 1ull)));
+    f[0] = c;
+    f[CH] = scale_i * exp2_fast(lg2 * c);
+    f[2 * CH] = scale_u * exp2_fast(lg2 * (static_cast<float>(__popcll(live)) - c));
+  };
+  // loads that stand between products: those of a set that every wave takes an
+  // equal share of
+  constexpr bool SPREAD = M::XE2 && !DOTS && decltype(ly)::N % NW == 0 && decltype(lz)::N % NW == 0;
+  constexpr int NY = decltype(ly)::PER, NZ = decltype(lz)::PER;
+  int byte_next = 1;
   if (nch > 0) {
-    live = live_of(0);
+    live = live_of(0, mask_byte(0));
+    byte_next = mask_byte(1);
+    if (w == 0) factors(0, live);
     if constexpr (M::SLOTS == 2) issue_yz(0, 0, live);
-    issue_xe(0, live);
+    issue_xe(0, 0, live);
   }
   const size_t nstat = (static_cast<size_t>(Tn) + CH - 1) / CH;
   for (int ci = 0; ci < nch; ++ci) {
     const int t0 = chunk_start(ci), slot = M::SLOTS == 2 ? ci & 1 : 0;
+    const bool more = ci + 1 < nch;
     char* tile = sm + slot * M::SET;
-    float* fc = reinterpret_cast<float*>(sm + M::F) + (ci & 1) * 3 * CH;  // c, row factors, source weights
-    float *frf = fc + CH, *fsw = fc + 2 * CH;
+    char* xe = sm + (M::XE2 ? slot * M::XE : 0);
+    const float* fc = reinterpret_cast<const float*>(sm + M::F) + (ci & 1) * 3 * CH;
+    const float *frf = fc + CH, *fsw = fc + 2 * CH;
     if constexpr (M::SLOTS == 1) {
       lds_barrier();  // the chunk before is read
       issue_yz(ci, 0, live);
     }
     const int L = __popcll(live);
     counted += L;
-    if (w == 0 && l < CH) {
-      const float c = static_cast<float>(__popcll(live & (((rev ? 1ull : 2ull) << l) - 1ull)));
-      fc[l] = c;
-      frf[l] = scale_i * exp2_fast(lg2 * c);
-      fsw[l] = scale_u * exp2_fast(lg2 * (static_cast<float>(L) - c));
-    }
     // this wave's part of the tiles has arrived (what it stored after asking for
     // them, MT stores at least, may be on the way still)
     if (OUT && M::SLOTS == 2 && !staged && ci > 0) wait_vm<MT>();
     else wait_vm<0>();
     lds_barrier();
-    if (ci + 1 < nch) {
-      live_next = live_of(ci + 1);
-      if constexpr (M::SLOTS == 2) issue_yz(ci + 1, slot ^ 1, live_next);
+    if (more) {
+      live_next = live_of(ci + 1, byte_next);
+      byte_next = mask_byte(ci + 2);
+      if (w == NW - 1) factors(ci + 1, live_next);
     }
+    i32x4 dny, dnz, dnx;
+    uint32_t ony[NY], onz[NZ], onx[NY];
+    if constexpr (SPREAD) {
+      const int tn = chunk_start(more ? ci + 1 : ci);
+      dny = rows(wk.y.p, yH, yh, KDr, tn);
+      dnz = rows(wk.z.p, zH, zh, N, tn);
+      dnx = rows(wk.x.p, xH, xh, KDr, tn);
+      if (!more) dny[2] = dnz[2] = dnx[2] = 0;  // (nothing is read)
+#pragma unroll
+      for (int k = 0; k < NY; ++k) ony[k] = onx[k] = ly.off[k];
+#pragma unroll
+      for (int k = 0; k < NZ; ++k) onz[k] = lz.off[k];
+      if (masked) {
+#pragma unroll
+        for (int k = 0; k < NY; ++k) {
+          const uint32_t o = ly.live_off(k, w, l, live_next);
+          ony[k] = rev ? ony[k] : o;
+          onx[k] = rev ? o : onx[k];
+        }
+#pragma unroll
+        for (int k = 0; k < NZ; ++k) onz[k] = rev ? onz[k] : lz.live_off(k, w, l, live_next);
+      }
+    } else if (more) {
+      if constexpr (M::SLOTS == 2) issue_yz(ci + 1, slot ^ 1, live_next);
+      if constexpr (M::XE2) issue_xe(ci + 1, slot ^ 1, live_next);
+    }
+    char* next_tile = sm + (slot ^ 1) * M::SET;
+    char* next_xe = sm + (slot ^ 1) * M::XE;
+    auto spread_yz = [&](int k) {
+      if constexpr (SPREAD) {
+        if (k < NY) dma16_ahead(dny, next_tile + M::Y + (k * NW + w) * 1024, ony[k < NY ? k : 0]);
+        else if (k < NY + NZ)
+          dma16_ahead(dnz, next_tile + M::Z + ((k - NY) * NW + w) * 1024, onz[k < NY + NZ && k >= NY ? k - NY : 0]);
+      }
+    };
+    auto spread_x = [&](int k) {
+      if constexpr (SPREAD)
+        if (k < NY) dma16_ahead(dnx, next_xe + M::X + (k * NW + w) * 1024, onx[k < NY ? k : 0]);
+    };
     if (staged && ci > 0) store_staged(ci - 1);
 
     f32x4 acc[MT][NTL];
     if constexpr (OUT) {
       // ---- P, transposed tiles (rows j, columns i).  Needed are the lower ones
       // and, for 32-deep products with z, those up to the next even tile: runs of
-      // TW tiles of one row, one run to a wave at a time
+      // TW tiles of one row, one run to a wave at a time.
       float intra = 0.f;
       constexpr int TW = BF && NW < 12 ? 2 : 1, RUNS = BF ? 12 / TW : 3;
-      for (int run = w; run < RUNS; run += NW) {
-        int mt, nt0;
+      f32x4 pt[TW], pu[TW];
+      auto run_rows = [&](int run, int& mt, int& nt0) {
         if constexpr (!BF) {
           mt = run > 0;
           nt0 = run - mt;
@@ -363,24 +439,27 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
           mt = run < 4 ? run >> 1 : 2 + ((run - 4) >> 2);
           nt0 = run < 4 ? run & 1 : (run - 4) & 3;
         }
-        f32x4 t[TW], u[TW];
+      };
+      auto p_products = [&](int run) {
+        int mt, nt0;
+        run_rows(run, mt, nt0);
 #pragma unroll
-        for (int q = 0; q < TW; ++q) t[q] = u[q] = f4zero();
-        const char *py = tile + M::Y + nt0 * 16 * PX * 16, *px = sm + M::X + mt * 16 * PX * 16;
-        const char *pz = tile + M::Z + nt0 * 16 * PZ * 16, *pe = sm + M::E + mt * 16 * PZ * 16;
+        for (int q = 0; q < TW; ++q) pt[q] = pu[q] = f4zero();
+        const char *py = tile + M::Y + nt0 * 16 * PX * 16, *px = xe + M::X + mt * 16 * PX * 16;
+        const char *pz = tile + M::Z + nt0 * 16 * PZ * 16, *pe = xe + M::E + mt * 16 * PZ * 16;
         if constexpr (BF) {
 #pragma unroll
           for (int ks = 0; ks < KD / 32; ++ks) {
             const bf16x8 xa = load_bf16x8(px + at_x(0, ks));
 #pragma unroll
-            for (int q = 0; q < TW; ++q) t[q] = mfma16(load_bf16x8(py + at_x(q, ks)), xa, t[q]);
+            for (int q = 0; q < TW; ++q) pt[q] = mfma16(load_bf16x8(py + at_x(q, ks)), xa, pt[q]);
           }
           if constexpr (DOTS) {
 #pragma unroll
             for (int ks = 0; ks < M::COLS / 32; ++ks) {
               const bf16x8 ea = load_bf16x8(pe + at_z(0, ks));
 #pragma unroll
-              for (int q = 0; q < TW; ++q) u[q] = mfma16(load_bf16x8(pz + at_z(q, ks)), ea, u[q]);
+              for (int q = 0; q < TW; ++q) pu[q] = mfma16(load_bf16x8(pz + at_z(q, ks)), ea, pu[q]);
             }
           }
         } else {
@@ -389,7 +468,7 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
             const f32x4 yv = *reinterpret_cast<const f32x4*>(py + at_x(0, ks));
             const f32x4 xv = *reinterpret_cast<const f32x4*>(px + at_x(0, ks));
 #pragma unroll
-            for (int r = 0; r < 4; ++r) t[0] = mfma16f(yv[r], xv[r], t[0]);
+            for (int r = 0; r < 4; ++r) pt[0] = mfma16f(yv[r], xv[r], pt[0]);
           }
           if constexpr (DOTS) {
 #pragma unroll
@@ -397,10 +476,14 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
               const f32x4 zv = *reinterpret_cast<const f32x4*>(pz + at_z(0, ks));
               const f32x4 ev = *reinterpret_cast<const f32x4*>(pe + at_z(0, ks));
 #pragma unroll
-              for (int r = 0; r < 4; ++r) u[0] = mfma16f(zv[r], ev[r], u[0]);
+              for (int r = 0; r < 4; ++r) pu[0] = mfma16f(zv[r], ev[r], pu[0]);
             }
           }
         }
+      };
+      auto p_write = [&](int run, bool mine) {
+        int mt, nt0;
+        run_rows(run, mt, nt0);
         const float c_i = fc[16 * mt + lr];
         char* pp = sm + M::P + (16 * mt + lr) * PP * 16;
 #pragma unroll
@@ -411,14 +494,27 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
           for (int r = 0; r < 4; ++r) {
             const float dn = c_i - c_j[r];
             const bool in = 16 * nt + 4 * g + r <= 16 * mt + lr;
-            t[q][r] = in ? t[q][r] * exp2_fast(lg2 * dn) * scale_p : 0.f;
-            if constexpr (DOTS) intra += in ? dn * t[q][r] * u[q][r] : 0.f;
+            pt[q][r] = in ? pt[q][r] * exp2_fast(lg2 * dn) * scale_p : 0.f;
+            if constexpr (DOTS) intra += in ? dn * pt[q][r] * pu[q][r] : 0.f;
           }
+          if (!mine) continue;
           if constexpr (BF)
-            *reinterpret_cast<uint2*>(pp + (((2 * nt + (g >> 1)) ^ key(lr)) * 16 + (g & 1) * 8)) =
-                pack4_bf16(t[q][0], t[q][1], t[q][2], t[q][3]);
+            *reinterpret_cast<uint2*>(pp + (((2 * nt + (g >> 1)) ^ key<PP>(lr)) * 16 + (g & 1) * 8)) =
+                pack4_bf16(pt[q][0], pt[q][1], pt[q][2], pt[q][3]);
           else
-            *reinterpret_cast<f32x4*>(pp + ((4 * nt + g) ^ key(lr)) * 16) = t[q];
+            *reinterpret_cast<f32x4*>(pp + ((4 * nt + g) ^ key<PP>(lr)) * 16) = pt[q];
+        }
+      };
+      // Where there is a wave for every run, P's products go ahead of those with
+      // the state and the rest of its making behind them, in one stretch of code
+      // (a wave without a run repeats the last one's products).
+      constexpr bool ONE = BF && NW >= RUNS && !DOTS;
+      if constexpr (ONE) {
+        p_products(min(w, RUNS - 1));
+      } else {
+        for (int run = w; run < RUNS; run += NW) {
+          p_products(run);
+          p_write(run, true);
         }
       }
       // ---- S^T x, transposed tiles (rows are columns of w, columns are steps)
@@ -431,7 +527,8 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
         for (int ks = 0; ks < KD / 32; ++ks) {
           bf16x8 xa[MT];
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) xa[mt] = load_bf16x8(sm + M::X + at_x(mt, ks));
+          for (int mt = 0; mt < MT; ++mt) xa[mt] = load_bf16x8(xe + M::X + at_x(mt, ks));
+          spread_yz(ks);
 #pragma unroll
           for (int n = 0; n < NTL; ++n) {
             float v[8];
@@ -453,13 +550,16 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
         for (int i = 0; i < KT; ++i)
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            const f32x4 xv = *reinterpret_cast<const f32x4*>(sm + M::X + at_x(mt, i));
+            const f32x4 xv = *reinterpret_cast<const f32x4*>(xe + M::X + at_x(mt, i));
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
               for (int n = 0; n < NTL; ++n) acc[mt][n] = mfma16f(S[i][n][r], xv[r], acc[mt][n]);
           }
       }
+#pragma unroll
+      for (int k = BF ? KD / 32 : 0; k < NY + NZ; ++k) spread_yz(k);
+      if constexpr (ONE) p_write(min(w, RUNS - 1), w < RUNS);
       float s0 = 0.f, s1 = 0.f;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
@@ -473,14 +573,14 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
             float ev[4];
             if constexpr (BF) {
               const uint2 u = *reinterpret_cast<const uint2*>(
-                  sm + M::E + (row * PZ + ((c >> 3) ^ key(lr))) * 16 + (c & 4) * 2);
+                  xe + M::E + (row * PZ + ((c >> 3) ^ key<PZ>(lr))) * 16 + (c & 4) * 2);
               ev[0] = __uint_as_float(u.x << 16);
               ev[1] = __uint_as_float(u.x & 0xffff0000u);
               ev[2] = __uint_as_float(u.y << 16);
               ev[3] = __uint_as_float(u.y & 0xffff0000u);
             } else {
               *reinterpret_cast<f32x4*>(ev) =
-                  *reinterpret_cast<const f32x4*>(sm + M::E + (row * PZ + ((c >> 2) ^ key(lr))) * 16);
+                  *reinterpret_cast<const f32x4*>(xe + M::E + (row * PZ + ((c >> 2) ^ key<PZ>(lr))) * 16);
             }
             float f = 0.f;
 #pragma unroll
@@ -502,7 +602,12 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
         }
       }
     }
-    // ---- products with z: P z, and the state's update
+    if constexpr (OUT && !M::XE2) {
+      lds_barrier();  // P is whole, x and e are read
+      if (more) issue_xe(ci + 1, 0, live_next);
+    }
+
+    // ---- the state's update
     const float gL = exp2_fast(lg2 * static_cast<float>(L));
 #pragma unroll
     for (int i = 0; i < KT; ++i)
@@ -510,52 +615,42 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
       for (int n = 0; n < NTL; ++n)
 #pragma unroll
         for (int r = 0; r < 4; ++r) S[i][n][r] *= gL;
-    if constexpr (OUT) {
-      lds_barrier();  // P is whole, x and e are read
-      if (ci + 1 < nch) issue_xe(ci + 1, live_next);
-    }
-
+    uint4 zu[BF ? CH / 32 : 1][NTL];  // z as operands
+    float zv[BF ? 1 : CH / 16][NTL][4];
     if constexpr (BF) {
+      constexpr int YH = NW >= 12 ? 4 : KT > 8 ? KT / 2 : KT;  // y tiles held at a time
 #pragma unroll
       for (int kt = 0; kt < CH / 32; ++kt) {
-        float sw[8];
-        *reinterpret_cast<f32x4*>(sw) = *reinterpret_cast<const f32x4*>(fsw + 32 * kt + 8 * g);
-        *reinterpret_cast<f32x4*>(sw + 4) = *reinterpret_cast<const f32x4*>(fsw + 32 * kt + 8 * g + 4);
-        // reads first, so that the products with P and the splitting of z run
-        // while y's arrive; then products on different state tiles in turn
-        uint4 zu[NTL];
-        constexpr int YH = KT > 8 ? KT / 2 : KT;  // y tiles held at a time
-        bf16x8 zp[NTL][SPU], pa[MT], ya[YH];
+        // y's reads ahead of the splitting of z; then products on different state
+        // tiles in turn
+        bf16x8 zp[NTL][SPU], ya[YH];
         auto load_y = [&](int i) {
-          const char* yt = tile + M::Y + kt * 32 * PX * 16 + (i / 4) * 128 + (i & 1) * 8;
-          const uint2 y0 = lds_read_tr16(yt + ty[(i / 2) & 1][0]), y1 = lds_read_tr16(yt + ty[(i / 2) & 1][1]);
+          const int ks = i / 2;
+          const char* yt = tile + M::Y + kt * 32 * PX * 16 + (ks / QX) * QX * 64 + (i & 1) * 8;
+          const uint2 y0 = lds_read_tr16(yt + ty[ks % QX][0]);
+          const uint2 y1 = lds_read_tr16(yt + ty[ks % QX][1]);
           return as_bf16x8(make_uint4(y0.x, y0.y, y1.x, y1.y));
         };
 #pragma unroll
         for (int n = 0; n < NTL; ++n) {
           const char* zt = tile + M::Z + kt * 32 * PZ * 16;
           const uint2 z0 = lds_read_tr16(zt + tz[n][0]), z1 = lds_read_tr16(zt + tz[n][1]);
-          zu[n] = make_uint4(z0.x, z0.y, z1.x, z1.y);
+          zu[kt][n] = make_uint4(z0.x, z0.y, z1.x, z1.y);
         }
-        if constexpr (OUT) {
-#pragma unroll
-          for (int mt = 2 * kt; mt < MT; ++mt)
-            pa[mt] = load_bf16x8(sm + M::P + ((16 * mt + lr) * PP + ((4 * kt + g) ^ key(lr))) * 16);
-        }
+        float sw[8];
+        *reinterpret_cast<f32x4*>(sw) = *reinterpret_cast<const f32x4*>(fsw + 32 * kt + 8 * g);
+        *reinterpret_cast<f32x4*>(sw + 4) = *reinterpret_cast<const f32x4*>(fsw + 32 * kt + 8 * g + 4);
 #pragma unroll
         for (int i = 0; i < YH; ++i) ya[i] = load_y(i);
 #pragma unroll
         for (int n = 0; n < NTL; ++n) {
-          if constexpr (OUT) {
-#pragma unroll
-            for (int mt = 2 * kt; mt < MT; ++mt) acc[mt][n] = mfma16(as_bf16x8(zu[n]), pa[mt], acc[mt][n]);
-          }
           float v[8];
-          Vec16<bf16>::unpack(zu[n], v);
+          Vec16<bf16>::unpack(zu[kt][n], v);
 #pragma unroll
           for (int k = 0; k < 8; ++k) v[k] *= sw[k];
           split8<SPU>(v, zp[n]);
         }
+        spread_x(2 * kt);
 #pragma unroll
         for (int i0 = 0; i0 < KT; i0 += YH) {
           if (i0 > 0) {
@@ -569,11 +664,11 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
 #pragma unroll
               for (int n = 0; n < NTL; ++n) S[i0 + i][n] = mfma16(ya[i], zp[n][s], S[i0 + i][n]);
         }
+        spread_x(2 * kt + 1);
       }
     } else {
 #pragma unroll
       for (int bq = 0; bq < CH / 16; ++bq) {
-        float zv[NTL][4];
         const f32x4 sw = *reinterpret_cast<const f32x4*>(fsw + 16 * bq + 4 * g);
 #pragma unroll
         for (int n = 0; n < NTL; ++n) {
@@ -581,17 +676,8 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int row = 16 * bq + 4 * g + r;
-            zv[n][r] = *reinterpret_cast<const float*>(tile + M::Z + (row * PZ + ((c >> 2) ^ key(row))) * 16 + (c & 3) * 4);
-          }
-        }
-        if constexpr (OUT) {
-#pragma unroll
-          for (int mt = bq; mt < MT; ++mt) {
-            const f32x4 pv = *reinterpret_cast<const f32x4*>(sm + M::P + ((16 * mt + lr) * PP + ((4 * bq + g) ^ key(lr))) * 16);
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-              for (int n = 0; n < NTL; ++n) acc[mt][n] = mfma16f(zv[n][r], pv[r], acc[mt][n]);
+            zv[bq][n][r] =
+                *reinterpret_cast<const float*>(tile + M::Z + (row * PZ + ((c >> 2) ^ key<PZ>(row))) * 16 + (c & 3) * 4);
           }
         }
 #pragma unroll
@@ -600,9 +686,38 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
           for (int r = 0; r < 4; ++r) {
             const int row = 16 * bq + 4 * g + r;
             const float yv = *reinterpret_cast<const float*>(
-                tile + M::Y + (row * PX + ((4 * i + (lr >> 2)) ^ key(row))) * 16 + (lr & 3) * 4);
+                tile + M::Y + (row * PX + ((4 * i + (lr >> 2)) ^ key<PX>(row))) * 16 + (lr & 3) * 4);
 #pragma unroll
-            for (int n = 0; n < NTL; ++n) S[i][n] = mfma16f(yv, zv[n][r] * sw[r], S[i][n]);
+            for (int n = 0; n < NTL; ++n) S[i][n] = mfma16f(yv, zv[bq][n][r] * sw[r], S[i][n]);
+          }
+      }
+    }
+#pragma unroll
+    for (int k = BF ? 2 * (CH / 32) : 0; k < NY; ++k) spread_x(k);
+
+    // ---- P z
+    if constexpr (OUT) {
+      if constexpr (M::XE2) lds_barrier();  // P is whole
+      if constexpr (BF) {
+#pragma unroll
+        for (int kt = 0; kt < CH / 32; ++kt)
+#pragma unroll
+          for (int mt = 2 * kt; mt < MT; ++mt) {
+            const bf16x8 pa = load_bf16x8(sm + M::P + ((16 * mt + lr) * PP + ((4 * kt + g) ^ key<PP>(lr))) * 16);
+#pragma unroll
+            for (int n = 0; n < NTL; ++n) acc[mt][n] = mfma16(as_bf16x8(zu[kt][n]), pa, acc[mt][n]);
+          }
+      } else {
+#pragma unroll
+        for (int bq = 0; bq < CH / 16; ++bq)
+#pragma unroll
+          for (int mt = bq; mt < MT; ++mt) {
+            const f32x4 pv =
+                *reinterpret_cast<const f32x4*>(sm + M::P + ((16 * mt + lr) * PP + ((4 * bq + g) ^ key<PP>(lr))) * 16);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+              for (int n = 0; n < NTL; ++n) acc[mt][n] = mfma16f(zv[bq][n][r], pv[r], acc[mt][n]);
           }
       }
     }
@@ -615,7 +730,7 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
 #pragma unroll
             for (int n = 0; n < NTL; ++n) {
               const int c = column(n, 4 * g), row = 16 * mt + lr;
-              *reinterpret_cast<uint2*>(sm + M::O + (row * PZ + ((c >> 3) ^ key(lr))) * 16 + (c & 4) * 2) =
+              *reinterpret_cast<uint2*>(sm + M::O + (row * PZ + ((c >> 3) ^ key<PZ>(lr))) * 16 + (c & 4) * 2) =
                   pack4_bf16(acc[mt][n][0], acc[mt][n][1], acc[mt][n][2], acc[mt][n][3]);
             }
         }
@@ -644,6 +759,7 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
     lds_barrier();
     store_staged(nch - 1);
   }
+  wait_vm<0>();  // no load to LDS outlives the workgroup
 
   // ---- the state behind the segment
   float* dst = nullptr;
