@@ -8,7 +8,9 @@ call fails, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -142,6 +144,8 @@ def _p(x):
 
 
 def _check(x, name, shape, dtype, device):
+    if x.dtype == dtype and x.shape == shape and x.device == device and x.is_contiguous():
+        return
     if x.dtype != dtype:
         raise TypeError("%s: expected %s, got %s" % (name, dtype, x.dtype))
     if tuple(x.shape) != tuple(shape):
@@ -525,6 +529,26 @@ def decode_conv(x, conv_w, conv_state, a, b, A_log, dt_bias, Hk, Dk, Hv, Dv, sta
     return o, state_out, conv_state_out
 
 
+# The entry points below are also called for single tokens, where a call's time on
+# the host counts: pointers go as plain integers, sizes are asked for once for each
+# set of dims, and the current device is only switched where it is another one.
+
+def _a(x):
+    return None if x is None else x.data_ptr()
+
+
+@functools.lru_cache(maxsize=256)
+def _decay_ws(fn, *dims):
+    return _query(fn, Dims(*dims))
+
+
+def _on_device(dev):
+    """The context of a call on dev's tensors and its current stream."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
 # ---- linear attention with a decay for each head (gdn_decay_fwd / gdn_decay_bwd)
 
 def _check_decay(d, q, k, v, lg, state0, mask):
@@ -553,13 +577,13 @@ def decay_fwd(q, k, v, lg, state0=None, mask=None, *, scale=None, state_out=None
         state_out = torch.empty((d.B, d.Hv, d.Dk, d.Dv), dtype=torch.float32, device=dev)
     else:
         _check(state_out, "state_out", (d.B, d.Hv, d.Dk, d.Dv), torch.float32, dev)
-    wsb = _query("gdn_decay_fwd_workspace_bytes", d)
+    wsb = _decay_ws("gdn_decay_fwd_workspace_bytes", d.B, d.T, d.Hk, d.Hv, d.Dk, d.Dv, d.dtype, d.algo, 0)
     o = torch.empty((d.B, d.T, d.Hv, d.Dv), dtype=q.dtype, device=dev)
     ws = torch.empty((wsb,), dtype=torch.uint8, device=dev) if wsb else None
-    with torch.cuda.device(dev):
-        rc = lib().gdn_decay_fwd(ctypes.byref(d), _p(q), _p(k), _p(v), _p(lg),
-                                 d.Dk ** -0.5 if scale is None else scale, _p(state0), _p(mask), _p(o),
-                                 _p(state_out), _p(ws), wsb, _stream(dev))
+    with _on_device(dev):
+        rc = lib().gdn_decay_fwd(d, _a(q), _a(k), _a(v), _a(lg), d.Dk ** -0.5 if scale is None else scale,
+                                 _a(state0), _a(mask), _a(o), _a(state_out), _a(ws), wsb,
+                                 torch.cuda.current_stream(dev).cuda_stream)
     if rc:
         raise GdnError("gdn_decay_fwd", rc)
     return o, state_out
@@ -573,16 +597,16 @@ def decay_bwd(q, k, v, lg, state0, mask, dO, dS_final=None, *, scale=None, algo=
     _check(dO, "dO", (d.B, d.T, d.Hv, d.Dv), q.dtype, dev)
     if dS_final is not None:
         _check(dS_final, "dS_final", (d.B, d.Hv, d.Dk, d.Dv), torch.float32, dev)
-    wsb = _query("gdn_decay_bwd_workspace_bytes", d)
+    wsb = _decay_ws("gdn_decay_bwd_workspace_bytes", d.B, d.T, d.Hk, d.Hv, d.Dk, d.Dv, d.dtype, d.algo, 0)
     out = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
                dlg=torch.empty_like(lg),
                dstate=torch.empty((d.B, d.Hv, d.Dk, d.Dv), dtype=torch.float32, device=dev))
     ws = torch.empty((wsb,), dtype=torch.uint8, device=dev) if wsb else None
-    with torch.cuda.device(dev):
-        rc = lib().gdn_decay_bwd(ctypes.byref(d), _p(q), _p(k), _p(v), _p(lg),
-                                 d.Dk ** -0.5 if scale is None else scale, _p(state0), _p(mask), _p(dO),
-                                 _p(dS_final), *[_p(out[n]) for n in ("dq", "dk", "dv", "dlg", "dstate")],
-                                 _p(ws), wsb, _stream(dev))
+    with _on_device(dev):
+        rc = lib().gdn_decay_bwd(d, _a(q), _a(k), _a(v), _a(lg), d.Dk ** -0.5 if scale is None else scale,
+                                 _a(state0), _a(mask), _a(dO), _a(dS_final),
+                                 *[_a(out[n]) for n in ("dq", "dk", "dv", "dlg", "dstate")], _a(ws), wsb,
+                                 torch.cuda.current_stream(dev).cuda_stream)
     if rc:
         raise GdnError("gdn_decay_bwd", rc)
     return out
@@ -661,9 +685,9 @@ def norm_rope(q, k, wq, wk, rope=None, pos=None, *, eps=1e-6, w_offset=0.0, inte
     d = _norm_dims(q, k, wq, wk, rope, pos, eps, w_offset, interleaved)
     oq = torch.empty((d.B, d.T, d.Hq, d.D), dtype=q.dtype, device=q.device)
     ok = torch.empty((d.B, d.T, d.Hk, d.D), dtype=q.dtype, device=q.device)
-    with torch.cuda.device(q.device):
-        rc = lib().gdn_norm_rope_fwd(ctypes.byref(d), _p(q), _p(k), _p(wq), _p(wk), _p(rope), _p(pos), _p(oq),
-                                     _p(ok), _stream(q.device))
+    with _on_device(q.device):
+        rc = lib().gdn_norm_rope_fwd(d, _a(q), _a(k), _a(wq), _a(wk), _a(rope), _a(pos), _a(oq), _a(ok),
+                                     torch.cuda.current_stream(q.device).cuda_stream)
     if rc:
         raise GdnError("gdn_norm_rope_fwd", rc)
     return oq, ok
@@ -679,10 +703,10 @@ def norm_rope_bwd(q, k, wq, wk, rope, pos, dyq, dyk, *, eps=1e-6, w_offset=0.0, 
                dwk=torch.empty_like(wk))
     wsb = _query("gdn_norm_rope_bwd_workspace_bytes", d)
     ws = torch.empty((wsb,), dtype=torch.uint8, device=dev) if wsb else None
-    with torch.cuda.device(dev):
-        rc = lib().gdn_norm_rope_bwd(ctypes.byref(d), _p(q), _p(k), _p(wq), _p(wk), _p(rope), _p(pos), _p(dyq),
-                                     _p(dyk), *[_p(out[n]) for n in ("dq", "dk", "dwq", "dwk")], _p(ws), wsb,
-                                     _stream(dev))
+    with _on_device(dev):
+        rc = lib().gdn_norm_rope_bwd(d, _a(q), _a(k), _a(wq), _a(wk), _a(rope), _a(pos), _a(dyq), _a(dyk),
+                                     *[_a(out[n]) for n in ("dq", "dk", "dwq", "dwk")], _a(ws), wsb,
+                                     torch.cuda.current_stream(dev).cuda_stream)
     if rc:
         raise GdnError("gdn_norm_rope_bwd", rc)
     return out

@@ -10,7 +10,8 @@
 namespace gdn {
 
 constexpr int kDecayChunk = 64;   // steps per chunk; segments are whole chunks
-constexpr int kDecayMaxSeg = 512; // segments of one sequence
+constexpr int kDecayMaxSeg = 4096; // segments of one sequence
+constexpr int kDecayMaxT = 1 << 25;  // steps: segments of the backward hold up to 128 chunks
 
 struct DecayDims {
   int B, T, Hk, Hv, Dk, Dv;
@@ -45,11 +46,17 @@ struct DecayWalk {
   // states [Dk, Dv] fp32 per (b, h): element (channel, column) at
   // channel * sr + column * sc
   int sr, sc;
-  const float* start;       // [B*Hv] states the walk starts from, with one segment (null: zeros)
+  const float* start;       // [B*Hv] states the sequence starts from (null: zeros)
   const float* seg_start;   // [nseg, B*Hv] start states (null: one segment)
-  float* end;               // state behind the sequence, with one segment (else null)
-  float* seg_sum;           // the walk only sums its segment's update into [nseg, B*Hv] (else null)
-  float* seg_steps;         //   and writes its valid steps into [B, nseg] (may be null)
+  float* end;               // state behind the sequence (null: not written)
+  // A sum (the walk that only sums its segments' updates) writes [nseg, B*Hv]
+  // states here, in the order of the kernel's registers if seg_native (then
+  // decay_sum_floats() each), and its segments' valid steps into [B, nseg] (if not
+  // null).  A walk with seg_sum starts from start and the native sums before its
+  // segment, and the first segment's writes end from all of them.
+  float* seg_sum;
+  float* seg_steps;
+  int seg_native;
   float* dots;              // sums for dlg (else null); see DecayStats
   const float* cross;       // [B*Hv] states, dotted with the end state of every segment (dlg):
   const float* seg_cross;   //   first segment's, and [nseg, B*Hv]
@@ -109,7 +116,8 @@ struct DecayStepArgs {
 
 int decay_waves(int N);     // waves of a walk with N columns
 
-hipError_t launch_decay_walk(const DecayWalkArgs& a, bool bf16, hipStream_t st);
+size_t decay_sum_floats(int KD, int N);
+hipError_t launch_decay_walk(const DecayWalkArgs& a, bool sum, bool bf16, hipStream_t st);
 hipError_t launch_decay_chain(const DecayChainArgs* a, int n, hipStream_t st);
 hipError_t launch_decay_reduce(const DecayReduceArgs& a, hipStream_t st);
 hipError_t launch_decay_group(const DecayGroupArgs& a, bool bf16, hipStream_t st);

@@ -6,10 +6,21 @@
 
 namespace gdn {
 
+size_t decay_sum_floats(int KD, int N) {
+  auto up = [](int n) { return static_cast<size_t>(n <= 64 ? 64 : n <= 128 ? 128 : n <= 192 ? 192 : 256); };
+  return up(KD) * up(N);
+}
+
 int decay_waves(int N) { return N <= 64 ? 4 : N <= 128 ? 8 : N <= 192 ? 12 : 8; }
 
-hipError_t launch_decay_walk(const DecayWalkArgs& a, bool bf, hipStream_t st) {
+hipError_t launch_decay_walk(const DecayWalkArgs& a, bool sum, bool bf, hipStream_t st) {
   const int KD = a.walk[0].KD;
+  if (sum) {
+    if (KD <= 64) return bf ? decay_sum_bf16_64(a, st) : decay_sum_f32_64(a, st);
+    if (KD <= 128) return bf ? decay_sum_bf16_128(a, st) : decay_sum_f32_128(a, st);
+    if (KD <= 192) return bf ? decay_sum_bf16_192(a, st) : decay_sum_f32_192(a, st);
+    return bf ? decay_sum_bf16_256(a, st) : decay_sum_f32_256(a, st);
+  }
   if (KD <= 64) return bf ? decay_walk_bf16_64(a, st) : decay_walk_f32_64(a, st);
   if (KD <= 128) return bf ? decay_walk_bf16_128(a, st) : decay_walk_f32_128(a, st);
   if (KD <= 192) return bf ? decay_walk_bf16_192(a, st) : decay_walk_f32_192(a, st);
@@ -88,44 +99,59 @@ __global__ void __launch_bounds__(64) chain_kernel(ChainArgs aa) {
 // starting at each segment from the dot of the two states there, so that
 // rounding does not build up over a long sequence.  Where g^L is below 2^-24
 // nothing that counts passes through.
+// A workgroup to a head takes tiles of whole segments, up to 256 chunks: a thread
+// adds up one chunk's sums over the waves, then a thread to each segment follows
+// its boundaries.
 __global__ void __launch_bounds__(256) reduce_kernel(DecayReduceArgs a) {
   const DecayDims& d = a.d;
-  const int h = blockIdx.x, n = d.B * a.nseg;
-  const int nstat = (d.T + a.sub - 1) / a.sub, per = a.seg * kDecayChunk / a.sub;
+  const int h = blockIdx.x, tid = threadIdx.x;
+  const int nstat = (d.T + a.sub - 1) / a.sub, per = a.seg * kDecayChunk / a.sub;  // per <= 256 (see the cut)
+  const int segs = 256 / per, tiles = (a.nseg + segs - 1) / segs;
   const float lg2 = log2_decay(a.lg[h]);
+  __shared__ float sa[256], sb[256], sl[256];
+  __shared__ double part[256];
   double total = 0.0;
-  for (int i = threadIdx.x; i < n; i += 256) {
-    const int b = i / a.nseg, s = i % a.nseg;
+  for (int i = 0; i < d.B * tiles; ++i) {
+    const int b = i / tiles, s0 = (i % tiles) * segs;
     const size_t bh = static_cast<size_t>(b) * d.Hv + h;
-    double X = 0.0;
-    for (int w = 0; w < a.nwv; ++w) X += a.vx[(bh * a.nseg + s) * a.nwv + w];
-    const int c1 = min(nstat, (s + 1) * per);
-    for (int c = s * per; c < c1; ++c) {
-      double a0 = 0, a1 = 0, in = 0, b0 = 0, b1 = 0;
+    const int c = s0 * per + tid;
+    if (tid < segs * per && c < nstat) {
       const float* q = a.qa + (bh * nstat + c) * a.nwk * kDecayQStats;
       const float* k = a.kb + (bh * nstat + c) * a.nwk * kDecayKStats;
-      const float L = k[2];
+      float a0 = 0.f, b0 = 0.f;
+      double in = 0.0;
       for (int w = 0; w < a.nwk; ++w) {
         a0 += q[w * kDecayQStats];
-        a1 += q[w * kDecayQStats + 1];
-        in += q[w * kDecayQStats + 2];
         b0 += k[w * kDecayKStats];
-        b1 += k[w * kDecayKStats + 1];
+        in += static_cast<double>(q[w * kDecayQStats + 1]) + q[w * kDecayQStats + 2] + k[w * kDecayKStats + 1];
       }
-      total += in + a1 + b1;
-      const double through = lg2 * L < -24.f ? 0.0 : X - a0;
-      total += L * through;
-      X = through + b0;
+      total += in;
+      sa[tid] = a0;
+      sb[tid] = b0;
+      sl[tid] = k[2];
     }
-  }
-  __shared__ double part[256];
-  part[threadIdx.x] = total;
-  __syncthreads();
-  for (int m = 128; m >= 1; m >>= 1) {
-    if (threadIdx.x < m) part[threadIdx.x] += part[threadIdx.x + m];
+    __syncthreads();
+    const int s = s0 + tid;
+    if (tid < segs && s < a.nseg) {
+      double X = 0.0;
+      for (int w = 0; w < a.nwv; ++w) X += a.vx[(bh * a.nseg + s) * a.nwv + w];
+      const int n = min(per, nstat - s * per);
+      for (int k = 0; k < n; ++k) {
+        const float L = sl[tid * per + k];
+        const double through = lg2 * L < -24.f ? 0.0 : X - sa[tid * per + k];
+        total += L * through;
+        X = through + sb[tid * per + k];
+      }
+    }
     __syncthreads();
   }
-  if (threadIdx.x == 0) a.dlg[h] = static_cast<float>(part[0]);
+  part[tid] = total;
+  __syncthreads();
+  for (int m = 128; m >= 1; m >>= 1) {
+    if (tid < m) part[tid] += part[tid + m];
+    __syncthreads();
+  }
+  if (tid == 0) a.dlg[h] = static_cast<float>(part[0]);
 }
 
 // ---- dq / dk of the key heads: their value heads' rows summed in fp32, in

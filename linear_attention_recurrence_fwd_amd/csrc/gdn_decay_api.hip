@@ -27,7 +27,7 @@ int check_dims(const gdn_dims* p, bool bwd, DecayDims* out) {
   if (p->Dk % 8 || p->Dv % 8 || p->Dk > 256 || p->Dv > 256) return GDN_ERR_UNSUPPORTED;
   // counts that the kernels hold in 32 bits: steps, heads, (b, h) pairs times
   // their slices or segments (the tensors themselves are addressed in 64)
-  if (p->T > INT_MAX / 2 || p->Hv > INT_MAX / 1024 || p->B > INT_MAX / 1024 ||
+  if (p->T > gdn::kDecayMaxT || p->Hv > INT_MAX / 1024 || p->B > INT_MAX / 1024 ||
       static_cast<double>(p->B) * p->Hv * gdn::kDecayMaxSeg * 2 > INT_MAX ||
       static_cast<double>(p->B) * p->T * p->Hv > 9.0e12)
     return GDN_ERR_UNSUPPORTED;
@@ -37,6 +37,9 @@ int check_dims(const gdn_dims* p, bool bwd, DecayDims* out) {
 }
 
 bool use_step(const gdn_dims* p) { return p->algo == GDN_ALGO_SCAN || (p->algo == GDN_ALGO_AUTO && p->T == 1); }
+
+// Segments up to which the forward's walks add up the sums before them themselves.
+constexpr int kPrefixSegments = 8;
 
 // Chunks per segment and segments.
 struct Cut {
@@ -80,7 +83,8 @@ Layout layout(const gdn_dims* p, const DecayDims& d, bool bwd) {
   };
   const Cut c = cut(p, d, bwd);
   const size_t bh = static_cast<size_t>(d.B) * d.Hv;
-  const size_t states = static_cast<size_t>(c.n) * bh * d.Dk * d.Dv;
+  // (the forward's sums may lie in the walks' padded order)
+  const size_t states = static_cast<size_t>(c.n) * bh * (bwd ? static_cast<size_t>(d.Dk) * d.Dv : gdn::decay_sum_floats(d.Dk, d.Dv));
   if (c.n > 1) {
     L.S = take(states);
     L.steps = take(static_cast<size_t>(d.B) * c.n);
@@ -215,17 +219,27 @@ int gdn_decay_fwd(const gdn_dims* d, const void* q, const void* k, const void* v
   w.end = state_out;
   gdn::DecayWalkArgs a{dd, lg, mask, c.n, c.seg, 1, {w, w}};
   if (c.n > 1) {
-    float* S = at<float>(ws, L.S);
+    float *S = at<float>(ws, L.S), *steps = at<float>(ws, L.steps);
+    // Few segments: each walk adds up the sums before its own.  Many, or a state
+    // updated in place (which the first segment would read while the last one
+    // writes it): a chain makes every start state first.
+    const bool prefix = c.n <= kPrefixSegments && state_out != state0;
     gdn::DecayWalkArgs sum = a;
     sum.walk[0].seg_sum = S;
-    sum.walk[0].seg_steps = at<float>(ws, L.steps);
-    if (gdn::launch_decay_walk(sum, bf, st) != hipSuccess) return GDN_ERR_HIP;
-    const gdn::DecayChainArgs ch{dd, lg, at<float>(ws, L.steps), c.n, S, state0, state_out, 0};
-    if (gdn::launch_decay_chain(&ch, 1, st) != hipSuccess) return GDN_ERR_HIP;
-    a.walk[0].seg_start = S;
-    a.walk[0].end = nullptr;
+    sum.walk[0].seg_steps = steps;
+    sum.walk[0].seg_native = prefix;
+    if (gdn::launch_decay_walk(sum, true, bf, st) != hipSuccess) return GDN_ERR_HIP;
+    if (prefix) {
+      a.walk[0].seg_sum = S;
+      a.walk[0].seg_steps = steps;
+    } else {
+      const gdn::DecayChainArgs ch{dd, lg, steps, c.n, S, state0, state_out, 0};
+      if (gdn::launch_decay_chain(&ch, 1, st) != hipSuccess) return GDN_ERR_HIP;
+      a.walk[0].seg_start = S;
+      a.walk[0].end = nullptr;
+    }
   }
-  return gdn::launch_decay_walk(a, bf, st) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+  return gdn::launch_decay_walk(a, false, bf, st) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
 }
 
 int gdn_decay_bwd(const gdn_dims* d, const void* q, const void* k, const void* v, const float* lg,
@@ -294,7 +308,7 @@ int gdn_decay_bwd(const gdn_dims* d, const void* q, const void* k, const void* v
     wr.seg_sum = R;
     ws_.seg_steps = at<float>(ws, L.steps);
     const gdn::DecayWalkArgs sum{dd, lg, mask, c.n, c.seg, 2, {ws_, wr}};
-    if (gdn::launch_decay_walk(sum, bf, st) != hipSuccess) return GDN_ERR_HIP;
+    if (gdn::launch_decay_walk(sum, true, bf, st) != hipSuccess) return GDN_ERR_HIP;
     const gdn::DecayChainArgs ch[2] = {{dd, lg, at<float>(ws, L.steps), c.n, S, state0, at<float>(ws, L.end), 0},
                                        {dd, lg, at<float>(ws, L.steps), c.n, R, dS_final, dstate, 1}};
     if (gdn::launch_decay_chain(ch, 2, st) != hipSuccess) return GDN_ERR_HIP;
@@ -305,9 +319,9 @@ int gdn_decay_bwd(const gdn_dims* d, const void* q, const void* k, const void* v
     wv.end = nullptr;
   }
   const gdn::DecayWalkArgs av{dd, lg, mask, c.n, c.seg, 1, {wv, wv}};
-  if (gdn::launch_decay_walk(av, bf, st) != hipSuccess) return GDN_ERR_HIP;
+  if (gdn::launch_decay_walk(av, false, bf, st) != hipSuccess) return GDN_ERR_HIP;
   const gdn::DecayWalkArgs aqk{dd, lg, mask, c.n, c.seg, 2, {wq, wk}};
-  if (gdn::launch_decay_walk(aqk, bf, st) != hipSuccess) return GDN_ERR_HIP;
+  if (gdn::launch_decay_walk(aqk, false, bf, st) != hipSuccess) return GDN_ERR_HIP;
   if (grouped && dd.T > 0) {
     const gdn::DecayGroupArgs ga{dd, at<float>(ws, L.pq), at<float>(ws, L.pk), dq, dk};
     if (gdn::launch_decay_group(ga, bf, st) != hipSuccess) return GDN_ERR_HIP;

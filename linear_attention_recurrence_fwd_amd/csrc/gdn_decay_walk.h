@@ -84,6 +84,10 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v + __shfl_xor(v, 32);
 }
 
+template <int N> struct Int {
+  static constexpr int v = N;
+};
+
 template <typename T> struct Cfg;
 template <> struct Cfg<bf16> {
   static constexpr int CH = 64, EPP = 8;
@@ -200,36 +204,91 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
     return ch < KDr && col < N ? 4u * static_cast<uint32_t>(ch * sr + col * sc) : kOff;
   };
 
+  // Segment sums that only walks of this kind read lie in the order of the
+  // registers: [KT NTL tiles][wave][lane][4].
+  const size_t native = static_cast<size_t>(KT) * NTL * NW * 256;
+  auto native_of = [&](int s) {
+    return wk.seg_sum + (static_cast<size_t>(s) * BH + bh) * native + (w * 64 + l) * 4;
+  };
   f32x4 S[KT][NTL];
   const float* src = nullptr;
+  const bool prefix = OUT && wk.seg_sum != nullptr;  // starts from the sums before it
   if (OUT) {
     if (wk.seg_start) src = wk.seg_start + (static_cast<size_t>(sg) * BH + bh) * hs;
-    else if (wk.start) src = wk.start + bh * hs;  // (one segment)
+    else if (wk.start) src = wk.start + bh * hs;
   }
-  {
+  auto load_start = [&]() {
     const rsrc_t rs = make_rsrc(src, src ? hbytes : 0);
 #pragma unroll
     for (int i = 0; i < KT; ++i)
 #pragma unroll
       for (int n = 0; n < NTL; ++n) {
-        if constexpr (!OUT) {
-          S[i][n] = f4zero();
+        const uint32_t o = state_off(i, n);
+        if (sr == 1) {
+          const float4 v = buf_f4(rs, o);
+          S[i][n] = f32x4{v.x, v.y, v.z, v.w};
         } else {
-          const uint32_t o = state_off(i, n);
-          if (sr == 1) {
-            const float4 v = buf_f4(rs, o);
-            S[i][n] = f32x4{v.x, v.y, v.z, v.w};
-          } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) S[i][n][r] = buf_f1(rs, o + 4u * static_cast<uint32_t>(r * sr));
-          }
+          for (int r = 0; r < 4; ++r) S[i][n][r] = buf_f1(rs, o + 4u * static_cast<uint32_t>(r * sr));
         }
       }
+  };
+  auto store_state = [&](float* dst) {
+    const rsrc_t rd = make_rsrc(dst, hbytes);
+#pragma unroll
+    for (int i = 0; i < KT; ++i)
+#pragma unroll
+      for (int n = 0; n < NTL; ++n) {
+        const uint32_t o = state_off(i, n);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[i][n][r]), rd, o + 4u * static_cast<uint32_t>(r * sr), 0, 0);
+      }
+  };
+  // S <- (S g^N0 + U0) g^N1 + U1 ... over the first `count` sums, in walk order
+  // (forward); two sums' loads are in flight at a time
+  auto add_sums = [&](int count) {
+    for (int s = 0; s < count; s += 2) {
+      f32x4 U[2][KT][NTL];
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        if (s + q < count) {
+          const float* u = native_of(s + q);
+#pragma unroll
+          for (int i = 0; i < KT; ++i)
+#pragma unroll
+            for (int n = 0; n < NTL; ++n)
+              U[q][i][n] = *reinterpret_cast<const f32x4*>(u + static_cast<size_t>(i * NTL + n) * NW * 256);
+        }
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        if (s + q < count) {
+          const float f = exp2_fast(lg2 * wk.seg_steps[b * nseg + s + q]);
+#pragma unroll
+          for (int i = 0; i < KT; ++i)
+#pragma unroll
+            for (int n = 0; n < NTL; ++n)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) S[i][n][r] = fmaf(f, S[i][n][r], U[q][i][n][r]);
+        }
+    }
+  };
+  if constexpr (OUT) {
+    load_start();
+    if constexpr (!DOTS)
+      if (prefix) add_sums(sg);
+  } else {
+#pragma unroll
+    for (int i = 0; i < KT; ++i)
+#pragma unroll
+      for (int n = 0; n < NTL; ++n) S[i][n] = f4zero();
   }
 
   const int t_lo = sg * a.seg * kDecayChunk, t_hi = min(Tn, t_lo + a.seg * kDecayChunk);
   const int nch = t_hi > t_lo ? (t_hi - t_lo + CH - 1) / CH : 0;
-  auto chunk_start = [&](int ci) { return t_lo + (rev ? nch - 1 - ci : ci) * CH; };
+  // (sums go through the chunks from the walk's end, so that the steps behind a
+  // chunk are counted when its weights are made and the state needs no decay)
+  auto chunk_start = [&](int ci) { return t_lo + (rev == OUT ? nch - 1 - ci : ci) * CH; };
   // the mask byte of this lane's step of a chunk (walk order; any where there is
   // no such step), and the live steps
   auto mask_byte = [&](int ci) -> int {
@@ -335,13 +394,13 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
   unsigned long long live = 0, live_next = 0;
   int counted = 0;  // valid steps of the segment
   // a chunk's c, row factors and source weights
-  auto factors = [&](int ci, unsigned long long live) {
+  auto factors = [&](int ci, unsigned long long live, int behind) {
     if (l >= CH) return;
     float* f = reinterpret_cast<float*>(sm + M::F) + (ci & 1) * 3 * CH + l;
     const float c = static_cast<float>(__popcll(live & (((rev ? 1ull : 2ull) << l) - 1ull)));
     f[0] = c;
     f[CH] = scale_i * exp2_fast(lg2 * c);
-    f[2 * CH] = scale_u * exp2_fast(lg2 * (static_cast<float>(__popcll(live)) - c));
+    f[2 * CH] = scale_u * exp2_fast(lg2 * (static_cast<float>(behind + __popcll(live)) - c));
   };
   // loads that stand between products: those of a set that every wave takes an
   // equal share of
@@ -351,7 +410,7 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
   if (nch > 0) {
     live = live_of(0, mask_byte(0));
     byte_next = mask_byte(1);
-    if (w == 0) factors(0, live);
+    if (w == 0) factors(0, live, 0);
     if constexpr (M::SLOTS == 2) issue_yz(0, 0, live);
     issue_xe(0, 0, live);
   }
@@ -377,7 +436,7 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
     if (more) {
       live_next = live_of(ci + 1, byte_next);
       byte_next = mask_byte(ci + 2);
-      if (w == NW - 1) factors(ci + 1, live_next);
+      if (w == NW - 1) factors(ci + 1, live_next, OUT ? 0 : counted);
     }
     i32x4 dny, dnz, dnx;
     uint32_t ony[NY], onz[NZ], onx[NY];
@@ -608,13 +667,15 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
     }
 
     // ---- the state's update
-    const float gL = exp2_fast(lg2 * static_cast<float>(L));
+    if constexpr (OUT) {
+      const float gL = exp2_fast(lg2 * static_cast<float>(L));
 #pragma unroll
-    for (int i = 0; i < KT; ++i)
+      for (int i = 0; i < KT; ++i)
 #pragma unroll
-      for (int n = 0; n < NTL; ++n)
+        for (int n = 0; n < NTL; ++n)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) S[i][n][r] *= gL;
+          for (int r = 0; r < 4; ++r) S[i][n][r] *= gL;
+    }
     uint4 zu[BF ? CH / 32 : 1][NTL];  // z as operands
     float zv[BF ? 1 : CH / 16][NTL][4];
     if constexpr (BF) {
@@ -765,11 +826,20 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
   float* dst = nullptr;
   const float* crs = nullptr;
   if constexpr (OUT) {
-    if (wk.end) dst = wk.end + bh * hs;  // (one segment)
+    if (wk.end && !prefix) dst = wk.end + bh * hs;  // (one segment)
     if (wk.seg_cross) crs = wk.seg_cross + (static_cast<size_t>(sg) * BH + bh) * hs;
     else if (wk.cross) crs = wk.cross + bh * hs;
   } else {
-    dst = wk.seg_sum + (static_cast<size_t>(sg) * BH + bh) * hs;
+    if (wk.seg_native) {
+      float* o = native_of(sg);
+#pragma unroll
+      for (int i = 0; i < KT; ++i)
+#pragma unroll
+        for (int n = 0; n < NTL; ++n)
+          *reinterpret_cast<f32x4*>(o + static_cast<size_t>(i * NTL + n) * NW * 256) = S[i][n];
+    } else {
+      dst = wk.seg_sum + (static_cast<size_t>(sg) * BH + bh) * hs;
+    }
     if (wk.seg_steps && h == 0 && threadIdx.x == 0) wk.seg_steps[b * nseg + sg] = static_cast<float>(counted);
   }
   float dot = 0.f;
@@ -784,17 +854,13 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
         for (int r = 0; r < 4; ++r) dot = fmaf(S[i][n][r], buf_f1(rc, o + 4u * static_cast<uint32_t>(r * sr)), dot);
       }
   }
-  if (dst) {
-    const rsrc_t rd = make_rsrc(dst, hbytes);
-#pragma unroll
-    for (int i = 0; i < KT; ++i)
-#pragma unroll
-      for (int n = 0; n < NTL; ++n) {
-        const uint32_t o = state_off(i, n);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[i][n][r]), rd, o + 4u * static_cast<uint32_t>(r * sr), 0, 0);
-      }
+  if (dst) store_state(dst);
+  if constexpr (OUT && !DOTS) {
+    if (prefix && wk.end && sg == 0) {  // the final state, by the walk that had no sums to add
+      load_start();
+      add_sums(nseg);
+      store_state(wk.end + bh * hs);
+    }
   }
   if constexpr (OUT && !DOTS) {
     if (wk.dots) {
@@ -809,9 +875,8 @@ hipError_t launch_nw(const DecayWalkArgs& a, hipStream_t st) {
   const int n = a.d.B * a.d.Hv * a.nseg;
   const dim3 grid((n + 7) / 8 * 8, a.nwalk);
   const DecayWalk& w = a.walk[0];
-  if (w.seg_sum) walk_kernel<T, KD, NW, NTL, false, false, 1, 3><<<grid, 64 * NW, 0, st>>>(a);
-  else if (w.e.p) walk_kernel<T, KD, NW, NTL, true, true, 3, 3><<<grid, 64 * NW, 0, st>>>(a);
-  else if (w.end || w.dots) walk_kernel<T, KD, NW, NTL, true, false, 1, 3><<<grid, 64 * NW, 0, st>>>(a);
+  if (w.e.p) walk_kernel<T, KD, NW, NTL, true, true, 3, 3><<<grid, 64 * NW, 0, st>>>(a);
+  else if ((w.end && !w.seg_sum) || w.dots) walk_kernel<T, KD, NW, NTL, true, false, 1, 3><<<grid, 64 * NW, 0, st>>>(a);
   else walk_kernel<T, KD, NW, NTL, true, false, 1, 2><<<grid, 64 * NW, 0, st>>>(a);
   return hipGetLastError();
 }
@@ -824,16 +889,37 @@ template <typename T, int KD> hipError_t launch_kd(const DecayWalkArgs& a, hipSt
   return launch_nw<T, KD, 8, 2>(a, st);
 }
 
+template <typename T, int KD> hipError_t launch_sum_kd(const DecayWalkArgs& a, hipStream_t st) {
+  const int n = a.d.B * a.d.Hv * a.nseg, N = a.walk[0].N;
+  const dim3 grid((n + 7) / 8 * 8, a.nwalk);
+  auto go = [&](auto nw, auto ntl) {
+    walk_kernel<T, KD, decltype(nw)::v, decltype(ntl)::v, false, false, 1, 3><<<grid, 64 * decltype(nw)::v, 0, st>>>(a);
+  };
+  if (N <= 64) go(Int<4>{}, Int<1>{});
+  else if (N <= 128) go(Int<8>{}, Int<1>{});
+  else if (N <= 192) go(Int<12>{}, Int<1>{});
+  else go(Int<8>{}, Int<2>{});
+  return hipGetLastError();
+}
+
 }  // namespace decay
 
 // One translation unit per (type, channel class): gdn_decay_walk_*.hip.
 hipError_t decay_walk_bf16_64(const DecayWalkArgs& a, hipStream_t st);
+hipError_t decay_sum_bf16_64(const DecayWalkArgs& a, hipStream_t st);
 hipError_t decay_walk_bf16_128(const DecayWalkArgs& a, hipStream_t st);
+hipError_t decay_sum_bf16_128(const DecayWalkArgs& a, hipStream_t st);
 hipError_t decay_walk_bf16_192(const DecayWalkArgs& a, hipStream_t st);
+hipError_t decay_sum_bf16_192(const DecayWalkArgs& a, hipStream_t st);
 hipError_t decay_walk_bf16_256(const DecayWalkArgs& a, hipStream_t st);
+hipError_t decay_sum_bf16_256(const DecayWalkArgs& a, hipStream_t st);
 hipError_t decay_walk_f32_64(const DecayWalkArgs& a, hipStream_t st);
+hipError_t decay_sum_f32_64(const DecayWalkArgs& a, hipStream_t st);
 hipError_t decay_walk_f32_128(const DecayWalkArgs& a, hipStream_t st);
+hipError_t decay_sum_f32_128(const DecayWalkArgs& a, hipStream_t st);
 hipError_t decay_walk_f32_192(const DecayWalkArgs& a, hipStream_t st);
+hipError_t decay_sum_f32_192(const DecayWalkArgs& a, hipStream_t st);
 hipError_t decay_walk_f32_256(const DecayWalkArgs& a, hipStream_t st);
+hipError_t decay_sum_f32_256(const DecayWalkArgs& a, hipStream_t st);
 
 }  // namespace gdn

@@ -3,4 +3,5 @@
 
 namespace gdn {
 hipError_t decay_walk_f32_192(const DecayWalkArgs& a, hipStream_t st) { return decay::launch_kd<float, 192>(a, st); }
+hipError_t decay_sum_f32_192(const DecayWalkArgs& a, hipStream_t st) { return decay::launch_sum_kd<float, 192>(a, st); }
 }  // namespace gdn

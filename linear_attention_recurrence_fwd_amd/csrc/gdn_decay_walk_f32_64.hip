@@ -3,4 +3,5 @@
 
 namespace gdn {
 hipError_t decay_walk_f32_64(const DecayWalkArgs& a, hipStream_t st) { return decay::launch_kd<float, 64>(a, st); }
+hipError_t decay_sum_f32_64(const DecayWalkArgs& a, hipStream_t st) { return decay::launch_sum_kd<float, 64>(a, st); }
 }  // namespace gdn

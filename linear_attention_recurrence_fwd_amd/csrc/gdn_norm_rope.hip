@@ -290,20 +290,23 @@ __global__ void __launch_bounds__(256) bwd_kernel(NormRopeArgs a, Work wk) {
   }
 }
 
-// dw: the blocks' parts summed in a fixed order, one workgroup for 16 of the 2 D
-// sums, each by 16 lanes.
-__global__ void __launch_bounds__(256) dw_kernel(NormRopeArgs a) {
-  const int c = blockIdx.x * 16 + (threadIdx.x & 15), row = threadIdx.x >> 4;
-  double s = 0.0;
-  if (c < 2 * a.D)
-    for (int b = row; b < a.blocks; b += 16) s += a.part[static_cast<size_t>(b) * 2 * a.D + c];
-  __shared__ double red[16][16];
-  red[row][threadIdx.x & 15] = s;
-  __syncthreads();
-  if (row == 0 && c < 2 * a.D) {
-    for (int k = 1; k < 16; ++k) s += red[k][threadIdx.x & 15];
-    (c < a.D ? a.dwq : a.dwk)[c % a.D] = static_cast<float>(s);
+// dw: the blocks' parts summed in a fixed order, one workgroup for 8 of the 2 D
+// sums, each by 128 lanes whose loads are independent.
+__global__ void __launch_bounds__(1024) dw_kernel(NormRopeArgs a) {
+  const int c = blockIdx.x * 8 + (threadIdx.x & 7), row = threadIdx.x >> 3;
+  float s = 0.f;
+  if (c < 2 * a.D) {
+#pragma unroll 4
+    for (int b = row; b < a.blocks; b += 128) s += a.part[static_cast<size_t>(b) * 2 * a.D + c];
   }
+  __shared__ float red[128][9];
+  red[row][threadIdx.x & 7] = s;
+  __syncthreads();
+  for (int m = 64; m >= 1; m >>= 1) {
+    if (row < m) red[row][threadIdx.x & 7] += red[row + m][threadIdx.x & 7];
+    __syncthreads();
+  }
+  if (row == 0 && c < 2 * a.D) (c < a.D ? a.dwq : a.dwk)[c % a.D] = red[0][threadIdx.x & 7];
 }
 
 int lanes_for(int D) {
@@ -342,7 +345,7 @@ hipError_t launch_lph(const NormRopeArgs& a, bool bwd, hipStream_t st) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  dw_kernel<<<(2 * a.D + 15) / 16, 256, 0, st>>>(a);
+  dw_kernel<<<a.D / 4, 1024, 0, st>>>(a);
   return hipGetLastError();
 }
 
