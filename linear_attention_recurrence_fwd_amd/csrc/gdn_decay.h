@@ -72,7 +72,7 @@ struct DecayWalkArgs {
 };
 
 // What the backward's walks hand to the reduction for dlg, fp32:
-//   dq walk: per (b, h, chunk, wave) the sums a0, a1 and the in-chunk sum
+//   dq walk: per (b, h, chunk, wave) the sums a0, a1 (see reduce_kernel) and the in-chunk sum
 //   dk walk: per (b, h, chunk, wave) the sums b0, b1, and the chunk's valid steps
 //   dv walk: per (b, h, segment, wave) the dot of the states at its start
 struct DecayReduceArgs {
@@ -85,6 +85,30 @@ struct DecayReduceArgs {
 };
 constexpr int kDecayQStats = 3, kDecayKStats = 3;
 
+// dq and dk of the key heads (bf16), with the sums for dlg (laid out as the
+// walks', four waves to each block of 64 columns).
+struct DecayKeysArgs {
+  DecayDims d;
+  const float* lg;
+  float scale;
+  const uint8_t* mask;
+  int nseg, seg;
+  const void *q, *k, *v, *dO;
+  const float *state0, *dS;   // one segment: start states (may be null)
+  const float *S, *R;         // else [nseg, B*Hv] start states of both directions
+  void *dq, *dk;              // [B, T, Hk, Dk]
+  float *pq, *pk;             // or, where a key head's value heads go in parts, [B, T, Hk*parts, Dk] fp32
+  float *qa, *kb;
+};
+// Value heads of a key head that one workgroup goes through: the states of all of
+// them fit the registers (256 columns of channels to a wave of 16 columns).
+inline int decay_heads_together(int G, int Dv) {
+  const int most = 2;
+  for (int n = most; n > 1; --n)
+    if (G % n == 0) return n;
+  return 1;
+}
+
 struct DecayChainArgs {
   DecayDims d;
   const float* lg;
@@ -96,10 +120,12 @@ struct DecayChainArgs {
   int reverse;
 };
 
-// dq / dk of a key head: the sum of its value heads' rows, rounded once.
+// dq / dk of a key head: the sum of its value heads' (or parts of them) rows,
+// rounded once.
 struct DecayGroupArgs {
   DecayDims d;
-  const float *pq, *pk;     // [B, T, Hv, Dk] fp32
+  int parts;                // of a key head
+  const float *pq, *pk;     // [B, T, Hk*parts, Dk] fp32
   void *dq, *dk;            // [B, T, Hk, Dk]
 };
 
@@ -118,6 +144,7 @@ int decay_waves(int N);     // waves of a walk with N columns
 
 size_t decay_sum_floats(int KD, int N);
 hipError_t launch_decay_walk(const DecayWalkArgs& a, bool sum, bool bf16, hipStream_t st);
+hipError_t launch_decay_keys(const DecayKeysArgs& a, hipStream_t st);
 hipError_t launch_decay_chain(const DecayChainArgs* a, int n, hipStream_t st);
 hipError_t launch_decay_reduce(const DecayReduceArgs& a, hipStream_t st);
 hipError_t launch_decay_group(const DecayGroupArgs& a, bool bf16, hipStream_t st);

@@ -27,6 +27,18 @@ hipError_t launch_decay_walk(const DecayWalkArgs& a, bool sum, bool bf, hipStrea
   return bf ? decay_walk_bf16_256(a, st) : decay_walk_f32_256(a, st);
 }
 
+hipError_t decay_keys_64(const DecayKeysArgs& a, hipStream_t st);
+hipError_t decay_keys_128(const DecayKeysArgs& a, hipStream_t st);
+hipError_t decay_keys_192(const DecayKeysArgs& a, hipStream_t st);
+hipError_t decay_keys_256(const DecayKeysArgs& a, hipStream_t st);
+
+hipError_t launch_decay_keys(const DecayKeysArgs& a, hipStream_t st) {
+  if (a.d.Dv <= 64) return decay_keys_64(a, st);
+  if (a.d.Dv <= 128) return decay_keys_128(a, st);
+  if (a.d.Dv <= 192) return decay_keys_192(a, st);
+  return decay_keys_256(a, st);
+}
+
 namespace {
 
 using decay::exp2_fast;
@@ -159,7 +171,7 @@ __global__ void __launch_bounds__(256) reduce_kernel(DecayReduceArgs a) {
 template <typename T>
 __global__ void __launch_bounds__(256) group_kernel(DecayGroupArgs a, size_t n) {
   const DecayDims& d = a.d;
-  const int G = d.G();
+  const int G = a.parts;
   const float* src = blockIdx.y ? a.pk : a.pq;
   T* dst = static_cast<T*>(blockIdx.y ? a.dk : a.dq);
   for (size_t i = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < n;

@@ -73,6 +73,16 @@ struct Layout {
   size_t total;
 };
 
+// The waves that leave sums for dlg for a (b, h), and the parts in which a key
+// head's value heads leave their dq and dk rows: the bf16 kernel goes through
+// several value heads together, the fp32 walks through one.
+int key_waves(const gdn_dims* p, const DecayDims& d) {
+  return p->dtype == GDN_BF16 ? 4 * ((d.Dk + 63) / 64) : gdn::decay_waves(d.Dk);
+}
+int key_parts(const gdn_dims* p, const DecayDims& d) {
+  return p->dtype == GDN_BF16 ? d.G() / gdn::decay_heads_together(d.G(), d.Dv) : d.G();
+}
+
 Layout layout(const gdn_dims* p, const DecayDims& d, bool bwd) {
   Layout L{};
   size_t off = 0;
@@ -95,12 +105,12 @@ Layout layout(const gdn_dims* p, const DecayDims& d, bool bwd) {
       L.end = take(bh * d.Dk * d.Dv);
     }
     const int sub = p->dtype == GDN_BF16 ? 64 : 32;
-    const size_t nstat = (static_cast<size_t>(d.T) + sub - 1) / sub, nwk = gdn::decay_waves(d.Dk);
+    const size_t nstat = (static_cast<size_t>(d.T) + sub - 1) / sub, nwk = key_waves(p, d);
     L.qa = take(bh * nstat * nwk * gdn::kDecayQStats);
     L.kb = take(bh * nstat * nwk * gdn::kDecayKStats);
     L.vx = take(bh * c.n * gdn::decay_waves(d.Dv));
-    if (d.G() > 1) {
-      const size_t rows = static_cast<size_t>(d.B) * d.T * d.Hv * d.Dk;
+    if (key_parts(p, d) > 1) {
+      const size_t rows = static_cast<size_t>(d.B) * d.T * d.Hk * key_parts(p, d) * d.Dk;
       L.pq = take(rows);
       L.pk = take(rows);
     }
@@ -258,32 +268,9 @@ int gdn_decay_bwd(const gdn_dims* d, const void* q, const void* k, const void* v
   const bool bf = d->dtype == GDN_BF16;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const Cut c = cut(d, dd, true);
-  const bool grouped = dd.G() > 1;
-
-  gdn::DecayWalk wq = walk_vk(dd);  // dq
-  wq.x = val_rows(dd, dO);
-  wq.y = val_rows(dd, v);
-  wq.z = key_rows(dd, k);
-  wq.e = key_rows(dd, q);
-  wq.w = grouped ? at<void>(ws, L.pq) : dq;
-  wq.w32 = grouped;
-  wq.scale_p = wq.scale_i = scale;
-  wq.scale_u = 1.f;
-  wq.start = state0;
-  wq.dots = at<float>(ws, L.qa);
-
-  gdn::DecayWalk wk = walk_vk(dd);  // dk
-  wk.x = val_rows(dd, v);
-  wk.y = val_rows(dd, dO);
-  wk.z = key_rows(dd, q);
-  wk.e = key_rows(dd, k);
-  wk.w = grouped ? at<void>(ws, L.pk) : dk;
-  wk.w32 = grouped;
-  wk.reverse = 1;
-  wk.scale_p = wk.scale_u = scale;
-  wk.scale_i = 1.f;
-  wk.start = dS_final;
-  wk.dots = at<float>(ws, L.kb);
+  const int parts = key_parts(d, dd);
+  float *qa = at<float>(ws, L.qa), *kb = at<float>(ws, L.kb), *vx = at<float>(ws, L.vx);
+  float *pq = at<float>(ws, L.pq), *pk = at<float>(ws, L.pk);  // (read and written with parts only)
 
   gdn::DecayWalk wv = walk_kv(dd);  // dv, dstate
   wv.x = key_rows(dd, k);
@@ -295,39 +282,67 @@ int gdn_decay_bwd(const gdn_dims* d, const void* q, const void* k, const void* v
   wv.scale_i = 1.f;
   wv.start = dS_final;
   wv.end = dstate;
-  wv.dots = at<float>(ws, L.vx);
+  wv.dots = vx;
   wv.cross = state0;
 
+  float *S = nullptr, *R = nullptr;
   if (c.n > 1) {
-    float *S = at<float>(ws, L.S), *R = at<float>(ws, L.R);
-    gdn::DecayWalk ws_ = walk_kv(dd), wr = wv;
-    ws_.y = key_rows(dd, k);
-    ws_.z = val_rows(dd, v);
-    ws_.scale_u = 1.f;
-    ws_.seg_sum = S;
-    wr.seg_sum = R;
-    ws_.seg_steps = at<float>(ws, L.steps);
-    const gdn::DecayWalkArgs sum{dd, lg, mask, c.n, c.seg, 2, {ws_, wr}};
+    S = at<float>(ws, L.S);
+    R = at<float>(ws, L.R);
+    float* steps = at<float>(ws, L.steps);
+    gdn::DecayWalk us = walk_kv(dd), ur = wv;
+    us.y = key_rows(dd, k);
+    us.z = val_rows(dd, v);
+    us.scale_u = 1.f;
+    us.seg_sum = S;
+    us.seg_steps = steps;
+    ur.seg_sum = R;
+    const gdn::DecayWalkArgs sum{dd, lg, mask, c.n, c.seg, 2, {us, ur}};
     if (gdn::launch_decay_walk(sum, true, bf, st) != hipSuccess) return GDN_ERR_HIP;
-    const gdn::DecayChainArgs ch[2] = {{dd, lg, at<float>(ws, L.steps), c.n, S, state0, at<float>(ws, L.end), 0},
-                                       {dd, lg, at<float>(ws, L.steps), c.n, R, dS_final, dstate, 1}};
+    const gdn::DecayChainArgs ch[2] = {{dd, lg, steps, c.n, S, state0, at<float>(ws, L.end), 0},
+                                       {dd, lg, steps, c.n, R, dS_final, dstate, 1}};
     if (gdn::launch_decay_chain(ch, 2, st) != hipSuccess) return GDN_ERR_HIP;
-    wq.seg_start = S;
-    wk.seg_start = R;
     wv.seg_start = R;
     wv.seg_cross = S;
     wv.end = nullptr;
   }
   const gdn::DecayWalkArgs av{dd, lg, mask, c.n, c.seg, 1, {wv, wv}};
   if (gdn::launch_decay_walk(av, false, bf, st) != hipSuccess) return GDN_ERR_HIP;
-  const gdn::DecayWalkArgs aqk{dd, lg, mask, c.n, c.seg, 2, {wq, wk}};
-  if (gdn::launch_decay_walk(aqk, false, bf, st) != hipSuccess) return GDN_ERR_HIP;
-  if (grouped && dd.T > 0) {
-    const gdn::DecayGroupArgs ga{dd, at<float>(ws, L.pq), at<float>(ws, L.pk), dq, dk};
+  if (bf) {
+    const gdn::DecayKeysArgs ka{dd, lg, scale, mask, c.n, c.seg, q, k, v, dO, state0, dS_final, S, R, dq, dk, pq, pk, qa, kb};
+    if (dd.T > 0 && gdn::launch_decay_keys(ka, st) != hipSuccess) return GDN_ERR_HIP;
+  } else {
+    gdn::DecayWalk wq = walk_vk(dd);  // dq
+    wq.x = val_rows(dd, dO);
+    wq.y = val_rows(dd, v);
+    wq.z = key_rows(dd, k);
+    wq.e = key_rows(dd, q);
+    wq.w = parts > 1 ? pq : dq;
+    wq.scale_p = wq.scale_i = scale;
+    wq.scale_u = 1.f;
+    wq.start = state0;
+    wq.seg_start = S;
+    wq.dots = qa;
+    gdn::DecayWalk wk = walk_vk(dd);  // dk
+    wk.x = val_rows(dd, v);
+    wk.y = val_rows(dd, dO);
+    wk.z = key_rows(dd, q);
+    wk.e = key_rows(dd, k);
+    wk.w = parts > 1 ? pk : dk;
+    wk.reverse = 1;
+    wk.scale_p = wk.scale_u = scale;
+    wk.scale_i = 1.f;
+    wk.start = dS_final;
+    wk.seg_start = R;
+    wk.dots = kb;
+    const gdn::DecayWalkArgs aqk{dd, lg, mask, c.n, c.seg, 2, {wq, wk}};
+    if (dd.T > 0 && gdn::launch_decay_walk(aqk, false, false, st) != hipSuccess) return GDN_ERR_HIP;
+  }
+  if (parts > 1 && dd.T > 0) {
+    const gdn::DecayGroupArgs ga{dd, parts, pq, pk, dq, dk};
     if (gdn::launch_decay_group(ga, bf, st) != hipSuccess) return GDN_ERR_HIP;
   }
-  const gdn::DecayReduceArgs ra{dd, lg, c.n, c.seg, bf ? 64 : 32, wq.dots, wk.dots, wv.dots,
-                                gdn::decay_waves(dd.Dk), gdn::decay_waves(dd.Dv), dlg};
+  const gdn::DecayReduceArgs ra{dd, lg, c.n, c.seg, bf ? 64 : 32, qa, kb, vx, key_waves(d, dd), gdn::decay_waves(dd.Dv), dlg};
   return gdn::launch_decay_reduce(ra, st) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
 }
 

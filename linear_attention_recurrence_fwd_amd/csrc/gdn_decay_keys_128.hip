@@ -1,0 +1,6 @@
+// dq and dk of the decay operator, bf16, value heads of up to 128 channels.
+#include "gdn_decay_keys.h"
+
+namespace gdn {
+hipError_t decay_keys_128(const DecayKeysArgs& a, hipStream_t st) { return decay::launch_keys<128>(a, st); }
+}  // namespace gdn

@@ -875,8 +875,10 @@ hipError_t launch_nw(const DecayWalkArgs& a, hipStream_t st) {
   const int n = a.d.B * a.d.Hv * a.nseg;
   const dim3 grid((n + 7) / 8 * 8, a.nwalk);
   const DecayWalk& w = a.walk[0];
-  if (w.e.p) walk_kernel<T, KD, NW, NTL, true, true, 3, 3><<<grid, 64 * NW, 0, st>>>(a);
-  else if ((w.end && !w.seg_sum) || w.dots) walk_kernel<T, KD, NW, NTL, true, false, 1, 3><<<grid, 64 * NW, 0, st>>>(a);
+  if (w.e.p) {
+    if constexpr (sizeof(T) == 4) walk_kernel<T, KD, NW, NTL, true, true, 1, 3><<<grid, 64 * NW, 0, st>>>(a);
+    else return hipErrorInvalidValue;  // (keys_kernel's)
+  } else if ((w.end && !w.seg_sum) || w.dots) walk_kernel<T, KD, NW, NTL, true, false, 1, 3><<<grid, 64 * NW, 0, st>>>(a);
   else walk_kernel<T, KD, NW, NTL, true, false, 1, 2><<<grid, 64 * NW, 0, st>>>(a);
   return hipGetLastError();
 }
