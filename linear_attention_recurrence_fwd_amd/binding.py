@@ -542,11 +542,17 @@ def _decay_ws(fn, *dims):
     return _query(fn, Dims(*dims))
 
 
+_here = contextlib.nullcontext()
+
+
 def _on_device(dev):
-    """The context of a call on dev's tensors and its current stream."""
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+    """The context of a call on dev's tensors."""
+    return _here if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+# the handle of a device's current stream, without the object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 # ---- linear attention with a decay for each head (gdn_decay_fwd / gdn_decay_bwd)
@@ -574,16 +580,17 @@ def decay_fwd(q, k, v, lg, state0=None, mask=None, *, scale=None, state_out=None
     _check_decay(d, q, k, v, lg, state0, mask)
     dev = q.device
     if state_out is None:
-        state_out = torch.empty((d.B, d.Hv, d.Dk, d.Dv), dtype=torch.float32, device=dev)
+        state_out = (torch.empty((d.B, d.Hv, d.Dk, d.Dv), dtype=torch.float32, device=dev) if state0 is None
+                     else torch.empty_like(state0))
     else:
         _check(state_out, "state_out", (d.B, d.Hv, d.Dk, d.Dv), torch.float32, dev)
     wsb = _decay_ws("gdn_decay_fwd_workspace_bytes", d.B, d.T, d.Hk, d.Hv, d.Dk, d.Dv, d.dtype, d.algo, 0)
-    o = torch.empty((d.B, d.T, d.Hv, d.Dv), dtype=q.dtype, device=dev)
+    o = torch.empty_like(v)
     ws = torch.empty((wsb,), dtype=torch.uint8, device=dev) if wsb else None
     with _on_device(dev):
         rc = lib().gdn_decay_fwd(d, _a(q), _a(k), _a(v), _a(lg), d.Dk ** -0.5 if scale is None else scale,
                                  _a(state0), _a(mask), _a(o), _a(state_out), _a(ws), wsb,
-                                 torch.cuda.current_stream(dev).cuda_stream)
+                                 _raw_stream(dev.index))
     if rc:
         raise GdnError("gdn_decay_fwd", rc)
     return o, state_out
@@ -606,7 +613,7 @@ def decay_bwd(q, k, v, lg, state0, mask, dO, dS_final=None, *, scale=None, algo=
         rc = lib().gdn_decay_bwd(d, _a(q), _a(k), _a(v), _a(lg), d.Dk ** -0.5 if scale is None else scale,
                                  _a(state0), _a(mask), _a(dO), _a(dS_final),
                                  *[_a(out[n]) for n in ("dq", "dk", "dv", "dlg", "dstate")], _a(ws), wsb,
-                                 torch.cuda.current_stream(dev).cuda_stream)
+                                 _raw_stream(dev.index))
     if rc:
         raise GdnError("gdn_decay_bwd", rc)
     return out
@@ -644,11 +651,14 @@ def rope_table(P, R, base=10000.0, device="cuda"):
 def _token_stride(x, name):
     """Elements between the rows of consecutive tokens of [B, T, H, D]; the
     heads of a token are dense, the tokens evenly spaced over batch and time."""
+    if x.is_contiguous():
+        return 0
     B, T, H, D = x.shape
-    if (D > 1 and x.stride(3) != 1) or (H > 1 and x.stride(2) != D):
+    sb, st, sh, sd = x.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
         raise ValueError("%s: the heads of a token must be contiguous" % name)
-    st = x.stride(1) if T > 1 else x.stride(0) if B > 1 else H * D
-    if B > 1 and T > 1 and x.stride(0) != T * st:
+    st = st if T > 1 else sb if B > 1 else H * D
+    if B > 1 and T > 1 and sb != T * st:
         raise ValueError("%s: tokens must be evenly spaced over batch and time" % name)
     return st
 
@@ -657,13 +667,13 @@ def _norm_dims(q, k, wq, wk, rope, pos, eps, w_offset, interleaved):
     dev, dt = q.device, q.dtype
     if dev.type != "cuda":
         raise ValueError("gdn runs on the GPU; got device %s" % dev)
-    if dt not in (torch.float32, torch.bfloat16):
+    if dt != torch.bfloat16 and dt != torch.float32:
         raise TypeError("q: expected float32 or bfloat16, got %s" % dt)
     B, T, Hq, D = q.shape
     Hk = k.shape[2]
     if k.dtype != dt:
         raise TypeError("k: expected %s, got %s" % (dt, k.dtype))
-    if tuple(k.shape) != (B, T, Hk, D) or k.device != dev:
+    if k.shape != (B, T, Hk, D) or k.device != dev:
         raise ValueError("k: expected shape %s on %s, got %s on %s" % ((B, T, Hk, D), dev, tuple(k.shape), k.device))
     _check(wq, "wq", (D,), torch.float32, dev)
     _check(wk, "wk", (D,), torch.float32, dev)
@@ -687,7 +697,7 @@ def norm_rope(q, k, wq, wk, rope=None, pos=None, *, eps=1e-6, w_offset=0.0, inte
     ok = torch.empty((d.B, d.T, d.Hk, d.D), dtype=q.dtype, device=q.device)
     with _on_device(q.device):
         rc = lib().gdn_norm_rope_fwd(d, _a(q), _a(k), _a(wq), _a(wk), _a(rope), _a(pos), _a(oq), _a(ok),
-                                     torch.cuda.current_stream(q.device).cuda_stream)
+                                     _raw_stream(q.device.index))
     if rc:
         raise GdnError("gdn_norm_rope_fwd", rc)
     return oq, ok
@@ -706,7 +716,7 @@ def norm_rope_bwd(q, k, wq, wk, rope, pos, dyq, dyk, *, eps=1e-6, w_offset=0.0, 
     with _on_device(dev):
         rc = lib().gdn_norm_rope_bwd(d, _a(q), _a(k), _a(wq), _a(wk), _a(rope), _a(pos), _a(dyq), _a(dyk),
                                      *[_a(out[n]) for n in ("dq", "dk", "dwq", "dwk")], _a(ws), wsb,
-                                     torch.cuda.current_stream(dev).cuda_stream)
+                                     _raw_stream(dev.index))
     if rc:
         raise GdnError("gdn_norm_rope_bwd", rc)
     return out

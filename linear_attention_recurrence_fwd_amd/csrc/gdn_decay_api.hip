@@ -48,10 +48,10 @@ struct Cut {
 Cut cut(const gdn_dims* p, const DecayDims& d, bool bwd) {
   const int nc = d.nchunk();
   int n = 1;
-  if (p->algo != GDN_ALGO_CHUNK && nc > 1) {
-    const int want = 256, bh = d.B * d.Hv;
-    n = (want + bh - 1) / bh;
-  }
+  // one workgroup to a compute unit, and no second round of a few: at 48 (b, h)
+  // and 16 chunks, 4 segments (192 workgroups) take 37 us, 6 (288) 47 us; at 64
+  // and 32 chunks, 4 (256) take 72 us, 8 (512) 94 us
+  if (p->algo != GDN_ALGO_CHUNK && nc > 1) n = 256 / (d.B * d.Hv);
   // the backward's sums for dlg follow the boundaries chunk by chunk from the
   // start of a segment: short segments keep their rounding down
   if (bwd && n < (nc + 15) / 16) n = (nc + 15) / 16;
