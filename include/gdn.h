@@ -295,7 +295,7 @@ int gdn_bwd_vg(const gdn_dims* d, const void* q, const void* k, const void* v, c
  * read into anything, NaN or not) and still reads o.  Value head h reads
  * query/key head h / G, the state is [B,Hv,Dk,Dv] fp32 and is carried, as in
  * gdn_fwd.  q and k are taken as they are (no normalisation).
- *   d         Dk, Dv: multiples of 8 from 8 to 256, T up to 2^25 (else
+ *   d         Dk, Dv: multiples of 8 from 8 to 256, T up to 2^30 (else
  *             GDN_ERR_UNSUPPORTED; the tensors may exceed 2^31 elements);
  *             save is ignored; algo:
  *               SCAN        the per-step recurrence (forward only)

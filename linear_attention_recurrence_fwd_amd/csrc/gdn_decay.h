@@ -10,8 +10,8 @@
 namespace gdn {
 
 constexpr int kDecayChunk = 64;   // steps per chunk; segments are whole chunks
-constexpr int kDecayMaxSeg = 4096; // segments of one sequence
-constexpr int kDecayMaxT = 1 << 25;  // steps: segments of the backward hold up to 128 chunks
+constexpr int kDecayMaxSeg = 512;      // segments of one sequence
+constexpr int kDecayMaxT = 1 << 30;    // steps of one sequence
 
 struct DecayDims {
   int B, T, Hk, Hv, Dk, Dv;
@@ -57,9 +57,10 @@ struct DecayWalk {
   float* seg_sum;
   float* seg_steps;
   int seg_native;
-  float* dots;              // sums for dlg (else null); see DecayStats
-  const float* cross;       // [B*Hv] states, dotted with the end state of every segment (dlg):
-  const float* seg_cross;   //   first segment's, and [nseg, B*Hv]
+  // the dq walk: its part of dlg, fp64 [B*Hv, nseg, waves], from what e gives and
+  // the loss's derivative in the state behind the segment (R; [nseg, B*Hv] seg_R)
+  double* grad;
+  const float *R, *seg_R;
 };
 
 struct DecayWalkArgs {
@@ -71,22 +72,16 @@ struct DecayWalkArgs {
   DecayWalk walk[2];        // walks of one launch, with the same KD, N class
 };
 
-// What the backward's walks hand to the reduction for dlg, fp32:
-//   dq walk: per (b, h, chunk, wave) the sums a0, a1 (see reduce_kernel) and the in-chunk sum
-//   dk walk: per (b, h, chunk, wave) the sums b0, b1, and the chunk's valid steps
-//   dv walk: per (b, h, segment, wave) the dot of the states at its start
+// dlg of a head: the sum of its walks' parts, n of them for each b.
 struct DecayReduceArgs {
   DecayDims d;
-  const float* lg;
-  int nseg, seg, sub;       // sub: steps per stats chunk (64 bf16, 32 fp32)
-  const float *qa, *kb, *vx;
-  int nwk, nwv;             // waves of the dq / dk walks, and of the dv walk
+  int n;
+  const double* grad;       // [B*Hv, n]
   float* dlg;               // [Hv]
 };
-constexpr int kDecayQStats = 3, kDecayKStats = 3;
 
-// dq and dk of the key heads (bf16), with the sums for dlg (laid out as the
-// walks', four waves to each block of 64 columns).
+// dq and dk of the key heads (bf16), and the parts of dlg ([B*Hv, nseg, 4 waves to
+// each block of 64 columns]).
 struct DecayKeysArgs {
   DecayDims d;
   const float* lg;
@@ -98,16 +93,12 @@ struct DecayKeysArgs {
   const float *S, *R;         // else [nseg, B*Hv] start states of both directions
   void *dq, *dk;              // [B, T, Hk, Dk]
   float *pq, *pk;             // or, where a key head's value heads go in parts, [B, T, Hk*parts, Dk] fp32
-  float *qa, *kb;
+  double* grad;
 };
-// Value heads of a key head that one workgroup goes through: the states of all of
-// them fit the registers (256 columns of channels to a wave of 16 columns).
-inline int decay_heads_together(int G, int Dv) {
-  const int most = 2;
-  for (int n = most; n > 1; --n)
-    if (G % n == 0) return n;
-  return 1;
-}
+// Value heads of a key head that one workgroup goes through for dk.  Two: four
+// states of 128 channels leave too few registers (9B layer, 2048 steps: 75 us with
+// two, 113 us with four).  For dq, which carries as many derivatives, one.
+inline int decay_heads_together(int G) { return G % 2 == 0 ? 2 : 1; }
 
 struct DecayChainArgs {
   DecayDims d;
@@ -124,7 +115,7 @@ struct DecayChainArgs {
 // rounded once.
 struct DecayGroupArgs {
   DecayDims d;
-  int parts;                // of a key head
+  int parts[2];             // of a key head, for dq and for dk (1: nothing to do)
   const float *pq, *pk;     // [B, T, Hk*parts, Dk] fp32
   void *dq, *dk;            // [B, T, Hk, Dk]
 };

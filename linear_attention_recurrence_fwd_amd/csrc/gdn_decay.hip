@@ -100,62 +100,14 @@ __global__ void __launch_bounds__(64) chain_kernel(ChainArgs aa) {
   *reinterpret_cast<float4*>(a.end + bh * hs + e) = run;
 }
 
-// ---- dlg of one head.  A pair of a source step j and a later step i that reads
-// it weighs (valid steps after j up to i) times its share of the loss,
-//   f_ij = scale g^(n_i - n_j) (q_i . k_j)(dO_i . v_j),
-// likewise with the initial state for a source and dS_final for a reader.  Per
-// chunk: pairs inside it are summed in the dq walk; of pairs that enter, a1
-// holds the part of their steps inside the chunk (a0: the pairs' plain sum);
-// of pairs that leave, b1 (b0); pairs that pass through it cross all of its L
-// steps.  What crosses a boundary, X, follows from a0 and b0 chunk by chunk,
-// starting at each segment from the dot of the two states there, so that
-// rounding does not build up over a long sequence.  Where g^L is below 2^-24
-// nothing that counts passes through.
-// A workgroup to a head takes tiles of whole segments, up to 256 chunks: a thread
-// adds up one chunk's sums over the waves, then a thread to each segment follows
-// its boundaries.
+// ---- dlg of one head: its parts summed in a fixed order.
 __global__ void __launch_bounds__(256) reduce_kernel(DecayReduceArgs a) {
-  const DecayDims& d = a.d;
   const int h = blockIdx.x, tid = threadIdx.x;
-  const int nstat = (d.T + a.sub - 1) / a.sub, per = a.seg * kDecayChunk / a.sub;  // per <= 256 (see the cut)
-  const int segs = 256 / per, tiles = (a.nseg + segs - 1) / segs;
-  const float lg2 = log2_decay(a.lg[h]);
-  __shared__ float sa[256], sb[256], sl[256];
   __shared__ double part[256];
   double total = 0.0;
-  for (int i = 0; i < d.B * tiles; ++i) {
-    const int b = i / tiles, s0 = (i % tiles) * segs;
-    const size_t bh = static_cast<size_t>(b) * d.Hv + h;
-    const int c = s0 * per + tid;
-    if (tid < segs * per && c < nstat) {
-      const float* q = a.qa + (bh * nstat + c) * a.nwk * kDecayQStats;
-      const float* k = a.kb + (bh * nstat + c) * a.nwk * kDecayKStats;
-      float a0 = 0.f, b0 = 0.f;
-      double in = 0.0;
-      for (int w = 0; w < a.nwk; ++w) {
-        a0 += q[w * kDecayQStats];
-        b0 += k[w * kDecayKStats];
-        in += static_cast<double>(q[w * kDecayQStats + 1]) + q[w * kDecayQStats + 2] + k[w * kDecayKStats + 1];
-      }
-      total += in;
-      sa[tid] = a0;
-      sb[tid] = b0;
-      sl[tid] = k[2];
-    }
-    __syncthreads();
-    const int s = s0 + tid;
-    if (tid < segs && s < a.nseg) {
-      double X = 0.0;
-      for (int w = 0; w < a.nwv; ++w) X += a.vx[(bh * a.nseg + s) * a.nwv + w];
-      const int n = min(per, nstat - s * per);
-      for (int k = 0; k < n; ++k) {
-        const float L = sl[tid * per + k];
-        const double through = lg2 * L < -24.f ? 0.0 : X - sa[tid * per + k];
-        total += L * through;
-        X = through + sb[tid * per + k];
-      }
-    }
-    __syncthreads();
+  for (int b = 0; b < a.d.B; ++b) {
+    const double* p = a.grad + (static_cast<size_t>(b) * a.d.Hv + h) * a.n;
+    for (int i = tid; i < a.n; i += 256) total += p[i];
   }
   part[tid] = total;
   __syncthreads();
@@ -171,7 +123,8 @@ __global__ void __launch_bounds__(256) reduce_kernel(DecayReduceArgs a) {
 template <typename T>
 __global__ void __launch_bounds__(256) group_kernel(DecayGroupArgs a, size_t n) {
   const DecayDims& d = a.d;
-  const int G = a.parts;
+  const int G = a.parts[blockIdx.y];
+  if (G == 1) return;
   const float* src = blockIdx.y ? a.pk : a.pq;
   T* dst = static_cast<T*>(blockIdx.y ? a.dk : a.dq);
   for (size_t i = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < n;

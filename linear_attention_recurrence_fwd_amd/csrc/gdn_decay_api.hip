@@ -52,12 +52,21 @@ Cut cut(const gdn_dims* p, const DecayDims& d, bool bwd) {
   // and 16 chunks, 4 segments (192 workgroups) take 37 us, 6 (288) 47 us; at 64
   // and 32 chunks, 4 (256) take 72 us, 8 (512) 94 us
   if (p->algo != GDN_ALGO_CHUNK && nc > 1) n = 256 / (d.B * d.Hv);
-  // the backward's sums for dlg follow the boundaries chunk by chunk from the
-  // start of a segment: short segments keep their rounding down
-  if (bwd && n < (nc + 15) / 16) n = (nc + 15) / 16;
   if (n > gdn::kDecayMaxSeg) n = gdn::kDecayMaxSeg;
   if (n > nc) n = nc;
   if (n < 1) n = 1;
+  // Segments pay where a pass over all chunks costs more than one over a
+  // segment's, its sums (0.6 of a pass) and a launch and the states' traffic, in
+  // chunks' times (3 us forward in bf16, 8 backward, 12 and more in fp32; the
+  // states' part grows with their number).  128 x 128 heads, us, one pass against
+  // segments: 8 heads, 130 steps 15 / 20, 512 steps 31 / 25; 64 heads, 512 steps
+  // 31 / 35, 1024 steps 55 / 42; backward 64 heads, 512 steps 79 / 86, 1024 steps
+  // 139 / 121; fp32 8 heads, 256 steps 55 / 32.
+  if (n > 1) {
+    const float seg = static_cast<float>((nc + n - 1) / n), states = static_cast<float>(d.B) * d.Hv * n / 256.f;
+    const float extra = p->dtype != GDN_BF16 ? 1.4f + states : bwd ? 1.5f + 6.f * states : 2.5f + 3.5f * states;
+    if (static_cast<float>(nc) <= 1.6f * seg + extra) n = 1;
+  }
   Cut c;
   c.seg = nc ? (nc + n - 1) / n : 1;
   c.n = nc ? (nc + c.seg - 1) / c.seg : 1;
@@ -67,20 +76,20 @@ Cut cut(const gdn_dims* p, const DecayDims& d, bool bwd) {
 struct Layout {
   size_t S, R;            // segment states, forward and backward in time
   size_t steps;           // valid steps of the segments
-  size_t end;             // the backward's recomputed final state
-  size_t qa, kb, vx;      // sums for dlg
+  size_t end;             // the backward's recomputed final state (not read)
+  size_t grad;            // parts of dlg
   size_t pq, pk;          // rows of grouped heads
   size_t total;
 };
 
-// The waves that leave sums for dlg for a (b, h), and the parts in which a key
+// The waves that leave parts of dlg for a (b, h) and segment, and the parts in which a key
 // head's value heads leave their dq and dk rows: the bf16 kernel goes through
 // several value heads together, the fp32 walks through one.
 int key_waves(const gdn_dims* p, const DecayDims& d) {
   return p->dtype == GDN_BF16 ? 4 * ((d.Dk + 63) / 64) : gdn::decay_waves(d.Dk);
 }
-int key_parts(const gdn_dims* p, const DecayDims& d) {
-  return p->dtype == GDN_BF16 ? d.G() / gdn::decay_heads_together(d.G(), d.Dv) : d.G();
+int key_parts(const gdn_dims* p, const DecayDims& d, bool dq) {
+  return p->dtype == GDN_BF16 && !dq ? d.G() / gdn::decay_heads_together(d.G()) : d.G();
 }
 
 Layout layout(const gdn_dims* p, const DecayDims& d, bool bwd) {
@@ -104,16 +113,11 @@ Layout layout(const gdn_dims* p, const DecayDims& d, bool bwd) {
       L.R = take(states);
       L.end = take(bh * d.Dk * d.Dv);
     }
-    const int sub = p->dtype == GDN_BF16 ? 64 : 32;
-    const size_t nstat = (static_cast<size_t>(d.T) + sub - 1) / sub, nwk = key_waves(p, d);
-    L.qa = take(bh * nstat * nwk * gdn::kDecayQStats);
-    L.kb = take(bh * nstat * nwk * gdn::kDecayKStats);
-    L.vx = take(bh * c.n * gdn::decay_waves(d.Dv));
-    if (key_parts(p, d) > 1) {
-      const size_t rows = static_cast<size_t>(d.B) * d.T * d.Hk * key_parts(p, d) * d.Dk;
-      L.pq = take(rows);
-      L.pk = take(rows);
-    }
+    L.grad = take(2 * bh * c.n * key_waves(p, d));  // fp64
+    const size_t rows = static_cast<size_t>(d.B) * d.T * d.Hk * d.Dk;
+    const int nq = key_parts(p, d, true), nk = key_parts(p, d, false);
+    if (nq > 1) L.pq = take(rows * nq);
+    if (nk > 1) L.pk = take(rows * nk);
   }
   L.total = off;
   return L;
@@ -268,8 +272,8 @@ int gdn_decay_bwd(const gdn_dims* d, const void* q, const void* k, const void* v
   const bool bf = d->dtype == GDN_BF16;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const Cut c = cut(d, dd, true);
-  const int parts = key_parts(d, dd);
-  float *qa = at<float>(ws, L.qa), *kb = at<float>(ws, L.kb), *vx = at<float>(ws, L.vx);
+  const int nq = key_parts(d, dd, true), nk = key_parts(d, dd, false);
+  double* grad = at<double>(ws, L.grad);
   float *pq = at<float>(ws, L.pq), *pk = at<float>(ws, L.pk);  // (read and written with parts only)
 
   gdn::DecayWalk wv = walk_kv(dd);  // dv, dstate
@@ -282,8 +286,6 @@ int gdn_decay_bwd(const gdn_dims* d, const void* q, const void* k, const void* v
   wv.scale_i = 1.f;
   wv.start = dS_final;
   wv.end = dstate;
-  wv.dots = vx;
-  wv.cross = state0;
 
   float *S = nullptr, *R = nullptr;
   if (c.n > 1) {
@@ -303,46 +305,46 @@ int gdn_decay_bwd(const gdn_dims* d, const void* q, const void* k, const void* v
                                        {dd, lg, steps, c.n, R, dS_final, dstate, 1}};
     if (gdn::launch_decay_chain(ch, 2, st) != hipSuccess) return GDN_ERR_HIP;
     wv.seg_start = R;
-    wv.seg_cross = S;
     wv.end = nullptr;
   }
   const gdn::DecayWalkArgs av{dd, lg, mask, c.n, c.seg, 1, {wv, wv}};
   if (gdn::launch_decay_walk(av, false, bf, st) != hipSuccess) return GDN_ERR_HIP;
   if (bf) {
-    const gdn::DecayKeysArgs ka{dd, lg, scale, mask, c.n, c.seg, q, k, v, dO, state0, dS_final, S, R, dq, dk, pq, pk, qa, kb};
-    if (dd.T > 0 && gdn::launch_decay_keys(ka, st) != hipSuccess) return GDN_ERR_HIP;
+    const gdn::DecayKeysArgs ka{dd, lg, scale, mask, c.n, c.seg, q, k, v, dO, state0, dS_final, S, R, dq, dk, pq, pk, grad};
+    if (gdn::launch_decay_keys(ka, st) != hipSuccess) return GDN_ERR_HIP;
   } else {
     gdn::DecayWalk wq = walk_vk(dd);  // dq
     wq.x = val_rows(dd, dO);
     wq.y = val_rows(dd, v);
     wq.z = key_rows(dd, k);
     wq.e = key_rows(dd, q);
-    wq.w = parts > 1 ? pq : dq;
+    wq.w = nq > 1 ? pq : dq;
     wq.scale_p = wq.scale_i = scale;
     wq.scale_u = 1.f;
     wq.start = state0;
     wq.seg_start = S;
-    wq.dots = qa;
+    wq.grad = grad;
+    wq.R = dS_final;
+    wq.seg_R = R;
     gdn::DecayWalk wk = walk_vk(dd);  // dk
     wk.x = val_rows(dd, v);
     wk.y = val_rows(dd, dO);
     wk.z = key_rows(dd, q);
-    wk.e = key_rows(dd, k);
-    wk.w = parts > 1 ? pk : dk;
+    wk.w = nk > 1 ? pk : dk;
     wk.reverse = 1;
     wk.scale_p = wk.scale_u = scale;
     wk.scale_i = 1.f;
     wk.start = dS_final;
     wk.seg_start = R;
-    wk.dots = kb;
-    const gdn::DecayWalkArgs aqk{dd, lg, mask, c.n, c.seg, 2, {wq, wk}};
-    if (dd.T > 0 && gdn::launch_decay_walk(aqk, false, false, st) != hipSuccess) return GDN_ERR_HIP;
+    const gdn::DecayWalkArgs aq{dd, lg, mask, c.n, c.seg, 1, {wq, wq}}, ak{dd, lg, mask, c.n, c.seg, 1, {wk, wk}};
+    if (gdn::launch_decay_walk(aq, false, false, st) != hipSuccess) return GDN_ERR_HIP;
+    if (gdn::launch_decay_walk(ak, false, false, st) != hipSuccess) return GDN_ERR_HIP;
   }
-  if (parts > 1 && dd.T > 0) {
-    const gdn::DecayGroupArgs ga{dd, parts, pq, pk, dq, dk};
+  if ((nq > 1 || nk > 1) && dd.T > 0) {
+    const gdn::DecayGroupArgs ga{dd, {nq, nk}, pq, pk, dq, dk};
     if (gdn::launch_decay_group(ga, bf, st) != hipSuccess) return GDN_ERR_HIP;
   }
-  const gdn::DecayReduceArgs ra{dd, lg, c.n, c.seg, bf ? 64 : 32, qa, kb, vx, key_waves(d, dd), gdn::decay_waves(dd.Dv), dlg};
+  const gdn::DecayReduceArgs ra{dd, c.n * key_waves(d, dd), grad, dlg};
   return gdn::launch_decay_reduce(ra, st) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
 }
 

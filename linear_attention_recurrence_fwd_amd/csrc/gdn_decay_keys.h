@@ -2,7 +2,10 @@
 // together.  See DecayKeysArgs in gdn_decay.h and the walk kernel
 // (gdn_decay_walk.h), whose parts this one is made of:
 //   dq: x = dO, y = v,  z = k, e = q, forward in time;  w summed over the heads
-//   dk: x = v,  y = dO, z = q, e = k, backward in time
+//   dk: x = v,  y = dO, z = q, backward in time
+// dq carries the states' derivatives in lg beside them (E, see the walk kernel), with
+// all products that reach dlg in three bf16 parts; dk's state and sums reach bf16
+// results only (one part against x, two in its update).
 //
 // A workgroup of four waves owns 64 columns of GH value heads' transposed states
 // [Dv, Dk], all in registers (wave w: 16 columns of every head's), and for each
@@ -26,10 +29,10 @@ template <int KD> struct KeysLds {
   static constexpr int CH = 64, PX = KD / 8, PZ = 8, PP = 8;
   static constexpr int XB = CH * PX * 16, ZB = CH * PZ * 16;
   static constexpr int Y = 0, X = 2 * XB, Z = X + XB, E = Z + ZB, P = E + ZB, F = P + CH * PP * 16;
-  static constexpr int TOTAL = F + 2 * 3 * CH * 4;
+  static constexpr int TOTAL = F + 2 * 4 * CH * 4;
 };
 
-template <int KD, int GH>
+template <int KD, int GH, bool DQ>
 __global__ void __launch_bounds__(256, KD <= 128 ? 2 : 1) keys_kernel(DecayKeysArgs a) {
   using M = KeysLds<KD>;
   constexpr int CH = M::CH, PX = M::PX, PZ = M::PZ, PP = M::PP, MT = 4, KT = KD / 16, NW = 4;
@@ -41,13 +44,15 @@ __global__ void __launch_bounds__(256, KD <= 128 ? 2 : 1) keys_kernel(DecayKeysA
   // blocks of columns fastest, then a key head's parts: they share rows
   const int cb = it % ncb * 64, hp = it / ncb % (Hk * parts), sg = it / (ncb * Hk * parts) % nseg;
   const int b = it / (ncb * Hk * parts * nseg), hk = hp / parts, h0 = hp * GH;
-  const bool rev = blockIdx.y != 0;
+  constexpr bool rev = !DQ;
+  constexpr int SP = DQ ? 3 : 1, SU = DQ ? 3 : 2;  // bf16 parts of the state, of what it sums
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, lr = l & 15, g = l >> 4;
   const size_t bT = static_cast<size_t>(b) * Tn;
   const uint8_t* mrow = a.mask ? a.mask + bT : nullptr;
   const bool masked = mrow != nullptr;
+  const uint32_t lds0 = lds_addr(sm);
   const bf16 *xp = static_cast<const bf16*>(rev ? a.v : a.dO), *yp = static_cast<const bf16*>(rev ? a.dO : a.v);
-  const bf16 *zp_ = static_cast<const bf16*>(rev ? a.q : a.k), *ep = static_cast<const bf16*>(rev ? a.k : a.q);
+  const bf16 *zp_ = static_cast<const bf16*>(rev ? a.q : a.k), *ep = static_cast<const bf16*>(a.q);
   // scale on P, on the product with the state, on the state's update
   const float scale_p = a.scale, scale_i = rev ? 1.f : a.scale, scale_u = rev ? a.scale : 1.f;
   float lg2[GH];
@@ -56,7 +61,8 @@ __global__ void __launch_bounds__(256, KD <= 128 ? 2 : 1) keys_kernel(DecayKeysA
 
   // ---- start states, element (channel c of Dv, column k of Dk) at k Dv + c
   const int col = cb + 16 * w + lr;
-  f32x4 S[GH][KT];
+  f32x4 S[GH][KT], E[DQ ? GH : 1][KT];
+  double grad[GH];
 #pragma unroll
   for (int q = 0; q < GH; ++q) {
     const size_t hs = static_cast<size_t>(Dk) * Dv, bh = static_cast<size_t>(b) * Hv + h0 + q;
@@ -69,7 +75,9 @@ __global__ void __launch_bounds__(256, KD <= 128 ? 2 : 1) keys_kernel(DecayKeysA
       const int ch = 32 * (i / 2) + 8 * g + 4 * (i % 2);
       const float4 v = buf_f4(rs, ch < Dv && col < Dk ? 4u * static_cast<uint32_t>(col * Dv + ch) : kOff);
       S[q][i] = f32x4{v.x, v.y, v.z, v.w};
+      if constexpr (DQ) E[q][i] = f4zero();
     }
+    grad[q] = 0.0;
   }
 
   const int t_lo = sg * a.seg * kDecayChunk, t_hi = min(Tn, t_lo + a.seg * kDecayChunk);
@@ -94,36 +102,29 @@ __global__ void __launch_bounds__(256, KD <= 128 ? 2 : 1) keys_kernel(DecayKeysA
   };
   auto issue_x = [&](int ci, int q, unsigned long long live) {
     const i32x4 dx = rows(xp, Hv, h0 + q, Dv, chunk_start(ci), 0);
-    if (masked && rev) lx.load_live(dx, sm + M::X, w, l, live);
-    else lx.load(dx, sm + M::X, w, l);
+    if (masked && rev) lx.load_live(dx, lds0 + M::X, w, l, live);
+    else lx.load(dx, lds0 + M::X, w, l);
   };
   auto issue_y = [&](int ci, int q, int slot, unsigned long long live) {
     const i32x4 dy = rows(yp, Hv, h0 + q, Dv, chunk_start(ci), 0);
-    if (masked && !rev) lx.load_live(dy, sm + M::Y + slot * M::XB, w, l, live);
-    else lx.load(dy, sm + M::Y + slot * M::XB, w, l);
+    if (masked && !rev) lx.load_live(dy, lds0 + M::Y + slot * M::XB, w, l, live);
+    else lx.load(dy, lds0 + M::Y + slot * M::XB, w, l);
   };
   auto issue_ze = [&](int ci, unsigned long long live) {
-    const i32x4 dz = rows(zp_, Hk, hk, Dk, chunk_start(ci), cb), de = rows(ep, Hk, hk, Dk, chunk_start(ci), cb);
-    if (masked) {
-      if (rev) {
-        lz.load(dz, sm + M::Z, w, l);
-        lz.load_live(de, sm + M::E, w, l, live);
-      } else {
-        lz.load_live(dz, sm + M::Z, w, l, live);
-        lz.load(de, sm + M::E, w, l);
-      }
-    } else {
-      lz.load(dz, sm + M::Z, w, l);
-      lz.load(de, sm + M::E, w, l);
-    }
+    const i32x4 dz = rows(zp_, Hk, hk, Dk, chunk_start(ci), cb);
+    if (masked && !rev) lz.load_live(dz, lds0 + M::Z, w, l, live);
+    else lz.load(dz, lds0 + M::Z, w, l);
+    if constexpr (DQ) lz.load(rows(ep, Hk, hk, Dk, chunk_start(ci), cb), lds0 + M::E, w, l);
   };
-  // c, row factors and source weights of a chunk for head q
+  // c, row factors, source weights, and these times the steps left, for head q
   auto factors = [&](int set, float lg2q, unsigned long long live) {
-    float* f = reinterpret_cast<float*>(sm + M::F) + set * 3 * CH + l;
+    float* f = reinterpret_cast<float*>(sm + M::F) + set * 4 * CH + l;
     const float c = static_cast<float>(__popcll(live & (((rev ? 1ull : 2ull) << l) - 1ull)));
+    const float left = static_cast<float>(__popcll(live)) - c;
     f[0] = c;
     f[CH] = scale_i * exp2_fast(lg2q * c);
-    f[2 * CH] = scale_u * exp2_fast(lg2q * (static_cast<float>(__popcll(live)) - c));
+    f[2 * CH] = scale_u * exp2_fast(lg2q * left);
+    f[3 * CH] = left * f[2 * CH];
   };
 
   // operand places, as in the walk kernel; piece 4 e further is 64 e in the place's
@@ -164,19 +165,18 @@ __global__ void __launch_bounds__(256, KD <= 128 ? 2 : 1) keys_kernel(DecayKeysA
       reinterpret_cast<uint2*>(sm + M::P + (row * PP + (p ^ key<PP>(row))) * 16)[(l >> 1) & 1] = make_uint2(0, 0);
     }
   }
-  const size_t nstat = (static_cast<size_t>(Tn) + CH - 1) / CH;
   for (int ci = 0; ci < nch; ++ci) {
     const int t0 = chunk_start(ci), L = __popcll(live);
-    f32x4 acc[MT], pu[TP];
-    uint2 ev[MT];
+    f32x4 acc[MT], pu[DQ ? TP : 1];
+    uint2 ev[DQ ? MT : 1];
     uint4 zu[2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) acc[mt] = f4zero();
 #pragma unroll
     for (int q = 0; q < GH; ++q) {
       const int set = GH % 2 == 0 ? q & 1 : (ci * GH + q) & 1;
-      const char* ytile = sm + M::Y + set * M::XB;
-      const float *fc = reinterpret_cast<const float*>(sm + M::F) + set * 3 * CH, *frf = fc + CH, *fsw = fc + 2 * CH;
+      const uint32_t ytile = M::Y + set * M::XB;
+      const float *fc = reinterpret_cast<const float*>(sm + M::F) + set * 4 * CH, *frf = fc + CH, *fsw = fc + 2 * CH;
       // (the stores of the last chunk's results are asked for behind the loads)
       if (q == 0 && ci > 0) wait_vm<MT>();
       else wait_vm<0>();
@@ -200,21 +200,23 @@ __global__ void __launch_bounds__(256, KD <= 128 ? 2 : 1) keys_kernel(DecayKeysA
 
       // ---- what the heads share: e . z tiles, e at the results' places, z
       if (q == 0) {
+        if constexpr (DQ) {
 #pragma unroll
-        for (int k = 0; k < TP; ++k) {
-          int mt, nt;
-          pu[k] = f4zero();
-          if (!rev && tile_of(k, mt, nt)) {
+          for (int k = 0; k < TP; ++k) {
+            int mt, nt;
+            pu[k] = f4zero();
+            if (tile_of(k, mt, nt)) {
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
-              pu[k] = mfma16(load_bf16x8(sm + M::Z + rz[ks] + nt * 16 * PZ * 16),
-                             load_bf16x8(sm + M::E + rz[ks] + mt * 16 * PZ * 16), pu[k]);
+              for (int ks = 0; ks < 2; ++ks)
+                pu[k] = mfma16(load_bf16x8(sm + M::Z + rz[ks] + nt * 16 * PZ * 16),
+                               load_bf16x8(sm + M::E + rz[ks] + mt * 16 * PZ * 16), pu[k]);
+            }
           }
-        }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const int row = 16 * mt + lr, p = 2 * w + (g >> 1);
-          ev[mt] = reinterpret_cast<const uint2*>(sm + M::E + (row * PZ + (p ^ key<PZ>(lr))) * 16)[g & 1];
+          for (int mt = 0; mt < MT; ++mt) {
+            const int row = 16 * mt + lr, p = 2 * w + (g >> 1);
+            ev[mt] = reinterpret_cast<const uint2*>(sm + M::E + (row * PZ + (p ^ key<PZ>(lr))) * 16)[g & 1];
+          }
         }
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt) {
@@ -231,9 +233,9 @@ __global__ void __launch_bounds__(256, KD <= 128 ? 2 : 1) keys_kernel(DecayKeysA
         int mt, nt;
         if (!tile_of(k, mt, nt)) continue;
         f32x4 t = f4zero();
-        const char *py = ytile + nt * 16 * PX * 16, *px = sm + M::X + mt * 16 * PX * 16;
+        const uint32_t py = ytile + nt * 16 * PX * 16, px = M::X + mt * 16 * PX * 16;
 #pragma unroll
-        for (int ks = 0; ks < KD / 32; ++ks) t = mfma16(load_bf16x8(py + at_x(0, ks)), load_bf16x8(px + at_x(0, ks)), t);
+        for (int ks = 0; ks < KD / 32; ++ks) t = mfma16(load_bf16x8(sm + (py + at_x(0, ks))), load_bf16x8(sm + (px + at_x(0, ks))), t);
         const float c_i = fc[16 * mt + lr];
         const f32x4 c_j = *reinterpret_cast<const f32x4*>(fc + 16 * nt + 4 * g);
         float dn[4];
@@ -246,59 +248,64 @@ __global__ void __launch_bounds__(256, KD <= 128 ? 2 : 1) keys_kernel(DecayKeysA
 #pragma unroll
           for (int r = 0; r < 4; ++r) t[r] = 4 * g + r <= lr ? t[r] : 0.f;
         }
-        if (!rev) {
+        if constexpr (DQ) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) intra = fmaf(dn[r] * t[r], nt < mt || 4 * g + r <= lr ? pu[k][r] : 0.f, intra);
         }
         reinterpret_cast<uint2*>(sm + M::P + ((16 * mt + lr) * PP + ((2 * nt + (g >> 1)) ^ key<PP>(lr))) * 16)[g & 1] =
             pack4_bf16(t[0], t[1], t[2], t[3]);
       }
-      // ---- S^T x, its dots with e, and into the sum over the heads
-      f32x4 ai[MT];
+      // ---- S^T x into the sum over the heads, and with E^T x against e
+      f32x4 ai[MT], ae[DQ ? MT : 1];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) ai[mt] = f4zero();
-#pragma unroll
-      for (int ks = 0; ks < KD / 32; ++ks) {
-        bf16x8 xa[MT], part[3];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) xa[mt] = load_bf16x8(sm + M::X + at_x(mt, ks));
+      for (int mt = 0; mt < MT; ++mt) {
+        ai[mt] = f4zero();
+        if constexpr (DQ) ae[mt] = f4zero();
+      }
+      auto operand = [](const f32x4& s, const f32x4& t, bf16x8 (&part)[SP]) {
         float v[8];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          v[r] = S[q][2 * ks][r];
-          v[4 + r] = S[q][2 * ks + 1][r];
+          v[r] = s[r];
+          v[4 + r] = t[r];
         }
-        split8<3>(v, part);
+        split8<SP>(v, part);
+      };
 #pragma unroll
-        for (int s = 0; s < 3; ++s)
+      for (int ks = 0; ks < KD / 32; ++ks) {
+        bf16x8 xa[MT], part[SP];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) xa[mt] = load_bf16x8(sm + M::X + at_x(mt, ks));
+        operand(S[q][2 * ks], S[q][2 * ks + 1], part);
+#pragma unroll
+        for (int s = 0; s < SP; ++s)
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) ai[mt] = mfma16(part[s], xa[mt], ai[mt]);
+        if constexpr (DQ) {
+          operand(E[q][2 * ks], E[q][2 * ks + 1], part);
+#pragma unroll
+          for (int s = 0; s < SP; ++s)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) ae[mt] = mfma16(part[s], xa[mt], ae[mt]);
+        }
       }
-      float s0 = 0.f, s1 = 0.f;
+      float sum = 0.f;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const float rf = frf[16 * mt + lr], ct = fc[16 * mt + lr];
-        const float e[4] = {__uint_as_float(ev[mt].x << 16), __uint_as_float(ev[mt].x & 0xffff0000u),
-                            __uint_as_float(ev[mt].y << 16), __uint_as_float(ev[mt].y & 0xffff0000u)};
-        float f = 0.f;
+        const float rf = frf[16 * mt + lr];
+        if constexpr (DQ) {
+          const float ct = fc[16 * mt + lr];
+          const float e[4] = {__uint_as_float(ev[mt].x << 16), __uint_as_float(ev[mt].x & 0xffff0000u),
+                              __uint_as_float(ev[mt].y << 16), __uint_as_float(ev[mt].y & 0xffff0000u)};
+          float f = 0.f;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          f = fmaf(ai[mt][r], e[r], f);
-          acc[mt][r] = fmaf(ai[mt][r], rf, acc[mt][r]);
+          for (int r = 0; r < 4; ++r) f = fmaf(fmaf(ct, ai[mt][r], ae[mt][r]), e[r], f);
+          sum = fmaf(rf, f, sum);
         }
-        s0 = fmaf(f, rf, s0);
-        s1 = fmaf(f, rf * ct, s1);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[mt][r] = fmaf(ai[mt][r], rf, acc[mt][r]);
       }
-      s0 = wave_sum(s0);
-      s1 = wave_sum(s1);
-      intra = wave_sum(intra);
-      if (l == 0) {
-        const size_t at = ((static_cast<size_t>(b) * Hv + h0 + q) * nstat + t0 / CH) * (4 * ncb) + (cb >> 4) + w;
-        float* o = (rev ? a.kb : a.qa) + at * 3;
-        o[0] = s0;
-        o[1] = s1;
-        o[2] = rev ? static_cast<float>(L) : intra;
-      }
+      if constexpr (DQ) grad[q] += static_cast<double>(sum) + static_cast<double>(intra);
       lds_barrier();  // P is whole; x, and by the first head z and e, are read
       if (more) issue_x(cn, qn, ln);
       if (q == 0 && ci + 1 < nch) issue_ze(ci + 1, live_next);
@@ -308,31 +315,42 @@ __global__ void __launch_bounds__(256, KD <= 128 ? 2 : 1) keys_kernel(DecayKeysA
 #pragma unroll
       for (int i = 0; i < KT; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) S[q][i][r] *= gL;
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (DQ) E[q][i][r] = gL * fmaf(static_cast<float>(L), S[q][i][r], E[q][i][r]);
+          S[q][i][r] *= gL;
+        }
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt) {
-        constexpr int YH = 4;
-        float sw[8], v[8];
-        *reinterpret_cast<f32x4*>(sw) = *reinterpret_cast<const f32x4*>(fsw + 32 * kt + 8 * g);
-        *reinterpret_cast<f32x4*>(sw + 4) = *reinterpret_cast<const f32x4*>(fsw + 32 * kt + 8 * g + 4);
-        bf16x8 part[3], ya[YH];
-        Vec16<bf16>::unpack(zu[kt], v);
+        constexpr int YH = DQ ? 2 : 4;  // y tiles held at a time
+        bf16x8 part[SU], pe[DQ ? SU : 1], ya[YH];
+        auto weighted = [&](const float* f, bf16x8 (&p)[SU]) {
+          float sw[8], v[8];
+          *reinterpret_cast<f32x4*>(sw) = *reinterpret_cast<const f32x4*>(f + 32 * kt + 8 * g);
+          *reinterpret_cast<f32x4*>(sw + 4) = *reinterpret_cast<const f32x4*>(f + 32 * kt + 8 * g + 4);
+          Vec16<bf16>::unpack(zu[kt], v);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] *= sw[k];
-        split8<3>(v, part);
+          for (int k = 0; k < 8; ++k) v[k] *= sw[k];
+          split8<SU>(v, p);
+        };
+        weighted(fsw, part);
+        if constexpr (DQ) weighted(fsw + CH, pe);
 #pragma unroll
         for (int i0 = 0; i0 < KT; i0 += YH) {
 #pragma unroll
           for (int i = 0; i < YH; ++i) {
             const int ks = (i0 + i) / 2;
-            const char* yt = ytile + kt * 32 * PX * 16 + (ks / QX) * QX * 64 + (i & 1) * 8;
-            const uint2 y0 = lds_read_tr16(yt + (ty[0] ^ (ks % QX * 64u))), y1 = lds_read_tr16(yt + (ty[1] ^ (ks % QX * 64u)));
+            const uint32_t yt = ytile + kt * 32 * PX * 16 + (ks / QX) * QX * 64 + (i & 1) * 8;
+            const uint2 y0 = lds_read_tr16(sm + (yt + (ty[0] ^ (ks % QX * 64u))));
+            const uint2 y1 = lds_read_tr16(sm + (yt + (ty[1] ^ (ks % QX * 64u))));
             ya[i] = as_bf16x8(make_uint4(y0.x, y0.y, y1.x, y1.y));
           }
 #pragma unroll
-          for (int s = 0; s < 3; ++s)
+          for (int s = 0; s < SU; ++s)
 #pragma unroll
-            for (int i = 0; i < YH; ++i) S[q][i0 + i] = mfma16(ya[i], part[s], S[q][i0 + i]);
+            for (int i = 0; i < YH; ++i) {
+              S[q][i0 + i] = mfma16(ya[i], part[s], S[q][i0 + i]);
+              if constexpr (DQ) E[q][i0 + i] = mfma16(ya[i], pe[s], E[q][i0 + i]);
+            }
         }
 #pragma unroll
         for (int mt = 2 * kt; mt < MT; ++mt)
@@ -358,20 +376,33 @@ __global__ void __launch_bounds__(256, KD <= 128 ? 2 : 1) keys_kernel(DecayKeysA
     live = live_next;
   }
   wait_vm<0>();  // no load to LDS outlives the workgroup
+  if constexpr (DQ) {  // the derivative of the state behind the segment, against the loss's
+#pragma unroll
+    for (int q = 0; q < GH; ++q) {
+      const size_t hs = static_cast<size_t>(Dk) * Dv, bh = static_cast<size_t>(b) * Hv + h0 + q;
+      const float* R = nseg > 1 ? a.R + (static_cast<size_t>(sg) * a.d.B * Hv + bh) * hs : a.dS ? a.dS + bh * hs : nullptr;
+      const rsrc_t rc = make_rsrc(R, R ? hs * 4 : 0);
+#pragma unroll
+      for (int i = 0; i < KT; ++i) {
+        const int ch = 32 * (i / 2) + 8 * g + 4 * (i % 2);
+        const float4 v = buf_f4(rc, ch < Dv && col < Dk ? 4u * static_cast<uint32_t>(col * Dv + ch) : kOff);
+        grad[q] += static_cast<double>(fmaf(E[q][i][3], v.w, fmaf(E[q][i][2], v.z, fmaf(E[q][i][1], v.y, E[q][i][0] * v.x))));
+      }
+      const double t = wave_sum_f64_dpp(grad[q]);
+      if (l == 0) a.grad[(bh * nseg + sg) * (4 * ncb) + (cb >> 4) + w] = t;
+    }
+  }
 }
 
-template <int KD, int GH> hipError_t launch_keys_gh(const DecayKeysArgs& a, hipStream_t st) {
-  const int n = a.d.B * a.nseg * a.d.Hv / GH * ((a.d.Dk + 63) / 64);
-  keys_kernel<KD, GH><<<dim3((n + 7) / 8 * 8, 2), 256, 0, st>>>(a);
+template <int KD, int GH, bool DQ> hipError_t launch_keys_gh(const DecayKeysArgs& a, hipStream_t st) {
+  const int n = a.d.B * a.nseg * (a.d.Hv / GH) * ((a.d.Dk + 63) / 64);
+  keys_kernel<KD, GH, DQ><<<(n + 7) / 8 * 8, 256, 0, st>>>(a);
   return hipGetLastError();
 }
 template <int KD> hipError_t launch_keys(const DecayKeysArgs& a, hipStream_t st) {
-  switch (decay_heads_together(a.d.G(), a.d.Dv)) {
-    case 4: return launch_keys_gh<KD, KD <= 128 ? 4 : 2>(a, st);
-    case 3: return launch_keys_gh<KD, KD <= 128 ? 3 : 2>(a, st);
-    case 2: return launch_keys_gh<KD, 2>(a, st);
-    default: return launch_keys_gh<KD, 1>(a, st);
-  }
+  const hipError_t e = launch_keys_gh<KD, 1, true>(a, st);
+  if (e != hipSuccess) return e;
+  return decay_heads_together(a.d.G()) == 2 ? launch_keys_gh<KD, 2, false>(a, st) : launch_keys_gh<KD, 1, false>(a, st);
 }
 
 }  // namespace decay

@@ -20,8 +20,20 @@
 //     bits) where only bf16 results are read from this state;
 //   - the state against x: one bf16 part, as the result is rounded to bf16 (a
 //     relative error of at most 2^-8 for each product, independent between the
-//     products); three parts where the result also enters the fp32 sums for dlg;
+//     products); three parts where the result also enters the sums for dlg;
 //   - P: one bf16 part, as the result is rounded to bf16.
+//
+// dlg (DOTS; the dq walk, whose e is q).  The loss's derivative in lg, taken
+// forward: beside the state goes its derivative since the segment's start, E = dS /
+// d lg,
+//   E <- g^L (E + L S) + sum_j y_j ((L - c_j) g^(L - c_j) z_j)^T,
+// and with the segment's share of the loss in what it reads,
+//   dlg += sum_i g^c_i e_i . (c_i S + E)^T x_i + sum_ij (c_i - c_j) P_ij (e_i . z_j),
+// in the final state or later segments' reading through R, the loss's derivative in
+// the state behind the segment: dlg += <E, R>.  All of these are sums of products
+// with the distances as weights.  (From dq and dk the same sum would follow as
+// sum_i n_i q_i . dq_i - sum_j n_j k_j . dk_j, a difference of terms up to T times
+// larger: chunk by chunk that was off by 5e-4 in single heads, this by 1e-7.)
 //
 // Tiles go to LDS by direct loads into a second set, where two sets fit, while the
 // chunk's own are used; x and e, which are read first, into their only set otherwise
@@ -78,12 +90,6 @@ __device__ __forceinline__ int xcd_order(int blk, int n) {
   return (blk & 7) * per + (blk >> 3);
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-  v = row_sum16(v);
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
-}
-
 template <int N> struct Int {
   static constexpr int v = N;
 };
@@ -117,18 +123,27 @@ constexpr uint32_t kOff = 0x80000000u;  // an offset past every descriptor here
 template <typename T, int KD, int NW, int NTL, bool OUT, bool DOTS>
 struct Lds {
   static constexpr int CH = Cfg<T>::CH, EPP = Cfg<T>::EPP, MAX = 160 * 1024;
-  static constexpr int COLS = 16 * NW * NTL;
+  static constexpr int COLS = 16 * NW * NTL, NF = DOTS ? 4 : 3;
   static constexpr int PX = KD / EPP, PZ = COLS / EPP, PP = CH / EPP;  // pieces per row
   static constexpr int XB = CH * PX * 16, ZB = CH * PZ * 16;
   static constexpr int SET = XB + ZB, Y = 0, Z = XB;
   static constexpr int XE = (OUT ? XB : 0) + (DOTS ? ZB : 0);
-  static constexpr int REST = (OUT ? CH * PP * 16 : 0) + 2 * 3 * CH * 4;
+  static constexpr int REST = (OUT ? CH * PP * 16 : 0) + 2 * NF * CH * 4;
   static constexpr int SLOTS = 2 * SET + XE + REST <= MAX ? 2 : 1;
   static constexpr bool STAGE = OUT && sizeof(T) == 2 && SLOTS * SET + XE + REST + ZB <= MAX;
   static constexpr bool XE2 = OUT && SLOTS == 2 && 2 * (SET + XE) + REST + (STAGE ? ZB : 0) <= MAX;
   static constexpr int X = SLOTS * SET, E = X + XB, P = X + (XE2 ? 2 : 1) * XE, O = P + (OUT ? CH * PP * 16 : 0);
-  static constexpr int F = O + (STAGE ? ZB : 0), TOTAL = F + 2 * 3 * CH * 4;
+  static constexpr int F = O + (STAGE ? ZB : 0), TOTAL = F + 2 * NF * CH * 4;
 };
+
+// dma16 to an LDS address; and for a place that nothing reads before the next
+// barrier, without the clobber that would keep LDS reads from moving past it.
+__device__ __forceinline__ void dma16_to(const i32x4& r, uint32_t lds, uint32_t off) {
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(r), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ void dma16_ahead(const i32x4& r, uint32_t lds, uint32_t off) {
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(r), "{m0}"(lds));
+}
 
 // Loads of one tile by this wave: 64 pieces at a time.
 template <int CH, int PPR, int EPP, int NW> struct Loader {
@@ -147,23 +162,18 @@ template <int CH, int PPR, int EPP, int NW> struct Loader {
     const int r = ((k * NW + w) * 64 + l) / PPR;
     return (live >> r) & 1 ? off[k] : kOff;
   }
-  __device__ __forceinline__ void load(const i32x4& desc, char* dst, int w, int l) const {
+  // dst: the tile's LDS address
+  __device__ __forceinline__ void load(const i32x4& desc, uint32_t dst, int w, int l) const {
 #pragma unroll
     for (int k = 0; k < PER; ++k)
-      if (N % NW == 0 || k * NW + w < N) dma16(desc, dst + (k * NW + w) * 1024, off[k]);
+      if (N % NW == 0 || k * NW + w < N) dma16_to(desc, dst + (k * NW + w) * 1024, off[k]);
   }
-  __device__ __forceinline__ void load_live(const i32x4& desc, char* dst, int w, int l, unsigned long long live) const {
+  __device__ __forceinline__ void load_live(const i32x4& desc, uint32_t dst, int w, int l, unsigned long long live) const {
 #pragma unroll
     for (int k = 0; k < PER; ++k)
-      if (N % NW == 0 || k * NW + w < N) dma16(desc, dst + (k * NW + w) * 1024, live_off(k, w, l, live));
+      if (N % NW == 0 || k * NW + w < N) dma16_to(desc, dst + (k * NW + w) * 1024, live_off(k, w, l, live));
   }
 };
-
-// dma16 for a place that nothing reads before the next barrier: without the clobber
-// that would keep LDS reads from moving past it.
-__device__ __forceinline__ void dma16_ahead(const i32x4& r, const void* lds, uint32_t off) {
-  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(r), "{m0}"(lds_addr(lds)));
-}
 
 // SPS: bf16 parts of the state in the products with x; SPU: of the weighted z
 // that the state sums.
@@ -210,7 +220,8 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
   auto native_of = [&](int s) {
     return wk.seg_sum + (static_cast<size_t>(s) * BH + bh) * native + (w * 64 + l) * 4;
   };
-  f32x4 S[KT][NTL];
+  f32x4 S[KT][NTL], E[DOTS ? KT : 1][NTL];
+  double grad = 0.0;  // this lane's part of dlg
   const float* src = nullptr;
   const bool prefix = OUT && wk.seg_sum != nullptr;  // starts from the sums before it
   if (OUT) {
@@ -277,6 +288,12 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
     load_start();
     if constexpr (!DOTS)
       if (prefix) add_sums(sg);
+    if constexpr (DOTS) {
+#pragma unroll
+      for (int i = 0; i < KT; ++i)
+#pragma unroll
+        for (int n = 0; n < NTL; ++n) E[i][n] = f4zero();
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < KT; ++i)
@@ -316,8 +333,9 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
   };
   const int xh = h / xg, yh = h / yg, zh = h / zg;
   const bool masked = mrow != nullptr;
+  const uint32_t lds0 = lds_addr(sm);
   auto issue_yz = [&](int ci, int slot, unsigned long long live) {
-    char* s = sm + slot * M::SET;
+    const uint32_t s = lds0 + slot * M::SET;
     const int t0 = chunk_start(ci);
     const i32x4 dy = rows(wk.y.p, yH, yh, KDr, t0), dz = rows(wk.z.p, zH, zh, N, t0);
     if (masked && !rev) {
@@ -329,7 +347,7 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
     }
   };
   auto issue_xe = [&](int ci, int slot, unsigned long long live) {  // x has y's row length, e has z's
-    char* s = sm + (M::XE2 ? slot * M::XE : 0);
+    const uint32_t s = lds0 + (M::XE2 ? slot * M::XE : 0);
     const int t0 = chunk_start(ci);
     if constexpr (OUT) {
       const i32x4 dx = rows(wk.x.p, xH, xh, KDr, t0);
@@ -393,14 +411,16 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
 
   unsigned long long live = 0, live_next = 0;
   int counted = 0;  // valid steps of the segment
-  // a chunk's c, row factors and source weights
+  // a chunk's c, row factors, source weights, and these times the steps left
   auto factors = [&](int ci, unsigned long long live, int behind) {
     if (l >= CH) return;
-    float* f = reinterpret_cast<float*>(sm + M::F) + (ci & 1) * 3 * CH + l;
+    float* f = reinterpret_cast<float*>(sm + M::F) + (ci & 1) * M::NF * CH + l;
     const float c = static_cast<float>(__popcll(live & (((rev ? 1ull : 2ull) << l) - 1ull)));
     f[0] = c;
     f[CH] = scale_i * exp2_fast(lg2 * c);
-    f[2 * CH] = scale_u * exp2_fast(lg2 * (static_cast<float>(behind + __popcll(live)) - c));
+    const float left = static_cast<float>(behind + __popcll(live)) - c;
+    f[2 * CH] = scale_u * exp2_fast(lg2 * left);
+    if constexpr (DOTS) f[3 * CH] = left * f[2 * CH];
   };
   // loads that stand between products: those of a set that every wave takes an
   // equal share of
@@ -414,13 +434,12 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
     if constexpr (M::SLOTS == 2) issue_yz(0, 0, live);
     issue_xe(0, 0, live);
   }
-  const size_t nstat = (static_cast<size_t>(Tn) + CH - 1) / CH;
   for (int ci = 0; ci < nch; ++ci) {
     const int t0 = chunk_start(ci), slot = M::SLOTS == 2 ? ci & 1 : 0;
     const bool more = ci + 1 < nch;
     char* tile = sm + slot * M::SET;
     char* xe = sm + (M::XE2 ? slot * M::XE : 0);
-    const float* fc = reinterpret_cast<const float*>(sm + M::F) + (ci & 1) * 3 * CH;
+    const float* fc = reinterpret_cast<const float*>(sm + M::F) + (ci & 1) * M::NF * CH;
     const float *frf = fc + CH, *fsw = fc + 2 * CH;
     if constexpr (M::SLOTS == 1) {
       lds_barrier();  // the chunk before is read
@@ -464,8 +483,7 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
       if constexpr (M::SLOTS == 2) issue_yz(ci + 1, slot ^ 1, live_next);
       if constexpr (M::XE2) issue_xe(ci + 1, slot ^ 1, live_next);
     }
-    char* next_tile = sm + (slot ^ 1) * M::SET;
-    char* next_xe = sm + (slot ^ 1) * M::XE;
+    const uint32_t next_tile = lds0 + (slot ^ 1) * M::SET, next_xe = lds0 + (slot ^ 1) * M::XE;
     auto spread_yz = [&](int k) {
       if constexpr (SPREAD) {
         if (k < NY) dma16_ahead(dny, next_tile + M::Y + (k * NW + w) * 1024, ony[k < NY ? k : 0]);
@@ -581,6 +599,13 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int n = 0; n < NTL; ++n) acc[mt][n] = f4zero();
+      f32x4 ae[DOTS ? MT : 1][NTL];
+      if constexpr (DOTS) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int n = 0; n < NTL; ++n) ae[mt][n] = f4zero();
+      }
       if constexpr (BF) {
 #pragma unroll
         for (int ks = 0; ks < KD / 32; ++ks) {
@@ -613,53 +638,34 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
-              for (int n = 0; n < NTL; ++n) acc[mt][n] = mfma16f(S[i][n][r], xv[r], acc[mt][n]);
+              for (int n = 0; n < NTL; ++n) {
+                acc[mt][n] = mfma16f(S[i][n][r], xv[r], acc[mt][n]);
+                if constexpr (DOTS) ae[mt][n] = mfma16f(E[i][n][r], xv[r], ae[mt][n]);
+              }
           }
       }
 #pragma unroll
       for (int k = BF ? KD / 32 : 0; k < NY + NZ; ++k) spread_yz(k);
       if constexpr (ONE) p_write(min(w, RUNS - 1), w < RUNS);
-      float s0 = 0.f, s1 = 0.f;
+      float s = 0.f;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         const float rf = frf[16 * mt + lr], ct = fc[16 * mt + lr];
 #pragma unroll
         for (int n = 0; n < NTL; ++n) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[mt][n][r] *= rf;
           if constexpr (DOTS) {
             const int c = column(n, 4 * g), row = 16 * mt + lr;  // four columns from here
-            float ev[4];
-            if constexpr (BF) {
-              const uint2 u = *reinterpret_cast<const uint2*>(
-                  xe + M::E + (row * PZ + ((c >> 3) ^ key<PZ>(lr))) * 16 + (c & 4) * 2);
-              ev[0] = __uint_as_float(u.x << 16);
-              ev[1] = __uint_as_float(u.x & 0xffff0000u);
-              ev[2] = __uint_as_float(u.y << 16);
-              ev[3] = __uint_as_float(u.y & 0xffff0000u);
-            } else {
-              *reinterpret_cast<f32x4*>(ev) =
-                  *reinterpret_cast<const f32x4*>(xe + M::E + (row * PZ + ((c >> 2) ^ key<PZ>(lr))) * 16);
-            }
+            const f32x4 ev = *reinterpret_cast<const f32x4*>(xe + M::E + (row * PZ + ((c >> 2) ^ key<PZ>(lr))) * 16);
             float f = 0.f;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) f = fmaf(acc[mt][n][r], ev[r], f);
-            s0 += f;
-            s1 = fmaf(ct, f, s1);
+            for (int r = 0; r < 4; ++r) f = fmaf(fmaf(ct, acc[mt][n][r], ae[mt][n][r]), ev[r], f);
+            s = fmaf(rf, f, s);
           }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[mt][n][r] *= rf;
         }
       }
-      if constexpr (DOTS) {
-        s0 = wave_sum(s0);
-        s1 = wave_sum(s1);
-        intra = wave_sum(intra);
-        if (l == 0) {
-          float* o = wk.dots + ((static_cast<size_t>(bh) * nstat + t0 / CH) * NW + w) * 3;
-          o[0] = s0;
-          o[1] = s1;
-          o[2] = rev ? static_cast<float>(L) : intra;
-        }
-      }
+      if constexpr (DOTS) grad += static_cast<double>(s) + static_cast<double>(intra);
     }
     if constexpr (OUT && !M::XE2) {
       lds_barrier();  // P is whole, x and e are read
@@ -674,7 +680,10 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
 #pragma unroll
         for (int n = 0; n < NTL; ++n)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) S[i][n][r] *= gL;
+          for (int r = 0; r < 4; ++r) {
+            if constexpr (DOTS) E[i][n][r] = gL * fmaf(static_cast<float>(L), S[i][n][r], E[i][n][r]);
+            S[i][n][r] *= gL;
+          }
     }
     uint4 zu[BF ? CH / 32 : 1][NTL];  // z as operands
     float zv[BF ? 1 : CH / 16][NTL][4];
@@ -731,6 +740,7 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
 #pragma unroll
       for (int bq = 0; bq < CH / 16; ++bq) {
         const f32x4 sw = *reinterpret_cast<const f32x4*>(fsw + 16 * bq + 4 * g);
+        const f32x4 se = DOTS ? *reinterpret_cast<const f32x4*>(fsw + CH + 16 * bq + 4 * g) : f4zero();
 #pragma unroll
         for (int n = 0; n < NTL; ++n) {
           const int c = column(n, lr);
@@ -749,7 +759,10 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
             const float yv = *reinterpret_cast<const float*>(
                 tile + M::Y + (row * PX + ((4 * i + (lr >> 2)) ^ key<PX>(row))) * 16 + (lr & 3) * 4);
 #pragma unroll
-            for (int n = 0; n < NTL; ++n) S[i][n] = mfma16f(yv, zv[bq][n][r] * sw[r], S[i][n]);
+            for (int n = 0; n < NTL; ++n) {
+              S[i][n] = mfma16f(yv, zv[bq][n][r] * sw[r], S[i][n]);
+              if constexpr (DOTS) E[i][n] = mfma16f(yv, zv[bq][n][r] * se[r], E[i][n]);
+            }
           }
       }
     }
@@ -824,11 +837,8 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
 
   // ---- the state behind the segment
   float* dst = nullptr;
-  const float* crs = nullptr;
   if constexpr (OUT) {
     if (wk.end && !prefix) dst = wk.end + bh * hs;  // (one segment)
-    if (wk.seg_cross) crs = wk.seg_cross + (static_cast<size_t>(sg) * BH + bh) * hs;
-    else if (wk.cross) crs = wk.cross + bh * hs;
   } else {
     if (wk.seg_native) {
       float* o = native_of(sg);
@@ -842,18 +852,6 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
     }
     if (wk.seg_steps && h == 0 && threadIdx.x == 0) wk.seg_steps[b * nseg + sg] = static_cast<float>(counted);
   }
-  float dot = 0.f;
-  if (crs) {
-    const rsrc_t rc = make_rsrc(crs, hbytes);
-#pragma unroll
-    for (int i = 0; i < KT; ++i)
-#pragma unroll
-      for (int n = 0; n < NTL; ++n) {
-        const uint32_t o = state_off(i, n);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) dot = fmaf(S[i][n][r], buf_f1(rc, o + 4u * static_cast<uint32_t>(r * sr)), dot);
-      }
-  }
   if (dst) store_state(dst);
   if constexpr (OUT && !DOTS) {
     if (prefix && wk.end && sg == 0) {  // the final state, by the walk that had no sums to add
@@ -862,11 +860,18 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
       store_state(wk.end + bh * hs);
     }
   }
-  if constexpr (OUT && !DOTS) {
-    if (wk.dots) {
-      dot = wave_sum(dot);
-      if (l == 0) wk.dots[(static_cast<size_t>(bh) * nseg + sg) * NW + w] = dot;
-    }
+  if constexpr (DOTS) {
+    const float* R = wk.seg_R ? wk.seg_R + (static_cast<size_t>(sg) * BH + bh) * hs : wk.R ? wk.R + bh * hs : nullptr;
+    const rsrc_t rc = make_rsrc(R, R ? hbytes : 0);
+#pragma unroll
+    for (int i = 0; i < KT; ++i)
+#pragma unroll
+      for (int n = 0; n < NTL; ++n) {
+        const float4 v = buf_f4(rc, state_off(i, n));  // (sr is 1 in these walks)
+        grad += static_cast<double>(fmaf(E[i][n][3], v.w, fmaf(E[i][n][2], v.z, fmaf(E[i][n][1], v.y, E[i][n][0] * v.x))));
+      }
+    grad = wave_sum_f64_dpp(grad);
+    if (l == 0) wk.grad[(static_cast<size_t>(bh) * nseg + sg) * NW + w] = grad;
   }
 }
 
@@ -878,7 +883,7 @@ hipError_t launch_nw(const DecayWalkArgs& a, hipStream_t st) {
   if (w.e.p) {
     if constexpr (sizeof(T) == 4) walk_kernel<T, KD, NW, NTL, true, true, 1, 3><<<grid, 64 * NW, 0, st>>>(a);
     else return hipErrorInvalidValue;  // (keys_kernel's)
-  } else if ((w.end && !w.seg_sum) || w.dots) walk_kernel<T, KD, NW, NTL, true, false, 1, 3><<<grid, 64 * NW, 0, st>>>(a);
+  } else if (w.end && !w.seg_sum) walk_kernel<T, KD, NW, NTL, true, false, 1, 3><<<grid, 64 * NW, 0, st>>>(a);
   else walk_kernel<T, KD, NW, NTL, true, false, 1, 2><<<grid, 64 * NW, 0, st>>>(a);
   return hipGetLastError();
 }
