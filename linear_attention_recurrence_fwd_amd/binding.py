@@ -658,8 +658,8 @@ def _token_stride(x, name):
     if (D > 1 and sd != 1) or (H > 1 and sh != D):
         raise ValueError("%s: the heads of a token must be contiguous" % name)
     st = st if T > 1 else sb if B > 1 else H * D
-    if B > 1 and T > 1 and sb != T * st:
-        raise ValueError("%s: tokens must be evenly spaced over batch and time" % name)
+    if st < H * D or (B > 1 and T > 1 and sb != T * st):
+        raise ValueError("%s: tokens must be evenly spaced over batch and time, without overlap" % name)
     return st
 
 

@@ -26,10 +26,11 @@ int check_dims(const gdn_dims* p, bool bwd, DecayDims* out) {
   if (bwd && p->algo == GDN_ALGO_SCAN) return GDN_ERR_UNSUPPORTED;
   if (p->Dk % 8 || p->Dv % 8 || p->Dk > 256 || p->Dv > 256) return GDN_ERR_UNSUPPORTED;
   // counts that the kernels hold in 32 bits: steps, heads, (b, h) pairs times
-  // their slices or segments (the tensors themselves are addressed in 64)
+  // their slices or segments, and the bytes of 64 steps' rows (the tensors
+  // themselves are addressed in 64)
   if (p->T > gdn::kDecayMaxT || p->Hv > INT_MAX / 1024 || p->B > INT_MAX / 1024 ||
       static_cast<double>(p->B) * p->Hv * gdn::kDecayMaxSeg * 2 > INT_MAX ||
-      static_cast<double>(p->B) * p->T * p->Hv > 9.0e12)
+      static_cast<double>(p->B) * p->T * p->Hv > 9.0e12 || p->Hv * (p->Dk > p->Dv ? p->Dk : p->Dv) > (1 << 22))
     return GDN_ERR_UNSUPPORTED;
   *out = DecayDims{static_cast<int>(p->B),  static_cast<int>(p->T),  static_cast<int>(p->Hk),
                    static_cast<int>(p->Hv), static_cast<int>(p->Dk), static_cast<int>(p->Dv)};

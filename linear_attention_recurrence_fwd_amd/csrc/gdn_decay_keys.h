@@ -368,6 +368,7 @@ __global__ void __launch_bounds__(256, KD <= 128 ? 2 : 1) keys_kernel(DecayKeysA
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         const int row = 16 * mt + lr;
+        if (masked && rev && !((live >> row) & 1)) acc[mt] = f4zero();  // a masked step's, whatever its factors are
         const uint32_t o = c < Dk ? (static_cast<uint32_t>(rev ? CH - 1 - row : row) * H * Dk + c) * es : kOff;
         if (es == 4) buf_store_u4(rw, o, __builtin_bit_cast(uint4, acc[mt]));
         else buf_store_u2(rw, o, pack4_bf16(acc[mt][0], acc[mt][1], acc[mt][2], acc[mt][3]));

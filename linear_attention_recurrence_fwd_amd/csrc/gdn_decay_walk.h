@@ -797,6 +797,13 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
     }
 
     if constexpr (OUT) {
+      if (masked && rev) {  // masked steps give zeros, whatever their factors are
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int n = 0; n < NTL; ++n)
+            if (!((live >> (16 * mt + lr)) & 1)) acc[mt][n] = f4zero();
+      }
       if (staged) {
         if constexpr (M::STAGE) {
 #pragma unroll

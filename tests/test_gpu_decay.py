@@ -163,7 +163,8 @@ def test_empty(algo):
 
 
 def bits(x):
-    return x.view(torch.uint8) if x.dtype == BF else x
+    """The stored bits (a NaN equals itself)."""
+    return x.view(torch.uint8)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
@@ -174,7 +175,7 @@ def test_carry_in_place_and_repeats(dtype):
     c = up(t)
     o, st = binding.decay_fwd(c["q"], c["k"], c["v"], c["lg"], c["state0"], c["mask"])
     o2, st2 = binding.decay_fwd(c["q"], c["k"], c["v"], c["lg"], c["state0"], c["mask"])
-    assert torch.equal(bits(o), bits(o2)) and torch.equal(st, st2)
+    assert torch.equal(bits(o), bits(o2)) and torch.equal(bits(st), bits(st2))
     s = c["state0"].clone()
     o3, s3 = binding.decay_fwd(c["q"], c["k"], c["v"], c["lg"], s, c["mask"], state_out=s)
     assert s3.data_ptr() == s.data_ptr() and torch.equal(s, st) and torch.equal(bits(o3), bits(o))
@@ -197,3 +198,157 @@ def test_carry_in_place_and_repeats(dtype):
     got = torch.cat(outs, 1).double().cpu()
     assert (got - ro).norm() <= R.NORM[dtype == BF] * ro.norm()
     assert (s.double().cpu() - rst).norm() <= R.NORM[False] * rst.norm()
+
+
+def test_infinite_cotangents_keep_masked_rows_zero():
+    """dO may hold anything: dk and dv of masked steps stay zero."""
+    for dtype in (BF, F32):
+        t = make(1, 70, 1, 2, 64, 64, dtype, 31, "some")
+        t["mask"][0, 10:60:3] = 1
+        t["dO"][0, 40] = float("inf")
+        c = up(t)
+        c["k"].nan_to_num_(0.0, 0.0, 0.0)
+        c["v"].nan_to_num_(0.0, 0.0, 0.0)
+        g = binding.decay_bwd(c["q"], c["k"], c["v"], c["lg"], c["state0"], c["mask"], c["dO"], c["dS"])
+        bad = c["mask"][0] == 0
+        assert (g["dk"][0, bad] == 0).all() and (g["dv"][0, bad] == 0).all()
+
+
+def test_untouched_memory():
+    """Rows behind a call's own output stay as they were (outputs in the middle of
+    a larger buffer, through the C entry)."""
+    import ctypes
+    for T, dtype in ((1, BF), (67, BF), (67, F32)):
+        t = up(make(1, T, 1, 2, 64, 40, dtype, 41))
+        d = binding.make_dims(1, T, 1, 2, 64, 40, dtype)
+        n = T * 2 * 40
+        buf = torch.full((n + 4096,), 7.0, dtype=dtype, device="cuda")
+        st = torch.full((2 * 64 * 40 + 4096,), 7.0, device="cuda")
+        wsb = binding._query("gdn_decay_fwd_workspace_bytes", d)
+        ws = torch.empty((max(wsb, 1),), dtype=torch.uint8, device="cuda")
+        o_at, s_at = buf[2048:], st[2048:]
+        rc = binding.lib().gdn_decay_fwd(
+            ctypes.byref(d), *[binding._p(t[x]) for x in ("q", "k", "v", "lg")], 1.0, binding._p(t["state0"]), None,
+            binding._p(o_at), binding._p(s_at), binding._p(ws), wsb, binding._stream(buf.device))
+        torch.cuda.synchronize()
+        assert rc == 0
+        assert (buf[:2048] == 7).all() and (buf[2048 + n:] == 7).all()
+        assert (st[:2048] == 7).all() and (st[2048 + 2 * 64 * 40:] == 7).all()
+
+
+def test_tensors_past_2_31_elements():
+    """v, o, dO and dv of 2.3e9 elements.  With a decay of zero every step stands
+    alone: o_t = scale (q_t . k_t) v_t, dv_t = scale (q_t . k_t) dO_t, dq_t = scale
+    (dO_t . v_t) k_t, so each row is checked by itself, within the bounds of two
+    roundings to bf16 (2^-8 each) and fp32 sums."""
+    T, Hv, Dk, Dv = 140_003, 128, 8, 128
+    assert T * Hv * Dv > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(3)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda", dtype=BF)  # noqa: E731
+    q, k, v, dO = r(1, T, 1, Dk), r(1, T, 1, Dk), r(1, T, Hv, Dv), r(1, T, Hv, Dv)
+    lg = torch.full((Hv,), float("-inf"), device="cuda")
+    say("[decay] T=%d Hv=%d: %d elements" % (T, Hv, T * Hv * Dv))
+    o, _ = binding.decay_fwd(q, k, v, lg, None, None, scale=1.0)
+    torch.cuda.synchronize()
+    qk = (q.float() * k.float()).sum(-1, keepdim=True)
+    tol = 2.0 ** -7 + 2.0 ** -16
+    for t0 in (0, 64 * 1000, 131_072, T - 200):
+        s = slice(t0, t0 + 200)
+        ref = qk[:, s] * v[:, s].float()
+        assert ((o[:, s].float() - ref).abs() <= tol * ref.abs() + 1e-30).all(), t0
+    del o
+    gr = binding.decay_bwd(q, k, v, lg, None, None, dO, scale=1.0)
+    torch.cuda.synchronize()
+    for t0 in (0, 64 * 1000, 131_072, T - 200):
+        s = slice(t0, t0 + 200)
+        ref = qk[:, s] * dO[:, s].float()
+        assert ((gr["dv"][:, s].float() - ref).abs() <= tol * ref.abs() + 1e-30).all(), t0
+        dot = (dO[:, s].float() * v[:, s].float()).sum(-1, keepdim=True)
+        ref, mag = (dot * k[:, s].float()).sum(2), (dot * k[:, s].float()).abs().sum(2)
+        assert ((gr["dq"][:, s, 0].float() - ref).abs() <= tol * mag).all(), t0
+
+
+def _mixer(B, T, dtype, seed):
+    """Inputs of a whole mixer: packed projection, norms, rotation, decay."""
+    g = torch.Generator().manual_seed(seed)
+    Hk, Hv, D = 2, 4, 64
+    rnd = lambda *s, dt=dtype: torch.randn(s, generator=g).to(dt)  # noqa: E731
+    return dict(qk=rnd(B, T, 2 * Hk * D), v=rnd(B, T, Hv, D), dO=rnd(B, T, Hv, D), wq=1 + 0.1 * rnd(D, dt=F32),
+                wk=1 + 0.1 * rnd(D, dt=F32), rope=binding.rope_table(512, 32, device="cpu"),
+                lg=-torch.exp2(-6.0 * torch.rand((Hv,), generator=g)), state0=rnd(B, Hv, D, D, dt=F32)), Hk, Hv, D
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_mixer_together(dtype):
+    """The norm with rotation on slices of a packed projection, then the decay
+    operator, and gradients through both, against the 64-bit chain.  bf16: q and
+    k are rounded between the two (2^-8 each, on top of the operator's own), so
+    the normwise bound is twice the operator's."""
+    B, T = 2, 150
+    t, Hk, Hv, D = _mixer(B, T, dtype, 77)
+    c = {n: x.cuda() for n, x in t.items()}
+    leaves = [c[n].requires_grad_(True) for n in ("qk", "v", "wq", "wk", "lg", "state0")]
+    q, k = (x.reshape(B, T, Hk, D) for x in c["qk"].split(Hk * D, -1))
+    q, k = c["qk"][..., : Hk * D].view(B, T, Hk, D), c["qk"][..., Hk * D:].view(B, T, Hk, D)
+    qn, kn = binding.NormRope.apply(q, k, c["wq"], c["wk"], c["rope"])
+    o, st = binding.DecayAttention.apply(qn, kn, c["v"], c["lg"], c["state0"])
+    got = torch.autograd.grad((o.float() * c["dO"].float()).sum() + st.sum(), leaves)
+    z = {n: f64(x).requires_grad_(True) for n, x in t.items() if n not in ("dO", "rope")}
+    q64, k64 = R.norm_rope(z["qk"][..., : Hk * D].reshape(B, T, Hk, D), z["qk"][..., Hk * D:].reshape(B, T, Hk, D),
+                           z["wq"], z["wk"], f64(t["rope"]), None)
+    ro, rst = R.decay(q64, k64, z["v"], z["lg"], z["state0"])
+    ref = torch.autograd.grad((ro * f64(t["dO"])).sum() + rst.sum(), [z[n] for n in ("qk", "v", "wq", "wk", "lg", "state0")])
+    for n, a, b in [("o", o, ro), ("state", st, rst)] + list(zip(("qk", "v", "wq", "wk", "lg", "state0"), got, ref)):
+        e = ((a.detach().double().cpu() - b.detach()).norm() / b.detach().norm()).item()
+        say("[mixer] %s %s %.1e" % (dtype, n, e))
+        assert e <= 2 * R.NORM[dtype == BF], (n, e)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_graph_stream_and_two_at_once(dtype):
+    """Captured into a graph on a side stream and replayed on changed inputs, with
+    eager work between the replays; and calls on two streams at a time: the same
+    bits as eager calls."""
+    t = up(make(2, 300, 2, 4, 64, 64, dtype, 51, "behind"))
+    u = up(make(2, 300, 2, 4, 64, 64, dtype, 52, "behind"))
+    args = lambda x: (x["q"], x["k"], x["v"], x["lg"], x["state0"], x["mask"])  # noqa: E731
+
+    def work(x):
+        o, st = binding.decay_fwd(*args(x))
+        g = binding.decay_bwd(*args(x), x["dO"], x["dS"])
+        q1 = x["q"][:, :1].contiguous()
+        o1, st1 = binding.decay_fwd(q1, x["k"][:, :1].contiguous(), x["v"][:, :1].contiguous(), x["lg"], st, None)
+        nq, nk = binding.norm_rope(x["q"], x["q"], w, w, rope)
+        n = binding.norm_rope_bwd(x["q"], x["q"], w, w, rope, None, x["q"], x["q"])
+        return [o, st, o1, st1, nq, nk] + [g[i] for i in sorted(g)] + [n[i] for i in sorted(n)]
+    w = torch.ones((64,), device="cuda")
+    rope = binding.rope_table(300, 64)
+    want_t, want_u = [x.clone() for x in work(t)], [x.clone() for x in work(u)]
+    torch.cuda.synchronize()
+    # two streams at a time
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(3):
+        with torch.cuda.stream(s1):
+            a = work(t)
+        with torch.cuda.stream(s2):
+            b = work(u)
+        got.append((a, b))
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert all(torch.equal(bits(x), bits(y)) for x, y in zip(a, want_t))
+        assert all(torch.equal(bits(x), bits(y)) for x, y in zip(b, want_u))
+    # a graph, replayed on other inputs
+    buf = {n: None if x is None else x.clone() for n, x in t.items()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = work(buf)
+    for src, want in ((t, want_t), (u, want_u), (t, want_t), (u, want_u)):
+        for n in buf:
+            if buf[n] is not None:
+                buf[n].copy_(src[n])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(bits(x), bits(y)) for x, y in zip(out, want))
+        work(t)  # eager work between the replays
+        torch.cuda.synchronize()
