@@ -306,7 +306,7 @@ int gdn_bwd_vg(const gdn_dims* d, const void* q, const void* k, const void* v, c
  *                           run in parallel: their state sums, a chain over
  *                           them, then their outputs (one pass where one
  *                           segment is best)
- *               AUTO        SCAN for single steps, else CHUNK_TPAR
+ *               AUTO        SCAN for calls of a few steps (T <= 4), else CHUNK_TPAR
  *             bf16 tensors are multiplied by bf16 matrix products with fp32
  *             sums (the state keeps fp32 precision), fp32 ones by fp32
  *             products.

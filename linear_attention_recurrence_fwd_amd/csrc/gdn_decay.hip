@@ -145,9 +145,38 @@ __global__ void __launch_bounds__(256) group_kernel(DecayGroupArgs a, size_t n) 
 }
 
 // ---- single steps, S <- g S + k v^T, o = scale S^T q, T of them in turn.  The
-// state is the whole traffic of a single step, read and written once.  One
-// wave per 32 columns of one (b, h): lane 8 rg + cq holds rows rg RL .. + RL - 1 of
-// columns 4 cq .. + 3, so eight lanes cover 128 contiguous bytes of a row.
+// state is the whole traffic of a single step, read and written once (64 sequences
+// of 32 heads of 128 x 128: 268 MB in 45 us, 5.9 TB/s, part of it still cached).  One wave per 32 columns of
+// one (b, h): lane 8 rg + cq holds rows rg RL .. + RL - 1 of columns 4 cq .. + 3,
+// so eight lanes cover 128 contiguous bytes of a row.  The next step's q, k and v
+// are asked for ahead of the step's own sums.
+
+// N consecutive values (from a place that can be read); zeros where in is false.
+template <typename T, int N> __device__ __forceinline__ void load_row(const T* p, bool in, float* out) {
+  constexpr int B = N * static_cast<int>(sizeof(T));
+  if constexpr (B >= 16) {
+    constexpr int E = Vec16<T>::N;
+#pragma unroll
+    for (int i = 0; i < N / E; ++i) Vec16<T>::unpack(reinterpret_cast<const uint4*>(p)[i], out + i * E);
+  } else {
+    uint32_t u[B / 4];
+    if constexpr (B == 8) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      u[0] = v.x;
+      u[1] = v.y;
+    } else {
+      u[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if constexpr (sizeof(T) == 4) out[i] = __uint_as_float(u[i]);
+      else out[i] = __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) out[i] = in ? out[i] : 0.f;
+}
+
 template <typename T, int DK>
 __global__ void __launch_bounds__(64) step_kernel(DecayStepArgs p, int slices) {
   constexpr int RL = DK / 8;
@@ -156,47 +185,66 @@ __global__ void __launch_bounds__(64) step_kernel(DecayStepArgs p, int slices) {
   const int l = threadIdx.x, rg = l >> 3, cq = l & 7, col = 32 * w + 4 * cq;
   const size_t hs = static_cast<size_t>(d.Dk) * d.Dv;
   const uint32_t bytes = static_cast<uint32_t>(hs * 4);
-  // rows past Dk lie past the descriptor's size; columns past Dv are sent there
+  // Dk and Dv are multiples of 8, so P rows of a lane, and its columns, are all
+  // there or none.  State entries that are not there are sent past the descriptor's
+  // size; the values of q, k and v are read from the head's start and dropped.
+  constexpr int P = RL < 8 ? RL : 8;
+  const bool on = col < d.Dv;
   uint32_t off[RL];
 #pragma unroll
   for (int r = 0; r < RL; ++r)
-    off[r] = col < d.Dv && rg * RL + r < d.Dk ? 4u * ((rg * RL + r) * d.Dv + col) : 0xfffffff0u;
+    off[r] = on && rg * RL + r < d.Dk ? 4u * ((rg * RL + r) * d.Dv + col) : 0xfffffff0u;
   const rsrc_t rs0 = make_rsrc(p.state0 ? static_cast<const void*>(p.state0 + bh * hs) : p.state_out, p.state0 ? bytes : 0);
   float4 s[RL];
 #pragma unroll
   for (int r = 0; r < RL; ++r) s[r] = buf_f4(rs0, off[r]);
   const float gate = exp2_fast(log2_decay(p.lg[h]));
+  const size_t qs = static_cast<size_t>(d.Hk) * d.Dk, vs = static_cast<size_t>(d.Hv) * d.Dv;
+  const size_t bt0 = static_cast<size_t>(b) * d.T;
+  const T* qr = static_cast<const T*>(p.q) + bt0 * qs + static_cast<size_t>(j) * d.Dk;
+  const T* kr = static_cast<const T*>(p.k) + bt0 * qs + static_cast<size_t>(j) * d.Dk;
+  const T* vr = static_cast<const T*>(p.v) + bt0 * vs + static_cast<size_t>(h) * d.Dv + (on ? col : 0);
+  float q[RL], k[RL], v[4];
+  int live = 1;
+  auto load = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < RL; i += P) {
+      const bool in = rg * RL + i < d.Dk;
+      const int at = in ? rg * RL + i : 0;
+      load_row<T, P>(qr + t * qs + at, in, q + i);
+      load_row<T, P>(kr + t * qs + at, in, k + i);
+    }
+    load_row<T, 4>(vr + t * vs, on, v);
+    live = p.mask == nullptr ? 1 : p.mask[bt0 + t];
+  };
+  if (d.T > 0) load(0);
   for (int t = 0; t < d.T; ++t) {
-    const size_t bt = static_cast<size_t>(b) * d.T + t;
-    const T* qr = static_cast<const T*>(p.q) + (bt * d.Hk + j) * d.Dk;
-    const T* kr = static_cast<const T*>(p.k) + (bt * d.Hk + j) * d.Dk;
-    const T* vr = static_cast<const T*>(p.v) + (bt * d.Hv + h) * d.Dv + col;
-    const bool on = col < d.Dv;
-    float q[RL], k[RL], v[4];
+    float qt[RL], kt[RL], vt[4];
 #pragma unroll
     for (int r = 0; r < RL; ++r) {
-      const bool in = rg * RL + r < d.Dk;
-      q[r] = in ? to_f32(qr[rg * RL + r]) * p.scale : 0.f;
-      k[r] = in ? to_f32(kr[rg * RL + r]) : 0.f;
+      qt[r] = q[r] * p.scale;
+      kt[r] = k[r];
     }
 #pragma unroll
-    for (int c = 0; c < 4; ++c) v[c] = on ? to_f32(vr[c]) : 0.f;
-    if (p.mask == nullptr || p.mask[bt] != 0) {
+    for (int c = 0; c < 4; ++c) vt[c] = v[c];
+    const bool valid = live != 0;
+    if (t + 1 < d.T) load(t + 1);
+    if (valid) {
 #pragma unroll
       for (int r = 0; r < RL; ++r) {
-        s[r].x = fmaf(k[r], v[0], gate * s[r].x);
-        s[r].y = fmaf(k[r], v[1], gate * s[r].y);
-        s[r].z = fmaf(k[r], v[2], gate * s[r].z);
-        s[r].w = fmaf(k[r], v[3], gate * s[r].w);
+        s[r].x = fmaf(kt[r], vt[0], gate * s[r].x);
+        s[r].y = fmaf(kt[r], vt[1], gate * s[r].y);
+        s[r].z = fmaf(kt[r], vt[2], gate * s[r].z);
+        s[r].w = fmaf(kt[r], vt[3], gate * s[r].w);
       }
     }
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int r = 0; r < RL; ++r) {
-      o.x = fmaf(q[r], s[r].x, o.x);
-      o.y = fmaf(q[r], s[r].y, o.y);
-      o.z = fmaf(q[r], s[r].z, o.z);
-      o.w = fmaf(q[r], s[r].w, o.w);
+      o.x = fmaf(qt[r], s[r].x, o.x);
+      o.y = fmaf(qt[r], s[r].y, o.y);
+      o.z = fmaf(qt[r], s[r].z, o.z);
+      o.w = fmaf(qt[r], s[r].w, o.w);
     }
 #pragma unroll
     for (int m = 8; m <= 32; m <<= 1) {
@@ -206,7 +254,7 @@ __global__ void __launch_bounds__(64) step_kernel(DecayStepArgs p, int slices) {
       o.w += __shfl_xor(o.w, m);
     }
     if (rg == 0 && on) {
-      T* orow = static_cast<T*>(p.o) + (bt * d.Hv + h) * d.Dv + col;
+      T* orow = static_cast<T*>(p.o) + (bt0 + t) * vs + static_cast<size_t>(h) * d.Dv + col;
       if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(orow) = pack4_bf16(o.x, o.y, o.z, o.w);
       else *reinterpret_cast<float4*>(orow) = o;
     }

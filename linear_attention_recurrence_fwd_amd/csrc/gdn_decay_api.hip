@@ -37,7 +37,17 @@ int check_dims(const gdn_dims* p, bool bwd, DecayDims* out) {
   return GDN_OK;
 }
 
-bool use_step(const gdn_dims* p) { return p->algo == GDN_ALGO_SCAN || (p->algo == GDN_ALGO_AUTO && p->T == 1); }
+// Calls of a few steps take the steps in turn.  us in turn / by chunks, in a graph:
+//   heads                        T = 1        T = 4        T = 6        T = 8
+//   1 x 32, 128 x 128, bf16   4.2 /  8.6   6.2 /  8.7   7.8 /  8.6   9.5 /  8.6
+//   64 x 32, 128 x 128, bf16 43.8 / 70.8  51.0 / 73.3  56.3 / 75.4  62.2 / 77.2
+//   8 x 8, 64 x 32, bf16      3.2 /  6.2   4.8 /  6.2   5.9 /  6.2   7.0 /  6.3
+//   4 x 64, 192 x 128, bf16  10.1 / 15.6  14.1 / 15.6  16.9 / 15.6  19.4 / 15.9
+//   1 x 32, 128 x 128, fp32   3.8 / 11.2   5.9 / 11.2   7.5 / 11.3   9.1 / 11.3
+constexpr int kFewSteps = 4;
+bool use_step(const gdn_dims* p) {
+  return p->algo == GDN_ALGO_SCAN || (p->algo == GDN_ALGO_AUTO && p->T <= kFewSteps);
+}
 
 // Segments up to which the forward's walks add up the sums before them themselves.
 constexpr int kPrefixSegments = 8;

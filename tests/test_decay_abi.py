@@ -36,6 +36,7 @@ def test_decay_bad_dims(dims, code):
 def test_decay_sizes():
     for dt in (B.GDN_F32, B.GDN_BF16):
         assert size("gdn_decay_fwd_workspace_bytes", B.make_dims(3, 1, 2, 4, 64, 40, dt)) == (0, 0)  # a single step
+        assert size("gdn_decay_fwd_workspace_bytes", B.make_dims(3, 4, 2, 4, 64, 40, dt)) == (0, 0)  # a few
         assert size("gdn_decay_fwd_workspace_bytes", B.make_dims(3, 500, 2, 4, 64, 40, dt, B.ALGO_CHUNK)) == (0, 0)
         assert size("gdn_decay_fwd_workspace_bytes", B.make_dims(3, 500, 2, 4, 64, 40, dt, B.ALGO_SCAN)) == (0, 0)
         n = size("gdn_decay_fwd_workspace_bytes", B.make_dims(1, 32768, 2, 4, 128, 128, dt))

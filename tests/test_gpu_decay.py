@@ -147,6 +147,25 @@ def test_decays(lg):
     run_both(t, tag="lg %g" % lg)
 
 
+@pytest.mark.parametrize("T", [1, 2, 4, 5])
+@pytest.mark.parametrize("Dk,Dv", [(8, 8), (16, 40), (24, 96), (40, 8), (64, 32), (72, 136), (128, 128), (136, 24), (200, 64),
+                                   (248, 256), (256, 200)])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_few_steps(dtype, Dk, Dv, T):
+    """Calls of a few steps and the first length behind them, at every class of head."""
+    say("[decay few] dtype=%s Dk=%d Dv=%d T=%d" % (dtype, Dk, Dv, T))
+    run_both(make(3, T, 2, 6, Dk, Dv, dtype, Dk + Dv + T, "some"), bwd=False, tag="few %d %d %d" % (Dk, Dv, T))
+
+
+@pytest.mark.parametrize("G", [3, 4, 6, 8])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T", [100, 1300])
+def test_groups(T, dtype, G):
+    """Value heads that share a key head: their gradients are summed, in twos and one by one."""
+    say("[decay groups] dtype=%s G=%d T=%d" % (dtype, G, T))
+    run_both(make(2, T, 2, 2 * G, 64, 72, dtype, 17 * G + T, "behind"), tag="G %d T %d" % (G, T))
+
+
 def test_no_state_and_scale():
     run_both(make(2, 100, 2, 2, 64, 64, BF, 5, state=False), tag="no state")
     run_both(make(1, 100, 1, 2, 64, 64, F32, 6), scale=-2.5, tag="scale")
