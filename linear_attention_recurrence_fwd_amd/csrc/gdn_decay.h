@@ -36,8 +36,7 @@ struct DecayRows {
 //   dv: x = k,  y = q,  z = dO, backward in time, start dS_final
 struct DecayWalk {
   DecayRows x, y, z, e;   // e: what the outputs are dotted with (dlg), [.., N]
-  void* w;                // [B, T, Hv, N]
-  int w32;                // w holds fp32 (partial rows of grouped heads)
+  void* w;                // [B, T, Hv, N], of the tensors' type
   int KD, N;              // channels and columns
   int reverse;            // backward in time
   float scale_p;          // on the products x . y
@@ -107,7 +106,7 @@ struct DecayChainArgs {
   int nseg;
   float* states;            // [nseg, B*Hv, Dk*Dv]: segment sums in, start states out
   const float* start;       // may be null
-  float* end;               // state behind the last segment walked (may alias start)
+  float* end;               // state behind the last segment walked (may alias start; null: not written)
   int reverse;
 };
 

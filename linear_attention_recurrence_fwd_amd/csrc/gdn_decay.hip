@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(64) chain_kernel(ChainArgs aa) {
       }
     }
   }
-  *reinterpret_cast<float4*>(a.end + bh * hs + e) = run;
+  if (a.end) *reinterpret_cast<float4*>(a.end + bh * hs + e) = run;
 }
 
 // ---- dlg of one head: its parts summed in a fixed order.
@@ -146,10 +146,12 @@ __global__ void __launch_bounds__(256) group_kernel(DecayGroupArgs a, size_t n) 
 
 // ---- single steps, S <- g S + k v^T, o = scale S^T q, T of them in turn.  The
 // state is the whole traffic of a single step, read and written once (64 sequences
-// of 32 heads of 128 x 128: 268 MB in 45 us, 5.9 TB/s, part of it still cached).  One wave per 32 columns of
-// one (b, h): lane 8 rg + cq holds rows rg RL .. + RL - 1 of columns 4 cq .. + 3,
-// so eight lanes cover 128 contiguous bytes of a row.  The next step's q, k and v
-// are asked for ahead of the step's own sums.
+// of 32 heads of 128 x 128: 268 MB in 45 us, 5.9 TB/s, part of it still cached;
+// one of them: 4 MB in 4 us, a launch and two trips to memory).  One wave per 32
+// columns of one (b, h): lane 8 rg + cq holds rows rg RL .. + RL - 1 of columns 4 cq
+// .. + 3, so eight lanes cover 128 contiguous bytes of a row.  The next step's q, k
+// and v are asked for ahead of the step's own sums, as whole pieces of a row (element
+// by element the 64 sequences take 56 us).
 
 // N consecutive values (from a place that can be read); zeros where in is false.
 template <typename T, int N> __device__ __forceinline__ void load_row(const T* p, bool in, float* out) {

@@ -87,7 +87,6 @@ Cut cut(const gdn_dims* p, const DecayDims& d, bool bwd) {
 struct Layout {
   size_t S, R;            // segment states, forward and backward in time
   size_t steps;           // valid steps of the segments
-  size_t end;             // the backward's recomputed final state (not read)
   size_t grad;            // parts of dlg
   size_t pq, pk;          // rows of grouped heads
   size_t total;
@@ -120,10 +119,7 @@ Layout layout(const gdn_dims* p, const DecayDims& d, bool bwd) {
     L.steps = take(static_cast<size_t>(d.B) * c.n);
   }
   if (bwd) {
-    if (c.n > 1) {
-      L.R = take(states);
-      L.end = take(bh * d.Dk * d.Dv);
-    }
+    if (c.n > 1) L.R = take(states);
     L.grad = take(2 * bh * c.n * key_waves(p, d));  // fp64
     const size_t rows = static_cast<size_t>(d.B) * d.T * d.Hk * d.Dk;
     const int nq = key_parts(p, d, true), nk = key_parts(p, d, false);
@@ -136,9 +132,6 @@ Layout layout(const gdn_dims* p, const DecayDims& d, bool bwd) {
 
 template <typename P> P* at(void* ws, size_t off) { return reinterpret_cast<P*>(static_cast<char*>(ws) + off); }
 
-struct Rows {
-  gdn::DecayRows key, val;
-};
 gdn::DecayRows key_rows(const DecayDims& d, const void* p) { return gdn::DecayRows{p, d.Hk, d.Dk, d.G()}; }
 gdn::DecayRows val_rows(const DecayDims& d, const void* p) { return gdn::DecayRows{p, d.Hv, d.Dv, 1}; }
 
@@ -312,7 +305,7 @@ int gdn_decay_bwd(const gdn_dims* d, const void* q, const void* k, const void* v
     ur.seg_sum = R;
     const gdn::DecayWalkArgs sum{dd, lg, mask, c.n, c.seg, 2, {us, ur}};
     if (gdn::launch_decay_walk(sum, true, bf, st) != hipSuccess) return GDN_ERR_HIP;
-    const gdn::DecayChainArgs ch[2] = {{dd, lg, steps, c.n, S, state0, at<float>(ws, L.end), 0},
+    const gdn::DecayChainArgs ch[2] = {{dd, lg, steps, c.n, S, state0, nullptr, 0},
                                        {dd, lg, steps, c.n, R, dS_final, dstate, 1}};
     if (gdn::launch_decay_chain(ch, 2, st) != hipSuccess) return GDN_ERR_HIP;
     wv.seg_start = R;

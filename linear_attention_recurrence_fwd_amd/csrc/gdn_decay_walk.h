@@ -20,10 +20,10 @@
 //     bits) where only bf16 results are read from this state;
 //   - the state against x: one bf16 part, as the result is rounded to bf16 (a
 //     relative error of at most 2^-8 for each product, independent between the
-//     products); three parts where the result also enters the sums for dlg;
+//     products);
 //   - P: one bf16 part, as the result is rounded to bf16.
 //
-// dlg (DOTS; the dq walk, whose e is q).  The loss's derivative in lg, taken
+// dlg (DOTS; the fp32 dq walk, whose e is q).  The loss's derivative in lg, taken
 // forward: beside the state goes its derivative since the segment's start, E = dS /
 // d lg,
 //   E <- g^L (E + L S) + sum_j y_j ((L - c_j) g^(L - c_j) z_j)^T,
@@ -175,12 +175,12 @@ template <int CH, int PPR, int EPP, int NW> struct Loader {
   }
 };
 
-// SPS: bf16 parts of the state in the products with x; SPU: of the weighted z
-// that the state sums.
-template <typename T, int KD, int NW, int NTL, bool OUT, bool DOTS, int SPS, int SPU>
+// SPU: bf16 parts of the weighted z that the state sums.
+template <typename T, int KD, int NW, int NTL, bool OUT, bool DOTS, int SPU>
 __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
   using M = Lds<T, KD, NW, NTL, OUT, DOTS>;
   constexpr bool BF = sizeof(T) == 2;
+  static_assert(!(BF && DOTS), "bf16 dq rows come from keys_kernel");
   constexpr int CH = M::CH, EPP = M::EPP, PX = M::PX, PZ = M::PZ, PP = M::PP, MT = CH / 16, KT = KD / 16;
   __shared__ __attribute__((aligned(16))) char sm[M::TOTAL];
   const int Hv = a.d.Hv, Tn = a.d.T, BH = a.d.B * Hv, nseg = a.nseg, n_items = BH * nseg;
@@ -362,14 +362,14 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
   };
   // results of a chunk: rows behind the sequence and columns past N lie past the
   // descriptor
-  auto out_rows = [&](int t0, int es) {
+  constexpr int es = sizeof(T);
+  auto out_rows = [&](int t0) {
     return make_rsrc(static_cast<char*>(wk.w) + ((bT + t0) * Hv + h) * N * es,
                      (static_cast<size_t>(min(Tn - t0, CH) - 1) * Hv * N + N) * es);
   };
-  const bool staged = M::STAGE && !wk.w32;
   auto store_staged = [&](int ci) {
     if constexpr (M::STAGE) {
-      const rsrc_t rw = out_rows(chunk_start(ci), 2);
+      const rsrc_t rw = out_rows(chunk_start(ci));
       constexpr int NS = CH * PZ / 64;
 #pragma unroll
       for (int k = 0; k < (NS + NW - 1) / NW; ++k) {
@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
     counted += L;
     // this wave's part of the tiles has arrived (what it stored after asking for
     // them, MT stores at least, may be on the way still)
-    if (OUT && M::SLOTS == 2 && !staged && ci > 0) wait_vm<MT>();
+    if (OUT && M::SLOTS == 2 && !M::STAGE && ci > 0) wait_vm<MT>();
     else wait_vm<0>();
     lds_barrier();
     if (more) {
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
       if constexpr (SPREAD)
         if (k < NY) dma16_ahead(dnx, next_xe + M::X + (k * NW + w) * 1024, onx[k < NY ? k : 0]);
     };
-    if (staged && ci > 0) store_staged(ci - 1);
+    if (M::STAGE && ci > 0) store_staged(ci - 1);
 
     f32x4 acc[MT][NTL];
     if constexpr (OUT) {
@@ -530,14 +530,6 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
             const bf16x8 xa = load_bf16x8(px + at_x(0, ks));
 #pragma unroll
             for (int q = 0; q < TW; ++q) pt[q] = mfma16(load_bf16x8(py + at_x(q, ks)), xa, pt[q]);
-          }
-          if constexpr (DOTS) {
-#pragma unroll
-            for (int ks = 0; ks < M::COLS / 32; ++ks) {
-              const bf16x8 ea = load_bf16x8(pe + at_z(0, ks));
-#pragma unroll
-              for (int q = 0; q < TW; ++q) pu[q] = mfma16(load_bf16x8(pz + at_z(q, ks)), ea, pu[q]);
-            }
           }
         } else {
 #pragma unroll
@@ -585,7 +577,7 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
       // Where there is a wave for every run, P's products go ahead of those with
       // the state and the rest of its making behind them, in one stretch of code
       // (a wave without a run repeats the last one's products).
-      constexpr bool ONE = BF && NW >= RUNS && !DOTS;
+      constexpr bool ONE = BF && NW >= RUNS;
       if constexpr (ONE) {
         p_products(min(w, RUNS - 1));
       } else {
@@ -621,12 +613,10 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
               v[r] = S[2 * ks][n][r];
               v[4 + r] = S[2 * ks + 1][n][r];
             }
-            bf16x8 part[SPS];
-            split8<SPS>(v, part);
+            bf16x8 part[1];
+            split8<1>(v, part);
 #pragma unroll
-            for (int s = 0; s < SPS; ++s)
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) acc[mt][n] = mfma16(part[s], xa[mt], acc[mt][n]);
+            for (int mt = 0; mt < MT; ++mt) acc[mt][n] = mfma16(part[0], xa[mt], acc[mt][n]);
           }
         }
       } else {
@@ -804,20 +794,17 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
           for (int n = 0; n < NTL; ++n)
             if (!((live >> (16 * mt + lr)) & 1)) acc[mt][n] = f4zero();
       }
-      if (staged) {
-        if constexpr (M::STAGE) {
+      if constexpr (M::STAGE) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int n = 0; n < NTL; ++n) {
-              const int c = column(n, 4 * g), row = 16 * mt + lr;
-              *reinterpret_cast<uint2*>(sm + M::O + (row * PZ + ((c >> 3) ^ key<PZ>(lr))) * 16 + (c & 4) * 2) =
-                  pack4_bf16(acc[mt][n][0], acc[mt][n][1], acc[mt][n][2], acc[mt][n][3]);
-            }
-        }
+          for (int n = 0; n < NTL; ++n) {
+            const int c = column(n, 4 * g), row = 16 * mt + lr;
+            *reinterpret_cast<uint2*>(sm + M::O + (row * PZ + ((c >> 3) ^ key<PZ>(lr))) * 16 + (c & 4) * 2) =
+                pack4_bf16(acc[mt][n][0], acc[mt][n][1], acc[mt][n][2], acc[mt][n][3]);
+          }
       } else {
-        const bool wide = !BF || wk.w32;
-        const rsrc_t rw = out_rows(t0, wide ? 4 : 2);
+        const rsrc_t rw = out_rows(t0);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           const int row = 16 * mt + lr;
@@ -825,7 +812,7 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
 #pragma unroll
           for (int n = 0; n < NTL; ++n) {
             const int c = column(n, 4 * g);
-            if (wide) buf_store_u4(rw, c < N ? (ro + c) * 4u : kOff, __builtin_bit_cast(uint4, acc[mt][n]));
+            if constexpr (!BF) buf_store_u4(rw, c < N ? (ro + c) * 4u : kOff, __builtin_bit_cast(uint4, acc[mt][n]));
             else
               buf_store_u2(rw, c < N ? (ro + c) * 2u : kOff,
                            pack4_bf16(acc[mt][n][0], acc[mt][n][1], acc[mt][n][2], acc[mt][n][3]));
@@ -836,7 +823,7 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
     live = live_next;
   }
 
-  if (staged && nch > 0) {
+  if (M::STAGE && nch > 0) {
     lds_barrier();
     store_staged(nch - 1);
   }
@@ -888,10 +875,10 @@ hipError_t launch_nw(const DecayWalkArgs& a, hipStream_t st) {
   const dim3 grid((n + 7) / 8 * 8, a.nwalk);
   const DecayWalk& w = a.walk[0];
   if (w.e.p) {
-    if constexpr (sizeof(T) == 4) walk_kernel<T, KD, NW, NTL, true, true, 1, 3><<<grid, 64 * NW, 0, st>>>(a);
+    if constexpr (sizeof(T) == 4) walk_kernel<T, KD, NW, NTL, true, true, 3><<<grid, 64 * NW, 0, st>>>(a);
     else return hipErrorInvalidValue;  // (keys_kernel's)
-  } else if (w.end && !w.seg_sum) walk_kernel<T, KD, NW, NTL, true, false, 1, 3><<<grid, 64 * NW, 0, st>>>(a);
-  else walk_kernel<T, KD, NW, NTL, true, false, 1, 2><<<grid, 64 * NW, 0, st>>>(a);
+  } else if (w.end && !w.seg_sum) walk_kernel<T, KD, NW, NTL, true, false, 3><<<grid, 64 * NW, 0, st>>>(a);
+  else walk_kernel<T, KD, NW, NTL, true, false, 2><<<grid, 64 * NW, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -907,7 +894,7 @@ template <typename T, int KD> hipError_t launch_sum_kd(const DecayWalkArgs& a, h
   const int n = a.d.B * a.d.Hv * a.nseg, N = a.walk[0].N;
   const dim3 grid((n + 7) / 8 * 8, a.nwalk);
   auto go = [&](auto nw, auto ntl) {
-    walk_kernel<T, KD, decltype(nw)::v, decltype(ntl)::v, false, false, 1, 3><<<grid, 64 * decltype(nw)::v, 0, st>>>(a);
+    walk_kernel<T, KD, decltype(nw)::v, decltype(ntl)::v, false, false, 3><<<grid, 64 * decltype(nw)::v, 0, st>>>(a);
   };
   if (N <= 64) go(Int<4>{}, Int<1>{});
   else if (N <= 128) go(Int<8>{}, Int<1>{});

@@ -184,7 +184,6 @@ __global__ void __launch_bounds__(256) fwd_kernel(NormRopeArgs a, Work wk) {
     const int H = part ? a.Hk : a.Hq, base = part ? wk.gq : 0;
     const T* src = static_cast<const T*>(part ? a.k : a.q) + token * (part ? a.ks : a.qs);
     T* dst = static_cast<T*>(part ? a.ok : a.oq) + token * H * a.D;
-#pragma unroll 4
     for (int g = lo; g < hi; ++g) {
       const int head = (g - base) * RPW + sub_row;
       const bool on = ln.on && head < H;
@@ -240,7 +239,6 @@ __global__ void __launch_bounds__(256) bwd_kernel(NormRopeArgs a, Work wk) {
       const T* src = static_cast<const T*>(part ? a.k : a.q) + token * (part ? a.ks : a.qs);
       const T* dyp = static_cast<const T*>(part ? a.dyk : a.dyq) + token * H * a.D;
       T* dst = static_cast<T*>(part ? a.ok : a.oq) + token * H * a.D;
-#pragma unroll 2
       for (int g = lo; g < hi; ++g) {
         const int head = (g - base) * RPW + sub_row;
         const bool on = ln.on && head < H;
