@@ -340,9 +340,8 @@ int gdn_decay_bwd(const gdn_dims* d, const void* q, const void* k, const void* v
     wk.scale_i = 1.f;
     wk.start = dS_final;
     wk.seg_start = R;
-    const gdn::DecayWalkArgs aq{dd, lg, mask, c.n, c.seg, 1, {wq, wq}}, ak{dd, lg, mask, c.n, c.seg, 1, {wk, wk}};
-    if (gdn::launch_decay_walk(aq, false, false, st) != hipSuccess) return GDN_ERR_HIP;
-    if (gdn::launch_decay_walk(ak, false, false, st) != hipSuccess) return GDN_ERR_HIP;
+    const gdn::DecayWalkArgs aqk{dd, lg, mask, c.n, c.seg, 2, {wq, wk}};
+    if (gdn::launch_decay_walk(aqk, false, false, st) != hipSuccess) return GDN_ERR_HIP;
   }
   if ((nq > 1 || nk > 1) && dd.T > 0) {
     const gdn::DecayGroupArgs ga{dd, {nq, nk}, pq, pk, dq, dk};

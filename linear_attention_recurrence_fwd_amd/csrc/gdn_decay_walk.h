@@ -175,18 +175,16 @@ template <int CH, int PPR, int EPP, int NW> struct Loader {
   }
 };
 
-// SPU: bf16 parts of the weighted z that the state sums.
+// Workgroup `block` of walk wk; SPU: bf16 parts of the weighted z that the state sums.
 template <typename T, int KD, int NW, int NTL, bool OUT, bool DOTS, int SPU>
-__global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
+__device__ __forceinline__ void walk(const DecayWalkArgs& a, const DecayWalk& wk, int block, char* sm) {
   using M = Lds<T, KD, NW, NTL, OUT, DOTS>;
   constexpr bool BF = sizeof(T) == 2;
   static_assert(!(BF && DOTS), "bf16 dq rows come from keys_kernel");
   constexpr int CH = M::CH, EPP = M::EPP, PX = M::PX, PZ = M::PZ, PP = M::PP, MT = CH / 16, KT = KD / 16;
-  __shared__ __attribute__((aligned(16))) char sm[M::TOTAL];
   const int Hv = a.d.Hv, Tn = a.d.T, BH = a.d.B * Hv, nseg = a.nseg, n_items = BH * nseg;
-  const int it = xcd_order(blockIdx.x, n_items);
+  const int it = xcd_order(block, n_items);
   if (it >= n_items) return;
-  const DecayWalk& wk = a.walk[blockIdx.y];
   // value heads fastest: the heads of a group run side by side
   const int h = it % Hv, sg = (it / Hv) % nseg, b = it / (Hv * nseg), bh = b * Hv + h;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, lr = l & 15, g = l >> 4;
@@ -869,16 +867,34 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
   }
 }
 
+template <typename T, int KD, int NW, int NTL, bool OUT, int SPU>
+__global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
+  __shared__ __attribute__((aligned(16))) char sm[Lds<T, KD, NW, NTL, OUT, false>::TOTAL];
+  walk<T, KD, NW, NTL, OUT, false, SPU>(a, a.walk[blockIdx.y], blockIdx.x, sm);
+}
+
+// dq (walk 0) and dk of fp32 tensors in one launch, dq's longer walks first: a few
+// heads' walks fill a part of the chip each (at 72 (b, h) and segments of 64 x 128
+// heads 26 us, one after the other 20 + 15 us).
+template <int KD, int NW, int NTL> __global__ void __launch_bounds__(64 * NW) pair_kernel(DecayWalkArgs a) {
+  // (dk's may be the larger one: two sets of its tiles fit where one of dq's does)
+  constexpr int DQ = Lds<float, KD, NW, NTL, true, true>::TOTAL, DK = Lds<float, KD, NW, NTL, true, false>::TOTAL;
+  __shared__ __attribute__((aligned(16))) char sm[DQ > DK ? DQ : DK];
+  if (blockIdx.y == 0) walk<float, KD, NW, NTL, true, true, 3>(a, a.walk[0], blockIdx.x, sm);
+  else walk<float, KD, NW, NTL, true, false, 3>(a, a.walk[1], blockIdx.x, sm);
+}
+
 template <typename T, int KD, int NW, int NTL>
 hipError_t launch_nw(const DecayWalkArgs& a, hipStream_t st) {
   const int n = a.d.B * a.d.Hv * a.nseg;
   const dim3 grid((n + 7) / 8 * 8, a.nwalk);
   const DecayWalk& w = a.walk[0];
+  constexpr int SPU = sizeof(T) == 2 ? 2 : 3;  // where only the tensors' type is read from the state
   if (w.e.p) {
-    if constexpr (sizeof(T) == 4) walk_kernel<T, KD, NW, NTL, true, true, 3><<<grid, 64 * NW, 0, st>>>(a);
+    if constexpr (sizeof(T) == 4) pair_kernel<KD, NW, NTL><<<grid, 64 * NW, 0, st>>>(a);
     else return hipErrorInvalidValue;  // (keys_kernel's)
-  } else if (w.end && !w.seg_sum) walk_kernel<T, KD, NW, NTL, true, false, 3><<<grid, 64 * NW, 0, st>>>(a);
-  else walk_kernel<T, KD, NW, NTL, true, false, 2><<<grid, 64 * NW, 0, st>>>(a);
+  } else if (w.end && !w.seg_sum) walk_kernel<T, KD, NW, NTL, true, 3><<<grid, 64 * NW, 0, st>>>(a);
+  else walk_kernel<T, KD, NW, NTL, true, SPU><<<grid, 64 * NW, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -894,7 +910,7 @@ template <typename T, int KD> hipError_t launch_sum_kd(const DecayWalkArgs& a, h
   const int n = a.d.B * a.d.Hv * a.nseg, N = a.walk[0].N;
   const dim3 grid((n + 7) / 8 * 8, a.nwalk);
   auto go = [&](auto nw, auto ntl) {
-    walk_kernel<T, KD, decltype(nw)::v, decltype(ntl)::v, false, false, 3><<<grid, 64 * decltype(nw)::v, 0, st>>>(a);
+    walk_kernel<T, KD, decltype(nw)::v, decltype(ntl)::v, false, 3><<<grid, 64 * decltype(nw)::v, 0, st>>>(a);
   };
   if (N <= 64) go(Int<4>{}, Int<1>{});
   else if (N <= 128) go(Int<8>{}, Int<1>{});
