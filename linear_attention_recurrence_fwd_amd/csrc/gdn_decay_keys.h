@@ -18,6 +18,11 @@
 // the heads are gone through.  Two workgroups fit a compute unit for Dv <= 128, and
 // one's products fill the other's waits.  The blocks of 64 columns repeat P, a tenth
 // of the products.
+//
+// dq's bound are vector instructions (half of its cycles; matrix products a third):
+// of some 1000 a wave and chunk, 560 cut the two states and what they sum into bf16
+// parts.  Two parts for dlg would save a third of them and leave errors of 2^-17 in
+// each product, which a dlg of cancelling terms shows.  dk is bound like the walks.
 #pragma once
 
 #include "gdn_decay_walk.h"

@@ -45,6 +45,16 @@
 // Results in bf16 go to LDS and from there to memory a chunk later, as whole
 // rows: a wave's own columns would be 32 bytes of a row at a time, which costs the
 // memory pipeline four times the cycles.
+//
+// Measured, bf16: 64 value heads of 192 x 128, 2048 steps in 4 segments of 8 chunks
+// (one workgroup of 8 waves to a compute unit): the sums 24 us, the output walks 45
+// to 52 us, with 101 MB of rows 1.4 TB/s together.  4 heads of 128 x 128, 32768 steps
+// in 64 segments: 20 and 33 us, 1.6 TB/s with the chain's 10 us.  A chunk costs 1.4 us
+// as a sum and 2.3 us as outputs (128 x 128), a launch with its first tiles and its
+// states' way in and out 9 to 15 us.  Of a walk's cycles matrix products take 29%,
+// vector instructions 34%, LDS reads 39%: the bound is their order inside a chunk (P
+// before P z, the old state before the new one, barriers between), with too few
+// registers for a second workgroup beside the state.
 #pragma once
 
 #include "gdn_dev.h"
@@ -874,8 +884,8 @@ __global__ void __launch_bounds__(64 * NW) walk_kernel(DecayWalkArgs a) {
 }
 
 // dq (walk 0) and dk of fp32 tensors in one launch, dq's longer walks first: a few
-// heads' walks fill a part of the chip each (at 72 (b, h) and segments of 64 x 128
-// heads 26 us, one after the other 20 + 15 us).
+// heads' walks fill a part of the chip each (8 heads of 64 x 96, 515 steps, 72
+// workgroups a walk: 20 us, one after the other 20 + 14 us).
 template <int KD, int NW, int NTL> __global__ void __launch_bounds__(64 * NW) pair_kernel(DecayWalkArgs a) {
   // (dk's may be the larger one: two sets of its tiles fit where one of dq's does)
   constexpr int DQ = Lds<float, KD, NW, NTL, true, true>::TOTAL, DK = Lds<float, KD, NW, NTL, true, false>::TOTAL;

@@ -15,6 +15,10 @@
 // the token instead of once for each head.  The other channel of a pair lies
 // eight or more channels away in another lane of the row (or in the same lane
 // when interleaved) and comes by a lane move of the raw storage.
+//
+// Bound by memory: 4096 tokens, 32 + 16 heads of 128, bf16: forward 103 MB in 21.5 us,
+// 4.8 TB/s (a large copy: 5.1); backward 153 MB in 29.4 us, 5.2 TB/s, and 4 us for
+// dw's parts.  64 tokens of 16 + 2 heads of 256: 4 us, a launch and a trip to memory.
 #include "gdn_dev.h"
 #include "gdn_decay.h"
 
