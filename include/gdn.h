@@ -315,7 +315,8 @@ int gdn_bwd_vg(const gdn_dims* d, const void* q, const void* k, const void* v, c
  *             overflows for any lg <= 0, and growth (lg > 0) overflows only
  *             where g^64 does.
  *   q, k, v, state0, mask, o, state_out: as gdn_fwd; state_out may alias state0
- *             exactly
+ *             exactly.  No output may overlap an input or another output
+ *             otherwise, in the VJP neither (else GDN_ERR_INVALID_ARG)
  * Alignment: q, k, v, o, dO, dq, dk, dv and the states 16 bytes (else
  * GDN_ERR_INVALID_ARG).  A NaN or Inf in a valid step reaches the outputs of
  * its whole chunk in the chunk forms, those of earlier steps included.
@@ -359,7 +360,8 @@ typedef struct gdn_norm_dims {
  *   cosines, then R/2 sines; NULL only with R = 0); pos [B,T] int32, NULL =
  *   0 .. T-1 in every sequence.  A position outside 0 .. P-1 turns its token's
  *   first R channels to NaN (and the weights' gradients with them).
- *   oq, ok, dyq, dyk, dq, dk: dense, as q and k.  No output may overlap an input.
+ *   oq, ok, dyq, dyk, dq, dk: dense, as q and k.  No output of rows may overlap an
+ *   input's or another output's (else GDN_ERR_INVALID_ARG).
  * The VJP takes the inputs again and recomputes the norms; dwq, dwk [D] fp32
  * are sums over all rows, in a fixed order.  Alignment: all but pos 16 bytes
  * (else GDN_ERR_INVALID_ARG).

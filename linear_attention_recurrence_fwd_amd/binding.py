@@ -631,6 +631,7 @@ class DecayAttention(torch.autograd.Function):
         return o, st
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dO, dS):
         q, k, v, lg, state0, mask = ctx.saved_tensors
         g = decay_bwd(q, k, v, lg, state0, mask, dO.contiguous(), None if dS is None else dS.contiguous(),
@@ -733,6 +734,7 @@ class NormRope(torch.autograd.Function):
         return norm_rope(q, k, wq, wk, rope, pos, **ctx.kw)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dyq, dyk):
         q, k, wq, wk, rope, pos = ctx.saved_tensors
         g = norm_rope_bwd(q, k, wq, wk, rope, pos, dyq.contiguous(), dyk.contiguous(), **ctx.kw)

@@ -15,6 +15,37 @@ bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0;
 template <typename... P> bool all_aligned(P... p) { return (aligned(p) && ...); }
 template <typename... P> bool all_given(P... p) { return (... && (p != nullptr)); }
 
+// A tensor's bytes; whether any of the outputs shares some with any input or other output.
+struct Range {
+  const void* p;
+  size_t n;
+};
+// Bytes of the tensors with key heads, with value heads, of the states, mask and lg.
+struct Sizes {
+  size_t key, val, state, mask, lg;
+  explicit Sizes(const gdn_dims* d) {
+    const size_t bt = static_cast<size_t>(d->B) * d->T * (d->dtype == GDN_BF16 ? 2 : 4);
+    key = bt * d->Hk * d->Dk;
+    val = bt * d->Hv * d->Dv;
+    state = static_cast<size_t>(d->B) * d->Hv * d->Dk * d->Dv * 4;
+    mask = static_cast<size_t>(d->B) * d->T;
+    lg = static_cast<size_t>(d->Hv) * 4;
+  }
+};
+bool overlap(const Range& a, const Range& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && x < y + b.n && y < x + a.n;
+}
+template <int NO, int NI> bool overlaps(const Range (&out)[NO], const Range (&in)[NI]) {
+  for (int i = 0; i < NO; ++i) {
+    for (const Range& r : in)
+      if (overlap(out[i], r)) return true;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return true;
+  }
+  return false;
+}
+
 int check_dims(const gdn_dims* p, bool bwd, DecayDims* out) {
   if (!p) return GDN_ERR_INVALID_ARG;
   if (p->B < 1 || p->T < 0 || p->Hk < 1 || p->Hv < 1 || p->Dk < 1 || p->Dv < 1) return GDN_ERR_INVALID_ARG;
@@ -185,6 +216,19 @@ int check_norm(const gdn_norm_dims* p, gdn::NormRopeArgs* a) {
   return GDN_OK;
 }
 
+// Bytes of the dense rows, and of the inputs' with their strides.
+struct NormSizes {
+  size_t q, k, qs, ks;
+  NormSizes(const gdn_norm_dims* d, const gdn::NormRopeArgs& a) {
+    const size_t es = d->dtype == GDN_BF16 ? 2 : 4, n = static_cast<size_t>(a.BT);
+    const size_t qr = static_cast<size_t>(d->Hq) * d->D, kr = static_cast<size_t>(d->Hk) * d->D;
+    q = n * qr * es;
+    k = n * kr * es;
+    qs = n ? ((n - 1) * a.qs + qr) * es : 0;
+    ks = n ? ((n - 1) * a.ks + kr) * es : 0;
+  }
+};
+
 }  // namespace
 
 extern "C" {
@@ -218,13 +262,18 @@ int gdn_decay_fwd(const gdn_dims* d, const void* q, const void* k, const void* v
   if (!all_aligned(q, k, v, state0, o, state_out)) return GDN_ERR_INVALID_ARG;
   const bool bf = d->dtype == GDN_BF16;
   hipStream_t st = static_cast<hipStream_t>(stream);
+  const Layout L = use_step(d) ? Layout{} : layout(d, dd, false);
+  if (L.total > ws_bytes || (L.total > 0 && !ws)) return GDN_ERR_WORKSPACE;
+  if (L.total > 0 && !aligned(ws)) return GDN_ERR_INVALID_ARG;
+  const Sizes z(d);
+  const Range out[] = {{o, z.val}, {state_out, z.state}, {ws, L.total}};
+  const Range in[] = {{q, z.key}, {k, z.key}, {v, z.val}, {lg, z.lg}, {mask, z.mask},
+                      {state0 == state_out ? nullptr : state0, z.state}};
+  if (overlaps(out, in)) return GDN_ERR_INVALID_ARG;
   if (use_step(d)) {
     const gdn::DecayStepArgs a{dd, q, k, v, lg, scale, state0, mask, o, state_out};
     return gdn::launch_decay_step(a, bf, st) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
   }
-  const Layout L = layout(d, dd, false);
-  if (L.total > ws_bytes || (L.total > 0 && !ws)) return GDN_ERR_WORKSPACE;
-  if (L.total > 0 && !aligned(ws)) return GDN_ERR_INVALID_ARG;
   const Cut c = cut(d, dd, false);
   gdn::DecayWalk w = walk_kv(dd);
   w.x = key_rows(dd, q);
@@ -273,6 +322,11 @@ int gdn_decay_bwd(const gdn_dims* d, const void* q, const void* k, const void* v
   const Layout L = layout(d, dd, true);
   if (L.total > ws_bytes || (L.total > 0 && !ws)) return GDN_ERR_WORKSPACE;
   if (L.total > 0 && !aligned(ws)) return GDN_ERR_INVALID_ARG;
+  const Sizes z(d);
+  const Range out[] = {{dq, z.key}, {dk, z.key}, {dv, z.val}, {dstate, z.state}, {dlg, z.lg}, {ws, L.total}};
+  const Range in[] = {{q, z.key}, {k, z.key}, {v, z.val}, {lg, z.lg}, {mask, z.mask},
+                      {dO, z.val}, {state0, z.state}, {dS_final, z.state}};
+  if (overlaps(out, in)) return GDN_ERR_INVALID_ARG;
   const bool bf = d->dtype == GDN_BF16;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const Cut c = cut(d, dd, true);
@@ -360,6 +414,9 @@ int gdn_norm_rope_fwd(const gdn_norm_dims* d, const void* q, const void* k, cons
   if (!all_given(wq, wk) || (a.R > 0 && !rope)) return GDN_ERR_INVALID_ARG;
   if (a.BT > 0 && !all_given(q, k, oq, ok)) return GDN_ERR_INVALID_ARG;
   if (!all_aligned(q, k, wq, wk, rope, oq, ok)) return GDN_ERR_INVALID_ARG;
+  const NormSizes z(d, a);
+  const Range out[] = {{oq, z.q}, {ok, z.k}}, in[] = {{q, z.qs}, {k, z.ks}};
+  if (overlaps(out, in)) return GDN_ERR_INVALID_ARG;
   a.q = q;
   a.k = k;
   a.wq = wq;
@@ -393,6 +450,9 @@ int gdn_norm_rope_bwd(const gdn_norm_dims* d, const void* q, const void* k, cons
   if (!all_aligned(q, k, wq, wk, rope, dyq, dyk, dq, dk, dwq, dwk)) return GDN_ERR_INVALID_ARG;
   const size_t need = align_up(static_cast<size_t>(a.blocks) * 2 * a.D * sizeof(float));
   if (need > ws_bytes || (need > 0 && !ws)) return GDN_ERR_WORKSPACE;
+  const NormSizes z(d, a);
+  const Range out[] = {{dq, z.q}, {dk, z.k}, {ws, need}}, in[] = {{q, z.qs}, {k, z.ks}, {dyq, z.q}, {dyk, z.k}};
+  if (overlaps(out, in)) return GDN_ERR_INVALID_ARG;
   a.q = q;
   a.k = k;
   a.wq = wq;

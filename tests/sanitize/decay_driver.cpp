@@ -18,7 +18,8 @@ void touch(const void* p, size_t bytes) {
   g_sink = c[0];
   g_sink = c[bytes - 1];
 }
-const void* const kFake = reinterpret_cast<void*>(4096);
+// Places of tensors that nothing reads here, far enough from each other and from the heap.
+void* fake(int i) { return reinterpret_cast<void*>(static_cast<uintptr_t>(i + 1) << 48); }
 size_t bh(const gdn::DecayDims& d) { return static_cast<size_t>(d.B) * d.Hv; }
 size_t states(const gdn::DecayDims& d, int n) { return n * bh(d) * d.Dk * d.Dv * 4; }
 }  // namespace
@@ -38,7 +39,8 @@ hipError_t launch_decay_walk(const DecayWalkArgs& a, bool, bool, hipStream_t) {
     touch(w.seg_start, states(a.d, a.nseg));
     touch(w.seg_R, states(a.d, a.nseg));
     touch(w.grad, bh(a.d) * a.nseg * decay_waves(w.N) * 8);
-    if (w.w32) touch(w.w, static_cast<size_t>(a.d.B) * a.d.T * a.d.Hv * w.N * 4);
+    // the fp32 dq and dk walks of grouped heads leave rows for the sum over a group
+    if (a.walk[0].e.p && a.d.G() > 1) touch(w.w, static_cast<size_t>(a.d.B) * a.d.T * a.d.Hv * w.N * 4);
   }
   ++g_launches;
   return hipSuccess;
@@ -60,7 +62,6 @@ hipError_t launch_decay_chain(const DecayChainArgs* a, int n, hipStream_t) {
   for (int i = 0; i < n; ++i) {
     touch(a[i].states, states(a[i].d, a[i].nseg));
     touch(a[i].seg_steps, static_cast<size_t>(a[i].d.B) * a[i].nseg * 4);
-    if (reinterpret_cast<uintptr_t>(a[i].end) > 65536) touch(a[i].end, states(a[i].d, 1));  // (else a placeholder)
   }
   ++g_launches;
   return hipSuccess;
@@ -105,10 +106,10 @@ hipError_t launch_norm_rope_bwd(const NormRopeArgs& a, bool, hipStream_t) {
   } while (0)
 
 int main() {
-  void* f = const_cast<void*>(kFake);
-  float* ff = static_cast<float*>(f);
-  const uint8_t* m = static_cast<const uint8_t*>(f);
-  void* other = reinterpret_cast<void*>(8192);
+  void *q = fake(0), *k = fake(1), *v = fake(2), *o = fake(3), *dO = fake(4), *dq = fake(5), *dk = fake(6), *dv = fake(7);
+  float *lg = static_cast<float*>(fake(8)), *s0 = static_cast<float*>(fake(9)), *s1 = static_cast<float*>(fake(10));
+  float *dS = static_cast<float*>(fake(11)), *ds = static_cast<float*>(fake(12)), *dlg = static_cast<float*>(fake(13));
+  const uint8_t* m = static_cast<const uint8_t*>(fake(14));
   const int64_t Ts[] = {0, 1, 2, 63, 64, 65, 200, 515, 1024, 2048, 40000};
   const int64_t heads[][2] = {{1, 1}, {1, 4}, {2, 6}, {3, 24}, {16, 64}, {40, 320}};
   const int64_t sizes[][2] = {{8, 8}, {64, 40}, {128, 128}, {192, 128}, {72, 256}, {256, 200}};
@@ -125,10 +126,10 @@ int main() {
               EXPECT(gdn_decay_fwd_workspace_bytes(&d, &n) == GDN_OK);
               if (n < (size_t{6} << 30)) {
                 void* ws = n ? malloc(n) : nullptr;
-                EXPECT(gdn_decay_fwd(&d, f, f, f, ff, 1.f, nullptr, m, f, ff, ws, n, nullptr) == GDN_OK);
-                EXPECT(gdn_decay_fwd(&d, f, f, f, ff, 1.f, ff, nullptr, f, static_cast<float*>(other), ws, n, nullptr) == GDN_OK);
-                EXPECT(gdn_decay_fwd(&d, f, f, f, ff, 1.f, ff, m, f, ff, ws, n, nullptr) == GDN_OK);  // in place
-                if (n) EXPECT(gdn_decay_fwd(&d, f, f, f, ff, 1.f, ff, m, f, ff, ws, n - 1, nullptr) == GDN_ERR_WORKSPACE);
+                EXPECT(gdn_decay_fwd(&d, q, k, v, lg, 1.f, nullptr, m, o, s1, ws, n, nullptr) == GDN_OK);
+                EXPECT(gdn_decay_fwd(&d, q, k, v, lg, 1.f, s0, nullptr, o, s1, ws, n, nullptr) == GDN_OK);
+                EXPECT(gdn_decay_fwd(&d, q, k, v, lg, 1.f, s0, m, o, s0, ws, n, nullptr) == GDN_OK);  // in place
+                if (n) EXPECT(gdn_decay_fwd(&d, q, k, v, lg, 1.f, s0, m, o, s0, ws, n - 1, nullptr) == GDN_ERR_WORKSPACE);
                 free(ws);
                 ++calls;
               }
@@ -136,8 +137,8 @@ int main() {
               EXPECT(rc == (algo == GDN_ALGO_SCAN ? GDN_ERR_UNSUPPORTED : GDN_OK));
               if (rc == GDN_OK && n < (size_t{6} << 30)) {
                 void* ws = malloc(n);
-                EXPECT(gdn_decay_bwd(&d, f, f, f, ff, 1.f, ff, m, f, ff, f, f, f, ff, ff, ws, n, nullptr) == GDN_OK);
-                EXPECT(gdn_decay_bwd(&d, f, f, f, ff, 1.f, ff, m, f, ff, f, f, f, ff, ff, ws, n - 1, nullptr) == GDN_ERR_WORKSPACE);
+                EXPECT(gdn_decay_bwd(&d, q, k, v, lg, 1.f, s0, m, dO, dS, dq, dk, dv, dlg, ds, ws, n, nullptr) == GDN_OK);
+                EXPECT(gdn_decay_bwd(&d, q, k, v, lg, 1.f, s0, m, dO, dS, dq, dk, dv, dlg, ds, ws, n - 1, nullptr) == GDN_ERR_WORKSPACE);
                 free(ws);
                 ++calls;
               }
@@ -150,8 +151,8 @@ int main() {
           size_t n = 0;
           EXPECT(gdn_norm_rope_bwd_workspace_bytes(&d, &n) == GDN_OK);
           void* ws = n ? malloc(n) : nullptr;
-          EXPECT(gdn_norm_rope_fwd(&d, f, f, ff, ff, ff, nullptr, f, f, nullptr) == GDN_OK);
-          EXPECT(gdn_norm_rope_bwd(&d, f, f, ff, ff, ff, nullptr, f, f, f, f, ff, ff, ws, n, nullptr) == GDN_OK);
+          EXPECT(gdn_norm_rope_fwd(&d, q, k, lg, s0, s1, nullptr, dq, dk, nullptr) == GDN_OK);
+          EXPECT(gdn_norm_rope_bwd(&d, q, k, lg, s0, s1, nullptr, v, dO, dq, dk, dS, ds, ws, n, nullptr) == GDN_OK);
           free(ws);
           ++calls;
         }

@@ -94,6 +94,64 @@ def test_decay_bwd_rejects_before_launch():
     assert call(p, None, need) == WORKSPACE
 
 
+def spread(n, step):
+    return [ctypes.c_void_p((1 << 30) + i * step) for i in range(n)]
+
+
+@pytest.mark.parametrize("T", [3, 100])
+def test_decay_refuses_overlaps(T):
+    """Outputs that share bytes with inputs or each other: by all of them, or by the last sixteen."""
+    lib, ws = B.lib(), ctypes.c_void_p(1 << 20)
+    d = B.make_dims(1, T, 2, 4, 64, 64, B.GDN_F32)
+    key, val, state = T * 2 * 64 * 4, T * 4 * 64 * 4, 4 * 64 * 64 * 4
+    f = spread(8, 1 << 20)  # q k v lg | state0 mask o state_out
+    nbytes = {0: key, 1: key, 2: val, 3: 16, 4: state, 6: val, 7: state}
+    for out in (6, 7):
+        for i in nbytes:
+            if i == out:
+                continue
+            for shift in (0, nbytes[i] - 16, 16 - nbytes[out]):
+                if (out, i, shift) == (7, 4, 0):
+                    continue  # in place
+                a = list(f)
+                a[out] = ctypes.c_void_p(f[i].value + shift)
+                assert lib.gdn_decay_fwd(ctypes.byref(d), *a[:4], 1.0, *a[4:], ws, 1 << 19, None) == INVALID, (out, i, shift)
+    g = spread(13, 1 << 20)  # q k v lg | state0 mask dO dS dq dk dv dlg dstate
+    nbytes = {0: key, 1: key, 2: val, 3: 16, 4: state, 6: val, 7: state, 8: key, 9: key, 10: val, 11: 16, 12: state}
+    for out in (8, 9, 10, 12):
+        for i in nbytes:
+            if i == out:
+                continue
+            for shift in (0, nbytes[i] - 16, 16 - nbytes[out]):
+                a = list(g)
+                a[out] = ctypes.c_void_p(g[i].value + shift)
+                assert lib.gdn_decay_bwd(ctypes.byref(d), *a[:4], 1.0, *a[4:], ws, 1 << 19, None) == INVALID, (out, i, shift)
+    for i in (6, 7):  # the workspace
+        if T > 4:
+            big = B.make_dims(1, 2048, 2, 4, 64, 64, B.GDN_BF16)
+            assert lib.gdn_decay_fwd(ctypes.byref(big), *f[:4], 1.0, *f[4:], f[i], 1 << 24, None) == INVALID
+
+
+def test_norm_refuses_overlaps():
+    lib, d = B.lib(), norm_dims(q_stride=6 * 64, k_stride=6 * 64)
+    q, k = 6 * 4 * 64 * 2, 6 * 2 * 64 * 2
+    f = spread(8, 1 << 20)  # q k wq wk rope pos oq ok
+    qs, ks = (5 * 6 + 4) * 64 * 2, (5 * 6 + 2) * 64 * 2
+    for out, n in ((6, q), (7, k)):
+        for i, m in ((0, qs), (1, ks), (13 - out, k if out == 6 else q)):
+            for shift in (0, m - 16, 16 - n):
+                a = list(f)
+                a[out] = ctypes.c_void_p(f[i].value + shift)
+                assert lib.gdn_norm_rope_fwd(ctypes.byref(d), *a, None) == INVALID, (out, i, shift)
+    g, ws = spread(12, 1 << 20), ctypes.c_void_p(1 << 20)  # q k wq wk rope pos dyq dyk dq dk dwq dwk
+    for out, n in ((8, q), (9, k)):
+        for i, m in ((0, qs), (1, ks), (6, q), (7, k), (17 - out, k if out == 8 else q)):
+            for shift in (0, m - 16, 16 - n):
+                a = list(g)
+                a[out] = ctypes.c_void_p(g[i].value + shift)
+                assert lib.gdn_norm_rope_bwd(ctypes.byref(d), *a, ws, 1 << 19, None) == INVALID, (out, i, shift)
+
+
 def norm_dims(**kw):
     v = dict(B=2, T=3, Hq=4, Hk=2, D=64, R=32, P=16, q_stride=0, k_stride=0, dtype=B.GDN_BF16, interleaved=0, eps=1e-6,
              w_offset=0.0)

@@ -323,6 +323,18 @@ def test_mixer_together(dtype):
         assert e <= 2 * R.NORM[dtype == BF], (n, e)
 
 
+def test_second_derivatives_refused():
+    """The VJPs have none of their own: asking for one is an error, not a zero."""
+    t, Hk, Hv, D = _mixer(1, 40, F32, 78)
+    c = {n: x.cuda() for n, x in t.items()}
+    q = c["qk"][..., : Hk * D].reshape(1, 40, Hk, D).contiguous().requires_grad_(True)
+    k = c["qk"][..., Hk * D:].reshape(1, 40, Hk, D).contiguous().requires_grad_(True)
+    for out in (binding.DecayAttention.apply(q, k, c["v"], c["lg"])[0], binding.NormRope.apply(q, k, c["wq"], c["wk"])[0]):
+        g, = torch.autograd.grad((out * out).sum(), [q], create_graph=True)
+        with pytest.raises(RuntimeError):
+            torch.autograd.grad(g.sum(), [q])
+
+
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 def test_graph_stream_and_two_at_once(dtype):
     """Captured into a graph on a side stream and replayed on changed inputs, with
