@@ -64,26 +64,9 @@ __device__ __forceinline__ void keys_walk(const DecayKeysArgs& a, int block, cha
 #pragma unroll
   for (int q = 0; q < GH; ++q) lg2[q] = log2_decay(a.lg[h0 + q]);
 
-  // ---- start states, element (channel c of Dv, column k of Dk) at k Dv + c
   const int col = cb + 16 * w + lr;
   f32x4 S[GH][KT], E[DQ ? GH : 1][KT];
   double grad[GH];
-#pragma unroll
-  for (int q = 0; q < GH; ++q) {
-    const size_t hs = static_cast<size_t>(Dk) * Dv, bh = static_cast<size_t>(b) * Hv + h0 + q;
-    const float* src = nseg > 1 ? (rev ? a.R : a.S) + (static_cast<size_t>(sg) * a.d.B * Hv + bh) * hs
-                                : (rev ? a.dS : a.state0);
-    if (nseg == 1 && src) src += bh * hs;
-    const rsrc_t rs = make_rsrc(src, src ? hs * 4 : 0);
-#pragma unroll
-    for (int i = 0; i < KT; ++i) {
-      const int ch = 32 * (i / 2) + 8 * g + 4 * (i % 2);
-      const float4 v = buf_f4(rs, ch < Dv && col < Dk ? 4u * static_cast<uint32_t>(col * Dv + ch) : kOff);
-      S[q][i] = f32x4{v.x, v.y, v.z, v.w};
-      if constexpr (DQ) E[q][i] = f4zero();
-    }
-    grad[q] = 0.0;
-  }
 
   const int t_lo = sg * a.seg * kDecayChunk, t_hi = min(Tn, t_lo + a.seg * kDecayChunk);
   const int nch = t_hi > t_lo ? (t_hi - t_lo + CH - 1) / CH : 0;
@@ -169,6 +152,23 @@ __device__ __forceinline__ void keys_walk(const DecayKeysArgs& a, int block, cha
       const int t = threadIdx.x >> 6, row = 32 * t + (l >> 2), p = 2 * (2 * t + 1) + (l & 1);
       reinterpret_cast<uint2*>(sm + M::P + (row * PP + (p ^ key<PP>(row))) * 16)[(l >> 1) & 1] = make_uint2(0, 0);
     }
+  }
+  // ---- start states (behind the first tiles' loads), element (channel c of Dv, column k of Dk) at k Dv + c
+#pragma unroll
+  for (int q = 0; q < GH; ++q) {
+    const size_t hs = static_cast<size_t>(Dk) * Dv, bh = static_cast<size_t>(b) * Hv + h0 + q;
+    const float* src = nseg > 1 ? (rev ? a.R : a.S) + (static_cast<size_t>(sg) * a.d.B * Hv + bh) * hs
+                                : (rev ? a.dS : a.state0);
+    if (nseg == 1 && src) src += bh * hs;
+    const rsrc_t rs = make_rsrc(src, src ? hs * 4 : 0);
+#pragma unroll
+    for (int i = 0; i < KT; ++i) {
+      const int ch = 32 * (i / 2) + 8 * g + 4 * (i % 2);
+      const float4 v = buf_f4(rs, ch < Dv && col < Dk ? 4u * static_cast<uint32_t>(col * Dv + ch) : kOff);
+      S[q][i] = f32x4{v.x, v.y, v.z, v.w};
+      if constexpr (DQ) E[q][i] = f4zero();
+    }
+    grad[q] = 0.0;
   }
   for (int ci = 0; ci < nch; ++ci) {
     const int t0 = chunk_start(ci), L = __popcll(live);

@@ -292,22 +292,6 @@ __device__ __forceinline__ void walk(const DecayWalkArgs& a, const DecayWalk& wk
         }
     }
   };
-  if constexpr (OUT) {
-    load_start();
-    if constexpr (!DOTS)
-      if (prefix) add_sums(sg);
-    if constexpr (DOTS) {
-#pragma unroll
-      for (int i = 0; i < KT; ++i)
-#pragma unroll
-        for (int n = 0; n < NTL; ++n) E[i][n] = f4zero();
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < KT; ++i)
-#pragma unroll
-      for (int n = 0; n < NTL; ++n) S[i][n] = f4zero();
-  }
 
   const int t_lo = sg * a.seg * kDecayChunk, t_hi = min(Tn, t_lo + a.seg * kDecayChunk);
   const int nch = t_hi > t_lo ? (t_hi - t_lo + CH - 1) / CH : 0;
@@ -441,6 +425,23 @@ __device__ __forceinline__ void walk(const DecayWalkArgs& a, const DecayWalk& wk
     if (w == 0) factors(0, live, 0);
     if constexpr (M::SLOTS == 2) issue_yz(0, 0, live);
     issue_xe(0, 0, live);
+  }
+  // (the state's loads behind those of the first tiles)
+  if constexpr (OUT) {
+    load_start();
+    if constexpr (!DOTS)
+      if (prefix) add_sums(sg);
+    if constexpr (DOTS) {
+#pragma unroll
+      for (int i = 0; i < KT; ++i)
+#pragma unroll
+        for (int n = 0; n < NTL; ++n) E[i][n] = f4zero();
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < KT; ++i)
+#pragma unroll
+      for (int n = 0; n < NTL; ++n) S[i][n] = f4zero();
   }
   for (int ci = 0; ci < nch; ++ci) {
     const int t0 = chunk_start(ci), slot = M::SLOTS == 2 ? ci & 1 : 0;
