@@ -530,16 +530,19 @@ def decode_conv(x, conv_w, conv_state, a, b, A_log, dt_bias, Hk, Dk, Hv, Dv, sta
 
 
 # The entry points below are also called for single tokens, where a call's time on
-# the host counts: pointers go as plain integers, sizes are asked for once for each
-# set of dims, and the current device is only switched where it is another one.
+# the host counts: pointers go as plain integers, dims are made and sizes asked for
+# once for each set of them, and the current device is only switched where it is
+# another one.
 
 def _a(x):
     return None if x is None else x.data_ptr()
 
 
 @functools.lru_cache(maxsize=256)
-def _decay_ws(fn, *dims):
-    return _query(fn, Dims(*dims))
+def _decay_dims(query, *dims):
+    """(dims, workspace bytes)"""
+    d = make_dims(*dims)
+    return d, _query(query, d)
 
 
 _here = contextlib.nullcontext()
@@ -557,18 +560,26 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 # ---- linear attention with a decay for each head (gdn_decay_fwd / gdn_decay_bwd)
 
-def _check_decay(d, q, k, v, lg, state0, mask):
+def _check_decay(query, q, k, v, lg, state0, mask, algo):
+    """(dims, workspace bytes, shape of the states) of checked arguments."""
     dev, dt = q.device, q.dtype
     if dev.type != "cuda":
         raise ValueError("gdn runs on the GPU; got device %s" % dev)
-    _check(q, "q", (d.B, d.T, d.Hk, d.Dk), dt, dev)
-    _check(k, "k", (d.B, d.T, d.Hk, d.Dk), dt, dev)
-    _check(v, "v", (d.B, d.T, d.Hv, d.Dv), dt, dev)
-    _check(lg, "lg", (d.Hv,), torch.float32, dev)
+    if dt != torch.bfloat16 and dt != torch.float32:
+        raise TypeError("q: expected float32 or bfloat16, got %s" % dt)
+    B, T, Hk, Dk = q.shape
+    Hv, Dv = v.shape[2], v.shape[3]
+    states = (B, Hv, Dk, Dv)
+    _check(q, "q", (B, T, Hk, Dk), dt, dev)
+    _check(k, "k", (B, T, Hk, Dk), dt, dev)
+    _check(v, "v", (B, T, Hv, Dv), dt, dev)
+    _check(lg, "lg", (Hv,), torch.float32, dev)
     if state0 is not None:
-        _check(state0, "state0", (d.B, d.Hv, d.Dk, d.Dv), torch.float32, dev)
+        _check(state0, "state0", states, torch.float32, dev)
     if mask is not None:
-        _check(mask, "mask", (d.B, d.T), torch.uint8, dev)
+        _check(mask, "mask", (B, T), torch.uint8, dev)
+    d, wsb = _decay_dims(query, B, T, Hk, Hv, Dk, Dv, dt, algo)
+    return d, wsb, states
 
 
 def decay_fwd(q, k, v, lg, state0=None, mask=None, *, scale=None, state_out=None, algo=ALGO_AUTO):
@@ -576,19 +587,17 @@ def decay_fwd(q, k, v, lg, state0=None, mask=None, *, scale=None, state_out=None
     + k v^T, o = scale S^T q (scale: Dk^-1/2 by default), T = 1 for a single
     token.  Returns (o, state_out).  Pass state_out=state0 to update the state
     in place."""
-    d = _dims_of(q, v, algo)
-    _check_decay(d, q, k, v, lg, state0, mask)
+    d, wsb, states = _check_decay("gdn_decay_fwd_workspace_bytes", q, k, v, lg, state0, mask, algo)
     dev = q.device
     if state_out is None:
-        state_out = (torch.empty((d.B, d.Hv, d.Dk, d.Dv), dtype=torch.float32, device=dev) if state0 is None
+        state_out = (torch.empty(states, dtype=torch.float32, device=dev) if state0 is None
                      else torch.empty_like(state0))
     else:
-        _check(state_out, "state_out", (d.B, d.Hv, d.Dk, d.Dv), torch.float32, dev)
-    wsb = _decay_ws("gdn_decay_fwd_workspace_bytes", d.B, d.T, d.Hk, d.Hv, d.Dk, d.Dv, d.dtype, d.algo, 0)
+        _check(state_out, "state_out", states, torch.float32, dev)
     o = torch.empty_like(v)
     ws = torch.empty((wsb,), dtype=torch.uint8, device=dev) if wsb else None
     with _on_device(dev):
-        rc = lib().gdn_decay_fwd(d, _a(q), _a(k), _a(v), _a(lg), d.Dk ** -0.5 if scale is None else scale,
+        rc = lib().gdn_decay_fwd(d, _a(q), _a(k), _a(v), _a(lg), states[2] ** -0.5 if scale is None else scale,
                                  _a(state0), _a(mask), _a(o), _a(state_out), _a(ws), wsb,
                                  _raw_stream(dev.index))
     if rc:
@@ -598,19 +607,17 @@ def decay_fwd(q, k, v, lg, state0=None, mask=None, *, scale=None, state_out=None
 
 def decay_bwd(q, k, v, lg, state0, mask, dO, dS_final=None, *, scale=None, algo=ALGO_AUTO):
     """VJP of decay_fwd.  Returns dict(dq, dk, dv, dlg, dstate)."""
-    d = _dims_of(q, v, algo)
-    _check_decay(d, q, k, v, lg, state0, mask)
+    d, wsb, states = _check_decay("gdn_decay_bwd_workspace_bytes", q, k, v, lg, state0, mask, algo)
     dev = q.device
-    _check(dO, "dO", (d.B, d.T, d.Hv, d.Dv), q.dtype, dev)
+    _check(dO, "dO", v.shape, q.dtype, dev)
     if dS_final is not None:
-        _check(dS_final, "dS_final", (d.B, d.Hv, d.Dk, d.Dv), torch.float32, dev)
-    wsb = _decay_ws("gdn_decay_bwd_workspace_bytes", d.B, d.T, d.Hk, d.Hv, d.Dk, d.Dv, d.dtype, d.algo, 0)
+        _check(dS_final, "dS_final", states, torch.float32, dev)
     out = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
                dlg=torch.empty_like(lg),
-               dstate=torch.empty((d.B, d.Hv, d.Dk, d.Dv), dtype=torch.float32, device=dev))
+               dstate=torch.empty(states, dtype=torch.float32, device=dev))
     ws = torch.empty((wsb,), dtype=torch.uint8, device=dev) if wsb else None
     with _on_device(dev):
-        rc = lib().gdn_decay_bwd(d, _a(q), _a(k), _a(v), _a(lg), d.Dk ** -0.5 if scale is None else scale,
+        rc = lib().gdn_decay_bwd(d, _a(q), _a(k), _a(v), _a(lg), states[2] ** -0.5 if scale is None else scale,
                                  _a(state0), _a(mask), _a(dO), _a(dS_final),
                                  *[_a(out[n]) for n in ("dq", "dk", "dv", "dlg", "dstate")], _a(ws), wsb,
                                  _raw_stream(dev.index))
@@ -694,11 +701,12 @@ def norm_rope(q, k, wq, wk, rope=None, pos=None, *, eps=1e-6, w_offset=0.0, inte
     table rope [P,R] at positions pos [B,T] int32 (0 .. T-1 by default), in one
     pass.  q and k may be slices of a packed projection.  Returns dense (q, k)."""
     d = _norm_dims(q, k, wq, wk, rope, pos, eps, w_offset, interleaved)
-    oq = torch.empty((d.B, d.T, d.Hq, d.D), dtype=q.dtype, device=q.device)
-    ok = torch.empty((d.B, d.T, d.Hk, d.D), dtype=q.dtype, device=q.device)
-    with _on_device(q.device):
+    dev, dt = q.device, q.dtype
+    oq = torch.empty((d.B, d.T, d.Hq, d.D), dtype=dt, device=dev)
+    ok = torch.empty((d.B, d.T, d.Hk, d.D), dtype=dt, device=dev)
+    with _on_device(dev):
         rc = lib().gdn_norm_rope_fwd(d, _a(q), _a(k), _a(wq), _a(wk), _a(rope), _a(pos), _a(oq), _a(ok),
-                                     _raw_stream(q.device.index))
+                                     _raw_stream(dev.index))
     if rc:
         raise GdnError("gdn_norm_rope_fwd", rc)
     return oq, ok
@@ -708,8 +716,8 @@ def norm_rope_bwd(q, k, wq, wk, rope, pos, dyq, dyk, *, eps=1e-6, w_offset=0.0, 
     """VJP of norm_rope.  Returns dict(dq, dk, dwq, dwk), dq and dk dense."""
     d = _norm_dims(q, k, wq, wk, rope, pos, eps, w_offset, interleaved)
     dev = q.device
-    _check(dyq, "dyq", (d.B, d.T, d.Hq, d.D), q.dtype, dev)
-    _check(dyk, "dyk", (d.B, d.T, d.Hk, d.D), q.dtype, dev)
+    _check(dyq, "dyq", q.shape, q.dtype, dev)
+    _check(dyk, "dyk", k.shape, q.dtype, dev)
     out = dict(dq=torch.empty_like(dyq), dk=torch.empty_like(dyk), dwq=torch.empty_like(wq),
                dwk=torch.empty_like(wk))
     wsb = _query("gdn_norm_rope_bwd_workspace_bytes", d)

@@ -10,7 +10,7 @@
 namespace gdn {
 
 constexpr int kDecayChunk = 64;   // steps per chunk; segments are whole chunks
-constexpr int kDecayMaxSeg = 512;      // segments of one sequence
+constexpr int kDecayMaxSeg = 256;      // segments of one sequence: one to a compute unit at most
 constexpr int kDecayMaxT = 1 << 30;    // steps of one sequence
 
 struct DecayDims {

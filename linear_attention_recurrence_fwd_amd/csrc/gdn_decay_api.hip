@@ -60,7 +60,7 @@ int check_dims(const gdn_dims* p, bool bwd, DecayDims* out) {
   // their slices or segments, and the bytes of 64 steps' rows (the tensors
   // themselves are addressed in 64)
   if (p->T > gdn::kDecayMaxT || p->Hv > INT_MAX / 1024 || p->B > INT_MAX / 1024 ||
-      static_cast<double>(p->B) * p->Hv * gdn::kDecayMaxSeg * 2 > INT_MAX ||
+      static_cast<double>(p->B) * p->Hv * gdn::kDecayMaxSeg * 4 > INT_MAX ||
       static_cast<double>(p->B) * p->T * p->Hv > 9.0e12 || p->Hv * (p->Dk > p->Dv ? p->Dk : p->Dv) > (1 << 22))
     return GDN_ERR_UNSUPPORTED;
   *out = DecayDims{static_cast<int>(p->B),  static_cast<int>(p->T),  static_cast<int>(p->Hk),
@@ -93,8 +93,7 @@ Cut cut(const gdn_dims* p, const DecayDims& d, bool bwd) {
   // one workgroup to a compute unit, and no second round of a few: at 48 (b, h)
   // and 16 chunks, 4 segments (192 workgroups) take 37 us, 6 (288) 47 us; at 64
   // and 32 chunks, 4 (256) take 72 us, 8 (512) 94 us
-  if (p->algo != GDN_ALGO_CHUNK && nc > 1) n = 256 / (d.B * d.Hv);
-  if (n > gdn::kDecayMaxSeg) n = gdn::kDecayMaxSeg;
+  if (p->algo != GDN_ALGO_CHUNK && nc > 1) n = gdn::kDecayMaxSeg / (d.B * d.Hv);
   if (n > nc) n = nc;
   if (n < 1) n = 1;
   // Segments pay where a pass over all chunks costs more than one over a
