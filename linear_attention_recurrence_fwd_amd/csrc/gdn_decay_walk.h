@@ -672,17 +672,14 @@ __device__ __forceinline__ void walk(const DecayWalkArgs& a, const DecayWalk& wk
     }
 
     // ---- the state's update
-    if constexpr (OUT) {
-      const float gL = exp2_fast(lg2 * static_cast<float>(L));
+    const float gL = OUT ? exp2_fast(lg2 * static_cast<float>(L)) : 1.f;
+    if constexpr (OUT && BF) {
 #pragma unroll
       for (int i = 0; i < KT; ++i)
 #pragma unroll
         for (int n = 0; n < NTL; ++n)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            if constexpr (DOTS) E[i][n][r] = gL * fmaf(static_cast<float>(L), S[i][n][r], E[i][n][r]);
-            S[i][n][r] *= gL;
-          }
+          for (int r = 0; r < 4; ++r) S[i][n][r] *= gL;
     }
     uint4 zu[BF ? CH / 32 : 1][NTL];  // z as operands
     float zv[BF ? 1 : CH / 16][NTL][4];
@@ -736,6 +733,10 @@ __device__ __forceinline__ void walk(const DecayWalkArgs& a, const DecayWalk& wk
         spread_x(2 * kt + 1);
       }
     } else {
+      // The chunk's own sum is made from zero and added to the state once: added
+      // product by product, every rounding would be one of the state's size, and
+      // dlg, a sum of both signs over all states, was off by up to three times as much.
+      float zs[CH / 16][NTL][4], ze[DOTS ? CH / 16 : 1][NTL][4];
 #pragma unroll
       for (int bq = 0; bq < CH / 16; ++bq) {
         const f32x4 sw = *reinterpret_cast<const f32x4*>(fsw + 16 * bq + 4 * g);
@@ -748,10 +749,21 @@ __device__ __forceinline__ void walk(const DecayWalkArgs& a, const DecayWalk& wk
             const int row = 16 * bq + 4 * g + r;
             zv[bq][n][r] =
                 *reinterpret_cast<const float*>(tile + M::Z + (row * PZ + ((c >> 2) ^ key<PZ>(row))) * 16 + (c & 3) * 4);
+            zs[bq][n][r] = zv[bq][n][r] * sw[r];
+            if constexpr (DOTS) ze[bq][n][r] = zv[bq][n][r] * se[r];
           }
         }
+      }
 #pragma unroll
-        for (int i = 0; i < KT; ++i)
+      for (int i = 0; i < KT; ++i) {
+        f32x4 U[NTL], UE[DOTS ? NTL : 1];
+#pragma unroll
+        for (int n = 0; n < NTL; ++n) {
+          U[n] = f4zero();
+          if constexpr (DOTS) UE[n] = f4zero();
+        }
+#pragma unroll
+        for (int bq = 0; bq < CH / 16; ++bq)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int row = 16 * bq + 4 * g + r;
@@ -759,9 +771,16 @@ __device__ __forceinline__ void walk(const DecayWalkArgs& a, const DecayWalk& wk
                 tile + M::Y + (row * PX + ((4 * i + (lr >> 2)) ^ key<PX>(row))) * 16 + (lr & 3) * 4);
 #pragma unroll
             for (int n = 0; n < NTL; ++n) {
-              S[i][n] = mfma16f(yv, zv[bq][n][r] * sw[r], S[i][n]);
-              if constexpr (DOTS) E[i][n] = mfma16f(yv, zv[bq][n][r] * se[r], E[i][n]);
+              U[n] = mfma16f(yv, zs[bq][n][r], U[n]);
+              if constexpr (DOTS) UE[n] = mfma16f(yv, ze[bq][n][r], UE[n]);
             }
+          }
+#pragma unroll
+        for (int n = 0; n < NTL; ++n)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if constexpr (DOTS) E[i][n][r] = fmaf(gL, fmaf(static_cast<float>(L), S[i][n][r], E[i][n][r]), UE[n][r]);
+            S[i][n][r] = OUT ? fmaf(gL, S[i][n][r], U[n][r]) : S[i][n][r] + U[n][r];
           }
       }
     }
