@@ -164,11 +164,15 @@ struct Work {
   int run, runs;   // groups of one run, runs of one token
 };
 
+// Workgroups of a forward launch in x, of 2^30 threads: a launch's threads are
+// counted in 32 bits in each direction.  More go on in y.
+constexpr int64_t kFwdBlocks = 1 << 22;
+
 template <typename T, int LPH, bool INTER>
 __global__ void __launch_bounds__(256) fwd_kernel(NormRopeArgs a, Work wk) {
   constexpr int RPW = 64 / LPH;
   const Lane<T, LPH, INTER> ln(a);
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int64_t item = (static_cast<int64_t>(blockIdx.y) * kFwdBlocks + blockIdx.x) * 4 + (threadIdx.x >> 6);
   const int64_t token = item / wk.runs;
   if (token >= a.BT) return;
   const int g0 = static_cast<int>(item % wk.runs) * wk.run, g1 = min(g0 + wk.run, wk.gq + wk.gk);
@@ -336,8 +340,10 @@ hipError_t launch_lph(const NormRopeArgs& a, bool bwd, hipStream_t st) {
   if (!bwd) {
     const Work w = work_of(a, 8192);
     const int64_t n = (a.BT * w.runs + 3) / 4;
-    if (a.interleaved) fwd_kernel<T, LPH, true><<<static_cast<unsigned>(n), 256, 0, st>>>(a, w);
-    else fwd_kernel<T, LPH, false><<<static_cast<unsigned>(n), 256, 0, st>>>(a, w);
+    const dim3 grid(static_cast<unsigned>(n < kFwdBlocks ? n : kFwdBlocks),
+                    static_cast<unsigned>((n + kFwdBlocks - 1) / kFwdBlocks));
+    if (a.interleaved) fwd_kernel<T, LPH, true><<<grid, 256, 0, st>>>(a, w);
+    else fwd_kernel<T, LPH, false><<<grid, 256, 0, st>>>(a, w);
     return hipGetLastError();
   }
   if (a.blocks > 0) {
