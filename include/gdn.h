@@ -296,8 +296,8 @@ int gdn_bwd_vg(const gdn_dims* d, const void* q, const void* k, const void* v, c
  * query/key head h / G, the state is [B,Hv,Dk,Dv] fp32 and is carried, as in
  * gdn_fwd.  q and k are taken as they are (no normalisation).
  *   d         Dk, Dv: multiples of 8 from 8 to 256, T up to 2^30,
- *             rows of Hv heads up to 2^22 elements (else GDN_ERR_UNSUPPORTED; the
- *             tensors may exceed 2^31 elements);
+ *             rows of Hv heads up to 2^22 elements, B Hv up to 2^21 - 64 (else
+ *             GDN_ERR_UNSUPPORTED; the tensors may exceed 2^31 elements);
  *             save is ignored; algo:
  *               SCAN        the per-step recurrence (forward only)
  *               CHUNK       64-step chunks on the matrix cores (32-step for

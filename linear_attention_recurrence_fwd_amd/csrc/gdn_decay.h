@@ -12,6 +12,7 @@ namespace gdn {
 constexpr int kDecayChunk = 64;   // steps per chunk; segments are whole chunks
 constexpr int kDecayMaxSeg = 256;      // segments of one sequence: one to a compute unit at most
 constexpr int kDecayMaxT = 1 << 30;    // steps of one sequence
+constexpr int kDecayMaxPairs = (1 << 21) - 64;  // (b, h) pairs
 
 struct DecayDims {
   int B, T, Hk, Hv, Dk, Dv;

@@ -56,11 +56,12 @@ int check_dims(const gdn_dims* p, bool bwd, DecayDims* out) {
     return GDN_ERR_INVALID_ARG;
   if (bwd && p->algo == GDN_ALGO_SCAN) return GDN_ERR_UNSUPPORTED;
   if (p->Dk % 8 || p->Dv % 8 || p->Dk > 256 || p->Dv > 256) return GDN_ERR_UNSUPPORTED;
-  // counts that the kernels hold in 32 bits: steps, heads, (b, h) pairs times
-  // their slices or segments, and the bytes of 64 steps' rows (the tensors
-  // themselves are addressed in 64)
-  if (p->T > gdn::kDecayMaxT || p->Hv > INT_MAX / 1024 || p->B > INT_MAX / 1024 ||
-      static_cast<double>(p->B) * p->Hv * gdn::kDecayMaxSeg * 4 > INT_MAX ||
+  // counts that are held in 32 bits: steps, heads, (b, h) pairs times their slices
+  // or segments, the threads of a launch over the pairs (dq's and dk's has up to
+  // eight workgroups of 256 to a pair), and the bytes of 64 steps' rows (the
+  // tensors themselves are addressed in 64)
+  if (p->T > gdn::kDecayMaxT || p->Hv > gdn::kDecayMaxPairs || p->B > gdn::kDecayMaxPairs ||
+      p->B * p->Hv > gdn::kDecayMaxPairs ||
       static_cast<double>(p->B) * p->T * p->Hv > 9.0e12 || p->Hv * (p->Dk > p->Dv ? p->Dk : p->Dv) > (1 << 22))
     return GDN_ERR_UNSUPPORTED;
   *out = DecayDims{static_cast<int>(p->B),  static_cast<int>(p->T),  static_cast<int>(p->Hk),

@@ -1,4 +1,4 @@
-// The query/key norm's entries with their real launch
+// The decay operator's and the query/key norm's entries with their real launch
 // code, built for the host alone: the runtime's launch is replaced by one that
 // looks at the grid.  A launch's threads are counted in 32 bits in each direction
 // and a workgroup holds 1024 at most; every size that an entry accepts has to keep
@@ -60,10 +60,12 @@ int main() {
       exit(1);
     }
   };
-  void *q = fake(0), *k = fake(1), *v = fake(2), *dO = fake(4), *dq = fake(5), *dk = fake(6);
+  void *q = fake(0), *k = fake(1), *v = fake(2), *o = fake(3), *dO = fake(4), *dq = fake(5), *dk = fake(6), *dv = fake(7);
   float *lg = static_cast<float*>(fake(8)), *s0 = static_cast<float*>(fake(9)), *s1 = static_cast<float*>(fake(10));
-  float *dS = static_cast<float*>(fake(11)), *ds = static_cast<float*>(fake(12));
+  float *dS = static_cast<float*>(fake(11)), *ds = static_cast<float*>(fake(12)), *dlg = static_cast<float*>(fake(13));
+  const uint8_t* m = static_cast<const uint8_t*>(fake(14));
   void* ws = fake(15);
+  const size_t room = size_t{1} << 47;
   for (int dt : {GDN_F32, GDN_BF16}) {
     // tokens by heads of the norm
     const int64_t tokens[][2] = {{1, 1},       {3, 7000},          {1, 1 << 24},        {1 << 24, 1},
@@ -79,6 +81,24 @@ int main() {
             expect(gdn_norm_rope_bwd(&d, q, k, lg, s0, s1, nullptr, v, dO, dq, dk, dS, ds, ws, n, nullptr), GDN_OK,
                    "norm bwd", t[0], t[1], H, D);
           }
+    // batches by heads of the decay operator: up to kMost pairs and kRow elements a row
+    constexpr int64_t kMost = (1 << 21) - 64, kRow = 1 << 22;
+    const int64_t bh[][3] = {{1, 1, 1},         {1, 3, 255},        {2, 2, 128},      {kMost, 1, 1}, {kMost / 2, 2, 2},
+                             {kMost / 4, 1, 4}, {kMost + 1, 1, 1},  {kMost / 2 + 1, 1, 2}, {1, 1, 1 << 14},
+                             {100, 1, 1 << 14}, {64, 1 << 14, 1 << 14}};
+    for (auto& h : bh)
+      for (int64_t T : {1, 4, 5, 64, 4097})
+        for (int64_t Dk : {8, 128, 192, 256})
+          for (int64_t Dv : {8, 128, 192, 256})
+            for (int algo : {GDN_ALGO_AUTO, GDN_ALGO_SCAN, GDN_ALGO_CHUNK}) {
+              const gdn_dims d{h[0], T, h[1], h[2], Dk, Dv, dt, algo, 0};
+              const int fit = h[0] * h[2] <= kMost && h[2] * (Dk > Dv ? Dk : Dv) <= kRow ? GDN_OK : GDN_ERR_UNSUPPORTED;
+              const int64_t sizes = Dk * 1000 + Dv;
+              expect(gdn_decay_fwd(&d, q, k, v, lg, 1.f, s0, m, o, s1, ws, room, nullptr), fit, "decay", h[0], h[2], T, sizes);
+              expect(gdn_decay_fwd(&d, q, k, v, lg, 1.f, s0, m, o, s0, ws, room, nullptr), fit, "in place", h[0], h[2], T, sizes);
+              expect(gdn_decay_bwd(&d, q, k, v, lg, 1.f, s0, m, dO, dS, dq, dk, dv, dlg, ds, ws, room, nullptr),
+                     algo == GDN_ALGO_SCAN ? GDN_ERR_UNSUPPORTED : fit, "decay bwd", h[0], h[2], T, sizes);
+            }
   }
   printf("ok: %ld calls, %ld launches\n", calls, g_launches);
   return 0;

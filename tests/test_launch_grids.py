@@ -1,4 +1,4 @@
-"""Every launch of the query/key norm keeps to what a
+"""Every launch of the decay operator and of the query/key norm keeps to what a
 launch can hold, at the largest sizes that the entries accept: their host code and
 launchers, built for the host alone, with the runtime's launch replaced by one that
 looks at the grid (sanitize/grid_driver.cpp).  No GPU is touched."""
