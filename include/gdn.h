@@ -360,8 +360,9 @@ typedef struct gdn_norm_dims {
  *   cosines, then R/2 sines; NULL only with R = 0); pos [B,T] int32, NULL =
  *   0 .. T-1 in every sequence.  A position outside 0 .. P-1 turns its token's
  *   first R channels to NaN (and the weights' gradients with them).
- *   oq, ok, dyq, dyk, dq, dk: dense, as q and k.  No output of rows may overlap an
- *   input's or another output's (else GDN_ERR_INVALID_ARG).
+ *   oq, ok, dyq, dyk, dq, dk: dense, as q and k.  No output may overlap an input,
+ *   another output or the workspace (else GDN_ERR_INVALID_ARG); dwq and dwk, which
+ *   are written when everything is read, may lie on inputs.
  * The VJP takes the inputs again and recomputes the norms; dwq, dwk [D] fp32
  * are sums over all rows, in a fixed order.  Alignment: all but pos 16 bytes
  * (else GDN_ERR_INVALID_ARG).

@@ -216,9 +216,10 @@ int check_norm(const gdn_norm_dims* p, gdn::NormRopeArgs* a) {
   return GDN_OK;
 }
 
-// Bytes of the dense rows, and of the inputs' with their strides.
+// Bytes of the dense rows, of the inputs' with their strides, of a weight, the
+// table and the positions.
 struct NormSizes {
-  size_t q, k, qs, ks;
+  size_t q, k, qs, ks, w, rope, pos;
   NormSizes(const gdn_norm_dims* d, const gdn::NormRopeArgs& a) {
     const size_t es = d->dtype == GDN_BF16 ? 2 : 4, n = static_cast<size_t>(a.BT);
     const size_t qr = static_cast<size_t>(d->Hq) * d->D, kr = static_cast<size_t>(d->Hk) * d->D;
@@ -226,6 +227,9 @@ struct NormSizes {
     k = n * kr * es;
     qs = n ? ((n - 1) * a.qs + qr) * es : 0;
     ks = n ? ((n - 1) * a.ks + kr) * es : 0;
+    w = static_cast<size_t>(d->D) * 4;
+    rope = static_cast<size_t>(d->P) * d->R * 4;
+    pos = n * 4;
   }
 };
 
@@ -415,7 +419,8 @@ int gdn_norm_rope_fwd(const gdn_norm_dims* d, const void* q, const void* k, cons
   if (a.BT > 0 && !all_given(q, k, oq, ok)) return GDN_ERR_INVALID_ARG;
   if (!all_aligned(q, k, wq, wk, rope, oq, ok)) return GDN_ERR_INVALID_ARG;
   const NormSizes z(d, a);
-  const Range out[] = {{oq, z.q}, {ok, z.k}}, in[] = {{q, z.qs}, {k, z.ks}};
+  const Range out[] = {{oq, z.q}, {ok, z.k}};
+  const Range in[] = {{q, z.qs}, {k, z.ks}, {wq, z.w}, {wk, z.w}, {rope, z.rope}, {pos, z.pos}};
   if (overlaps(out, in)) return GDN_ERR_INVALID_ARG;
   a.q = q;
   a.k = k;
@@ -451,8 +456,12 @@ int gdn_norm_rope_bwd(const gdn_norm_dims* d, const void* q, const void* k, cons
   const size_t need = align_up(static_cast<size_t>(a.blocks) * 2 * a.D * sizeof(float));
   if (need > ws_bytes || (need > 0 && !ws)) return GDN_ERR_WORKSPACE;
   const NormSizes z(d, a);
-  const Range out[] = {{dq, z.q}, {dk, z.k}, {ws, need}}, in[] = {{q, z.qs}, {k, z.ks}, {dyq, z.q}, {dyk, z.k}};
-  if (overlaps(out, in)) return GDN_ERR_INVALID_ARG;
+  const Range out[] = {{dq, z.q}, {dk, z.k}, {ws, need}};
+  const Range in[] = {{q, z.qs},  {k, z.ks},  {dyq, z.q},     {dyk, z.k},
+                      {wq, z.w}, {wk, z.w}, {rope, z.rope}, {pos, z.pos}};
+  // (the weights' gradients are written when all inputs are read)
+  const Range dw[] = {{dwq, z.w}, {dwk, z.w}};
+  if (overlaps(out, in) || overlaps(dw, out)) return GDN_ERR_INVALID_ARG;
   a.q = q;
   a.k = k;
   a.wq = wq;
