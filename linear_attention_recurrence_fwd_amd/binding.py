@@ -635,14 +635,17 @@ class DecayAttention(torch.autograd.Function):
         o, st = decay_fwd(q, k, v, lg, state0, mask, scale=scale)
         ctx.save_for_backward(q, k, v, lg, state0, mask)
         ctx.scale = scale
+        ctx.set_materialize_grads(False)  # a loss that does not use the state has no dS to read
         return o, st
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dO, dS):
+        if dO is None and dS is None:
+            return (None,) * 7
         q, k, v, lg, state0, mask = ctx.saved_tensors
-        g = decay_bwd(q, k, v, lg, state0, mask, dO.contiguous(), None if dS is None else dS.contiguous(),
-                      scale=ctx.scale)
+        g = decay_bwd(q, k, v, lg, state0, mask, torch.zeros_like(v) if dO is None else dO.contiguous(),
+                      None if dS is None else dS.contiguous(), scale=ctx.scale)
         return (g["dq"], g["dk"], g["dv"], g["dlg"], g["dstate"] if state0 is not None else None, None, None)
 
 
