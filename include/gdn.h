@@ -312,8 +312,10 @@ int gdn_bwd_vg(const gdn_dims* d, const void* q, const void* k, const void* v, c
  *             products.
  *   lg        [Hv] fp32, the log of the decay.  Meant for lg <= 0; -inf (g = 0)
  *             is allowed.  No quotient of decays is formed, so nothing
- *             overflows for any lg <= 0, and growth (lg > 0) overflows only
- *             where g^64 does.
+ *             overflows for any lg <= 0.  Growth (lg > 0) overflows where g^n
+ *             does, n the sequence's valid steps (segments form their own powers:
+ *             inf, and NaN where it meets a zero); with CHUNK, which forms none
+ *             above g^64, where that or a state does.
  *   q, k, v, state0, mask, o, state_out: as gdn_fwd; state_out may alias state0
  *             exactly.  No output may overlap an input or another output
  *             otherwise, in the VJP neither (else GDN_ERR_INVALID_ARG)
