@@ -60,6 +60,37 @@ def shares(c, outs, grads, b, s, interleaved):
     return e
 
 
+def weights(c, grads, interleaved):
+    """Shares of their bound that the weights' gradients take: sums over all rows,
+    here in 64 bits over runs of tokens; each off by at most (B T H + D + 16) 2^-24
+    times its terms' magnitudes.  Normwise the roundings are independent and the terms
+    of either sign: (D + 16) 2^-24 for the terms themselves and the root of their
+    number times 2^-24 for the sums, eight times that for what a partial sum may be
+    larger than the whole."""
+    e = {}
+    B, T, _, D = c["q"].shape
+    rope = None if c["rope"] is None else c["rope"].double()
+    wq, wk = (c[n].double().requires_grad_(True) for n in ("wq", "wk"))
+    sums, mags = [0.0, 0.0], [0.0, 0.0]
+    run = max(1, (1 << 22) // c["q"].shape[2] // D)
+    for b in range(B):
+        for t in range(0, T, run):
+            cut = lambda x: x[b:b + 1, t:t + run].double()  # noqa: E731
+            ref = R.norm_rope(cut(c["q"]), cut(c["k"]), wq, wk, rope, c["pos"][b:b + 1, t:t + run], interleaved=interleaved, **KW)
+            g = torch.autograd.grad((ref[0] * cut(c["dyq"])).sum() + (ref[1] * cut(c["dyk"])).sum(), [wq, wk])
+            for i, n in enumerate("qk"):
+                x = cut(c[n])
+                r = 1 / torch.sqrt((x * x).mean(-1, keepdim=True) + 1e-6)
+                sums[i] = sums[i] + g[i]
+                mags[i] = mags[i] + (x.abs() * r * 2 * cut(c["dy" + n]).abs().amax(-1, keepdim=True)).sum((0, 1, 2))
+    for i, n in enumerate("qk"):
+        terms = B * T * c[n].shape[2] + D + 16
+        d = grads["dw" + n].double() - sums[i]
+        e["dw" + n] = (d.abs() / (terms * 2.0 ** -24 * mags[i])).max().item()
+        e["dw" + n + " norm"] = (d.norm() / sums[i].norm() / (8 * (D + 16 + terms ** 0.5) * 2.0 ** -24)).item()
+    return e
+
+
 @pytest.mark.parametrize("size", [(1, (1 << 24) + 9, 2, 1, 16, 16), (3, (1 << 24) + 5, 1, 1, 8, 0), (1, (1 << 26) + 9, 1, 1, 8, 0)],
                          ids=lambda s: "x".join(map(str, s)))
 def test_more_tokens_than_one_direction_of_a_grid(size):
@@ -78,3 +109,32 @@ def test_more_tokens_than_one_direction_of_a_grid(size):
         for t in (0, (1 << 23) - 500, (1 << 24) - 600, T // 2, T - 1000):
             e = shares(c, outs, g, b, slice(t, t + 1000), False)
             assert all(x <= 1.0 for x in e.values()), (b, t, e)
+
+
+# B, T, Hq, Hk, D, R.  A wave takes 64 / lanes heads of a token at a time (lanes of eight
+# channels, a power of two) and a run of such groups: with so many tokens runs of two
+# and more, of which one has query and key heads, up to all heads of a token; and the
+# backward's waves take several of these.
+PROMPTS = [
+    (1, 3001, 20, 12, 128, 128), (2, 1500, 17, 7, 128, 64), (1, 2500, 7, 4, 256, 64), (3, 3333, 24, 9, 64, 32),
+    (1, 9001, 5, 2, 192, 192), (1, 2100, 6, 5, 512, 512), (1, 9000, 70, 65, 8, 0), (2, 5000, 40, 3, 40, 32),
+]
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("size", PROMPTS, ids=lambda s: "x".join(map(str, s)))
+def test_prompts(size, dtype, interleaved, packed):
+    say("[norm prompt] size=%s dtype=%s interleaved=%d packed=%d" % (size, dtype, interleaved, packed))
+    c = make(*size, dtype, sum(size), packed)
+    kw = dict(KW, interleaved=interleaved)
+    outs = binding.norm_rope(*[c[n] for n in ("q", "k", "wq", "wk", "rope", "pos")], **kw)
+    g = binding.norm_rope_bwd(*[c[n] for n in ("q", "k", "wq", "wk", "rope", "pos", "dyq", "dyk")], **kw)
+    torch.cuda.synchronize()
+    for b in range(size[0]):
+        e = shares(c, outs, g, b, slice(0, size[1]), interleaved)
+        assert all(x <= 1.0 for x in e.values()), (b, e)
+    e = weights(c, g, interleaved)
+    say("[norm prompt] shares of the weights' bounds: " + " ".join("%s=%.3f" % kv for kv in e.items()))
+    assert all(x <= 1.0 for x in e.values()), e
