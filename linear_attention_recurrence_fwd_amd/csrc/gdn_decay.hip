@@ -2,8 +2,6 @@
 // over segment states, the reductions of the backward, and the single steps.
 #include "gdn_decay_walk.h"
 
-#include <limits.h>
-
 namespace gdn {
 
 size_t decay_sum_floats(int KD, int N) {

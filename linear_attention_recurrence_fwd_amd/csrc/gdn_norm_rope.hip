@@ -82,8 +82,7 @@ struct Turn {
   float c[8], s[8];
 };
 
-template <typename T, int LPH, bool INTER>
-struct Lane {
+template <int LPH, bool INTER> struct Lane {
   int sub, c0, other;  // lane in the row, its first channel, the lane of the other channels
   bool on, turned;
   float sign;
@@ -151,7 +150,6 @@ struct Lane {
   }
 };
 
-template <int LPH>
 __device__ __forceinline__ void load_w(const float* w, const NormRopeArgs& a, int c0, bool on, float* out) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) out[i] = on ? w[c0 + i] + a.w_offset : 0.f;
@@ -171,7 +169,7 @@ constexpr int64_t kFwdBlocks = 1 << 22;
 template <typename T, int LPH, bool INTER>
 __global__ void __launch_bounds__(256) fwd_kernel(NormRopeArgs a, Work wk) {
   constexpr int RPW = 64 / LPH;
-  const Lane<T, LPH, INTER> ln(a);
+  const Lane<LPH, INTER> ln(a);
   const int64_t item = (static_cast<int64_t>(blockIdx.y) * kFwdBlocks + blockIdx.x) * 4 + (threadIdx.x >> 6);
   const int64_t token = item / wk.runs;
   if (token >= a.BT) return;
@@ -186,7 +184,7 @@ __global__ void __launch_bounds__(256) fwd_kernel(NormRopeArgs a, Work wk) {
     if (lo >= hi) continue;
     float wt[8], wo[8];
     const float* wp = part ? a.wk : a.wq;
-    load_w<LPH>(wp, a, ln.c0, ln.on, wt);
+    load_w(wp, a, ln.c0, ln.on, wt);
 #pragma unroll
     for (int i = 0; i < 8; ++i) wo[i] = __shfl(wt[i], ln.other);
     const int H = part ? a.Hk : a.Hq, base = part ? wk.gq : 0;
@@ -223,14 +221,14 @@ __global__ void __launch_bounds__(256) fwd_kernel(NormRopeArgs a, Work wk) {
 template <typename T, int LPH, bool INTER>
 __global__ void __launch_bounds__(256) bwd_kernel(NormRopeArgs a, Work wk) {
   constexpr int RPW = 64 / LPH;
-  const Lane<T, LPH, INTER> ln(a);
+  const Lane<LPH, INTER> ln(a);
   const int w = threadIdx.x >> 6, sub_row = (threadIdx.x & 63) / LPH;
   const float inv = 1.f / static_cast<float>(a.D);
   __shared__ float red[4][2][8 * LPH];
   float wt[2][8], dw[2][8];
 #pragma unroll
   for (int part = 0; part < 2; ++part) {
-    load_w<LPH>(part ? a.wk : a.wq, a, ln.c0, ln.on, wt[part]);
+    load_w(part ? a.wk : a.wq, a, ln.c0, ln.on, wt[part]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[part][i] = 0.f;
   }
