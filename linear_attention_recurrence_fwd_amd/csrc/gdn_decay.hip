@@ -180,6 +180,12 @@ template <typename T, int N> __device__ __forceinline__ void load_row(const T* p
   for (int i = 0; i < N; ++i) out[i] = in ? out[i] : 0.f;
 }
 
+// f x + t in x's place.  (The compiler makes the sum in t's and moves it back, a move
+// to each element: 7.9 us instead of 7.5 for 4 steps of 32 heads of 128 x 128.)
+__device__ __forceinline__ void times_plus(float& x, float f, float t) {
+  asm("v_fma_f32 %0, %1, %0, %2" : "+v"(x) : "v"(f), "v"(t));
+}
+
 template <typename T, int DK>
 __global__ void __launch_bounds__(64) step_kernel(DecayStepArgs p, int slices) {
   constexpr int RL = DK / 8;
@@ -201,7 +207,15 @@ __global__ void __launch_bounds__(64) step_kernel(DecayStepArgs p, int slices) {
   float4 s[RL];
 #pragma unroll
   for (int r = 0; r < RL; ++r) s[r] = buf_f4(rs0, off[r]);
-  const float gate = exp2_fast(log2_decay(p.lg[h]));
+  // The decay of a step in two parts, gate + rest: one fp32 number below one is off by
+  // up to 2^-25, the same at every step.  At lg = -3e-4 that left a state of thousands
+  // of steps 7e-5 off; with rest it is 1e-6, what the roundings of its sums come to.
+  // (Below -1/2 a state forgets within a few steps, and rest is of no use.)  A third
+  // product to each element: 4 steps of 32 heads of 128 x 128 take 7.5 us, without
+  // 6.9; single steps, which wait for memory, the same.
+  const float lg = p.lg[h], m = expm1f(lg);
+  const bool slow = fabsf(lg) < 0.5f;
+  const float gate = slow ? 1.f + m : exp2_fast(log2_decay(lg)), rest = slow ? (1.f - gate) + m : 0.f;
   const size_t qs = static_cast<size_t>(d.Hk) * d.Dk, vs = static_cast<size_t>(d.Hv) * d.Dv;
   const size_t bt0 = static_cast<size_t>(b) * d.T;
   const T* qr = static_cast<const T*>(p.q) + bt0 * qs + static_cast<size_t>(j) * d.Dk;
@@ -235,10 +249,10 @@ __global__ void __launch_bounds__(64) step_kernel(DecayStepArgs p, int slices) {
     if (valid) {
 #pragma unroll
       for (int r = 0; r < RL; ++r) {
-        s[r].x = fmaf(kt[r], vt[0], gate * s[r].x);
-        s[r].y = fmaf(kt[r], vt[1], gate * s[r].y);
-        s[r].z = fmaf(kt[r], vt[2], gate * s[r].z);
-        s[r].w = fmaf(kt[r], vt[3], gate * s[r].w);
+        times_plus(s[r].x, gate, fmaf(rest, s[r].x, kt[r] * vt[0]));
+        times_plus(s[r].y, gate, fmaf(rest, s[r].y, kt[r] * vt[1]));
+        times_plus(s[r].z, gate, fmaf(rest, s[r].z, kt[r] * vt[2]));
+        times_plus(s[r].w, gate, fmaf(rest, s[r].w, kt[r] * vt[3]));
       }
     }
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);

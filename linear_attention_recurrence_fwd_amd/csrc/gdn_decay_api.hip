@@ -70,12 +70,16 @@ int check_dims(const gdn_dims* p, bool bwd, DecayDims* out) {
 }
 
 // Calls of a few steps take the steps in turn.  us in turn / by chunks, in a graph:
-//   heads                        T = 1        T = 4        T = 6        T = 8
-//   1 x 32, 128 x 128, bf16   4.2 /  8.6   6.2 /  8.7   7.8 /  8.6   9.5 /  8.6
-//   64 x 32, 128 x 128, bf16 43.8 / 70.8  51.0 / 73.3  56.3 / 75.4  62.2 / 77.2
-//   8 x 8, 64 x 32, bf16      3.2 /  6.2   4.8 /  6.2   5.9 /  6.2   7.0 /  6.3
-//   4 x 64, 192 x 128, bf16  10.1 / 15.6  14.1 / 15.6  16.9 / 15.6  19.4 / 15.9
-//   1 x 32, 128 x 128, fp32   3.8 / 11.2   5.9 / 11.2   7.5 / 11.3   9.1 / 11.3
+//   heads                        T = 1         T = 4         T = 6         T = 8
+//   1 x 32, 128 x 128, bf16   4.9 /   9.4   7.6 /   9.4   9.5 /   9.5  11.5 /   9.4
+//   16 x 32, 128 x 128, bf16 15.1 /  24.1  18.0 /  24.2  20.6 /  24.1  23.2 /  24.2
+//   64 x 32, 128 x 128, bf16 46.2 /  81.1  62.0 /  81.4  71.0 /  82.0  78.9 /  82.2
+//   8 x 8, 64 x 32, bf16      4.1 /   6.7   5.9 /   6.7   7.2 /   6.7   8.6 /   6.7
+//   4 x 64, 192 x 128, bf16  12.3 /  16.4  16.7 /  16.5  19.7 /  16.1  22.6 /  16.8
+//   1 x 32, 128 x 128, fp32   4.6 /  11.7   7.3 /  11.7   9.2 /  11.8  11.0 /  11.8
+//   64 x 32, 128 x 128, fp32 47.0 / 102.6  64.3 / 103.8  73.5 / 104.5  83.0 / 105.8
+// Four is where the first of them draw level; large batches and fp32 would gain in
+// turn up to eight (by 4 to 30%), which this rule leaves.
 constexpr int kFewSteps = 4;
 bool use_step(const gdn_dims* p) {
   return p->algo == GDN_ALGO_SCAN || (p->algo == GDN_ALGO_AUTO && p->T <= kFewSteps);
