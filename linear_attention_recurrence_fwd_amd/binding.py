@@ -530,9 +530,10 @@ def decode_conv(x, conv_w, conv_state, a, b, A_log, dt_bias, Hk, Dk, Hv, Dv, sta
 
 
 # The entry points below are also called for single tokens, where a call's time on
-# the host counts: pointers go as plain integers, dims are made and sizes asked for
-# once for each set of them, and the current device is only switched where it is
-# another one.
+# the host counts: pointers go as plain integers, the current device is only switched
+# where it is another one, and the decay entries' dims are made and their sizes asked
+# for once for each set of them (the norm's, which also hold the strides, at every
+# call).
 
 def _a(x):
     return None if x is None else x.data_ptr()

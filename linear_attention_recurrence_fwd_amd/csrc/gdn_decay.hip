@@ -147,8 +147,8 @@ __global__ void __launch_bounds__(256) group_kernel(DecayGroupArgs a, size_t n) 
 
 // ---- single steps, S <- g S + k v^T, o = scale S^T q, T of them in turn.  The
 // state is the whole traffic of a single step, read and written once (64 sequences
-// of 32 heads of 128 x 128: 268 MB in 45 us, 5.9 TB/s, part of it still cached;
-// one of them: 4 MB in 4 us, a launch and two trips to memory).  One wave per 32
+// of 32 heads of 128 x 128: 268 MB in 43 us, 6.2 TB/s, part of it still cached;
+// one of them: 4 MB in 4.4 us, a launch and two trips to memory).  One wave per 32
 // columns of one (b, h): lane 8 rg + cq holds rows rg RL .. + RL - 1 of columns 4 cq
 // .. + 3, so eight lanes cover 128 contiguous bytes of a row.  The next step's q, k
 // and v are asked for ahead of the step's own sums, as whole pieces of a row (element

@@ -107,7 +107,9 @@ Cut cut(const gdn_dims* p, const DecayDims& d, bool bwd) {
   // states' part grows with their number).  128 x 128 heads, us, one pass against
   // segments: 8 heads, 130 steps 15 / 20, 512 steps 31 / 25; 64 heads, 512 steps
   // 31 / 35, 1024 steps 55 / 42; backward 64 heads, 512 steps 79 / 86, 1024 steps
-  // 139 / 121; fp32 8 heads, 256 steps 55 / 32.
+  // 139 / 121; fp32 8 heads, 256 steps 55 / 32.  (The rule knows pairs and chunks
+  // only: it leaves compute units idle at 129 to 255 (b, h), which stay one segment
+  // each, and does not weigh a wide head's dearer chunks and states.)
   if (n > 1) {
     const float seg = static_cast<float>((nc + n - 1) / n), states = static_cast<float>(d.B) * d.Hv * n / 256.f;
     const float extra = p->dtype != GDN_BF16 ? 1.4f + states : bwd ? 1.5f + 6.f * states : 2.5f + 3.5f * states;

@@ -1,9 +1,10 @@
 // The walk kernel of the decay operator (see DecayWalk in gdn_decay.h).
 //
 // A workgroup owns one segment of one (batch, value head) and goes through its
-// chunks of CH steps with the whole state in registers: wave w holds columns
+// chunks of CH steps with the whole state beside it: wave w holds columns
 // 16 NTL w .. of all KD channels, fp32, in the accumulator layout of the matrix
-// cores.  With c_i the valid steps of the chunk up to step i (counted in walk
+// cores.  These are registers for the narrower heads; the wider classes keep a part
+// in scratch (see below).  With c_i the valid steps of the chunk up to step i (counted in walk
 // order; up to and with i forward in time, before i backward), L its valid steps,
 // and g = e^lg:
 //   P_ij = [j <= i] g^(c_i - c_j) (x_i . y_j)
@@ -16,8 +17,8 @@
 // the fp32 ones for fp32 tensors.  Where bf16 operands are not tensors as they
 // were given, they are rounded as follows:
 //   - g^(L - c_j) z_j, which the state sums: as three bf16 parts (24 bits), so
-//     the state keeps fp32 precision over any number of steps; two parts (16
-//     bits) where only bf16 results are read from this state;
+//     the state keeps fp32 precision; two parts (16 bits) where only bf16 results
+//     are read from this state;
 //   - the state against x: one bf16 part, as the result is rounded to bf16 (a
 //     relative error of at most 2^-8 for each product, independent between the
 //     products);
@@ -55,6 +56,24 @@
 // vector instructions 34%, LDS reads 39%: the bound is their order inside a chunk (P
 // before P z, the old state before the new one, barriers between), with too few
 // registers for a second workgroup beside the state.
+//
+// One workgroup takes all columns of a head, whatever KD is, so wide heads do not
+// fit the registers.  Scratch of the output walks, bytes a lane, by classes KD x N:
+//   bf16          128 x 192 / 256   32 / 84;   192 x 192 / 256   84 / 384;
+//                 256 x 128 / 192 / 256   16 / 344 / 1168
+//   fp32          128 x 192 / 256  100 / 160;  192 x 128 / 192 / 256   120 / 552 / 976;
+//                 256 x 128 / 192 / 256  272 / 736 / 1504
+//   fp32 dq, dk   64 x 192 / 256   180 / 300;  128 x 128 / 192 / 256   88 / 576 / 1056;
+//                 192 x 128 / 192 / 256  668 / 1328 / 2424;  256 x 128 / 192 / 256
+//                 1016 / 1864 / 3284
+// (fp32 sums of 192 x 192 and wider 48 to 120; all else none.)  What it costs: 32 heads,
+// 2048 steps, forward and backward in us, 128 x 128, 192 x 192 and 256 x 256: bf16 49 and
+// 125, 86 and 288, 355 and 518; fp32 104 and 296, 403 and 1652, 760 and 3172, where
+// the products alone are 4 times those of 128 x 128.
+//
+// The decay of a chunk, g^L, is one fp32 number, and its rounding is the same for
+// every full chunk: a state that remembers n steps is off by n / CH times 2^-24 of
+// it at most (1e-5 at lg = -1e-4 for CH = 64).
 #pragma once
 
 #include "gdn_dev.h"
