@@ -554,6 +554,13 @@ def _on_device(dev):
     return _here if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
+def _cotangent(x):
+    """A gradient as the entries take it: dense, and at 16 bytes (autograd hands on
+    views into larger gradients, which may begin anywhere)."""
+    x = x.contiguous()
+    return x if x.data_ptr() % 16 == 0 else x.clone()
+
+
 # the handle of a device's current stream, without the object around it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -645,8 +652,8 @@ class DecayAttention(torch.autograd.Function):
         if dO is None and dS is None:
             return (None,) * 7
         q, k, v, lg, state0, mask = ctx.saved_tensors
-        g = decay_bwd(q, k, v, lg, state0, mask, torch.zeros_like(v) if dO is None else dO.contiguous(),
-                      None if dS is None else dS.contiguous(), scale=ctx.scale)
+        g = decay_bwd(q, k, v, lg, state0, mask, torch.zeros_like(v) if dO is None else _cotangent(dO),
+                      None if dS is None else _cotangent(dS), scale=ctx.scale)
         return (g["dq"], g["dk"], g["dv"], g["dlg"], g["dstate"] if state0 is not None else None, None, None)
 
 
@@ -749,5 +756,5 @@ class NormRope(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dyq, dyk):
         q, k, wq, wk, rope, pos = ctx.saved_tensors
-        g = norm_rope_bwd(q, k, wq, wk, rope, pos, dyq.contiguous(), dyk.contiguous(), **ctx.kw)
+        g = norm_rope_bwd(q, k, wq, wk, rope, pos, _cotangent(dyq), _cotangent(dyk), **ctx.kw)
         return (g["dq"], g["dk"], g["dwq"], g["dwk"]) + (None,) * 5
