@@ -138,3 +138,15 @@ def test_prompts(size, dtype, interleaved, packed):
     e = weights(c, g, interleaved)
     say("[norm prompt] shares of the weights' bounds: " + " ".join("%s=%.3f" % kv for kv in e.items()))
     assert all(x <= 1.0 for x in e.values()), e
+
+
+@pytest.mark.parametrize("Rr", [0, 32])
+def test_no_tokens(Rr):
+    """No rows: empty outputs, zero gradients of the weights."""
+    c = make(2, 0, 3, 2, 64, Rr, BF, 4, False)
+    for pos in (None, c["pos"]):
+        oq, ok = binding.norm_rope(c["q"], c["k"], c["wq"], c["wk"], c["rope"], pos, **KW)
+        g = binding.norm_rope_bwd(c["q"], c["k"], c["wq"], c["wk"], c["rope"], pos, c["dyq"], c["dyk"], **KW)
+        torch.cuda.synchronize()
+        assert oq.shape == g["dq"].shape == (2, 0, 3, 64) and ok.shape == g["dk"].shape == (2, 0, 2, 64)
+        assert (g["dwq"] == 0).all() and (g["dwk"] == 0).all()
