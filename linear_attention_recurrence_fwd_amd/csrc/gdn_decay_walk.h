@@ -4,9 +4,9 @@
 // chunks of CH steps with the whole state beside it: wave w holds columns
 // 16 NTL w .. of all KD channels, fp32, in the accumulator layout of the matrix
 // cores.  These are registers for the narrower heads; the wider classes keep a part
-// in scratch (see below).  With c_i the valid steps of the chunk up to step i (counted in walk
-// order; up to and with i forward in time, before i backward), L its valid steps,
-// and g = e^lg:
+// in scratch (see below).  With c_i the valid steps of the chunk up to step i
+// (counted in walk order; up to and with i forward in time, before i backward), L
+// its valid steps, and g = e^lg:
 //   P_ij = [j <= i] g^(c_i - c_j) (x_i . y_j)
 //   w_i  = g^c_i S^T x_i + sum_j P_ij z_j
 //   S   <- g^L S + sum_j y_j (g^(L - c_j) z_j)^T
@@ -72,8 +72,9 @@
 // the products alone are 4 times those of 128 x 128.
 //
 // The decay of a chunk, g^L, is one fp32 number, and its rounding is the same for
-// every full chunk: a state that remembers n steps is off by n / CH times 2^-24 of
-// it at most (1e-5 at lg = -1e-4 for CH = 64).
+// every full chunk, or every call of L steps: a state that remembers n steps is off by
+// n / L times 2^-24 of it at most (1e-5 at lg = -1e-4 for chunks of 64, where the
+// roundings of its sums come to 1e-6).
 #pragma once
 
 #include "gdn_dev.h"
