@@ -34,7 +34,7 @@ struct Sizes {
 };
 bool overlap(const Range& a, const Range& b) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return a.p && b.p && x < y + b.n && y < x + a.n;
+  return a.p && b.p && a.n && b.n && x < y + b.n && y < x + a.n;
 }
 template <int NO, int NI> bool overlaps(const Range (&out)[NO], const Range (&in)[NI]) {
   for (int i = 0; i < NO; ++i) {

@@ -59,3 +59,13 @@ def test_weight_gradients_off_each_other_and_the_workspace():
     for i in (2, 3, 4, 5):  # the workspace on what is read
         a = places(12)
         assert B.lib().gdn_norm_rope_bwd(ctypes.byref(dims()), *a, a[i], 1 << 20, None) == INVALID
+
+
+def test_nothing_overlaps_no_bytes():
+    """Without tokens there is nothing to write, wherever the outputs point (and no launch)."""
+    d = B.NormDims(2, 0, 4, 2, 64, 32, 4096, 0, 0, B.GDN_BF16, 0, 1e-6, 0.0)
+    for out in (6, 7):
+        for other in (2, 3, 4):
+            a = places(8)
+            a[out] = ctypes.c_void_p(a[other].value + 16)
+            assert B.lib().gdn_norm_rope_fwd(ctypes.byref(d), *a, None) == 0, (out, other)
