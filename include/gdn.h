@@ -384,6 +384,117 @@ int gdn_norm_rope_bwd(const gdn_norm_dims* d, const void* q, const void* k, cons
                       size_t ws_bytes, void* stream);
 
 /*
+ * The same with positions on A axes (time, height and width of images and video),
+ * and with or without the norm:
+ *   axis [R/2] uint8, the axis of each pair (NULL = all pairs on the first);
+ *   pos  [A,B,T] int32 (NULL = 0 .. T-1 on every axis), A from 1 to 4:
+ *       c = rope[pos[axis[i]][b][t]][i],  s = rope[pos[axis[i]][b][t]][R/2 + i]
+ *   wq, wk: both given, or both NULL: no norm (u = x; eps and w_offset unused).
+ * A position outside the table, or an axis outside 0 .. A-1, turns the pairs that
+ * it concerns to NaN (positions without axis: all R channels).  Otherwise as
+ * gdn_norm_rope_fwd / _bwd, the workspace query among them.  Without the norm the
+ * VJP reads neither q nor k (NULL allowed) and writes no dwq, dwk, and needs no
+ * workspace.
+ */
+int gdn_norm_rope_axes_fwd(const gdn_norm_dims* d, int32_t A, const void* q, const void* k,
+                           const float* wq, const float* wk, const float* rope, const uint8_t* axis,
+                           const int32_t* pos, void* oq, void* ok, void* stream);
+int gdn_norm_rope_axes_bwd(const gdn_norm_dims* d, int32_t A, const void* q, const void* k,
+                           const float* wq, const float* wk, const float* rope, const uint8_t* axis,
+                           const int32_t* pos, const void* dyq, const void* dyk, void* dq, void* dk,
+                           float* dwq, float* dwk, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Keys and values of sequences in pages: a pool of `pages` pages, each with room
+ * for `page` tokens of Hk heads of D channels, keys and values in two tensors of
+ * the same strides.  Row (page p, head h, token t) lies at
+ *   p * page_stride + h * head_stride + t * token_stride    (elements),
+ * so pages of whole tokens, pages head by head, and keys beside values in one
+ * tensor are all such pools.  A sequence's tokens 0, 1, ... lie in the pages of
+ * its row of a table [S, width] int32, page by page.
+ */
+typedef struct gdn_paged_dims {
+  int64_t N;                   /* tokens of the call: rows of q, k, v, o      */
+  int64_t S;                   /* sequences                                   */
+  int64_t Hq, Hk, D;           /* Hq % Hk == 0; D a multiple of 8 from 8 to 256 */
+  int64_t pages, page;         /* page: a power of two from 1 to 4096         */
+  int64_t width;               /* pages of a row of the table                 */
+  int64_t page_stride, head_stride, token_stride; /* multiples of 16 bytes;
+                                  rows of D elements must not overlap         */
+  int32_t dtype;               /* enum gdn_dtype: q, k, v, o and the pool     */
+} gdn_paged_dims;
+
+/*
+ * Appends the N tokens of a call to their sequences: with the norm and the
+ * rotation of gdn_norm_rope_axes_fwd, queries to oq and keys into the pool;
+ * values into the pool as they are.
+ *   cu   [S+1] int32: sequence s has the tokens cu[s] .. cu[s+1] - 1 (from 0 on,
+ *        not decreasing); NULL = N / S tokens each.  Rows behind cu[S] (a padded
+ *        batch) are neither read nor written.
+ *   past [S] int32: tokens of each sequence that the cache holds already; the i-th
+ *        new one goes to place past[s] + i.  A place behind the table's row, or on
+ *        a page outside 0 .. pages-1, is not written (the queries are).  Every
+ *        written place must belong to one token of the call.
+ *   pos  [A,N] int32, the positions of the rotation; NULL = first + past[s] + i on
+ *        every axis (first: the length of a prefix before the sequence, for one)
+ *   q [N,Hq,D], k, v [N,Hk,D]: tokens q_stride, k_stride, v_stride apart (0 =
+ *        dense); q and oq both NULL: keys and values alone.  oq dense.
+ *   wq, wk, rope, axis, P, R, A, interleaved, eps, w_offset: as above (wq, wk given
+ *        both, or neither; without q, wk alone)
+ * Outputs must not overlap inputs or each other (keys and values may lie in one
+ * tensor, row beside row).  Alignment: all but axis, pos, cu, past and the table 16 bytes.
+ */
+typedef struct gdn_turn {
+  int64_t P, R;                /* the table of cosines and sines              */
+  int64_t q_stride, k_stride, v_stride;
+  int64_t first;
+  int32_t A, interleaved;
+  float eps, w_offset;
+} gdn_turn;
+int gdn_paged_append(const gdn_paged_dims* d, const gdn_turn* t, const void* q, const void* k,
+                     const void* v, const float* wq, const float* wk, const float* rope,
+                     const uint8_t* axis, const int32_t* pos, const int32_t* table,
+                     const int32_t* past, const int32_t* cu, void* oq, void* k_pages, void* v_pages,
+                     void* stream);
+
+/*
+ * Softmax attention of the N tokens of a call over a prefix that all sequences
+ * share and over their own tokens in the pool, which it only reads:
+ *   o_i = sum_j p_ij v_j,   p_i = softmax_j(scale q_i . k_j)
+ * where j runs over the `prefix` tokens in the pages prefix_pages, and over the own
+ * tokens 0 .. lens[s] - n + i for the i-th of a sequence's n tokens (causal: the
+ * call's tokens are the last n of lens[s]).  Query head h reads key head h / G, G =
+ * Hq / Hk.  A token that sees no key at all gives zeros (and lse = -inf).
+ *   d            the pool and the table of the sequences' own pages
+ *   prefix       tokens of the prefix, up to 2^30; 0 without (prefix_pages NULL)
+ *   prefix_pages [ceil(prefix / page)] int32
+ *   max_q        no sequence has more tokens in the call than this (host; 1 .. N).
+ *                With cu NULL it is N / S whatever is given.
+ *   max_len      no lens[s] is larger than this (host; up to width * page, and 2^30;
+ *                the size of the launch and of the workspace go by it)
+ *   cu           as gdn_paged_append; rows behind cu[S] are left as they are
+ *   lens         [S] int32, own tokens of each sequence, the call's among them
+ *   q, o         [N,Hq,D] dtype, dense;   lse [N,Hq] fp32 (NULL: not written): the
+ *                logarithm (base e) of the sum of e^(scale q . k)
+ * A sequence with lens outside 0 .. max_len or more than max_q tokens gives NaN; a
+ * page outside 0 .. pages-1 counts as rows of NaN.  Rows of the pool behind lens,
+ * and behind the prefix's end, are not read into anything, NaN or not.
+ *
+ * bf16: products of bf16 by the matrix cores with fp32 sums; the softmax's
+ * statistics are fp32; the weights p are rounded to bf16 for the product with v
+ * (2^-9 of each, at random: 1.1e-3 of the result in 2-norm where its own rounding is
+ * 1.7e-3).  fp32: fp32 products and sums throughout.
+ * Deterministic: the keys are split by sizes alone, and joined in a fixed order.
+ */
+int gdn_prefix_attention_workspace_bytes(const gdn_paged_dims* d, int64_t prefix, int64_t max_q,
+                                         int64_t max_len, size_t* out);
+int gdn_prefix_attention(const gdn_paged_dims* d, const void* q, const void* k_pages,
+                         const void* v_pages, const int32_t* table, const int32_t* lens,
+                         const int32_t* prefix_pages, int64_t prefix, const int32_t* cu,
+                         int64_t max_q, int64_t max_len, float scale, void* o, float* lse, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/*
  * Optional per-kernel timing, for benchmarks and profilers.  While `events`
  * is non-NULL, each kernel that the following gdn_fwd / gdn_bwd calls launch
  * (in launch order, i = 0, 1, ...) records events[2i] on the call's stream

@@ -31,6 +31,8 @@ EXPORTS = ("gdn_ckpt_elems", "gdn_ckpt_bytes", "gdn_workspace_bytes", "gdn_fwd_w
            "gdn_bwd_vg_workspace_bytes", "gdn_fwd_vg", "gdn_bwd_vg",
            "gdn_decay_fwd_workspace_bytes", "gdn_decay_bwd_workspace_bytes", "gdn_decay_fwd", "gdn_decay_bwd",
            "gdn_norm_rope_fwd", "gdn_norm_rope_bwd_workspace_bytes", "gdn_norm_rope_bwd",
+           "gdn_norm_rope_axes_fwd", "gdn_norm_rope_axes_bwd",
+           "gdn_paged_append", "gdn_prefix_attention_workspace_bytes", "gdn_prefix_attention",
            "gdn_set_kernel_events",
            "gdn_status_string", "gdn_version")
 
@@ -47,6 +49,17 @@ class NormDims(ctypes.Structure):
                 ("P", ctypes.c_int64), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
                 ("dtype", ctypes.c_int32), ("interleaved", ctypes.c_int32),
                 ("eps", ctypes.c_float), ("w_offset", ctypes.c_float)]
+
+
+class PagedDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("N", "S", "Hq", "Hk", "D", "pages", "page", "width", "page_stride",
+                                              "head_stride", "token_stride")] + [("dtype", ctypes.c_int32)]
+
+
+class Turn(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("P", "R", "q_stride", "k_stride", "v_stride", "first")] + \
+               [("A", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("w_offset", ctypes.c_float)]
 
 
 class GdnError(RuntimeError):
@@ -100,6 +113,17 @@ def lib():
         L.gdn_norm_rope_bwd_workspace_bytes.restype = ctypes.c_int
         L.gdn_norm_rope_bwd.argtypes = [PN] + [P] * 13 + [S, P]
         L.gdn_norm_rope_bwd.restype = ctypes.c_int
+        L.gdn_norm_rope_axes_fwd.argtypes = [PN, ctypes.c_int32] + [P] * 10
+        L.gdn_norm_rope_axes_fwd.restype = ctypes.c_int
+        L.gdn_norm_rope_axes_bwd.argtypes = [PN, ctypes.c_int32] + [P] * 14 + [S, P]
+        L.gdn_norm_rope_axes_bwd.restype = ctypes.c_int
+        PP, I64 = ctypes.POINTER(PagedDims), ctypes.c_int64
+        L.gdn_paged_append.argtypes = [PP, ctypes.POINTER(Turn)] + [P] * 15
+        L.gdn_paged_append.restype = ctypes.c_int
+        L.gdn_prefix_attention_workspace_bytes.argtypes = [PP, I64, I64, I64, ctypes.POINTER(S)]
+        L.gdn_prefix_attention_workspace_bytes.restype = ctypes.c_int
+        L.gdn_prefix_attention.argtypes = [PP] + [P] * 6 + [I64, P, I64, I64, ctypes.c_float] + [P] * 3 + [S, P]
+        L.gdn_prefix_attention.restype = ctypes.c_int
         L.gdn_set_kernel_events.argtypes = [ctypes.POINTER(ctypes.c_void_p), ctypes.c_int]
         L.gdn_set_kernel_events.restype = ctypes.c_int
         L.gdn_status_string.argtypes = [ctypes.c_int]
@@ -694,8 +718,9 @@ def _norm_dims(q, k, wq, wk, rope, pos, eps, w_offset, interleaved):
         raise TypeError("k: expected %s, got %s" % (dt, k.dtype))
     if k.shape != (B, T, Hk, D) or k.device != dev:
         raise ValueError("k: expected shape %s on %s, got %s on %s" % ((B, T, Hk, D), dev, tuple(k.shape), k.device))
-    _check(wq, "wq", (D,), torch.float32, dev)
-    _check(wk, "wk", (D,), torch.float32, dev)
+    for w, name in ((wq, "wq"), (wk, "wk")):
+        if w is not None:
+            _check(w, name, (D,), torch.float32, dev)
     P, R = 0, 0
     if rope is not None:
         P, R = rope.shape
@@ -758,3 +783,247 @@ class NormRope(torch.autograd.Function):
         q, k, wq, wk, rope, pos = ctx.saved_tensors
         g = norm_rope_bwd(q, k, wq, wk, rope, pos, _cotangent(dyq), _cotangent(dyk), **ctx.kw)
         return (g["dq"], g["dk"], g["dwq"], g["dwk"]) + (None,) * 5
+
+
+# ---- rotation with positions on several axes (gdn_norm_rope_axes_fwd / _bwd)
+
+def axis_map(pairs, cycle=False, device="cuda"):
+    """The axis of each pair for the operators below: pairs[a] pairs turn by axis
+    a's position, in blocks (pairs of axis 0 first), or with cycle=True one of each
+    axis in turn while it has any left."""
+    if cycle:
+        left, out = list(pairs), []
+        while any(left):
+            for a in range(len(left)):
+                if left[a]:
+                    out.append(a)
+                    left[a] -= 1
+    else:
+        out = [a for a, n in enumerate(pairs) for _ in range(n)]
+    return torch.tensor(out, dtype=torch.uint8, device=device)
+
+
+def _axes_of(d, rope, axis, pos, tokens, dev):
+    """The number of axes of checked positions and axis map (without positions, as many
+    as there can be: they are the same on all)."""
+    if axis is not None:
+        _check(axis, "axis", (rope.shape[1] // 2 if rope is not None else 0,), torch.uint8, dev)
+    if pos is None:
+        return 4
+    if pos.dim() != 1 + len(tokens) or not 1 <= pos.shape[0] <= 4:
+        raise ValueError("pos: expected shape (1 .. 4 axes, %s), got %s" % (", ".join(map(str, tokens)), tuple(pos.shape)))
+    _check(pos, "pos", (pos.shape[0], *tokens), torch.int32, dev)
+    return pos.shape[0]
+
+
+def norm_rope_axes(q, k, wq=None, wk=None, rope=None, axis=None, pos=None, *, eps=1e-6, w_offset=0.0,
+                   interleaved=False):
+    """norm_rope with positions on up to four axes: pos [A,B,T] int32, axis [R/2]
+    uint8 the axis of each pair (axis_map).  Without wq and wk, the rotation alone."""
+    d, A = _norm_axes_dims(q, k, wq, wk, rope, axis, pos, eps, w_offset, interleaved)
+    dev, dt = q.device, q.dtype
+    oq = torch.empty((d.B, d.T, d.Hq, d.D), dtype=dt, device=dev)
+    ok = torch.empty((d.B, d.T, d.Hk, d.D), dtype=dt, device=dev)
+    with _on_device(dev):
+        rc = lib().gdn_norm_rope_axes_fwd(d, A, _a(q), _a(k), _a(wq), _a(wk), _a(rope), _a(axis), _a(pos), _a(oq),
+                                          _a(ok), _raw_stream(dev.index))
+    if rc:
+        raise GdnError("gdn_norm_rope_axes_fwd", rc)
+    return oq, ok
+
+
+def _norm_axes_dims(q, k, wq, wk, rope, axis, pos, eps, w_offset, interleaved):
+    if (wq is None) != (wk is None):
+        raise ValueError("wq and wk: both, or neither")
+    d = _norm_dims(q, k, wq, wk, rope, None, eps, w_offset, interleaved)
+    return d, _axes_of(d, rope, axis, pos, (d.B, d.T), q.device)
+
+
+def norm_rope_axes_bwd(q, k, wq, wk, rope, axis, pos, dyq, dyk, *, eps=1e-6, w_offset=0.0, interleaved=False):
+    """VJP of norm_rope_axes.  Returns dict(dq, dk, dwq, dwk), dq and dk dense, dwq and
+    dwk None without the norm."""
+    d, A = _norm_axes_dims(q, k, wq, wk, rope, axis, pos, eps, w_offset, interleaved)
+    dev = q.device
+    _check(dyq, "dyq", q.shape, q.dtype, dev)
+    _check(dyk, "dyk", k.shape, q.dtype, dev)
+    out = dict(dq=torch.empty_like(dyq), dk=torch.empty_like(dyk), dwq=None if wq is None else torch.empty_like(wq),
+               dwk=None if wk is None else torch.empty_like(wk))
+    wsb = 0 if wq is None else _query("gdn_norm_rope_bwd_workspace_bytes", d)
+    ws = torch.empty((wsb,), dtype=torch.uint8, device=dev) if wsb else None
+    with _on_device(dev):
+        rc = lib().gdn_norm_rope_axes_bwd(d, A, _a(q), _a(k), _a(wq), _a(wk), _a(rope), _a(axis), _a(pos), _a(dyq),
+                                          _a(dyk), *[_a(out[n]) for n in ("dq", "dk", "dwq", "dwk")], _a(ws), wsb,
+                                          _raw_stream(dev.index))
+    if rc:
+        raise GdnError("gdn_norm_rope_axes_bwd", rc)
+    return out
+
+
+class NormRopeAxes(torch.autograd.Function):
+    """Autograd wrapper of norm_rope_axes / norm_rope_axes_bwd: forward(q, k, wq, wk,
+    rope, axis, pos, eps, w_offset, interleaved) returns (q, k)."""
+
+    @staticmethod
+    def forward(ctx, q, k, wq=None, wk=None, rope=None, axis=None, pos=None, eps=1e-6, w_offset=0.0, interleaved=False):
+        ctx.save_for_backward(q, k, wq, wk, rope, axis, pos)
+        ctx.kw = dict(eps=eps, w_offset=w_offset, interleaved=interleaved)
+        return norm_rope_axes(q, k, wq, wk, rope, axis, pos, **ctx.kw)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dyq, dyk):
+        q, k, wq, wk, rope, axis, pos = ctx.saved_tensors
+        g = norm_rope_axes_bwd(q, k, wq, wk, rope, axis, pos, _cotangent(dyq), _cotangent(dyk), **ctx.kw)
+        return (g["dq"], g["dk"], g["dwq"], g["dwk"]) + (None,) * 6
+
+
+# ---- keys and values in pages (gdn_paged_append, gdn_prefix_attention)
+
+def _rows_stride(x, name, shape):
+    """Elements between the rows of consecutive tokens of [N, H, D] (0: dense)."""
+    if tuple(x.shape) != shape:
+        raise ValueError("%s: expected shape %s, got %s" % (name, shape, tuple(x.shape)))
+    if x.is_contiguous():
+        return 0
+    N, H, D = shape
+    sn, sh, sd = x.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D) or (N > 1 and sn < H * D):
+        raise ValueError("%s: the heads of a token must be contiguous, and tokens must not overlap" % name)
+    return sn if N > 1 else 0
+
+
+@functools.lru_cache(maxsize=256)
+def _paged_dims(*dims):
+    return PagedDims(*dims)
+
+
+@functools.lru_cache(maxsize=256)
+def _turn_dims(*dims):
+    return Turn(*dims)
+
+
+@functools.lru_cache(maxsize=256)
+def _attention_ws(prefix, max_q, max_len, *dims):
+    out = ctypes.c_size_t(0)
+    rc = lib().gdn_prefix_attention_workspace_bytes(_paged_dims(*dims), prefix, max_q, max_len, ctypes.byref(out))
+    if rc:
+        raise GdnError("gdn_prefix_attention_workspace_bytes", rc)
+    return out.value
+
+
+def _check_pool(k_pages, v_pages, table, cu, N, Hq, dt, dev):
+    """The dims of a checked pool and table."""
+    if dev.type != "cuda":
+        raise ValueError("gdn runs on the GPU; got device %s" % dev)
+    if dt != torch.bfloat16 and dt != torch.float32:
+        raise TypeError("expected float32 or bfloat16, got %s" % dt)
+    pages, Hk, page, D = k_pages.shape
+    for x, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        if x.dtype != dt:
+            raise TypeError("%s: expected %s, got %s" % (name, dt, x.dtype))
+        if x.shape != k_pages.shape or x.device != dev:
+            raise ValueError("%s: expected shape %s on %s, got %s on %s" % (name, tuple(k_pages.shape), dev,
+                                                                            tuple(x.shape), x.device))
+    strides = k_pages.stride()
+    if v_pages.stride() != strides or (D > 1 and strides[3] != 1):
+        raise ValueError("k_pages and v_pages: expected the same strides, and contiguous rows")
+    S, width = table.shape
+    _check(table, "table", (S, width), torch.int32, dev)
+    if cu is not None:
+        _check(cu, "cu", (S + 1,), torch.int32, dev)
+    return (N, S, Hq, Hk, D, pages, page, width, strides[0], strides[1], strides[2],
+            GDN_F32 if dt == torch.float32 else GDN_BF16)
+
+
+def paged_append(q, k, v, k_pages, v_pages, table, past, cu=None, *, wq=None, wk=None, rope=None, axis=None, pos=None,
+                 first=0, eps=1e-6, w_offset=0.0, interleaved=False, out=None):
+    """Appends the tokens of a call to a paged cache (gdn_paged_append): queries q
+    [N,Hq,D] and keys k [N,Hk,D] with the norm and the rotation of norm_rope_axes,
+    values v [N,Hk,D] as they are.  Keys and values go into k_pages, v_pages
+    [pages,Hk,page,D] (any strides with contiguous rows, the same for both), to place
+    past[s] + i of sequence s, whose pages are table[s].  Sequence s has the tokens
+    cu[s] .. cu[s+1] - 1, or N / S tokens each.  q, k, v may be slices of a packed
+    projection; q may be None.  Returns the turned queries (in out, if given)."""
+    N, Hk, D = k.shape
+    dev, dt = k.device, k.dtype
+    Hq = 0 if q is None else q.shape[1]
+    dims = _check_pool(k_pages, v_pages, table, cu, N, Hq, dt, dev)
+    if dims[3] != Hk or dims[4] != D:
+        raise ValueError("k: expected %d heads of %d, got %d of %d" % (dims[3], dims[4], Hk, D))
+    for x, name in ((q, "q"), (v, "v")):
+        if x is not None and x.dtype != dt:
+            raise TypeError("%s: expected %s, got %s" % (name, dt, x.dtype))
+        if x is not None and x.device != dev:
+            raise ValueError("%s: expected device %s, got %s" % (name, dev, x.device))
+    _check(past, "past", (dims[1],), torch.int32, dev)
+    for x, name in ((wq, "wq"), (wk, "wk")):
+        if x is not None:
+            _check(x, name, (D,), torch.float32, dev)
+    P, R = 0, 0
+    if rope is not None:
+        P, R = rope.shape
+        _check(rope, "rope", (P, R), torch.float32, dev)
+    A = _axes_of(None, rope, axis, pos, (N,), dev)
+    if q is None:
+        qs = 0
+        if out is not None:
+            raise ValueError("out without q")
+    else:
+        qs = _rows_stride(q, "q", (N, Hq, D))
+        if out is None:
+            out = torch.empty((N, Hq, D), dtype=dt, device=dev)
+        else:
+            _check(out, "out", (N, Hq, D), dt, dev)
+    turn = _turn_dims(P, R, qs, _rows_stride(k, "k", (N, Hk, D)), _rows_stride(v, "v", (N, Hk, D)), first, A,
+                      1 if interleaved else 0, eps, w_offset)
+    with _on_device(dev):
+        rc = lib().gdn_paged_append(_paged_dims(*dims), turn, _a(q), _a(k), _a(v), _a(wq), _a(wk), _a(rope), _a(axis),
+                                    _a(pos), _a(table), _a(past), _a(cu), _a(out), _a(k_pages), _a(v_pages),
+                                    _raw_stream(dev.index))
+    if rc:
+        raise GdnError("gdn_paged_append", rc)
+    return out
+
+
+def prefix_attention(q, k_pages, v_pages, table, lens, prefix_pages=None, prefix=0, cu=None, *, max_q=None,
+                     max_len=None, scale=None, out=None, lse=False):
+    """Softmax attention of new tokens over a shared prefix and their sequences' own
+    pages (gdn_prefix_attention): q [N,Hq,D] the tokens' queries, sequence s's being the
+    last of its lens[s] own tokens in the pages table[s]; the prefix's first `prefix`
+    tokens lie in prefix_pages.  cu as in paged_append.  max_q (N by default, with cu)
+    and max_len (the room of a table's row) bound a sequence's tokens in the call and its
+    own length: the launch goes by them.  scale: D^-1/2 by default.  Returns o [N,Hq,D]
+    (in out, if given), with lse=True (o, lse [N,Hq] fp32)."""
+    N, Hq, D = q.shape
+    dev, dt = q.device, q.dtype
+    dims = _check_pool(k_pages, v_pages, table, cu, N, Hq, dt, dev)
+    S, page = dims[1], dims[6]
+    _check(q, "q", (N, Hq, dims[4]), dt, dev)
+    _check(lens, "lens", (S,), torch.int32, dev)
+    if prefix_pages is not None:
+        _check(prefix_pages, "prefix_pages", prefix_pages.shape, torch.int32, dev)
+    if prefix and (prefix_pages is None or prefix_pages.dim() != 1 or prefix_pages.shape[0] * page < prefix):
+        raise ValueError("prefix_pages: %d tokens of a prefix need %d pages" % (prefix, -(-prefix // page)))
+    if max_len is None:
+        max_len = min(dims[7] * page, 1 << 30)
+    if cu is None:
+        if N % S:
+            raise ValueError("%d tokens of %d sequences: cu is needed" % (N, S))
+        max_q = N // S
+    elif max_q is None or max_q > N:
+        max_q = N
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check(out, "out", q.shape, dt, dev)
+    sums = torch.empty((N, Hq), dtype=torch.float32, device=dev) if lse else None
+    wsb = _attention_ws(prefix, max_q, max_len, *dims)
+    ws = torch.empty((wsb,), dtype=torch.uint8, device=dev) if wsb else None
+    with _on_device(dev):
+        rc = lib().gdn_prefix_attention(_paged_dims(*dims), _a(q), _a(k_pages), _a(v_pages), _a(table), _a(lens),
+                                        _a(prefix_pages) if prefix else None, prefix, _a(cu), max_q, max_len,
+                                        dims[4] ** -0.5 if scale is None else scale, _a(out), _a(sums), _a(ws), wsb,
+                                        _raw_stream(dev.index))
+    if rc:
+        raise GdnError("gdn_prefix_attention", rc)
+    return (out, sums) if lse else out

@@ -159,6 +159,11 @@ struct NormRopeArgs {
   float* part;              // backward: [blocks, 2, D]
   float *dwq, *dwk;
   int blocks;
+  // rotation with several axes (A of them; 0: the operator with one)
+  int A;
+  const uint8_t* axis;      // [R/2], may be null: all pairs on the first; pos is [A, BT]
+  int bare;                 // no norm and no weights
+  int back;                 // forward kernel: the inverse rotation (the VJP without norm)
 };
 int norm_rope_blocks(int64_t BT, int Hq, int Hk, int D, bool bf16);
 hipError_t launch_norm_rope_fwd(const NormRopeArgs& a, bool bf16, hipStream_t st);

@@ -2,6 +2,7 @@
 // in include/gdn.h): argument validation, workspace layout and launch order.
 // No allocation, no host sync.
 #include "../../include/gdn.h"
+#include "gdn_checks.h"
 #include "gdn_decay.h"
 
 #include <limits.h>
@@ -9,17 +10,13 @@
 namespace {
 
 using gdn::DecayDims;
+using gdn::align_up;
+using gdn::aligned;
+using gdn::all_aligned;
+using gdn::all_given;
+using gdn::overlaps;
+using gdn::Range;
 
-size_t align_up(size_t n) { return (n + 255) / 256 * 256; }
-bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-template <typename... P> bool all_aligned(P... p) { return (aligned(p) && ...); }
-template <typename... P> bool all_given(P... p) { return (... && (p != nullptr)); }
-
-// A tensor's bytes; whether any of the outputs shares some with any input or other output.
-struct Range {
-  const void* p;
-  size_t n;
-};
 // Bytes of the tensors with key heads, with value heads, of the states, mask and lg.
 struct Sizes {
   size_t key, val, state, mask, lg;
@@ -32,19 +29,6 @@ struct Sizes {
     lg = static_cast<size_t>(d->Hv) * 4;
   }
 };
-bool overlap(const Range& a, const Range& b) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return a.p && b.p && a.n && b.n && x < y + b.n && y < x + a.n;
-}
-template <int NO, int NI> bool overlaps(const Range (&out)[NO], const Range (&in)[NI]) {
-  for (int i = 0; i < NO; ++i) {
-    for (const Range& r : in)
-      if (overlap(out[i], r)) return true;
-    for (int j = 0; j < i; ++j)
-      if (overlap(out[i], out[j])) return true;
-  }
-  return false;
-}
 
 int check_dims(const gdn_dims* p, bool bwd, DecayDims* out) {
   if (!p) return GDN_ERR_INVALID_ARG;
@@ -219,6 +203,17 @@ int check_norm(const gdn_norm_dims* p, gdn::NormRopeArgs* a) {
   a->eps = p->eps;
   a->w_offset = p->w_offset;
   a->blocks = gdn::norm_rope_blocks(a->BT, a->Hq, a->Hk, a->D, p->dtype == GDN_BF16);
+  return GDN_OK;
+}
+
+// The rotation with A axes: weights for both norms or for none.
+int check_axes(const gdn_norm_dims* p, int32_t A, const float* wq, const float* wk, gdn::NormRopeArgs* a) {
+  const int rc = check_norm(p, a);
+  if (rc) return rc;
+  if (A < 1 || (wq == nullptr) != (wk == nullptr)) return GDN_ERR_INVALID_ARG;
+  if (A > 4) return GDN_ERR_UNSUPPORTED;
+  a->A = A;
+  a->bare = wq == nullptr;
   return GDN_OK;
 }
 
@@ -483,6 +478,85 @@ int gdn_norm_rope_bwd(const gdn_norm_dims* d, const void* q, const void* k, cons
   a.dwk = dwk;
   return gdn::launch_norm_rope_bwd(a, d->dtype == GDN_BF16, static_cast<hipStream_t>(stream)) == hipSuccess
              ? GDN_OK : GDN_ERR_HIP;
+}
+
+int gdn_norm_rope_axes_fwd(const gdn_norm_dims* d, int32_t A, const void* q, const void* k,
+                           const float* wq, const float* wk, const float* rope, const uint8_t* axis,
+                           const int32_t* pos, void* oq, void* ok, void* stream) {
+  gdn::NormRopeArgs a;
+  const int rc = check_axes(d, A, wq, wk, &a);
+  if (rc) return rc;
+  if (a.R > 0 && !rope) return GDN_ERR_INVALID_ARG;
+  if (a.BT > 0 && !all_given(q, k, oq, ok)) return GDN_ERR_INVALID_ARG;
+  if (!all_aligned(q, k, wq, wk, rope, oq, ok)) return GDN_ERR_INVALID_ARG;
+  const NormSizes z(d, a);
+  const Range out[] = {{oq, z.q}, {ok, z.k}};
+  const Range in[] = {{q, z.qs}, {k, z.ks}, {wq, z.w}, {wk, z.w}, {rope, z.rope}, {pos, z.pos * A},
+                      {axis, static_cast<size_t>(a.R / 2)}};
+  if (overlaps(out, in)) return GDN_ERR_INVALID_ARG;
+  a.q = q;
+  a.k = k;
+  a.wq = wq;
+  a.wk = wk;
+  a.rope = rope;
+  a.axis = axis;
+  a.pos = pos;
+  a.oq = oq;
+  a.ok = ok;
+  return gdn::launch_norm_rope_fwd(a, d->dtype == GDN_BF16, static_cast<hipStream_t>(stream)) == hipSuccess
+             ? GDN_OK : GDN_ERR_HIP;
+}
+
+int gdn_norm_rope_axes_bwd(const gdn_norm_dims* d, int32_t A, const void* q, const void* k,
+                           const float* wq, const float* wk, const float* rope, const uint8_t* axis,
+                           const int32_t* pos, const void* dyq, const void* dyk, void* dq, void* dk,
+                           float* dwq, float* dwk, void* ws, size_t ws_bytes, void* stream) {
+  gdn::NormRopeArgs a;
+  const int rc = check_axes(d, A, wq, wk, &a);
+  if (rc) return rc;
+  if (a.R > 0 && !rope) return GDN_ERR_INVALID_ARG;
+  if (a.BT > 0 && !all_given(dyq, dyk, dq, dk)) return GDN_ERR_INVALID_ARG;
+  if (!all_aligned(q, k, wq, wk, rope, dyq, dyk, dq, dk, dwq, dwk)) return GDN_ERR_INVALID_ARG;
+  const bool bf = d->dtype == GDN_BF16;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const NormSizes z(d, a);
+  a.rope = rope;
+  a.axis = axis;
+  a.pos = pos;
+  a.oq = dq;
+  a.ok = dk;
+  if (a.bare) {
+    // The rotation's VJP is the rotation back: a forward over the cotangents.
+    const Range out[] = {{dq, z.q}, {dk, z.k}};
+    const Range in[] = {{dyq, z.q}, {dyk, z.k}, {rope, z.rope}, {pos, z.pos * A}, {axis, static_cast<size_t>(a.R / 2)}};
+    if (overlaps(out, in)) return GDN_ERR_INVALID_ARG;
+    a.q = dyq;
+    a.k = dyk;
+    a.qs = d->Hq * d->D;
+    a.ks = d->Hk * d->D;
+    a.back = 1;
+    return gdn::launch_norm_rope_fwd(a, bf, st) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+  }
+  if (!all_given(dwq, dwk) || (a.BT > 0 && !all_given(q, k))) return GDN_ERR_INVALID_ARG;
+  const size_t need = align_up(static_cast<size_t>(a.blocks) * 2 * a.D * sizeof(float));
+  if (need > ws_bytes || (need > 0 && !ws)) return GDN_ERR_WORKSPACE;
+  if (need > 0 && !aligned(ws)) return GDN_ERR_INVALID_ARG;
+  const Range out[] = {{dq, z.q}, {dk, z.k}, {ws, need}};
+  const Range in[] = {{q, z.qs}, {k, z.ks}, {dyq, z.q}, {dyk, z.k}, {wq, z.w}, {wk, z.w}, {rope, z.rope},
+                      {pos, z.pos * A}, {axis, static_cast<size_t>(a.R / 2)}};
+  // (the weights' gradients are written when all inputs are read)
+  const Range dw[] = {{dwq, z.w}, {dwk, z.w}};
+  if (overlaps(out, in) || overlaps(dw, out)) return GDN_ERR_INVALID_ARG;
+  a.q = q;
+  a.k = k;
+  a.wq = wq;
+  a.wk = wk;
+  a.dyq = dyq;
+  a.dyk = dyk;
+  a.part = static_cast<float*>(ws);
+  a.dwq = dwq;
+  a.dwk = dwk;
+  return gdn::launch_norm_rope_bwd(a, bf, st) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
 }
 
 }  // extern "C"

@@ -21,140 +21,15 @@
 // dw's parts; fp32 201 MB in 41 us, 4.9 TB/s, and 302 MB in 51 us, 5.9 TB/s, a part of
 // it still cached.  64 tokens of 16 + 2 heads of 256, bf16 or fp32: 4 us, a launch and
 // a trip to memory.
-#include "gdn_dev.h"
 #include "gdn_decay.h"
+#include "gdn_rows.h"
 
 namespace gdn {
 namespace {
 
-template <typename T> struct Raw;  // eight channels as they are stored
-template <> struct Raw<bf16> {
-  uint4 u;
-  __device__ __forceinline__ void load(const bf16* p) { u = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void unpack(float* v) const { Vec16<bf16>::unpack(u, v); }
-  __device__ __forceinline__ Raw from_lane(int src) const {
-    Raw o;
-    o.u = make_uint4(__shfl(u.x, src), __shfl(u.y, src), __shfl(u.z, src), __shfl(u.w, src));
-    return o;
-  }
-  __device__ __forceinline__ static void store(bf16* p, const float* v) {
-    *reinterpret_cast<uint4*>(p) =
-        make_uint4(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]), pack2_bf16(v[4], v[5]), pack2_bf16(v[6], v[7]));
-  }
-};
-template <> struct Raw<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = *reinterpret_cast<const float4*>(p);
-    b = *reinterpret_cast<const float4*>(p + 4);
-  }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void unpack(float* v) const {
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  }
-  __device__ __forceinline__ Raw from_lane(int src) const {
-    Raw o;
-    o.a = make_float4(__shfl(a.x, src), __shfl(a.y, src), __shfl(a.z, src), __shfl(a.w, src));
-    o.b = make_float4(__shfl(b.x, src), __shfl(b.y, src), __shfl(b.z, src), __shfl(b.w, src));
-    return o;
-  }
-  __device__ __forceinline__ static void store(float* p, const float* v) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-  }
-};
-
-// Sum over the LPH lanes of a row; every lane gets the same bits.
-template <int LPH> __device__ __forceinline__ float row_sum(float v) {
-  if constexpr (LPH >= 2) v += dpp<kQuadXor1>(v);
-  if constexpr (LPH >= 4) v += dpp<kQuadXor2>(v);
-  if constexpr (LPH >= 8) v += dpp<kRowHalfMirror>(v);
-  if constexpr (LPH >= 16) v += dpp<kRowMirror>(v);
-  if constexpr (LPH >= 32) v += __shfl_xor(v, 16);
-  if constexpr (LPH >= 64) v += __shfl_xor(v, 32);
-  return v;
-}
-
-// What a lane keeps for a token: cos and sin of its channels' pairs.  A pair's
-// outputs are y1 = u1 cos - u2 sin, y2 = u2 cos + u1 sin, so a channel's is
-// its own u times cos plus the other's times -sin or sin.
-struct Turn {
-  float c[8], s[8];
-};
-
-template <int LPH, bool INTER> struct Lane {
-  int sub, c0, other;  // lane in the row, its first channel, the lane of the other channels
-  bool on, turned;
-  float sign;
-  __device__ __forceinline__ Lane(const NormRopeArgs& a) {
-    const int l = threadIdx.x & 63;
-    sub = l % LPH;
-    c0 = 8 * sub;
-    on = c0 < a.D;
-    turned = c0 < a.R;
-    const int half = a.R / 16;  // lanes of the first channels of the pairs
-    const int to = INTER || !turned ? sub : sub < half ? sub + half : sub - half;
-    other = (l - sub) + to;
-    sign = sub < half ? -1.f : 1.f;
-  }
-  // cos and sin at position pos (NaN where the table has no such row); back: of
-  // the inverse rotation
-  __device__ __forceinline__ void load(const NormRopeArgs& a, int64_t token, Turn& tn, bool back) const {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      tn.c[i] = 1.f;
-      tn.s[i] = 0.f;
-    }
-    if (!turned) return;
-    const int64_t pos = a.pos ? a.pos[token] : token % a.T;
-    const float flip = back ? -1.f : 1.f;
-    if (pos < 0 || pos >= a.P) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) tn.c[i] = tn.s[i] = __builtin_nanf("");
-      return;
-    }
-    const float* row = a.rope + pos * a.R;
-    if constexpr (INTER) {
-      const float4 c = *reinterpret_cast<const float4*>(row + c0 / 2);
-      const float4 s = *reinterpret_cast<const float4*>(row + a.R / 2 + c0 / 2);
-      const float cs[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        tn.c[i] = cs[i / 2];
-        tn.s[i] = (i & 1 ? flip : -flip) * ss[i / 2];
-      }
-    } else {
-      const int p0 = c0 < a.R / 2 ? c0 : c0 - a.R / 2;
-      Raw<float> c, s;
-      c.load(row + p0);
-      s.load(row + a.R / 2 + p0);
-      c.unpack(tn.c);
-      s.unpack(tn.s);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) tn.s[i] *= flip * sign;
-    }
-  }
-  // v turned, given the other channels' values (unused when interleaved)
-  __device__ __forceinline__ void turn(float* v, const float* o, const Turn& tn) const {
-    if constexpr (INTER) {
-#pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const float x = v[i], y = v[i + 1];
-        v[i] = turned ? x * tn.c[i] + y * tn.s[i] : x;
-        v[i + 1] = turned ? y * tn.c[i + 1] + x * tn.s[i + 1] : y;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = turned ? v[i] * tn.c[i] + o[i] * tn.s[i] : v[i];
-    }
-  }
-};
-
 __device__ __forceinline__ void load_w(const float* w, const NormRopeArgs& a, int c0, bool on, float* out) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) out[i] = on ? w[c0 + i] + a.w_offset : 0.f;
+  for (int i = 0; i < 8; ++i) out[i] = !on ? 0.f : w ? w[c0 + i] + a.w_offset : 1.f;
 }
 
 // A wave's work: token and run of head groups (a group: 64 / LPH heads); the
@@ -168,7 +43,7 @@ struct Work {
 // counted in 32 bits in each direction.  More go on in y.
 constexpr int64_t kFwdBlocks = 1 << 22;
 
-template <typename T, int LPH, bool INTER>
+template <typename T, int LPH, bool INTER, bool AXES>
 __global__ void __launch_bounds__(256) fwd_kernel(NormRopeArgs a, Work wk) {
   constexpr int RPW = 64 / LPH;
   const Lane<LPH, INTER> ln(a);
@@ -178,7 +53,7 @@ __global__ void __launch_bounds__(256) fwd_kernel(NormRopeArgs a, Work wk) {
   const int g0 = static_cast<int>(item % wk.runs) * wk.run, g1 = min(g0 + wk.run, wk.gq + wk.gk);
   const int sub_row = (threadIdx.x & 63) / LPH;
   Turn tn;
-  ln.load(a, token, tn, false);
+  ln.template load<AXES>(a, token, token % a.T, tn, AXES && a.back);
   const float inv = 1.f / static_cast<float>(a.D);
 #pragma unroll 1
   for (int part = 0; part < 2; ++part) {
@@ -203,7 +78,7 @@ __global__ void __launch_bounds__(256) fwd_kernel(NormRopeArgs a, Work wk) {
       float ss = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-      const float r = 1.f / sqrtf(row_sum<LPH>(ss) * inv + a.eps);
+      const float r = AXES && a.bare ? 1.f : 1.f / sqrtf(row_sum<LPH>(ss) * inv + a.eps);
       if constexpr (!INTER) {
         x.from_lane(ln.other).unpack(o);
 #pragma unroll
@@ -220,7 +95,7 @@ __global__ void __launch_bounds__(256) fwd_kernel(NormRopeArgs a, Work wk) {
 // The backward's blocks each take a run of tokens and leave their rows' part of
 // dw in the workspace, [block][2][D]: lanes sum over their rows, then the rows of
 // a wave, then the waves, all in a fixed order.
-template <typename T, int LPH, bool INTER>
+template <typename T, int LPH, bool INTER, bool AXES>
 __global__ void __launch_bounds__(256) bwd_kernel(NormRopeArgs a, Work wk) {
   constexpr int RPW = 64 / LPH;
   const Lane<LPH, INTER> ln(a);
@@ -239,7 +114,7 @@ __global__ void __launch_bounds__(256) bwd_kernel(NormRopeArgs a, Work wk) {
     const int64_t token = item / wk.runs;
     const int g0 = static_cast<int>(item % wk.runs) * wk.run, g1 = min(g0 + wk.run, wk.gq + wk.gk);
     Turn tn;
-    ln.load(a, token, tn, true);
+    ln.template load<AXES>(a, token, token % a.T, tn, true);
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
       const int lo = max(g0, part ? wk.gq : 0), hi = min(g1, part ? wk.gq + wk.gk : wk.gq);
@@ -315,12 +190,6 @@ __global__ void __launch_bounds__(1024) dw_kernel(NormRopeArgs a) {
   if (row == 0 && c < 2 * a.D) (c < a.D ? a.dwq : a.dwk)[c % a.D] = red[0][threadIdx.x & 7];
 }
 
-int lanes_for(int D) {
-  int n = 1;
-  while (8 * n < D) n *= 2;
-  return n;
-}
-
 Work work_of(const NormRopeArgs& a, int64_t waves) {
   const int rpw = 64 / lanes_for(a.D);
   Work w;
@@ -342,14 +211,24 @@ hipError_t launch_lph(const NormRopeArgs& a, bool bwd, hipStream_t st) {
     const int64_t n = (a.BT * w.runs + 3) / 4;
     const dim3 grid(static_cast<unsigned>(n < kFwdBlocks ? n : kFwdBlocks),
                     static_cast<unsigned>((n + kFwdBlocks - 1) / kFwdBlocks));
-    if (a.interleaved) fwd_kernel<T, LPH, true><<<grid, 256, 0, st>>>(a, w);
-    else fwd_kernel<T, LPH, false><<<grid, 256, 0, st>>>(a, w);
+    if (a.A) {
+      if (a.interleaved) fwd_kernel<T, LPH, true, true><<<grid, 256, 0, st>>>(a, w);
+      else fwd_kernel<T, LPH, false, true><<<grid, 256, 0, st>>>(a, w);
+    } else {
+      if (a.interleaved) fwd_kernel<T, LPH, true, false><<<grid, 256, 0, st>>>(a, w);
+      else fwd_kernel<T, LPH, false, false><<<grid, 256, 0, st>>>(a, w);
+    }
     return hipGetLastError();
   }
   if (a.blocks > 0) {
     const Work w = work_of(a, 8192);
-    if (a.interleaved) bwd_kernel<T, LPH, true><<<a.blocks, 256, 0, st>>>(a, w);
-    else bwd_kernel<T, LPH, false><<<a.blocks, 256, 0, st>>>(a, w);
+    if (a.A) {
+      if (a.interleaved) bwd_kernel<T, LPH, true, true><<<a.blocks, 256, 0, st>>>(a, w);
+      else bwd_kernel<T, LPH, false, true><<<a.blocks, 256, 0, st>>>(a, w);
+    } else {
+      if (a.interleaved) bwd_kernel<T, LPH, true, false><<<a.blocks, 256, 0, st>>>(a, w);
+      else bwd_kernel<T, LPH, false, false><<<a.blocks, 256, 0, st>>>(a, w);
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

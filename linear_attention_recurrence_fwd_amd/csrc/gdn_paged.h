@@ -1,0 +1,68 @@
+// Host-side interfaces of the paged cache's operators (appending with norm and
+// rotation; attention over a shared prefix and own pages): between their entry
+// points (gdn_paged_api.hip) and their kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace gdn {
+
+// Pool of pages; strides in bytes.
+struct PagePool {
+  int64_t ps, hs, ts;
+  int pages, shift;         // tokens of a page: 1 << shift
+};
+
+struct AppendArgs {
+  int64_t BT;               // tokens (rows of pos)
+  int S, per;               // sequences; tokens of each where cu is null
+  int Hq, Hk, D, R, P, A;
+  int64_t qs, ks, vs;       // elements from one token's rows to the next one's
+  int interleaved;
+  float eps, w_offset;
+  const void *q, *k, *v;
+  const float *wq, *wk;     // may be null: no norm
+  const float* rope;
+  const uint8_t* axis;
+  const int32_t* pos;
+  int64_t first;
+  const int32_t *table, *past, *cu;
+  int64_t width;
+  PagePool pool;
+  void *oq, *kp, *vp;
+};
+
+// Rows of the tokens N by the G query heads of a key head: row r is token r / G (of
+// the call, or of its sequence), head r % G.
+struct AttnArgs {
+  int N, S, per;            // tokens, sequences, tokens of each where cu is null
+  int Hq, Hk, G, D;
+  const void* q;
+  const void *kp, *vp;
+  PagePool pool;
+  const int32_t *table, *lens, *prefix_pages, *cu;
+  int64_t width;
+  int prefix, max_q, max_len;
+  float scale;
+  void* o;
+  float* lse;               // may be null
+  // The plan.  together: an item goes through the prefix and its sequence's own keys
+  // and writes the result.  Otherwise items of the prefix (rows of all sequences) and
+  // of own keys leave their parts in part / ml, [slot][N * Hq], the prefix's in the
+  // first p_split slots, joined by a second kernel.
+  int together;
+  int rows;                 // rows of an item
+  int p_tiles, p_split, p_chunk;  // items of the prefix: row tiles, splits, keys of a split
+  int o_tiles, o_split, o_chunk;  // of own keys, the tiles of each sequence
+  float* part;              // [slots][N * Hq][D], not divided by the sums
+  float2* ml;               // [slots][N * Hq] maximum (base 2) and sum
+};
+
+hipError_t launch_append(const AppendArgs& a, bool bf16, hipStream_t st);
+// Fills the plan; the bytes of part and of ml.
+void attn_plan(AttnArgs* a, bool bf16, size_t* part, size_t* ml);
+hipError_t launch_attn(const AttnArgs& a, bool bf16, hipStream_t st);
+
+}  // namespace gdn

@@ -1,0 +1,407 @@
+// Softmax attention of a batch's new tokens over a prefix that all sequences share
+// and over their own keys, in pages.
+//
+//   o_i = sum_j e^(s_ij - m_i) v_j / l_i,  s_ij = scale q_i . k_j,  l_i = sum_j e^(s_ij - m_i)
+//
+// in one pass over the keys with a running reference m and sum l; parts over
+// disjoint keys join by o = sum o_x e^(m_x - m), l = sum l_x e^(m_x - m).
+//
+// The rows of a key head's G query heads go together, and over the prefix those of
+// all sequences: the prefix's keys are read once for the batch (once for each tile
+// of rows), not once for each sequence.
+#include "gdn_prefix_attn.h"
+
+namespace gdn {
+namespace attn {
+namespace {
+
+typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
+
+// ---- few rows: 16 QB rows of queries, NW waves that share out the keys
+//
+// Each wave takes every NW-th tile of 16 keys and brings it to its own part of LDS by
+// direct loads, ST tiles ahead: no barriers, and 32 KB of keys and values of each
+// wave on their way.  Scores are formed transposed, keys by rows: a lane holds four
+// keys of one query, which is as the second product takes the weights, from
+// registers; the values' other operand comes by transposing reads (bf16) or single
+// words (fp32).  At the end the waves' results are joined through LDS.
+template <typename T, int DC, int QB, int NW> struct Few {
+  static constexpr int E = sizeof(T), KT = 16;
+  static constexpr int PR = DC * E / 16;                    // pieces of 16 bytes of a row
+  static constexpr int TILE = KT * PR * 16;                 // bytes of a tile of keys or values
+  static constexpr int ST = (NW == 4 ? 32768 : 65536) / (2 * TILE);
+  static constexpr int NL = TILE / 1024;                    // load instructions of a tile
+  static constexpr int RING = 2 * TILE * ST;
+  static constexpr int TS = 4 * ST;                         // tiles whose pages are held
+  static constexpr int ROW = DC + 4;                        // floats of a result's row in LDS
+  static constexpr int OUT = 16 * QB * ROW * 4;
+  static constexpr int WAVE = (RING > OUT ? RING : OUT);
+  static constexpr int LDS = NW * (WAVE + TS * KT * 4 + 16 * QB * 8);
+  static_assert(ST >= 2 && (ST - 1) * (2 * NL + 1) < 64, "waits count up to 63 loads");
+  static_assert(LDS <= 160 * 1024, "LDS");
+};
+
+__device__ __forceinline__ int swizzle(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
+
+template <typename T, int DC, int QB, int NW>
+__global__ void __launch_bounds__(64 * NW, 1) few_kernel(AttnArgs a) {
+  using F = Few<T, DC, QB, NW>;
+  constexpr bool BF = sizeof(T) == 2;
+  constexpr int KT = F::KT, PR = F::PR, ST = F::ST, NL = F::NL, TS = F::TS, NS = DC / 16;
+  __shared__ __align__(16) char lds[F::LDS];
+  const int w = threadIdx.x >> 6, l = threadIdx.x & 63, lr = l & 15, lg = l >> 4;
+  Keys<1> range;
+  const Item it = find_item(a, range);
+  if (it.empty) return;
+  Keys<KT> ks{range.plist, range.olist, range.p0, range.p1, range.o0, range.o1, 0, 0};
+  ks.count();
+  char* ring = lds + w * F::WAVE;
+  int32_t* pages = reinterpret_cast<int32_t*>(lds + NW * F::WAVE) + w * TS * KT;
+  float2* stats = reinterpret_cast<float2*>(lds + NW * (F::WAVE + TS * KT * 4));
+
+  // Queries, as the products take them: bf16 channels 32 st + 8 lg .. + 7 of row lr;
+  // fp32 channels 16 st + 4 lg .. + 3.
+  const int G = a.G, nrows = it.n * G;
+  uint4 q[QB][BF ? NS / 2 : NS];
+  int lim[QB];  // own keys that the row sees
+#pragma unroll
+  for (int b = 0; b < QB; ++b) {
+    const int r = it.row0 + 16 * b + lr, tok = r / G;
+    const bool on = r < nrows && !it.bad;
+    lim[b] = it.seen + tok;
+    const T* row = static_cast<const T*>(a.q) + (static_cast<int64_t>(it.t0 + (on ? tok : 0)) * a.Hq + it.hk * G + (on ? r % G : 0)) * a.D;
+#pragma unroll
+    for (int st = 0; st < (BF ? NS / 2 : NS); ++st) {
+      const int c = BF ? 32 * st + 8 * lg : 16 * st + 4 * lg;
+      q[b][st] = make_uint4(0, 0, 0, 0);
+      if (on && c < a.D) q[b][st] = *reinterpret_cast<const uint4*>(row + c);
+    }
+  }
+
+  f32x4 o[QB][NS];
+  float m[QB], sum[QB];
+#pragma unroll
+  for (int b = 0; b < QB; ++b) {
+    m[b] = -__builtin_inff();
+    sum[b] = 0.f;
+#pragma unroll
+    for (int d = 0; d < NS; ++d) o[b][d] = f4zero();
+  }
+
+  const int cnt = ks.n > w ? (ks.n - w + NW - 1) / NW : 0;  // this wave's tiles: w, w + NW, ...
+  const char *kb = static_cast<const char*>(a.kp) + it.hk * a.pool.hs, *vb = static_cast<const char*>(a.vp) + it.hk * a.pool.hs;
+  const int in_page = (1 << a.pool.shift) - 1;
+  auto page_of = [&](int x) {  // where the page of key lr of the wave's tile x is told
+    const int t = w + NW * (x < cnt ? x : cnt - 1), key = min(ks.first(t) + lr, ks.end(t) - 1);
+    return ks.list(t) + (key >> a.pool.shift);
+  };
+  auto load_pages = [&](int x) {
+    if (l < KT) load_lds4(page_of(x), pages + (x % TS) * KT);
+  };
+  auto load_tile = [&](int x) {
+    const int t = w + NW * x, key = ks.first(t) + lr;
+    const int page = pages[(x % TS) * KT + lr];
+    // offset of key lr's row; -1: behind the end, -2: no such page
+    int64_t off = page * a.pool.ps + (key & in_page) * a.pool.ts;
+    if (page < 0 || page >= a.pool.pages) off = -2;
+    if (key >= ks.end(t)) off = -1;
+    char* kt = ring + (x % ST) * 2 * F::TILE;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int row = (i * 64 + l) / PR, piece = ((i * 64 + l) % PR) ^ swizzle(row);
+      const int64_t from = (static_cast<int64_t>(__shfl(static_cast<int>(off >> 32), row)) << 32) |
+                           static_cast<uint32_t>(__shfl(static_cast<int>(off), row));
+      const bool fill = from < 0 || piece * 16 >= a.D * F::E;
+      const int64_t at = from + piece * 16;
+      const void* none = &kFill[from == -2 ? 1 : 0];
+      load_lds16(fill ? none : kb + at, kt + i * 1024);
+      load_lds16(fill ? none : vb + at, kt + F::TILE + i * 1024);
+    }
+  };
+
+  if (cnt > 0) {
+    for (int x = l; x < ST * KT; x += 64) {
+      const int t = x / KT, tt = w + NW * (t < cnt ? t : cnt - 1), key = min(ks.first(tt) + x % KT, ks.end(tt) - 1);
+      pages[x] = ks.list(tt)[key >> a.pool.shift];
+    }
+    wave_lds_sync();
+#pragma unroll 1
+    for (int x = 0; x < ST; ++x) {
+      load_pages(ST + x);
+      if (x < cnt) load_tile(x);
+    }
+  }
+#pragma unroll 1
+  for (int x = 0; x < cnt; ++x) {
+    // everything issued up to tile x's loads
+    if (x + ST <= cnt) wait_vm<(ST - 1) * (2 * NL + 1)>();
+    else wait_vm<0>();
+    const int t = w + NW * x, key0 = ks.first(t);
+    const char *kt = ring + (x % ST) * 2 * F::TILE, *vt = kt + F::TILE;
+    f32x4 s[QB];
+#pragma unroll
+    for (int b = 0; b < QB; ++b) s[b] = f4zero();
+    if constexpr (BF) {
+#pragma unroll
+      for (int st = 0; st < NS / 2; ++st) {
+        const bf16x8 k = load_bf16x8(kt + (lr * PR + ((4 * st + lg) ^ swizzle(lr))) * 16);
+#pragma unroll
+        for (int b = 0; b < QB; ++b) s[b] = mfma16(k, as_bf16x8(q[b][st]), s[b]);
+      }
+    } else {
+#pragma unroll
+      for (int st = 0; st < NS; ++st) {
+        const float4 k = *reinterpret_cast<const float4*>(kt + (lr * PR + ((4 * st + lg) ^ swizzle(lr))) * 16);
+#pragma unroll
+        for (int b = 0; b < QB; ++b) {
+          s[b] = mfma16f(k.x, __uint_as_float(q[b][st].x), s[b]);
+          s[b] = mfma16f(k.y, __uint_as_float(q[b][st].y), s[b]);
+          s[b] = mfma16f(k.z, __uint_as_float(q[b][st].z), s[b]);
+          s[b] = mfma16f(k.w, __uint_as_float(q[b][st].w), s[b]);
+        }
+      }
+    }
+    const int end = ks.end(t);
+    const bool own = ks.own(t);
+    bool move = false;
+#pragma unroll
+    for (int b = 0; b < QB; ++b) {
+      const int see = own ? min(end, lim[b]) : end;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        s[b][r] = key0 + 4 * lg + r < see ? s[b][r] * a.scale : -__builtin_inff();
+        move |= s[b][r] > m[b] + kSlack;
+      }
+    }
+    if (__any(move)) {
+#pragma unroll
+      for (int b = 0; b < QB; ++b) {
+        float top = fmaxf(fmaxf(s[b][0], s[b][1]), fmaxf(s[b][2], s[b][3]));
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        top = fmaxf(top, m[b]);
+        const float f = top == m[b] ? 1.f : __builtin_amdgcn_exp2f(m[b] - top);
+        m[b] = top;
+        sum[b] *= f;
+#pragma unroll
+        for (int d = 0; d < NS; ++d) o[b][d] *= f;
+      }
+    }
+    f32x4 p[QB];
+#pragma unroll
+    for (int b = 0; b < QB; ++b) {
+      const float ref = m[b] == -__builtin_inff() ? 0.f : m[b];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        p[b][r] = __builtin_amdgcn_exp2f(s[b][r] - ref);
+        sum[b] += p[b][r];
+      }
+    }
+    if constexpr (BF) {
+      s16x4 pb[QB];
+#pragma unroll
+      for (int b = 0; b < QB; ++b) pb[b] = __builtin_bit_cast(s16x4, pack4_bf16(p[b][0], p[b][1], p[b][2], p[b][3]));
+      const int row = 4 * lg + (lr >> 2), in = (lr & 1) * 8;
+#pragma unroll
+      for (int d = 0; d < NS; ++d) {
+        const uint2 v = lds_read_tr16(vt + (row * PR + ((2 * d + ((lr & 3) >> 1)) ^ swizzle(row))) * 16 + in);
+#pragma unroll
+        for (int b = 0; b < QB; ++b)
+          o[b][d] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, v), pb[b], o[b][d], 0, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int d = 0; d < NS; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 4 * lg + r;
+          const float v = *reinterpret_cast<const float*>(vt + (row * PR + ((4 * d + (lr >> 2)) ^ swizzle(row))) * 16 + (lr & 3) * 4);
+#pragma unroll
+          for (int b = 0; b < QB; ++b) o[b][d] = mfma16f(v, p[b][r], o[b][d]);
+        }
+    }
+    wave_lds_sync();  // what was read of this tile's place is in registers
+    if (x + ST < cnt) {
+      load_pages(x + 2 * ST);
+      load_tile(x + ST);
+    }
+  }
+
+  // Join the waves' results: row-major in LDS, then every thread a few channels.
+  float* mine = reinterpret_cast<float*>(ring);
+#pragma unroll
+  for (int b = 0; b < QB; ++b) {
+    float t = sum[b];
+    t += __shfl_xor(t, 16);
+    t += __shfl_xor(t, 32);
+    if (lg == 0) stats[w * 16 * QB + 16 * b + lr] = make_float2(m[b], t);
+#pragma unroll
+    for (int d = 0; d < NS; ++d)
+      *reinterpret_cast<float4*>(mine + (16 * b + lr) * F::ROW + 16 * d + 4 * lg) = make_float4(o[b][d][0], o[b][d][1], o[b][d][2], o[b][d][3]);
+  }
+  __syncthreads();
+  const int cols = a.D / 4, rows = min(16 * QB, nrows - it.row0);
+  for (int i = threadIdx.x; i < rows * cols; i += 64 * NW) {
+    const int r = i / cols, c = 4 * (i % cols);
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int x = 0; x < NW; ++x) top = fmaxf(top, stats[x * 16 * QB + r].x);
+    const float ref = top == -__builtin_inff() ? 0.f : top;
+    float t = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int x = 0; x < NW; ++x) {
+      const float2 ms = stats[x * 16 * QB + r];
+      const float f = __builtin_amdgcn_exp2f(ms.x - ref);
+      const float4 z = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(lds + x * F::WAVE) + r * F::ROW + c);
+      t += f * ms.y;
+      y.x += f * z.x;
+      y.y += f * z.y;
+      y.z += f * z.z;
+      y.w += f * z.w;
+    }
+    const int tok = (it.row0 + r) / G;
+    const int64_t row = static_cast<int64_t>(it.t0 + tok) * a.Hq + it.hk * G + (it.row0 + r) % G;
+    if (a.together) {
+      const float f = it.bad ? __builtin_nanf("") : t == 0.f ? 0.f : 1.f / t;
+      T* dst = static_cast<T*>(a.o) + row * a.D + c;
+      if constexpr (BF) *reinterpret_cast<uint2*>(dst) = pack4_bf16(y.x * f, y.y * f, y.z * f, y.w * f);
+      else *reinterpret_cast<float4*>(dst) = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
+      if (a.lse && c == 0) a.lse[row] = it.bad ? f : (top + log2f(t)) * kLn2;
+    } else {
+      const int64_t at = static_cast<int64_t>(it.slot) * a.N * a.Hq + row;
+      *reinterpret_cast<float4*>(a.part + at * a.D + c) = y;
+      if (c == 0) a.ml[at] = make_float2(top, t);
+    }
+  }
+  // The last tile of a sequence with more tokens than max_q also has the rows that no tile covers.
+  if (a.together && it.bad && it.row0 + a.rows >= a.max_q * G)
+    for (int64_t i = threadIdx.x; i < static_cast<int64_t>(nrows - it.row0 - a.rows) * a.D; i += 64 * NW) {
+      const int r = it.row0 + a.rows + static_cast<int>(i / a.D), c = static_cast<int>(i % a.D);
+      const int64_t row = static_cast<int64_t>(it.t0 + r / G) * a.Hq + it.hk * G + r % G;
+      static_cast<T*>(a.o)[row * a.D + c] = from_f32<T>(__builtin_nanf(""));
+      if (a.lse && c == 0) a.lse[row] = __builtin_nanf("");
+    }
+}
+
+// ---- the join of the parts
+//
+// 16 lanes to a row of up to 64 channels, 64 to one of 256: a lane has four channels.
+// The row's parts are the prefix's splits and those of its own keys that it sees.
+template <typename T, int LPR>
+__global__ void __launch_bounds__(256) join_kernel(AttnArgs a) {
+  const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / LPR;
+  const int c = 4 * (threadIdx.x % LPR);
+  const int64_t all = static_cast<int64_t>(a.N) * a.Hq;
+  if (row >= all) return;
+  const int tok = static_cast<int>(row / a.Hq);
+  int s, i, n;
+  if (a.cu) {
+    // the last sequence that begins at or before the token
+    int lo = -1, hi = a.S;  // cu[lo] <= tok < cu[hi + 1]
+    while (lo < hi) {
+      const int mid = lo + (hi - lo + 1) / 2;
+      if (a.cu[mid] <= tok) lo = mid;
+      else hi = mid - 1;
+    }
+    s = lo;
+    if (s < 0 || s >= a.S) return;
+    i = tok - a.cu[s];
+    n = a.cu[s + 1] - a.cu[s];
+  } else {
+    s = tok / a.per;
+    i = tok % a.per;
+    n = a.per;
+  }
+  const int len = a.lens[s];
+  const bool bad = len < 0 || len > a.max_len || n > a.max_q;
+  const int see = len - n + 1 + i;
+  const int parts = a.p_split + (bad || see <= 0 ? 0 : min(a.o_split, (see + a.o_chunk - 1) / a.o_chunk));
+  float m = -__builtin_inff();
+  for (int x = 0; x < parts; ++x) m = fmaxf(m, a.ml[x * all + row].x);
+  const float ref = m == -__builtin_inff() ? 0.f : m;
+  float t = 0.f;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (c < a.D)
+#pragma unroll 4
+    for (int x = 0; x < parts; ++x) {
+      const float2 ms = a.ml[x * all + row];
+      const float f = __builtin_amdgcn_exp2f(ms.x - ref);
+      const float4 z = *reinterpret_cast<const float4*>(a.part + (x * all + row) * a.D + c);
+      t += f * ms.y;
+      y.x += f * z.x;
+      y.y += f * z.y;
+      y.z += f * z.z;
+      y.w += f * z.w;
+    }
+  if (c >= a.D) return;
+  const float f = bad ? __builtin_nanf("") : t == 0.f ? 0.f : 1.f / t;
+  T* dst = static_cast<T*>(a.o) + row * a.D + c;
+  if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(dst) = pack4_bf16(y.x * f, y.y * f, y.z * f, y.w * f);
+  else *reinterpret_cast<float4*>(dst) = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
+  if (a.lse && c == 0) a.lse[row] = bad ? f : (m + log2f(t)) * kLn2;
+}
+
+template <typename T, int DC, int QB, int NW> hipError_t launch_few(const AttnArgs& a, unsigned items, hipStream_t st) {
+  few_kernel<T, DC, QB, NW><<<items, 64 * NW, 0, st>>>(a);
+  return hipGetLastError();
+}
+template <typename T, int DC> hipError_t launch_qb(const AttnArgs& a, unsigned items, hipStream_t st) {
+  constexpr int NW = sizeof(T) == 4 && DC > 128 ? 2 : 4;
+  return a.rows == 16 ? launch_few<T, DC, 1, NW>(a, items, st) : launch_few<T, DC, 2, NW>(a, items, st);
+}
+template <typename T> hipError_t launch_any(const AttnArgs& a, hipStream_t st) {
+  const unsigned p_items = a.together ? 0 : (a.p_split * a.Hk + 7) / 8 * 8 * a.p_tiles;
+  const unsigned items = p_items + static_cast<unsigned>(a.o_tiles) * a.Hk * a.S * a.o_split;
+  hipError_t e;
+  if (a.D <= 64) e = launch_qb<T, 64>(a, items, st);
+  else if (a.D <= 128) e = launch_qb<T, 128>(a, items, st);
+  else if (a.D <= 192) e = launch_qb<T, 192>(a, items, st);
+  else e = launch_qb<T, 256>(a, items, st);
+  if (e != hipSuccess || a.together) return e;
+  const int64_t rows = static_cast<int64_t>(a.N) * a.Hq;
+  if (a.D <= 64) join_kernel<T, 16><<<static_cast<unsigned>((rows + 15) / 16), 256, 0, st>>>(a);
+  else if (a.D <= 128) join_kernel<T, 32><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, st>>>(a);
+  else join_kernel<T, 64><<<static_cast<unsigned>((rows + 3) / 4), 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace attn
+
+void attn_plan(AttnArgs* a, bool bf, size_t* part, size_t* ml) {
+  (void)bf;
+  const int64_t own_rows = static_cast<int64_t>(a->max_q) * a->G, all_rows = static_cast<int64_t>(a->N) * a->G;
+  a->rows = own_rows <= 16 && (a->prefix == 0 || all_rows <= 16) ? 16 : 32;
+  a->o_tiles = static_cast<int>((own_rows + a->rows - 1) / a->rows);
+  const int64_t seq_items = static_cast<int64_t>(a->o_tiles) * a->Hk * a->S;
+  a->together = seq_items >= 512 || (a->prefix == 0 && a->max_len <= 256);
+  a->p_tiles = a->p_split = a->p_chunk = 0;
+  a->o_split = 1;
+  a->o_chunk = a->max_len > 0 ? a->max_len : 1;
+  *part = *ml = 0;
+  if (a->together) return;
+  if (a->prefix > 0) {
+    a->p_tiles = static_cast<int>((all_rows + a->rows - 1) / a->rows);
+    int64_t n = 512 / (static_cast<int64_t>(a->p_tiles) * a->Hk);
+    if (n < 1) n = 1;
+    a->p_chunk = static_cast<int>((a->prefix + n - 1) / n + 63) / 64 * 64;
+    if (a->p_chunk < 256) a->p_chunk = 256;
+    a->p_split = (a->prefix + a->p_chunk - 1) / a->p_chunk;
+  }
+  int64_t n = 1024 / seq_items;
+  if (n < 1) n = 1;
+  a->o_chunk = static_cast<int>((a->max_len + n - 1) / n + 63) / 64 * 64;
+  if (a->o_chunk < 256) a->o_chunk = 256;
+  a->o_split = (a->max_len + a->o_chunk - 1) / a->o_chunk;
+  const size_t rows = static_cast<size_t>(a->p_split + a->o_split) * a->N * a->Hq;
+  *part = rows * a->D * sizeof(float);
+  *ml = rows * sizeof(float2);
+}
+
+hipError_t launch_attn(const AttnArgs& a, bool bf, hipStream_t st) {
+  if (a.N == 0) return hipSuccess;
+  return bf ? attn::launch_any<bf16>(a, st) : attn::launch_any<float>(a, st);
+}
+
+}  // namespace gdn
