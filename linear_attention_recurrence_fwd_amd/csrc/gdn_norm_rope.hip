@@ -29,7 +29,7 @@ namespace {
 
 __device__ __forceinline__ void load_w(const float* w, const NormRopeArgs& a, int c0, bool on, float* out) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) out[i] = !on ? 0.f : w ? w[c0 + i] + a.w_offset : 1.f;
+  for (int i = 0; i < 8; ++i) out[i] = on ? w[c0 + i] + a.w_offset : 0.f;
 }
 
 // A wave's work: token and run of head groups (a group: 64 / LPH heads); the
@@ -45,51 +45,18 @@ constexpr int64_t kFwdBlocks = 1 << 22;
 
 template <typename T, int LPH, bool INTER, bool AXES>
 __global__ void __launch_bounds__(256) fwd_kernel(NormRopeArgs a, Work wk) {
-  constexpr int RPW = 64 / LPH;
   const Lane<LPH, INTER> ln(a);
   const int64_t item = (static_cast<int64_t>(blockIdx.y) * kFwdBlocks + blockIdx.x) * 4 + (threadIdx.x >> 6);
   const int64_t token = item / wk.runs;
   if (token >= a.BT) return;
   const int g0 = static_cast<int>(item % wk.runs) * wk.run, g1 = min(g0 + wk.run, wk.gq + wk.gk);
-  const int sub_row = (threadIdx.x & 63) / LPH;
-  Turn tn;
-  ln.template load<AXES>(a, token, token % a.T, tn, AXES && a.back);
-  const float inv = 1.f / static_cast<float>(a.D);
-#pragma unroll 1
-  for (int part = 0; part < 2; ++part) {
-    const int lo = max(g0, part ? wk.gq : 0), hi = min(g1, part ? wk.gq + wk.gk : wk.gq);
-    if (lo >= hi) continue;
-    float wt[8], wo[8];
-    const float* wp = part ? a.wk : a.wq;
-    load_w(wp, a, ln.c0, ln.on, wt);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) wo[i] = __shfl(wt[i], ln.other);
-    const int H = part ? a.Hk : a.Hq, base = part ? wk.gq : 0;
-    const T* src = static_cast<const T*>(part ? a.k : a.q) + token * (part ? a.ks : a.qs);
-    T* dst = static_cast<T*>(part ? a.ok : a.oq) + token * H * a.D;
-    for (int g = lo; g < hi; ++g) {
-      const int head = (g - base) * RPW + sub_row;
-      const bool on = ln.on && head < H;
-      Raw<T> x;
-      x.zero();
-      if (on) x.load(src + head * a.D + ln.c0);
-      float v[8], o[8];
-      x.unpack(v);
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-      const float r = AXES && a.bare ? 1.f : 1.f / sqrtf(row_sum<LPH>(ss) * inv + a.eps);
-      if constexpr (!INTER) {
-        x.from_lane(ln.other).unpack(o);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] *= r * wo[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= r * wt[i];
-      ln.turn(v, o, tn);
-      if (on) Raw<T>::store(dst + head * a.D + ln.c0, v);
-    }
-  }
+  const T* const src[2] = {static_cast<const T*>(a.q) + token * a.qs, static_cast<const T*>(a.k) + token * a.ks};
+  turn_rows<T, LPH, INTER, AXES, 2>(a, ln, token, g0, g1, wk.gq, wk.gk, src, [&](Turn& tn, char* (&dst)[3], int64_t (&step)[3]) {
+    ln.template load<AXES>(a, token, token % a.T, tn, AXES && a.back);
+    step[0] = step[1] = a.D * static_cast<int64_t>(sizeof(T));
+    dst[0] = static_cast<char*>(a.oq) + token * a.Hq * step[0];
+    dst[1] = static_cast<char*>(a.ok) + token * a.Hk * step[1];
+  });
 }
 
 // The backward's blocks each take a run of tokens and leave their rows' part of
@@ -136,7 +103,7 @@ __global__ void __launch_bounds__(256) bwd_kernel(NormRopeArgs a, Work wk) {
         x.unpack(v);
         y.unpack(e);
         if constexpr (!INTER) y.from_lane(ln.other).unpack(o);
-        ln.turn(e, o, tn);
+        ln.template turn<true>(e, o, tn);
         float ss = 0.f, ah = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {

@@ -48,12 +48,13 @@ struct AttnArgs {
   float scale;
   void* o;
   float* lse;               // may be null
-  // The plan.  together: an item goes through the prefix and its sequence's own keys
-  // and writes the result.  Otherwise items of the prefix (rows of all sequences) and
-  // of own keys leave their parts in part / ml, [slot][N * Hq], the prefix's in the
-  // first p_split slots, joined by a second kernel.
+  // The plan.  together (no prefix, and own keys that are not split): an item writes the
+  // result.  Otherwise items of the prefix (rows of all sequences) and of own keys leave
+  // their parts in part / ml, [slot][N * Hq], the prefix's in the first p_split slots,
+  // joined by another kernel.
   int together;
-  int rows;                 // rows of an item
+  int which;                // items of this launch: 1 the prefix's, 2 those of own keys (3 both)
+  int p_rows, o_rows;       // rows of an item
   int p_tiles, p_split, p_chunk;  // items of the prefix: row tiles, splits, keys of a split
   int o_tiles, o_split, o_chunk;  // of own keys, the tiles of each sequence
   float* part;              // [slots][N * Hq][D], not divided by the sums

@@ -37,76 +37,36 @@ __device__ __forceinline__ int find_sequence(const int32_t* cu, int S, int64_t t
 
 template <typename T, int LPH, bool INTER>
 __global__ void __launch_bounds__(256) append_kernel(AppendArgs a, Work wk) {
-  constexpr int RPW = 64 / LPH;
   const Lane<LPH, INTER> ln(a);
   const int64_t item = (static_cast<int64_t>(blockIdx.y) * kBlocks + blockIdx.x) * 4 + (threadIdx.x >> 6);
   const int64_t token = item / wk.runs;
   if (token >= a.BT) return;
-  int s;
-  int64_t i;
-  if (a.cu) {
-    s = find_sequence(a.cu, a.S, token);
-    if (s < 0 || s >= a.S) return;
-    i = token - a.cu[s];
-  } else {
-    s = static_cast<int>(token / a.per);
-    i = token % a.per;
-  }
-  const int64_t place = a.past[s] + i, in_row = place >> a.pool.shift;
-  const bool room = place >= 0 && in_row < a.width;
-  const int page = room ? a.table[s * a.width + in_row] : -1;
-  const bool write = page >= 0 && page < a.pool.pages;
-  const int64_t at = write ? page * a.pool.ps + (place & ((1 << a.pool.shift) - 1)) * a.pool.ts : 0;
   const int g0 = static_cast<int>(item % wk.runs) * wk.run, g1 = min(g0 + wk.run, wk.gq + 2 * wk.gk);
-  const int sub_row = (threadIdx.x & 63) / LPH;
-  Turn tn;
-  if (g0 < wk.gq + wk.gk) ln.template load<true>(a, token, a.first + place, tn, false);
-  const float inv = 1.f / static_cast<float>(a.D);
-#pragma unroll 1
-  for (int part = 0; part < 2; ++part) {
-    const int lo = max(g0, part ? wk.gq : 0), hi = min(g1, part ? wk.gq + wk.gk : wk.gq);
-    if (lo >= hi || (part && !write)) continue;
-    const float* wp = part ? a.wk : a.wq;
-    float wt[8], wo[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) wt[j] = !ln.on ? 0.f : wp ? wp[ln.c0 + j] + a.w_offset : 1.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) wo[j] = __shfl(wt[j], ln.other);
-    const int H = part ? a.Hk : a.Hq, base = part ? wk.gq : 0;
-    const T* src = static_cast<const T*>(part ? a.k : a.q) + token * (part ? a.ks : a.qs);
-    char* dst = part ? static_cast<char*>(a.kp) + at : static_cast<char*>(a.oq) + token * H * a.D * static_cast<int64_t>(sizeof(T));
-    const int64_t step = part ? a.pool.hs : a.D * static_cast<int64_t>(sizeof(T));
-    for (int g = lo; g < hi; ++g) {
-      const int head = (g - base) * RPW + sub_row;
-      const bool on = ln.on && head < H;
-      Raw<T> x;
-      x.zero();
-      if (on) x.load(src + head * a.D + ln.c0);
-      float v[8], o[8];
-      x.unpack(v);
-      float ss = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
-      const float r = wp ? 1.f / sqrtf(row_sum<LPH>(ss) * inv + a.eps) : 1.f;
-      if constexpr (!INTER) {
-        x.from_lane(ln.other).unpack(o);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] *= r * wo[j];
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= r * wt[j];
-      ln.turn(v, o, tn);
-      if (on) Raw<T>::store(reinterpret_cast<T*>(dst + head * step) + ln.c0, v);
+  const T* const src[3] = {static_cast<const T*>(a.q) + token * a.qs, static_cast<const T*>(a.k) + token * a.ks,
+                           static_cast<const T*>(a.v) + token * a.vs};
+  turn_rows<T, LPH, INTER, true, 3>(a, ln, token, g0, g1, wk.gq, wk.gk, src, [&](Turn& tn, char* (&dst)[3], int64_t (&step)[3]) {
+    dst[0] = dst[1] = dst[2] = nullptr;
+    step[0] = a.D * static_cast<int64_t>(sizeof(T));
+    step[1] = step[2] = a.pool.hs;
+    int s;
+    int64_t i;
+    if (a.cu) {
+      s = find_sequence(a.cu, a.S, token);
+      if (s < 0 || s >= a.S) return;  // (the rows are read, and not written)
+      i = token - a.cu[s];
+    } else {
+      s = static_cast<int>(token / a.per);
+      i = token % a.per;
     }
-  }
-  if (!write) return;
-  for (int g = max(g0, wk.gq + wk.gk); g < g1; ++g) {
-    const int head = (g - wk.gq - wk.gk) * RPW + sub_row;
-    if (!ln.on || head >= a.Hk) continue;
-    Raw<T> x;
-    x.load(static_cast<const T*>(a.v) + token * a.vs + head * a.D + ln.c0);
-    x.put(reinterpret_cast<T*>(static_cast<char*>(a.vp) + at + head * a.pool.hs) + ln.c0);
-  }
+    const int64_t place = a.past[s] + i, in_row = place >> a.pool.shift;
+    const int page = place >= 0 && in_row < a.width ? a.table[s * a.width + in_row] : -1;
+    if (g0 < wk.gq + wk.gk) ln.template load<true>(a, token, a.first + place, tn, false);
+    dst[0] = static_cast<char*>(a.oq) + token * a.Hq * step[0];
+    if (page < 0 || page >= a.pool.pages) return;
+    const int64_t at = page * a.pool.ps + (place & ((1 << a.pool.shift) - 1)) * a.pool.ts;
+    dst[1] = static_cast<char*>(a.kp) + at;
+    dst[2] = static_cast<char*>(a.vp) + at;
+  });
 }
 
 template <typename T, int LPH> hipError_t launch_lph(const AppendArgs& a, hipStream_t st) {

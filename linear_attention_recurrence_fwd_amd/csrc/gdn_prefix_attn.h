@@ -9,59 +9,64 @@ namespace attn {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // The statistics' reference maximum is moved when a score exceeds it by this (base 2):
-// the weights stay below 2^8 and keep their relative precision, and moving it, which
-// scales the result's registers, is rare.
-constexpr float kSlack = 8.f;
+// the weights stay below 2^16 (whatever their size, they keep their relative precision),
+// and moving it, which scales the result's registers, is rare.
+constexpr float kSlack = 16.f;
+constexpr float kMost = 65536.f;  // and of a lane's weights of 32 keys together, where these are watched
 
 // 16 bytes of zeros and of NaN (in either type): what the loads of keys behind the
 // end, and of keys on pages that do not exist, are pointed to.
 __device__ const uint4 kFill[2] = {{0, 0, 0, 0}, {0x7fc07fc0, 0x7fc07fc0, 0x7fc07fc0, 0x7fc07fc0}};
 
-// 16 bytes (4 bytes) to LDS at the wave's base + 16 (4) * lane, issued by inline
-// assembly like the buffer loads in gdn_dev.h; a pool may be larger than a
-// descriptor's 4 GiB.  Inactive lanes write nothing.
-__device__ __forceinline__ void load_lds16(const void* p, const void* lds) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "{m0}"(lds_addr(lds)) : "memory");
+// 16 bytes (4 bytes) of each lane to LDS at the wave's address + 16 (4) * lane, issued by
+// inline assembly like the buffer loads in gdn_dev.h; a pool may be larger than a
+// descriptor's 4 GiB.  Inactive lanes write nothing.  LDS addresses are plain numbers (of
+// a pointer every cast is checked for null).
+__device__ __forceinline__ uint32_t lds_of(const void* p) {
+  typedef __attribute__((address_space(3))) const void lds_t;
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_t*)p));
 }
-__device__ __forceinline__ void load_lds4(const void* p, const void* lds) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "{m0}"(lds_addr(lds)) : "memory");
+__device__ __forceinline__ void load_lds16(const void* p, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "{m0}"(lds) : "memory");
+}
+// From an address that is the same for the wave, and each lane's distance to it.  The
+// address may just have come out of a vector register (readfirstlane): a vector memory
+// instruction must not read such scalar registers within five wait states, which nobody
+// but this block can see to.
+__device__ __forceinline__ void load_lds16(const void* base, uint32_t off, uint32_t lds) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a >> 32));
+  base = reinterpret_cast<const void*>((static_cast<uint64_t>(hi) << 32) | lo);
+  asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ void load_lds4(const void* p, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "{m0}"(lds) : "memory");
 }
 
-// An item's keys: the prefix's p0 .. p1, then the sequence's own o0 .. o1, in tiles of
-// KT (each part begins a tile).
-template <int KT> struct Keys {
-  const int32_t *plist, *olist;
-  int p0, p1, o0, o1;
-  int np, n;  // tiles of the prefix, of both
-  __device__ __forceinline__ void count() {
-    np = p1 > p0 ? (p1 - p0 + KT - 1) / KT : 0;
-    n = np + (o1 > o0 ? (o1 - o0 + KT - 1) / KT : 0);
-  }
-  __device__ __forceinline__ bool own(int t) const { return t >= np; }
-  __device__ __forceinline__ int first(int t) const { return t < np ? p0 + KT * t : o0 + KT * (t - np); }
-  __device__ __forceinline__ int end(int t) const { return t < np ? p1 : o1; }
-  __device__ __forceinline__ const int32_t* list(int t) const { return t < np ? plist : olist; }
-};
+// Where 16-byte piece p of row r of a tile lies: place p ^ swizzle(r) of the row.  The
+// eight rows that a wide read takes at once, and the four rows of two pieces of a
+// transposing read, then lie on different banks.
+__device__ __forceinline__ int swizzle(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
 
-// What an item works on: rows row0 .. row0 + rows of the tokens t0 .. t0 + n (n G rows
-// in all) and key head hk; bad: the result is NaN.
+// What an item works on: rows from row0 on of the tokens t0 .. t0 + n - 1 (n G rows in
+// all) and key head hk, keys k0 .. k1 - 1 in the pages of list; bad: the result is NaN.
 struct Item {
   int t0, n, row0, hk, slot;
-  int seen;  // own keys that the sequence's first token sees (may be negative)
+  const int32_t* list;
+  int k0, k1;
+  int seen;  // keys that the first token sees (may be negative); each further one sees one more
   bool bad, empty;
 };
 
 // Items are numbered so that those which read the same keys of the prefix (row tiles
 // of one split and key head) run on the same XCD, one after the other: workgroups go
 // to the eight XCDs in turn.
-__device__ __forceinline__ Item find_item(const AttnArgs& a, Keys<1>& ks) {
+__device__ __forceinline__ Item find_item(const AttnArgs& a) {
   Item it{};
   int b = blockIdx.x;
-  const int pairs = a.p_split * a.Hk, p_items = (pairs + 7) / 8 * 8 * a.p_tiles;
-  ks.plist = a.prefix_pages;
-  ks.olist = nullptr;
-  ks.p0 = ks.p1 = ks.o0 = ks.o1 = 0;
-  if (!a.together && b < p_items) {
+  const int pairs = a.p_split * a.Hk, p_items = a.which & 1 ? (pairs + 7) / 8 * 8 * a.p_tiles : 0;
+  if (b < p_items) {
     const int pair = b / (8 * a.p_tiles) * 8 + b % 8, tile = b / 8 % a.p_tiles;
     if (pair >= pairs) {
       it.empty = true;
@@ -70,12 +75,14 @@ __device__ __forceinline__ Item find_item(const AttnArgs& a, Keys<1>& ks) {
     it.slot = pair / a.Hk;
     it.hk = pair % a.Hk;
     it.n = a.N;
-    it.row0 = tile * a.rows;
-    ks.p0 = it.slot * a.p_chunk;
-    ks.p1 = min(a.prefix, ks.p0 + a.p_chunk);
+    it.row0 = tile * a.p_rows;
+    it.list = a.prefix_pages;
+    it.k0 = it.slot * a.p_chunk;
+    it.k1 = min(a.prefix, it.k0 + a.p_chunk);
+    it.seen = 1 << 30;
     return it;
   }
-  if (!a.together) b -= p_items;
+  b -= p_items;
   // the splits of a sequence's keys outermost: those behind its end have nothing to do
   const int tile = b % a.o_tiles;
   b /= a.o_tiles;
@@ -83,21 +90,36 @@ __device__ __forceinline__ Item find_item(const AttnArgs& a, Keys<1>& ks) {
   b /= a.Hk;
   const int s = b % a.S, split = b / a.S;
   it.slot = a.p_split + split;
-  it.row0 = tile * a.rows;
+  it.row0 = tile * a.o_rows;
   const int end = a.cu ? min(a.cu[s + 1], a.N) : (s + 1) * a.per;
   it.t0 = a.cu ? max(a.cu[s], 0) : s * a.per;
   it.n = end - it.t0;
   const int len = a.lens[s];
   it.seen = len - it.n + 1;
   it.bad = len < 0 || len > a.max_len || it.n > a.max_q;
-  const int last = min(it.n - 1, (it.row0 + a.rows - 1) / a.G);  // the tile's last token
-  ks.olist = a.table + s * a.width;
-  ks.o0 = split * a.o_chunk;
-  ks.o1 = it.bad ? 0 : min(it.seen + last, ks.o0 + a.o_chunk);
-  if (a.together && !it.bad) ks.p1 = a.prefix;
-  it.empty = it.n <= 0 || (it.row0 >= it.n * a.G && !it.bad) || (!a.together && ks.o1 <= ks.o0);
+  const int last = min(it.n - 1, (it.row0 + a.o_rows - 1) / a.G);  // the tile's last token
+  it.list = a.table + s * a.width;
+  it.k0 = split * a.o_chunk;
+  it.k1 = it.bad ? 0 : min(it.seen + last, it.k0 + a.o_chunk);
+  it.empty = it.n <= 0 || (it.row0 >= it.n * a.G && !it.bad) || (!a.together && it.k1 <= it.k0);
   return it;
 }
+
+// The last tile of a sequence with more tokens than max_q also has the rows that no
+// tile covers.
+template <typename T>
+__device__ __forceinline__ void bad_rows(const AttnArgs& a, const Item& it, int nrows, int threads) {
+  const int begin = it.row0 + a.o_rows;
+  if (!it.bad || begin < a.max_q * a.G) return;
+  for (int64_t i = threadIdx.x; i < static_cast<int64_t>(nrows - begin) * a.D; i += threads) {
+    const int r = begin + static_cast<int>(i / a.D), c = static_cast<int>(i % a.D);
+    const int64_t row = static_cast<int64_t>(it.t0 + r / a.G) * a.Hq + it.hk * a.G + r % a.G;
+    static_cast<T*>(a.o)[row * a.D + c] = from_f32<T>(__builtin_nanf(""));
+    if (a.lse && c == 0) a.lse[row] = __builtin_nanf("");
+  }
+}
+
+hipError_t launch_many(const AttnArgs& a, int rows, unsigned items, hipStream_t st);
 
 }  // namespace attn
 }  // namespace gdn

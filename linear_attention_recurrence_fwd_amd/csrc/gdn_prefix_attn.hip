@@ -10,7 +10,6 @@
 // all sequences: the prefix's keys are read once for the batch (once for each tile
 // of rows), not once for each sequence.
 #include "gdn_prefix_attn.h"
-
 namespace gdn {
 namespace attn {
 namespace {
@@ -20,8 +19,8 @@ typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
 // ---- few rows: 16 QB rows of queries, NW waves that share out the keys
 //
 // Each wave takes every NW-th tile of 16 keys and brings it to its own part of LDS by
-// direct loads, ST tiles ahead: no barriers, and 32 KB of keys and values of each
-// wave on their way.  Scores are formed transposed, keys by rows: a lane holds four
+// direct loads, ST tiles ahead: no barriers, and 128 KB of keys and values on their way
+// to a compute unit.  Scores are formed transposed, keys by rows: a lane holds four
 // keys of one query, which is as the second product takes the weights, from
 // registers; the values' other operand comes by transposing reads (bf16) or single
 // words (fp32).  At the end the waves' results are joined through LDS.
@@ -29,7 +28,9 @@ template <typename T, int DC, int QB, int NW> struct Few {
   static constexpr int E = sizeof(T), KT = 16;
   static constexpr int PR = DC * E / 16;                    // pieces of 16 bytes of a row
   static constexpr int TILE = KT * PR * 16;                 // bytes of a tile of keys or values
-  static constexpr int ST = (NW == 4 ? 32768 : 65536) / (2 * TILE);
+  // two workgroups to a compute unit, so that one's begin and end lie beside the other's
+  // middle (fp32 of wide heads: one)
+  static constexpr int ST = (NW == 4 ? 16384 : sizeof(T) == 4 && DC > 128 ? 65536 : 32768) / (2 * TILE);
   static constexpr int NL = TILE / 1024;                    // load instructions of a tile
   static constexpr int RING = 2 * TILE * ST;
   static constexpr int TS = 4 * ST;                         // tiles whose pages are held
@@ -38,32 +39,31 @@ template <typename T, int DC, int QB, int NW> struct Few {
   static constexpr int WAVE = (RING > OUT ? RING : OUT);
   static constexpr int LDS = NW * (WAVE + TS * KT * 4 + 16 * QB * 8);
   static_assert(ST >= 2 && (ST - 1) * (2 * NL + 1) < 64, "waits count up to 63 loads");
-  static_assert(LDS <= 160 * 1024, "LDS");
+  static_assert(LDS <= (sizeof(T) == 4 && DC > 128 ? 160 : 80) * 1024, "LDS");
 };
 
-__device__ __forceinline__ int swizzle(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
 
 template <typename T, int DC, int QB, int NW>
-__global__ void __launch_bounds__(64 * NW, 1) few_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) few_kernel(AttnArgs a) {
   using F = Few<T, DC, QB, NW>;
   constexpr bool BF = sizeof(T) == 2;
   constexpr int KT = F::KT, PR = F::PR, ST = F::ST, NL = F::NL, TS = F::TS, NS = DC / 16;
   __shared__ __align__(16) char lds[F::LDS];
-  const int w = threadIdx.x >> 6, l = threadIdx.x & 63, lr = l & 15, lg = l >> 4;
-  Keys<1> range;
-  const Item it = find_item(a, range);
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, lr = l & 15, lg = l >> 4;
+  const Item it = find_item(a);
   if (it.empty) return;
-  Keys<KT> ks{range.plist, range.olist, range.p0, range.p1, range.o0, range.o1, 0, 0};
-  ks.count();
+  const int tiles = it.k1 > it.k0 ? (it.k1 - it.k0 + KT - 1) / KT : 0;
   char* ring = lds + w * F::WAVE;
+  const uint32_t ring_at = lds_of(lds) + w * F::WAVE;
   int32_t* pages = reinterpret_cast<int32_t*>(lds + NW * F::WAVE) + w * TS * KT;
+  const uint32_t pages_at = lds_of(lds) + NW * F::WAVE + w * TS * KT * 4;
   float2* stats = reinterpret_cast<float2*>(lds + NW * (F::WAVE + TS * KT * 4));
 
   // Queries, as the products take them: bf16 channels 32 st + 8 lg .. + 7 of row lr;
   // fp32 channels 16 st + 4 lg .. + 3.
   const int G = a.G, nrows = it.n * G;
   uint4 q[QB][BF ? NS / 2 : NS];
-  int lim[QB];  // own keys that the row sees
+  int lim[QB];  // keys that the row sees
 #pragma unroll
   for (int b = 0; b < QB; ++b) {
     const int r = it.row0 + 16 * b + lr, tok = r / G;
@@ -88,24 +88,44 @@ __global__ void __launch_bounds__(64 * NW, 1) few_kernel(AttnArgs a) {
     for (int d = 0; d < NS; ++d) o[b][d] = f4zero();
   }
 
-  const int cnt = ks.n > w ? (ks.n - w + NW - 1) / NW : 0;  // this wave's tiles: w, w + NW, ...
+  const int cnt = tiles > w ? (tiles - w + NW - 1) / NW : 0;  // this wave's tiles: w, w + NW, ...
   const char *kb = static_cast<const char*>(a.kp) + it.hk * a.pool.hs, *vb = static_cast<const char*>(a.vp) + it.hk * a.pool.hs;
   const int in_page = (1 << a.pool.shift) - 1;
   auto page_of = [&](int x) {  // where the page of key lr of the wave's tile x is told
-    const int t = w + NW * (x < cnt ? x : cnt - 1), key = min(ks.first(t) + lr, ks.end(t) - 1);
-    return ks.list(t) + (key >> a.pool.shift);
+    const int key = min(it.k0 + KT * (w + NW * (x < cnt ? x : cnt - 1)) + lr, it.k1 - 1);
+    return it.list + (key >> a.pool.shift);
   };
   auto load_pages = [&](int x) {
-    if (l < KT) load_lds4(page_of(x), pages + (x % TS) * KT);
+    if (l < KT) load_lds4(page_of(x), pages_at + (x % TS) * KT * 4);
   };
+  // A full tile lies in one page where pages hold it: one address for the wave, and each
+  // lane's constant distance from it.  (Row by row, the addresses cost as much as the
+  // tile's products.)
+  const bool one_page = (1 << a.pool.shift) >= KT && a.D == DC && a.pool.ts < (1 << 26);
+  uint32_t from_first[NL];
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const int row = (i * 64 + l) / PR, piece = ((i * 64 + l) % PR) ^ swizzle(row);
+    from_first[i] = row * static_cast<uint32_t>(a.pool.ts) + piece * 16;
+  }
   auto load_tile = [&](int x) {
-    const int t = w + NW * x, key = ks.first(t) + lr;
-    const int page = pages[(x % TS) * KT + lr];
+    const int key0 = it.k0 + KT * (w + NW * x), end = it.k1;
+    const int page = pages[(x % TS) * KT + lr], page_w = __builtin_amdgcn_readfirstlane(page);
+    const uint32_t kt = ring_at + (x % ST) * 2 * F::TILE;
+    if (one_page && key0 + KT <= end && page_w >= 0 && page_w < a.pool.pages) {
+      const int64_t off = page_w * a.pool.ps + (key0 & in_page) * a.pool.ts;
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        load_lds16(kb + off, from_first[i], kt + i * 1024);
+        load_lds16(vb + off, from_first[i], kt + F::TILE + i * 1024);
+      }
+      return;
+    }
     // offset of key lr's row; -1: behind the end, -2: no such page
+    const int key = key0 + lr;
     int64_t off = page * a.pool.ps + (key & in_page) * a.pool.ts;
     if (page < 0 || page >= a.pool.pages) off = -2;
-    if (key >= ks.end(t)) off = -1;
-    char* kt = ring + (x % ST) * 2 * F::TILE;
+    if (key >= end) off = -1;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
       const int row = (i * 64 + l) / PR, piece = ((i * 64 + l) % PR) ^ swizzle(row);
@@ -121,8 +141,8 @@ __global__ void __launch_bounds__(64 * NW, 1) few_kernel(AttnArgs a) {
 
   if (cnt > 0) {
     for (int x = l; x < ST * KT; x += 64) {
-      const int t = x / KT, tt = w + NW * (t < cnt ? t : cnt - 1), key = min(ks.first(tt) + x % KT, ks.end(tt) - 1);
-      pages[x] = ks.list(tt)[key >> a.pool.shift];
+      const int t = x / KT, key = min(it.k0 + KT * (w + NW * (t < cnt ? t : cnt - 1)) + x % KT, it.k1 - 1);
+      pages[x] = it.list[key >> a.pool.shift];
     }
     wave_lds_sync();
 #pragma unroll 1
@@ -136,7 +156,7 @@ __global__ void __launch_bounds__(64 * NW, 1) few_kernel(AttnArgs a) {
     // everything issued up to tile x's loads
     if (x + ST <= cnt) wait_vm<(ST - 1) * (2 * NL + 1)>();
     else wait_vm<0>();
-    const int t = w + NW * x, key0 = ks.first(t);
+    const int key0 = it.k0 + KT * (w + NW * x);
     const char *kt = ring + (x % ST) * 2 * F::TILE, *vt = kt + F::TILE;
     f32x4 s[QB];
 #pragma unroll
@@ -161,12 +181,10 @@ __global__ void __launch_bounds__(64 * NW, 1) few_kernel(AttnArgs a) {
         }
       }
     }
-    const int end = ks.end(t);
-    const bool own = ks.own(t);
     bool move = false;
 #pragma unroll
     for (int b = 0; b < QB; ++b) {
-      const int see = own ? min(end, lim[b]) : end;
+      const int see = min(it.k1, lim[b]);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         s[b][r] = key0 + 4 * lg + r < see ? s[b][r] * a.scale : -__builtin_inff();
@@ -194,7 +212,7 @@ __global__ void __launch_bounds__(64 * NW, 1) few_kernel(AttnArgs a) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         p[b][r] = __builtin_amdgcn_exp2f(s[b][r] - ref);
-        sum[b] += p[b][r];
+        sum[b] += p[b][r];  // (bf16: before they are rounded, so that lse is exact to 32 bits)
       }
     }
     if constexpr (BF) {
@@ -274,67 +292,86 @@ __global__ void __launch_bounds__(64 * NW, 1) few_kernel(AttnArgs a) {
       if (c == 0) a.ml[at] = make_float2(top, t);
     }
   }
-  // The last tile of a sequence with more tokens than max_q also has the rows that no tile covers.
-  if (a.together && it.bad && it.row0 + a.rows >= a.max_q * G)
-    for (int64_t i = threadIdx.x; i < static_cast<int64_t>(nrows - it.row0 - a.rows) * a.D; i += 64 * NW) {
-      const int r = it.row0 + a.rows + static_cast<int>(i / a.D), c = static_cast<int>(i % a.D);
-      const int64_t row = static_cast<int64_t>(it.t0 + r / G) * a.Hq + it.hk * G + r % G;
-      static_cast<T*>(a.o)[row * a.D + c] = from_f32<T>(__builtin_nanf(""));
-      if (a.lse && c == 0) a.lse[row] = __builtin_nanf("");
-    }
+  if (a.together) bad_rows<T>(a, it, nrows, 64 * NW);
 }
 
 // ---- the join of the parts
 //
-// 16 lanes to a row of up to 64 channels, 64 to one of 256: a lane has four channels.
-// The row's parts are the prefix's splits and those of its own keys that it sees.
-template <typename T, int LPR>
+// LPR lanes to a row, four channels each.  The row's parts are the prefix's splits and
+// those of its own keys that it sees.  WPR waves share them out, where there are few rows.
+template <typename T, int LPR, int WPR>
 __global__ void __launch_bounds__(256) join_kernel(AttnArgs a) {
-  const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / LPR;
+  constexpr int RB = 256 / LPR / WPR;  // rows of a workgroup
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int which = WPR == 1 ? 0 : wave, slot = WPR == 1 ? threadIdx.x / LPR : lane / LPR;
+  const int64_t all = static_cast<int64_t>(a.N) * a.Hq, row_ = static_cast<int64_t>(blockIdx.x) * RB + slot;
+  const int64_t row = row_ < all ? row_ : all - 1;
   const int c = 4 * (threadIdx.x % LPR);
-  const int64_t all = static_cast<int64_t>(a.N) * a.Hq;
-  if (row >= all) return;
   const int tok = static_cast<int>(row / a.Hq);
   int s, i, n;
   if (a.cu) {
     // the last sequence that begins at or before the token
-    int lo = -1, hi = a.S;  // cu[lo] <= tok < cu[hi + 1]
+    int lo = -1, hi = a.S;
     while (lo < hi) {
       const int mid = lo + (hi - lo + 1) / 2;
       if (a.cu[mid] <= tok) lo = mid;
       else hi = mid - 1;
     }
     s = lo;
-    if (s < 0 || s >= a.S) return;
-    i = tok - a.cu[s];
-    n = a.cu[s + 1] - a.cu[s];
+    const bool in = s >= 0 && s < a.S;
+    i = in ? tok - a.cu[s] : 0;
+    n = in ? a.cu[s + 1] - a.cu[s] : 0;
   } else {
     s = tok / a.per;
     i = tok % a.per;
     n = a.per;
   }
-  const int len = a.lens[s];
+  const bool mine = row_ < all && c < a.D && s >= 0 && s < a.S;
+  const int len = mine ? a.lens[s] : 0;
   const bool bad = len < 0 || len > a.max_len || n > a.max_q;
   const int see = len - n + 1 + i;
-  const int parts = a.p_split + (bad || see <= 0 ? 0 : min(a.o_split, (see + a.o_chunk - 1) / a.o_chunk));
+  const int parts = !mine ? 0 : a.p_split + (bad || see <= 0 ? 0 : min(a.o_split, (see + a.o_chunk - 1) / a.o_chunk));
   float m = -__builtin_inff();
-  for (int x = 0; x < parts; ++x) m = fmaxf(m, a.ml[x * all + row].x);
-  const float ref = m == -__builtin_inff() ? 0.f : m;
-  float t = 0.f;
-  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (c < a.D)
 #pragma unroll 4
-    for (int x = 0; x < parts; ++x) {
-      const float2 ms = a.ml[x * all + row];
-      const float f = __builtin_amdgcn_exp2f(ms.x - ref);
-      const float4 z = *reinterpret_cast<const float4*>(a.part + (x * all + row) * a.D + c);
-      t += f * ms.y;
+  for (int x = which; x < parts; x += WPR) m = fmaxf(m, a.ml[x * all + row].x);
+  float ref = m == -__builtin_inff() ? 0.f : m, t = 0.f;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int x = which; x < parts; x += WPR) {
+    const float2 ms = a.ml[x * all + row];
+    const float f = __builtin_amdgcn_exp2f(ms.x - ref);
+    const float4 z = *reinterpret_cast<const float4*>(a.part + (x * all + row) * a.D + c);
+    t += f * ms.y;
+    y.x += f * z.x;
+    y.y += f * z.y;
+    y.z += f * z.z;
+    y.w += f * z.w;
+  }
+  if constexpr (WPR > 1) {
+    __shared__ float4 ys[WPR][64];
+    __shared__ float2 ms[WPR][64];
+    ys[wave][lane] = y;
+    ms[wave][lane] = make_float2(m, t);
+    __syncthreads();
+    if (wave > 0) return;
+    m = -__builtin_inff();
+#pragma unroll
+    for (int x = 0; x < WPR; ++x) m = fmaxf(m, ms[x][lane].x);
+    ref = m == -__builtin_inff() ? 0.f : m;
+    t = 0.f;
+    y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int x = 0; x < WPR; ++x) {
+      const float f = __builtin_amdgcn_exp2f(ms[x][lane].x - ref);
+      const float4 z = ys[x][lane];
+      t += f * ms[x][lane].y;
       y.x += f * z.x;
       y.y += f * z.y;
       y.z += f * z.z;
       y.w += f * z.w;
     }
-  if (c >= a.D) return;
+  }
+  if (!mine) return;
   const float f = bad ? __builtin_nanf("") : t == 0.f ? 0.f : 1.f / t;
   T* dst = static_cast<T*>(a.o) + row * a.D + c;
   if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(dst) = pack4_bf16(y.x * f, y.y * f, y.z * f, y.w * f);
@@ -342,58 +379,121 @@ __global__ void __launch_bounds__(256) join_kernel(AttnArgs a) {
   if (a.lse && c == 0) a.lse[row] = bad ? f : (m + log2f(t)) * kLn2;
 }
 
+template <typename T, int LPR> hipError_t launch_join(const AttnArgs& a, hipStream_t st) {
+  const int64_t rows = static_cast<int64_t>(a.N) * a.Hq;
+  if (rows * LPR >= 65536 * 8) join_kernel<T, LPR, 1><<<static_cast<unsigned>((rows + 256 / LPR - 1) / (256 / LPR)), 256, 0, st>>>(a);
+  else join_kernel<T, LPR, 4><<<static_cast<unsigned>((rows + 64 / LPR - 1) / (64 / LPR)), 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
 template <typename T, int DC, int QB, int NW> hipError_t launch_few(const AttnArgs& a, unsigned items, hipStream_t st) {
   few_kernel<T, DC, QB, NW><<<items, 64 * NW, 0, st>>>(a);
   return hipGetLastError();
 }
-template <typename T, int DC> hipError_t launch_qb(const AttnArgs& a, unsigned items, hipStream_t st) {
-  constexpr int NW = sizeof(T) == 4 && DC > 128 ? 2 : 4;
-  return a.rows == 16 ? launch_few<T, DC, 1, NW>(a, items, st) : launch_few<T, DC, 2, NW>(a, items, st);
+template <typename T, int DC> hipError_t launch_qb(const AttnArgs& a, int rows, unsigned items, hipStream_t st) {
+  constexpr int NW = DC * sizeof(T) <= 256 ? 4 : 2;
+  return rows == 16 ? launch_few<T, DC, 1, NW>(a, items, st) : launch_few<T, DC, 2, NW>(a, items, st);
+}
+// The items of a launch (which of them: a.which), all of the same number of rows.
+template <typename T> hipError_t launch_items(AttnArgs a, int which, hipStream_t st) {
+  a.which = which;
+  const unsigned p_items = which & 1 ? (a.p_split * a.Hk + 7) / 8 * 8 * a.p_tiles : 0;
+  const unsigned items = p_items + (which & 2 ? static_cast<unsigned>(a.o_tiles) * a.Hk * a.S * a.o_split : 0);
+  const int rows = which & 2 ? a.o_rows : a.p_rows;
+  if (items == 0) return hipSuccess;
+  if (rows > 32) return launch_many(a, rows, items, st);  // (bf16 only)
+  if (a.D <= 64) return launch_qb<T, 64>(a, rows, items, st);
+  if (a.D <= 128) return launch_qb<T, 128>(a, rows, items, st);
+  if (a.D <= 192) return launch_qb<T, 192>(a, rows, items, st);
+  return launch_qb<T, 256>(a, rows, items, st);
 }
 template <typename T> hipError_t launch_any(const AttnArgs& a, hipStream_t st) {
-  const unsigned p_items = a.together ? 0 : (a.p_split * a.Hk + 7) / 8 * 8 * a.p_tiles;
-  const unsigned items = p_items + static_cast<unsigned>(a.o_tiles) * a.Hk * a.S * a.o_split;
   hipError_t e;
-  if (a.D <= 64) e = launch_qb<T, 64>(a, items, st);
-  else if (a.D <= 128) e = launch_qb<T, 128>(a, items, st);
-  else if (a.D <= 192) e = launch_qb<T, 192>(a, items, st);
-  else e = launch_qb<T, 256>(a, items, st);
-  if (e != hipSuccess || a.together) return e;
-  const int64_t rows = static_cast<int64_t>(a.N) * a.Hq;
-  if (a.D <= 64) join_kernel<T, 16><<<static_cast<unsigned>((rows + 15) / 16), 256, 0, st>>>(a);
-  else if (a.D <= 128) join_kernel<T, 32><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, st>>>(a);
-  else join_kernel<T, 64><<<static_cast<unsigned>((rows + 3) / 4), 256, 0, st>>>(a);
-  return hipGetLastError();
+  if (a.together) return launch_items<T>(a, 2, st);
+  if (a.p_rows == a.o_rows) {
+    e = launch_items<T>(a, 3, st);
+  } else {
+    e = launch_items<T>(a, 1, st);
+    if (e == hipSuccess) e = launch_items<T>(a, 2, st);
+  }
+  if (e != hipSuccess) return e;
+  if (a.D <= 64) return launch_join<T, 16>(a, st);
+  if (a.D <= 128) return launch_join<T, 32>(a, st);
+  return launch_join<T, 64>(a, st);
 }
 
 }  // namespace
 }  // namespace attn
 
-void attn_plan(AttnArgs* a, bool bf, size_t* part, size_t* ml) {
-  (void)bf;
-  const int64_t own_rows = static_cast<int64_t>(a->max_q) * a->G, all_rows = static_cast<int64_t>(a->N) * a->G;
-  a->rows = own_rows <= 16 && (a->prefix == 0 || all_rows <= 16) ? 16 : 32;
-  a->o_tiles = static_cast<int>((own_rows + a->rows - 1) / a->rows);
-  const int64_t seq_items = static_cast<int64_t>(a->o_tiles) * a->Hk * a->S;
-  a->together = seq_items >= 512 || (a->prefix == 0 && a->max_len <= 256);
-  a->p_tiles = a->p_split = a->p_chunk = 0;
-  a->o_split = 1;
-  a->o_chunk = a->max_len > 0 ? a->max_len : 1;
-  *part = *ml = 0;
-  if (a->together) return;
-  if (a->prefix > 0) {
-    a->p_tiles = static_cast<int>((all_rows + a->rows - 1) / a->rows);
-    int64_t n = 512 / (static_cast<int64_t>(a->p_tiles) * a->Hk);
-    if (n < 1) n = 1;
-    a->p_chunk = static_cast<int>((a->prefix + n - 1) / n + 63) / 64 * 64;
-    if (a->p_chunk < 256) a->p_chunk = 256;
-    a->p_split = (a->prefix + a->p_chunk - 1) / a->p_chunk;
+namespace {
+
+// What a launch's items cost, in us: each its keys and what it takes to begin and end,
+// `slots` of them at once; and the parts that are written and read back.
+struct Cost {
+  double key, item;
+  int slots;
+};
+Cost cost_of(int rows, int D, bool bf) {
+  if (rows > 32) return {4.0 * rows * D / (rows > 128 ? 3.0e6 : 2.6e6), 8.0, 256};
+  return {2.0 * D * (bf ? 2 : 4) / 9.0e3 * (bf ? 1.0 : 1.5) * (rows == 16 ? 1.0 : 1.3), 6.0, 512};
+}
+struct Split {
+  int chunk, n;  // keys of a split, splits
+  double us;
+};
+// Of all numbers of splits of len keys the cheapest.
+Split split(int64_t items, int64_t len, const Cost& c, double part_us) {
+  Split best{1, 0, 0.0};
+  for (int n = 1; n <= 256 && len > 0; ++n) {
+    const int64_t k = ((len + n - 1) / n + 63) / 64 * 64;
+    if (n > 1 && k < 128) break;
+    const int64_t count = (len + k - 1) / k, rounds = (items * count + c.slots - 1) / c.slots;
+    const double us = rounds * (k * c.key + c.item) + count * part_us;
+    if (n == 1 || us < best.us) best = Split{static_cast<int>(k), static_cast<int>(count), us};
   }
-  int64_t n = 1024 / seq_items;
-  if (n < 1) n = 1;
-  a->o_chunk = static_cast<int>((a->max_len + n - 1) / n + 63) / 64 * 64;
-  if (a->o_chunk < 256) a->o_chunk = 256;
-  a->o_split = (a->max_len + a->o_chunk - 1) / a->o_chunk;
+  return best;
+}
+
+}  // namespace
+
+// Rows of an item.  The kernel for many rows from 65 on: 64 sequences' 512 rows and
+// 32768 keys of 2 heads of 256 take 67 us with it (128 rows), 167 us without.  256 rows
+// where a tile of them is full twice.  Few rows, 16 or 32 (the prefix's and own keys' in
+// one launch): what the cost says.
+void attn_plan(AttnArgs* a, bool bf, size_t* part, size_t* ml) {
+  const int64_t own = static_cast<int64_t>(a->max_q) * a->G, all = static_cast<int64_t>(a->N) * a->G;
+  const double part_us = static_cast<double>(a->N) * a->Hq * a->D * 8 / 4.0e6;  // written and read, at 4 TB/s
+  auto many = [&](int64_t n) { return bf && n > 64; };
+  auto rows_many = [](int64_t n) { return n <= 512 ? 128 : 256; };
+  Split o{}, p{};
+  auto choose = [&](int o_rows, int p_rows) {
+    a->o_rows = o_rows;
+    a->p_rows = p_rows;
+    a->o_tiles = static_cast<int>((own + o_rows - 1) / o_rows);
+    a->p_tiles = a->prefix > 0 ? static_cast<int>((all + p_rows - 1) / p_rows) : 0;
+    o = split(static_cast<int64_t>(a->o_tiles) * a->Hk * a->S, a->max_len, cost_of(o_rows, a->D, bf), part_us);
+    p = split(static_cast<int64_t>(a->p_tiles) * a->Hk, a->prefix, cost_of(p_rows, a->D, bf), part_us);
+    return o.us + p.us;
+  };
+  const bool few_p = a->prefix > 0 && !many(all);
+  if (many(own)) {
+    choose(rows_many(own), rows_many(a->prefix > 0 ? all : own));
+  } else {
+    const int p_many = rows_many(all);
+    const double c16 = choose(16, few_p ? 16 : p_many), c32 = choose(32, few_p ? 32 : p_many);
+    if (c16 <= c32) choose(16, few_p ? 16 : p_many);
+  }
+  a->o_chunk = o.chunk;
+  a->o_split = o.n;
+  a->p_chunk = p.chunk;
+  a->p_split = p.n;
+  a->together = a->prefix == 0 && o.n <= 1;
+  *part = *ml = 0;
+  if (a->together) {
+    a->o_chunk = a->max_len > 0 ? a->max_len : 1;
+    a->o_split = 1;
+    return;
+  }
   const size_t rows = static_cast<size_t>(a->p_split + a->o_split) * a->N * a->Hq;
   *part = rows * a->D * sizeof(float);
   *ml = rows * sizeof(float2);

@@ -137,23 +137,39 @@ template <int LPH, bool INTER> struct Lane {
   __device__ __forceinline__ void load_axes(const Args& a, int64_t token, int64_t dflt, Turn& tn, float flip) const {
     constexpr int NP = INTER ? 4 : 8;
     const int p0 = INTER ? c0 / 2 : c0 < a.R / 2 ? c0 : c0 - a.R / 2;
-    int64_t at[4];
+    // (all loads are unconditional, from clamped places: under a condition each waits
+    // for the one before it)
+    int at[4];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) at[x] = !a.pos ? dflt : x < a.A ? a.pos[x * a.BT + token] : -1;
+    for (int x = 0; x < 4; ++x) at[x] = dflt < 0 || dflt >= a.P ? -1 : static_cast<int>(dflt);
+    if (a.pos) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) at[x] = a.pos[min(x, a.A - 1) * a.BT + token];
+    }
     int axis[NP];
 #pragma unroll
     for (int i = 0; i < NP; ++i) axis[i] = a.axis[p0 + i];
     float c[NP], s[NP];
+    int at_i[NP];
+    bool ok[NP];
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int64_t pos = axis[i] == 0 ? at[0] : axis[i] == 1 ? at[1] : axis[i] == 2 ? at[2] : at[3];
-      const bool ok = axis[i] < a.A && pos >= 0 && pos < a.P;
-      const float* row = a.rope + (ok ? pos : 0) * a.R;
-      c[i] = s[i] = __builtin_nanf("");
-      if (ok) {
-        c[i] = row[p0 + i];
-        s[i] = row[a.R / 2 + p0 + i];
+      at_i[i] = axis[i] == 0 ? at[0] : axis[i] == 1 ? at[1] : axis[i] == 2 ? at[2] : at[3];
+      ok[i] = axis[i] < a.A && at_i[i] >= 0 && at_i[i] < a.P;
+      c[i] = s[i] = 0.f;
+    }
+    if (a.P > 0) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const float* row = a.rope + static_cast<int64_t>(ok[i] ? at_i[i] : 0) * a.R + p0 + i;
+        c[i] = row[0];
+        s[i] = row[a.R / 2];
       }
+    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      c[i] = ok[i] ? c[i] : __builtin_nanf("");
+      s[i] = ok[i] ? s[i] : __builtin_nanf("");
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -161,22 +177,126 @@ template <int LPH, bool INTER> struct Lane {
       tn.s[i] = INTER ? (i & 1 ? flip : -flip) * s[i / 2] : flip * sign * s[i];
     }
   }
-  // v turned, given the other channels' values (unused when interleaved)
-  __device__ __forceinline__ void turn(float* v, const float* o, const Turn& tn) const {
+  // v turned, given the other channels' values (unused when interleaved).  Which of the
+  // two products is rounded is said here and not left to the compiler, so that every
+  // kernel that turns rows gives the same bits: the own one forward, the other one back.
+  template <bool BACK> __device__ __forceinline__ void turn(float* v, const float* o, const Turn& tn) const {
     if constexpr (INTER) {
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {
         const float x = v[i], y = v[i + 1];
-        v[i] = turned ? x * tn.c[i] + y * tn.s[i] : x;
-        v[i + 1] = turned ? y * tn.c[i + 1] + x * tn.s[i + 1] : y;
+        v[i] = turned ? fmaf(x, tn.c[i], y * tn.s[i]) : x;
+        v[i + 1] = turned ? fmaf(y, tn.c[i + 1], x * tn.s[i + 1]) : y;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = turned ? v[i] * tn.c[i] + o[i] * tn.s[i] : v[i];
+      for (int i = 0; i < 8; ++i) {
+        const float t = BACK ? fmaf(v[i], tn.c[i], o[i] * tn.s[i]) : fmaf(o[i], tn.s[i], v[i] * tn.c[i]);
+        v[i] = turned ? t : v[i];
+      }
     }
   }
 };
 
+
+// A wave's run of a token's head groups (64 / LPH heads each): the groups of the
+// query heads, then the key heads', then (PARTS = 3) the value heads', from g0 to g1.
+// Queries and keys are normed (where they have weights) and turned; values are copied.
+// A batch of rows is on its way while the one before it is worked on (rows one by one
+// left the wave waiting for each: 8192 tokens of 32 + 8 heads of 128, bf16, 47 us
+// against 37).  find is called once, behind the first batch's loads: it gives the
+// token's angles, and where each part's rows go (null: nowhere) and from one head to
+// the next, in bytes.
+template <typename T, int LPH, bool INTER, bool AXES, int PARTS, typename Args, typename Find>
+__device__ __forceinline__ void turn_rows(const Args& a, const Lane<LPH, INTER>& ln, int64_t token, int g0, int g1,
+                                          int gq, int gk, const T* const (&src)[PARTS], Find find) {
+  constexpr int RPW = 64 / LPH, U = sizeof(T) == 2 ? 4 : 2;
+  const int sub_row = (threadIdx.x & 63) / LPH;
+  const int begin[4] = {0, gq, gq + gk, gq + 2 * gk};
+  auto part_of = [&](int g) { return g < begin[1] ? 0 : PARTS == 2 || g < begin[2] ? 1 : 2; };
+  auto pick = [&](int part, auto x, auto y, auto z) { return part == 0 ? x : PARTS == 2 || part == 1 ? y : z; };
+  auto last = [&](int part) { return min(g1, pick(part, begin[1], begin[2], begin[3])); };  // the part's end in the run
+  auto fetch = [&](int g, Raw<T>(&x)[U]) {
+    const int part = part_of(g), end = last(part), base = pick(part, begin[0], begin[1], begin[2]);
+    const T* from = pick(part, src[0], src[1], src[PARTS - 1]);
+    const int H = part ? a.Hk : a.Hq;
+    // (from clamped places: a load under a condition waits for the one before it)
+    const int c0 = ln.on ? ln.c0 : 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u].load(from + min((min(g + u, end - 1) - base) * RPW + sub_row, H - 1) * a.D + c0);
+  };
+  if (g0 >= g1) return;
+  Raw<T> x[U];
+  fetch(g0, x);
+  Raw<float> raw[2];
+#pragma unroll
+  for (int part = 0; part < 2; ++part) {
+    const float* wp = part ? a.wk : a.wq;
+    raw[part].zero();
+    if (wp) raw[part].load(wp + (ln.on ? ln.c0 : 0));
+  }
+  Turn tn;
+  char* dst[3];
+  int64_t step[3];
+  find(tn, dst, step);
+  const float inv = 1.f / static_cast<float>(a.D);
+  float wt[8], wo[8];
+  int now = -1;
+#pragma unroll 1
+  for (int g = g0; g < g1;) {
+    const int part = part_of(g), end = last(part), next = min(g + U, end);
+    Raw<T> y[U];
+    if (next < g1) fetch(next, y);
+    const bool normed = !AXES || (part ? a.wk : a.wq) != nullptr;
+    if (part != now && part < 2) {
+      float w0[8], w1[8];
+      raw[0].unpack(w0);
+      raw[1].unpack(w1);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        wt[i] = normed ? (part ? w1[i] : w0[i]) + a.w_offset : 1.f;
+        wo[i] = __shfl(wt[i], ln.other);
+      }
+    }
+    now = part;
+    const int H = part ? a.Hk : a.Hq, base = pick(part, begin[0], begin[1], begin[2]);
+    char* to = pick(part, dst[0], dst[1], dst[PARTS - 1]);
+    const int64_t hop = pick(part, step[0], step[1], step[PARTS - 1]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (g + u >= end) break;
+      const int head = (g + u - base) * RPW + sub_row;
+      const bool on = ln.on && head < H && to;
+      T* out = reinterpret_cast<T*>(to + head * hop) + ln.c0;
+      if (PARTS == 3 && part == 2) {
+        if (on) x[u].put(out);
+        continue;
+      }
+      float v[8], o[8];
+      if (!ln.on) x[u].zero();
+      x[u].unpack(v);
+      float r = 1.f;
+      if (normed) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+        r = 1.f / sqrtf(row_sum<LPH>(ss) * inv + a.eps);
+      }
+      if constexpr (!INTER) {
+        x[u].from_lane(ln.other).unpack(o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] *= r * wo[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= r * wt[i];
+      ln.template turn<false>(v, o, tn);
+      if (on) Raw<T>::store(out, v);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = y[u];
+    g = next;
+  }
+}
 
 // The smallest power of two of lanes that holds a row.
 inline int lanes_for(int D) {
