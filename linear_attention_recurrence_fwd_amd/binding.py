@@ -2,7 +2,9 @@
 
 Argument marshalling only: this module checks dtypes/shapes, allocates the
 outputs and the workspace with torch (device memory), and passes raw pointers
-plus the current HIP stream to the library.  Every step of the computation runs
+plus the current HIP stream to the library.  The entries of the rotation with
+several axes and of the paged cache first take the same steps in native code
+(_calls), which leaves everything out of the ordinary to the functions here.  Every step of the computation runs
 in the library's kernels.  There is no fallback: if libgdn.so is missing or a
 call fails, an exception is raised.
 """
@@ -14,6 +16,11 @@ import functools
 import os
 
 import torch
+
+try:
+    from . import _calls  # the short way to the entries for single tokens (csrc/gdn_calls.cpp)
+except ImportError:  # not built: the long way, in this module, is whole without it
+    _calls = None
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
@@ -820,6 +827,10 @@ def norm_rope_axes(q, k, wq=None, wk=None, rope=None, axis=None, pos=None, *, ep
                    interleaved=False):
     """norm_rope with positions on up to four axes: pos [A,B,T] int32, axis [R/2]
     uint8 the axis of each pair (axis_map).  Without wq and wk, the rotation alone."""
+    if _calls is not None:
+        out = _calls.norm_rope_axes(q, k, wq, wk, rope, axis, pos, eps, w_offset, interleaved)
+        if out is not NotImplemented:
+            return out
     d, A = _norm_axes_dims(q, k, wq, wk, rope, axis, pos, eps, w_offset, interleaved)
     dev, dt = q.device, q.dtype
     oq = torch.empty((d.B, d.T, d.Hq, d.D), dtype=dt, device=dev)
@@ -842,6 +853,10 @@ def _norm_axes_dims(q, k, wq, wk, rope, axis, pos, eps, w_offset, interleaved):
 def norm_rope_axes_bwd(q, k, wq, wk, rope, axis, pos, dyq, dyk, *, eps=1e-6, w_offset=0.0, interleaved=False):
     """VJP of norm_rope_axes.  Returns dict(dq, dk, dwq, dwk), dq and dk dense, dwq and
     dwk None without the norm."""
+    if _calls is not None:
+        out = _calls.norm_rope_axes_bwd(q, k, wq, wk, rope, axis, pos, eps, w_offset, interleaved, dyq, dyk)
+        if out is not NotImplemented:
+            return out
     d, A = _norm_axes_dims(q, k, wq, wk, rope, axis, pos, eps, w_offset, interleaved)
     dev = q.device
     _check(dyq, "dyq", q.shape, q.dtype, dev)
@@ -944,6 +959,11 @@ def paged_append(q, k, v, k_pages, v_pages, table, past, cu=None, *, wq=None, wk
     past[s] + i of sequence s, whose pages are table[s].  Sequence s has the tokens
     cu[s] .. cu[s+1] - 1, or N / S tokens each.  q, k, v may be slices of a packed
     projection; q may be None.  Returns the turned queries (in out, if given)."""
+    if _calls is not None:
+        y = _calls.paged_append(q, k, v, k_pages, v_pages, table, past, cu, wq, wk, rope, axis, pos, first, eps, w_offset,
+                                interleaved, out)
+        if y is not NotImplemented:
+            return y
     N, Hk, D = k.shape
     dev, dt = k.device, k.dtype
     Hq = 0 if q is None else q.shape[1]
@@ -994,6 +1014,11 @@ def prefix_attention(q, k_pages, v_pages, table, lens, prefix_pages=None, prefix
     and max_len (the room of a table's row) bound a sequence's tokens in the call and its
     own length: the launch goes by them.  scale: D^-1/2 by default.  Returns o [N,Hq,D]
     (in out, if given), with lse=True (o, lse [N,Hq] fp32)."""
+    if _calls is not None:
+        y = _calls.prefix_attention(q, k_pages, v_pages, table, lens, prefix_pages, prefix, cu, max_q, max_len, scale, out,
+                                    lse)
+        if y is not NotImplemented:
+            return y
     N, Hq, D = q.shape
     dev, dt = q.device, q.dtype
     dims = _check_pool(k_pages, v_pages, table, cu, N, Hq, dt, dev)

@@ -1,4 +1,5 @@
-"""Build libgdn.so (gfx950) from csrc/*.hip with hipcc, in place.
+"""Build libgdn.so (gfx950) from csrc/*.hip with hipcc, and _calls.so (the short way
+from Python to it, host code) from csrc/gdn_calls.cpp with g++, in place.
 
 Each .hip file compiles to its own object (in parallel), then one shared
 library is linked.  Flags: -O3, gfx950 only, packed-fp32 instructions off,
@@ -18,6 +19,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgdn.so")
+CALLS = os.path.join(HERE, "_calls.so")
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=" + ARCH,
@@ -38,16 +40,47 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_calls() -> str:
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+
+    obj = os.path.join(OBJ, "gdn_calls.cpp.o")
+    dirs = [*include_paths(), "/opt/rocm/include", sysconfig.get_paths()["include"]]
+    r = subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+                        "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, *["-isystem" + d for d in dirs],
+                        "-c", os.path.join(CSRC, "gdn_calls.cpp"), "-o", obj], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for gdn_calls.cpp:\n%s" % r.stderr)
+    if r.stderr:
+        sys.stderr.write(r.stderr)
+    return obj
+
+
+def _link_calls(obj: str) -> None:
+    import torch
+
+    tmp = CALLS + ".tmp%d" % os.getpid()
+    subprocess.run(["g++", "-shared", obj, "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-L" + HERE,
+                    "-l:libgdn.so", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN",
+                    "-o", tmp], check=True)
+    os.replace(tmp, CALLS)
+
+
 def build(jobs: int | None = None) -> str:
     os.makedirs(OBJ, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
     jobs = jobs or min(len(srcs), os.cpu_count() or 4, 8)
     with cf.ThreadPoolExecutor(jobs) as ex:
+        calls = ex.submit(_compile_calls)
         objs = list(ex.map(_compile, srcs))
+        calls = calls.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     subprocess.run([HIPCC, "-shared", "-fPIC", "--offload-arch=" + ARCH, *objs, "-o", tmp],
                    check=True)
     os.replace(tmp, LIB)
+    _link_calls(calls)
     return LIB
 
 

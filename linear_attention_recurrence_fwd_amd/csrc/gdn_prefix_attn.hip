@@ -441,15 +441,17 @@ struct Split {
   int chunk, n;  // keys of a split, splits
   double us;
 };
-// Of all numbers of splits of len keys the cheapest.
+// Of the numbers of splits of len keys that fill one to eight rounds of the slots, and
+// one, the cheapest.
 Split split(int64_t items, int64_t len, const Cost& c, double part_us) {
   Split best{1, 0, 0.0};
-  for (int n = 1; n <= 256 && len > 0; ++n) {
-    const int64_t k = ((len + n - 1) / n + 63) / 64 * 64;
-    if (n > 1 && k < 128) break;
+  for (int round = 0; round <= 8 && len > 0; ++round) {
+    const int64_t n = round == 0 ? 1 : round * c.slots / items;
+    if (n < 1) continue;
+    const int64_t even = ((len + n - 1) / n + 63) / 64 * 64, k = n > 1 && even < 128 ? 128 : even;
     const int64_t count = (len + k - 1) / k, rounds = (items * count + c.slots - 1) / c.slots;
     const double us = rounds * (k * c.key + c.item) + count * part_us;
-    if (n == 1 || us < best.us) best = Split{static_cast<int>(k), static_cast<int>(count), us};
+    if (round == 0 || us < best.us) best = Split{static_cast<int>(k), static_cast<int>(count), us};
   }
   return best;
 }
