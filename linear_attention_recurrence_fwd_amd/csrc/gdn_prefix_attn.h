@@ -44,10 +44,18 @@ __device__ __forceinline__ void load_lds4(const void* p, uint32_t lds) {
   asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "{m0}"(lds) : "memory");
 }
 
-// Where 16-byte piece p of row r of a tile lies: place p ^ swizzle(r) of the row.  The
-// eight rows that a wide read takes at once, and the four rows of two pieces of a
-// transposing read, then lie on different banks.
-__device__ __forceinline__ int swizzle(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
+// Where 16-byte piece p of row r of a tile lies: place p ^ swizzle(r) of the row.  LDS
+// gives 256 bytes a cycle, 16 such pieces: to a wide read 16 lanes' (one piece of 16
+// rows), to a transposing read 32 lanes' (AROUND = 4: four pieces of four rows, or 2: two
+// of eight), to a read of single words 64 lanes' (AROUND = 0: four pieces of the rows r,
+// r + 4, r + 8, r + 12).  The swizzle puts each of these on sixteen different places,
+// modulo 16; rows of an odd number of 128 bytes have half of it from their parity.
+// (By three bits for all, half of the LDS's cycles in use were conflicts.)
+template <int PR, int AROUND> __device__ __forceinline__ int swizzle(int row) {
+  if (AROUND == 0) return (((row >> 2) & 3) << 2) | (row & 3);
+  if (AROUND == 4) return PR % 16 == 0 ? ((row & 3) << 2) | ((row >> 2) & 3) : (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+  return PR % 16 == 0 ? ((row & 7) << 1) | ((row >> 3) & 1) : (((row >> 1) & 3) << 1) | ((row >> 3) & 1);
+}
 
 // What an item works on: rows from row0 on of the tokens t0 .. t0 + n - 1 (n G rows in
 // all) and key head hk, keys k0 .. k1 - 1 in the pages of list; bad: the result is NaN.
@@ -119,7 +127,7 @@ __device__ __forceinline__ void bad_rows(const AttnArgs& a, const Item& it, int 
   }
 }
 
-hipError_t launch_many(const AttnArgs& a, int rows, unsigned items, hipStream_t st);
+hipError_t launch_many(const AttnArgs& a, unsigned items, hipStream_t st);  // items of 128 rows, bf16
 
 }  // namespace attn
 }  // namespace gdn

@@ -48,7 +48,8 @@ __global__ void __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) few_kernel(AttnArgs 
   using F = Few<T, DC, QB, NW>;
   constexpr bool BF = sizeof(T) == 2;
   constexpr int KT = F::KT, PR = F::PR, ST = F::ST, NL = F::NL, TS = F::TS, NS = DC / 16;
-  __shared__ __align__(16) char lds[F::LDS];
+  __shared__ __align__(256) char lds[F::LDS];
+  auto swz = [](int row) { return swizzle<PR, BF ? 2 : 0>(row); };
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, lr = l & 15, lg = l >> 4;
   const Item it = find_item(a);
   if (it.empty) return;
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) few_kernel(AttnArgs 
   uint32_t from_first[NL];
 #pragma unroll
   for (int i = 0; i < NL; ++i) {
-    const int row = (i * 64 + l) / PR, piece = ((i * 64 + l) % PR) ^ swizzle(row);
+    const int row = (i * 64 + l) / PR, piece = ((i * 64 + l) % PR) ^ swz(row);
     from_first[i] = row * static_cast<uint32_t>(a.pool.ts) + piece * 16;
   }
   auto load_tile = [&](int x) {
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) few_kernel(AttnArgs 
     if (key >= end) off = -1;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-      const int row = (i * 64 + l) / PR, piece = ((i * 64 + l) % PR) ^ swizzle(row);
+      const int row = (i * 64 + l) / PR, piece = ((i * 64 + l) % PR) ^ swz(row);
       const int64_t from = (static_cast<int64_t>(__shfl(static_cast<int>(off >> 32), row)) << 32) |
                            static_cast<uint32_t>(__shfl(static_cast<int>(off), row));
       const bool fill = from < 0 || piece * 16 >= a.D * F::E;
@@ -164,14 +165,14 @@ __global__ void __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) few_kernel(AttnArgs 
     if constexpr (BF) {
 #pragma unroll
       for (int st = 0; st < NS / 2; ++st) {
-        const bf16x8 k = load_bf16x8(kt + (lr * PR + ((4 * st + lg) ^ swizzle(lr))) * 16);
+        const bf16x8 k = load_bf16x8(kt + (lr * PR + ((4 * st + lg) ^ swz(lr))) * 16);
 #pragma unroll
         for (int b = 0; b < QB; ++b) s[b] = mfma16(k, as_bf16x8(q[b][st]), s[b]);
       }
     } else {
 #pragma unroll
       for (int st = 0; st < NS; ++st) {
-        const float4 k = *reinterpret_cast<const float4*>(kt + (lr * PR + ((4 * st + lg) ^ swizzle(lr))) * 16);
+        const float4 k = *reinterpret_cast<const float4*>(kt + (lr * PR + ((4 * st + lg) ^ swz(lr))) * 16);
 #pragma unroll
         for (int b = 0; b < QB; ++b) {
           s[b] = mfma16f(k.x, __uint_as_float(q[b][st].x), s[b]);
@@ -197,9 +198,9 @@ __global__ void __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) few_kernel(AttnArgs 
         float top = fmaxf(fmaxf(s[b][0], s[b][1]), fmaxf(s[b][2], s[b][3]));
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
-        top = fmaxf(top, m[b]);
-        const float f = top == m[b] ? 1.f : __builtin_amdgcn_exp2f(m[b] - top);
-        m[b] = top;
+        // (only of the rows that ask for it: a row's bits are its own, whatever lies beside it)
+        const float to = top > m[b] + kSlack ? top : m[b], f = to == m[b] ? 1.f : __builtin_amdgcn_exp2f(m[b] - to);
+        m[b] = to;
         sum[b] *= f;
 #pragma unroll
         for (int d = 0; d < NS; ++d) o[b][d] *= f;
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) few_kernel(AttnArgs 
       const int row = 4 * lg + (lr >> 2), in = (lr & 1) * 8;
 #pragma unroll
       for (int d = 0; d < NS; ++d) {
-        const uint2 v = lds_read_tr16(vt + (row * PR + ((2 * d + ((lr & 3) >> 1)) ^ swizzle(row))) * 16 + in);
+        const uint2 v = lds_read_tr16(vt + (row * PR + ((2 * d + ((lr & 3) >> 1)) ^ swz(row))) * 16 + in);
 #pragma unroll
         for (int b = 0; b < QB; ++b)
           o[b][d] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, v), pb[b], o[b][d], 0, 0, 0);
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) few_kernel(AttnArgs 
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int row = 4 * lg + r;
-          const float v = *reinterpret_cast<const float*>(vt + (row * PR + ((4 * d + (lr >> 2)) ^ swizzle(row))) * 16 + (lr & 3) * 4);
+          const float v = *reinterpret_cast<const float*>(vt + (row * PR + ((4 * d + (lr >> 2)) ^ swz(row))) * 16 + (lr & 3) * 4);
 #pragma unroll
           for (int b = 0; b < QB; ++b) o[b][d] = mfma16f(v, p[b][r], o[b][d]);
         }
@@ -401,7 +402,7 @@ template <typename T> hipError_t launch_items(AttnArgs a, int which, hipStream_t
   const unsigned items = p_items + (which & 2 ? static_cast<unsigned>(a.o_tiles) * a.Hk * a.S * a.o_split : 0);
   const int rows = which & 2 ? a.o_rows : a.p_rows;
   if (items == 0) return hipSuccess;
-  if (rows > 32) return launch_many(a, rows, items, st);  // (bf16 only)
+  if (rows > 32) return launch_many(a, items, st);  // (bf16 only)
   if (a.D <= 64) return launch_qb<T, 64>(a, rows, items, st);
   if (a.D <= 128) return launch_qb<T, 128>(a, rows, items, st);
   if (a.D <= 192) return launch_qb<T, 192>(a, rows, items, st);
@@ -434,7 +435,7 @@ struct Cost {
   int slots;
 };
 Cost cost_of(int rows, int D, bool bf) {
-  if (rows > 32) return {4.0 * rows * D / (rows > 128 ? 3.0e6 : 2.6e6), 8.0, 256};
+  if (rows > 32) return {4.0 * rows * D / 1.6e6, 14.0, 512};
   return {2.0 * D * (bf ? 2 : 4) / 9.0e3 * (bf ? 1.0 : 1.5) * (rows == 16 ? 1.0 : 1.3), 6.0, 512};
 }
 struct Split {
@@ -466,7 +467,6 @@ void attn_plan(AttnArgs* a, bool bf, size_t* part, size_t* ml) {
   const int64_t own = static_cast<int64_t>(a->max_q) * a->G, all = static_cast<int64_t>(a->N) * a->G;
   const double part_us = static_cast<double>(a->N) * a->Hq * a->D * 8 / 4.0e6;  // written and read, at 4 TB/s
   auto many = [&](int64_t n) { return bf && n > 64; };
-  auto rows_many = [](int64_t n) { return n <= 512 ? 128 : 256; };
   Split o{}, p{};
   auto choose = [&](int o_rows, int p_rows) {
     a->o_rows = o_rows;
@@ -479,11 +479,10 @@ void attn_plan(AttnArgs* a, bool bf, size_t* part, size_t* ml) {
   };
   const bool few_p = a->prefix > 0 && !many(all);
   if (many(own)) {
-    choose(rows_many(own), rows_many(a->prefix > 0 ? all : own));
+    choose(128, 128);
   } else {
-    const int p_many = rows_many(all);
-    const double c16 = choose(16, few_p ? 16 : p_many), c32 = choose(32, few_p ? 32 : p_many);
-    if (c16 <= c32) choose(16, few_p ? 16 : p_many);
+    const double c16 = choose(16, few_p ? 16 : 128), c32 = choose(32, few_p ? 32 : 128);
+    if (c16 <= c32) choose(16, few_p ? 16 : 128);
   }
   a->o_chunk = o.chunk;
   a->o_split = o.n;
