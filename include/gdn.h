@@ -478,13 +478,16 @@ int gdn_paged_append(const gdn_paged_dims* d, const gdn_turn* t, const void* q, 
  *                logarithm (base e) of the sum of e^(scale q . k)
  * A sequence with lens outside 0 .. max_len or more than max_q tokens gives NaN; a
  * page outside 0 .. pages-1 counts as rows of NaN.  Rows of the pool behind lens,
- * and behind the prefix's end, are not read into anything, NaN or not.
+ * and behind the prefix's end, are not read into anything, NaN or not.  A NaN or Inf
+ * in v of one of the call's own tokens may reach the call's earlier tokens of the same
+ * sequence (whose weight for it is 0); in k it reaches those that see it.
  *
  * bf16: products of bf16 by the matrix cores with fp32 sums; the softmax's
- * statistics are fp32; the weights p are rounded to bf16 for the product with v
- * (2^-9 of each, at random: 1.1e-3 of the result in 2-norm where its own rounding is
- * 1.7e-3).  fp32: fp32 products and sums throughout.
- * Deterministic: the keys are split by sizes alone, and joined in a fixed order.
+ * statistics are fp32 (of weights that are not rounded); the weights p are rounded to
+ * bf16 for the product with v (up to 2^-8 of each, at random: 1.7e-3 of the result in
+ * 2-norm beside its own rounding's 1.7e-3).  fp32: fp32 products and sums throughout.
+ * Deterministic: the keys are split by the sizes given on the host alone, and joined
+ * in a fixed order; what else is in the batch does not reach a row's bits otherwise.
  */
 int gdn_prefix_attention_workspace_bytes(const gdn_paged_dims* d, int64_t prefix, int64_t max_q,
                                          int64_t max_len, size_t* out);

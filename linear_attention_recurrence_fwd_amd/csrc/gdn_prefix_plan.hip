@@ -1,0 +1,79 @@
+// How the attention over a prefix and own pages is cut into items: host code alone.
+#include "gdn_paged.h"
+
+namespace gdn {
+namespace {
+
+// What a launch's items cost, in us: each its keys and what it takes to begin and end,
+// `slots` of them at once; and the parts that are written and read back.
+struct Cost {
+  double key, item;
+  int slots;
+};
+Cost cost_of(int rows, int D, bool bf) {
+  if (rows > 32) return {4.0 * rows * D / 1.6e6, 14.0, 512};
+  return {2.0 * D * (bf ? 2 : 4) / 9.0e3 * (bf ? 1.0 : 1.5) * (rows == 16 ? 1.0 : 1.3), 6.0, 512};
+}
+struct Split {
+  int chunk, n;  // keys of a split, splits
+  double us;
+};
+// Of the numbers of splits of len keys that fill one to eight rounds of the slots, and
+// one, the cheapest.
+Split split(int64_t items, int64_t len, const Cost& c, double part_us) {
+  Split best{1, 0, 0.0};
+  for (int round = 0; round <= 8 && len > 0; ++round) {
+    const int64_t n = round == 0 ? 1 : round * c.slots / items;
+    if (n < 1) continue;
+    const int64_t even = ((len + n - 1) / n + 63) / 64 * 64, k = n > 1 && even < 128 ? 128 : even;
+    const int64_t count = (len + k - 1) / k, rounds = (items * count + c.slots - 1) / c.slots;
+    const double us = rounds * (k * c.key + c.item) + count * part_us;
+    if (round == 0 || us < best.us) best = Split{static_cast<int>(k), static_cast<int>(count), us};
+  }
+  return best;
+}
+
+}  // namespace
+
+// Rows of an item.  The kernel for many rows from 65 on: 64 sequences' 512 rows and
+// 32768 keys of 2 heads of 256 take 67 us with it (128 rows), 167 us without.  256 rows
+// where a tile of them is full twice.  Few rows, 16 or 32 (the prefix's and own keys' in
+// one launch): what the cost says.
+void attn_plan(AttnArgs* a, bool bf, size_t* part, size_t* ml) {
+  const int64_t own = static_cast<int64_t>(a->max_q) * a->G, all = static_cast<int64_t>(a->N) * a->G;
+  const double part_us = static_cast<double>(a->N) * a->Hq * a->D * 8 / 4.0e6;  // written and read, at 4 TB/s
+  auto many = [&](int64_t n) { return bf && n > 64; };
+  Split o{}, p{};
+  auto choose = [&](int o_rows, int p_rows) {
+    a->o_rows = o_rows;
+    a->p_rows = p_rows;
+    a->o_tiles = static_cast<int>((own + o_rows - 1) / o_rows);
+    a->p_tiles = a->prefix > 0 ? static_cast<int>((all + p_rows - 1) / p_rows) : 0;
+    o = split(static_cast<int64_t>(a->o_tiles) * a->Hk * a->S, a->max_len, cost_of(o_rows, a->D, bf), part_us);
+    p = split(static_cast<int64_t>(a->p_tiles) * a->Hk, a->prefix, cost_of(p_rows, a->D, bf), part_us);
+    return o.us + p.us;
+  };
+  const bool few_p = a->prefix > 0 && !many(all);
+  if (many(own)) {
+    choose(128, 128);
+  } else {
+    const double c16 = choose(16, few_p ? 16 : 128), c32 = choose(32, few_p ? 32 : 128);
+    if (c16 <= c32) choose(16, few_p ? 16 : 128);
+  }
+  a->o_chunk = o.chunk;
+  a->o_split = o.n;
+  a->p_chunk = p.chunk;
+  a->p_split = p.n;
+  a->together = a->prefix == 0 && o.n <= 1;
+  *part = *ml = 0;
+  if (a->together) {
+    a->o_chunk = a->max_len > 0 ? a->max_len : 1;
+    a->o_split = 1;
+    return;
+  }
+  const size_t rows = static_cast<size_t>(a->p_split + a->o_split) * a->N * a->Hq;
+  *part = rows * a->D * sizeof(float);
+  *ml = rows * sizeof(float2);
+}
+
+}  // namespace gdn
