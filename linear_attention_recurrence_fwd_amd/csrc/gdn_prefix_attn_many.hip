@@ -8,9 +8,14 @@
 // taken as the scores' product left them (places 8 (e / 4) + 4 half + e % 4), and the
 // values' transposing reads follow, so no weight changes its lane.
 //
-// A 32x32x16 product takes 32 cycles of a SIMD and one operand of 1 KB from LDS, 8
-// cycles of the compute unit's one LDS: with four SIMDs both are full at once.  Two
-// waves on a SIMD let one's exponentials run beside the other's products.
+// A 32x32x16 product takes 32 cycles of a SIMD and one operand of 1 KB from LDS, 4
+// cycles of the compute unit's one LDS, so the products could keep the SIMDs busy three
+// quarters of the time beside the LDS.  What bounds the kernel is the issue of
+// instructions: two waves to a SIMD, each of which starts one in about four cycles, have
+// reads, exponentials, packing and waits to start beside each product.  Measured: 16
+// prompts of 20 to 290 tokens over 8192 shared keys, 32 heads of 128 on 8 key heads, 410
+// us of this kernel, 830 TFLOP/s (a large product of matrices reaches 1233 here); 64
+// single tokens over 32768 shared keys, 16 heads of 256 on 2, 59 us, 580 TFLOP/s.
 #include "gdn_prefix_attn.h"
 
 namespace gdn {
@@ -21,16 +26,16 @@ typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16;
 
 template <int DC> struct Many {
   static constexpr int W = 4, PR = DC / 8;                  // waves; pieces of 16 bytes of a row
-  static constexpr int BN = DC == 64 ? 64 : 32;             // keys of a tile
+  static constexpr int BN = DC <= 128 ? 64 : 32;            // keys of a tile
   static constexpr int XN = BN / 32;                        // blocks of 32 keys of a tile
   static constexpr int TILE = BN * PR * 16;                 // bytes of a tile of keys or values
-  static constexpr int ST = DC <= 128 ? 4 : DC == 192 ? 3 : 2;
+  static constexpr int ST = 2;                              // tiles in LDS
   static constexpr int RW = BN / W;                         // rows that a wave loads
   static constexpr int NL = TILE / 1024 / W;                // load instructions of a wave for a tile
-  static constexpr int TS = 2 * ST;                         // tiles whose pages are held
+  static constexpr int AHEAD_K = DC == 64 ? 4 : DC == 128 ? 8 : DC == 192 ? 4 : 3;  // operands read ahead: what
+  static constexpr int AHEAD_V = DC == 64 ? 4 : DC == 128 ? 4 : DC == 192 ? 3 : 2;  // registers are there for
   static constexpr int STAGE = 32 * 68 * 4;                 // a wave's 64 channels of its rows
-  static constexpr int RING = 2 * TILE * ST > W * STAGE ? 2 * TILE * ST : W * STAGE;
-  static constexpr int LDS = RING + W * TS * RW * 4;
+  static constexpr int PAGES = 2 * TILE * ST > W * STAGE ? 2 * TILE * ST : W * STAGE, LDS = PAGES + W * 256;
   static_assert(NL * 1024 * W == TILE && LDS <= 80 * 1024, "whole loads, two workgroups to a compute unit");
 };
 
@@ -48,9 +53,22 @@ __device__ __forceinline__ uint2 read_tr(uint32_t at, int off) {
   return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_t*>(at + off)));
 }
 
+// Has the compiler read the operands (READS to a product) of AHEAD products before the
+// first of N, and then each product's AHEAD ahead: left to itself it reads each operand
+// when it is wanted, and every product of the chain waits for the LDS.
+template <int N, int READS, int AHEAD> __device__ __forceinline__ void operands_ahead() {
+  __builtin_amdgcn_sched_group_barrier(0x100, READS * AHEAD, READS);  // LDS reads
+#pragma unroll
+  for (int i = 0; i < N - AHEAD; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, READS);  // products
+    __builtin_amdgcn_sched_group_barrier(0x100, READS, READS);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x8, AHEAD, READS);
+}
+
 template <int DC> __global__ void __launch_bounds__(256, 2) many_kernel(AttnArgs a) {
   using F = Many<DC>;
-  constexpr int PR = F::PR, ST = F::ST, NL = F::NL, TS = F::TS, RW = F::RW, BN = F::BN, XN = F::XN, NQ = DC / 16, ND = DC / 32;
+  constexpr int PR = F::PR, ST = F::ST, NL = F::NL, RW = F::RW, BN = F::BN, XN = F::XN, NQ = DC / 16, ND = DC / 32;
   __shared__ __align__(256) char lds[F::LDS];
   auto swz = [](int row) { return swizzle<PR, 4>(row); };
   constexpr int SW = PR % 16 == 0 ? 16 : 8;  // pieces among which the swizzle moves one
@@ -58,8 +76,7 @@ template <int DC> __global__ void __launch_bounds__(256, 2) many_kernel(AttnArgs
   const Item it = find_item(a);
   if (it.empty) return;
   const int cnt = it.k1 > it.k0 ? (it.k1 - it.k0 + BN - 1) / BN : 0;  // tiles
-  int32_t* pages = reinterpret_cast<int32_t*>(lds + F::RING) + w * TS * RW;
-  const uint32_t lds_at = lds_of(lds), pages_at = lds_at + F::RING + w * TS * RW * 4;
+  const uint32_t lds_at = lds_of(lds);
 
   const int G = a.G, nrows = it.n * G, row_w = it.row0 + 32 * w, row = row_w + lr;
   const bool on = row < nrows && !it.bad;
@@ -84,30 +101,52 @@ template <int DC> __global__ void __launch_bounds__(256, 2) many_kernel(AttnArgs
   float m = -__builtin_inff(), sum = 0.f;
 
   const char *kb = static_cast<const char*>(a.kp) + it.hk * a.pool.hs, *vb = static_cast<const char*>(a.vp) + it.hk * a.pool.hs;
-  const int in_page = (1 << a.pool.shift) - 1, lw = w * RW + (l % RW);
-  auto page_of = [&](int t) {
-    const int key = min(it.k0 + BN * (t < cnt ? t : cnt - 1) + lw, it.k1 - 1);
-    return it.list + (key >> a.pool.shift);
+  const int in_page = (1 << a.pool.shift) - 1;
+  const int lw = w * RW + l % RW;  // the row of a tile whose page this lane knows
+  const int32_t* pages = reinterpret_cast<const int32_t*>(lds + F::PAGES) + w * 64;
+  auto load_page = [&](int t) {
+    load_lds4(it.list + (min(it.k0 + BN * min(t, cnt - 1) + lw, it.k1 - 1) >> a.pool.shift), lds_at + F::PAGES + w * 256);
   };
   // The rows that a wave loads of a full tile lie in one page where pages hold them all:
-  // one address for the wave, and each lane's constant distance from it.
-  const bool one_page = (1 << a.pool.shift) >= RW && a.D == DC && a.pool.ts < (1 << 26);
-  uint32_t from_first[NL];
+  // one address for the wave, and each lane's constant distance from it.  Channels that
+  // there are not are not loaded (their places hold zeros from the start).
+  const bool one_page = (1 << a.pool.shift) >= RW && a.pool.ts < (1 << 19);
+  // At 256 channels, whose sums and queries fill the registers, the distances are worked
+  // out each time from the first load's: held, some of them lay in scratch memory, and
+  // reading one back waited for all loads under way (64 single tokens over 32768 shared
+  // keys: 112 us, worked out 59; at 128 channels 16 prompts over 8192 keys take 410 us
+  // with them held, 436 worked out).
+  constexpr int RL = 64 / PR;  // whole rows of a load
+  constexpr bool WHOLE = DC == 256;
+  const int place = ((l % PR) ^ swz(w * RW + l / PR)) * 16, first_at = l / PR * a.pool.ts;
+  uint32_t from_first[WHOLE ? 1 : NL];
+  if constexpr (!WHOLE) {
 #pragma unroll
-  for (int i = 0; i < NL; ++i) {
-    const int r = (i * 64 + l) / PR, piece = ((i * 64 + l) % PR) ^ swz(w * RW + r);
-    from_first[i] = r * static_cast<uint32_t>(a.pool.ts) + piece * 16;
+    for (int i = 0; i < NL; ++i) {
+      const int r = (i * 64 + l) / PR;
+      from_first[i] = r * static_cast<uint32_t>(a.pool.ts) + (((i * 64 + l) % PR) ^ swz(w * RW + r)) * 16;
+    }
   }
   auto load_tile = [&](int t) {
-    const int page = pages[(t % TS) * RW + l % RW];
-    const uint32_t kt = lds_at + (t % ST) * 2 * F::TILE + w * NL * 1024;
+    const int page = pages[l];
+    int place_ = place;
+    if constexpr (WHOLE) asm volatile("" : "+v"(place_));  // (not before the loop)
+    const uint32_t to = lds_at + (t % ST) * 2 * F::TILE + w * NL * 1024;
     const int key_w = it.k0 + BN * t + w * RW, page_w = __builtin_amdgcn_readfirstlane(page);
     if (one_page && key_w + RW <= it.k1 && page_w >= 0 && page_w < a.pool.pages) {
-      const int64_t off = page_w * a.pool.ps + (key_w & in_page) * a.pool.ts;
+      const int64_t off = page_w * a.pool.ps + static_cast<uint32_t>((key_w & in_page) * static_cast<uint32_t>(a.pool.ts));
+      const char *kr = kb + off, *vr = vb + off;
 #pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        load_lds16(kb + off, from_first[i], kt + i * 1024);
-        load_lds16(vb + off, from_first[i], kt + F::TILE + i * 1024);
+      for (int x = 0; x < 2 * NL; ++x) {
+        const int i = x % NL;
+        const uint32_t into = to + x / NL * F::TILE + i * 1024;
+        if constexpr (WHOLE) {
+          const int at = place_ ^ (swz(i * RL) * 16);
+          if (a.D == DC || at < a.D * 2) load_lds16((x < NL ? kr : vr) + i * RL * a.pool.ts, at + first_at, into);
+        } else {
+          const int piece = ((i * 64 + l) % PR) ^ swz(w * RW + (i * 64 + l) / PR);
+          if (a.D == DC || piece * 16 < a.D * 2) load_lds16(x < NL ? kr : vr, from_first[i], into);
+        }
       }
       return;
     }
@@ -117,17 +156,15 @@ template <int DC> __global__ void __launch_bounds__(256, 2) many_kernel(AttnArgs
     if (key >= it.k1) off = -1;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-      const int r = (i * 64 + l) / PR, piece = ((i * 64 + l) % PR) ^ swz(w * RW + r);
+      const int r = (i * 64 + l) / PR;
+      const int at = WHOLE ? place_ ^ (swz(i * RL) * 16) : (((i * 64 + l) % PR) ^ swz(w * RW + r)) * 16;
       const int64_t from = (static_cast<int64_t>(__shfl(static_cast<int>(off >> 32), r)) << 32) |
                            static_cast<uint32_t>(__shfl(static_cast<int>(off), r));
-      const bool fill = from < 0 || piece * 16 >= a.D * 2;
+      const bool fill = from < 0 || at >= a.D * 2;
       const void* none = &kFill[from == -2 ? 1 : 0];
-      load_lds16(fill ? none : kb + from + piece * 16, kt + i * 1024);
-      load_lds16(fill ? none : vb + from + piece * 16, kt + F::TILE + i * 1024);
+      load_lds16(fill ? none : kb + (from + at), to + i * 1024);
+      load_lds16(fill ? none : vb + (from + at), to + F::TILE + i * 1024);
     }
-  };
-  auto load_pages = [&](int t) {
-    if (l < RW) load_lds4(page_of(t), pages_at + (t % TS) * RW * 4);
   };
 
   // Where the products' operands lie in a tile.  A piece further along a row is its
@@ -140,128 +177,141 @@ template <int DC> __global__ void __launch_bounds__(256, 2) many_kernel(AttnArgs
     for (int i = 0; i < 2; ++i) va[i] = lds_at + F::TILE + (r + 8 * i) * PR * 16 + (col ^ swz(r + 8 * i)) * 16 + (sl & 1) * 8;
   }
 
-  if (cnt > 0) {
-    if (l < RW)
-      for (int t = 0; t < ST - 1; ++t) pages[t * RW + l] = *page_of(t);
-    wave_lds_sync();
-#pragma unroll 1
-    for (int t = 0; t < ST - 1; ++t) {
-      load_pages(t + ST - 1);
-      if (t < cnt) load_tile(t);
-    }
-  }
-  // The wave's blocks of 32 keys, one after the other.  Where it is: tile t, block x of
-  // it, the block's first key, the bytes to its tile, and how many of its keys every row
-  // of the wave sees.
-  int t = -1, x = XN - 1, key0 = 0, all_see = 0;
-  uint32_t at = 0;
-  auto next_block = [&]() {
-    if (x + 1 < XN) {
-      ++x;
-      key0 += 32;
-      all_see -= 32;
-      at += 32 * PR * 16;
-      return;
-    }
-    ++t;
-    x = 0;
-    // this wave's part of tile t has come; behind the barrier everyone's has, and
-    // everyone is done with tile t - 1, whose place tile t + ST - 1 takes
-    if (t + ST - 1 <= cnt) wait_vm<(ST - 2) * (2 * NL + 1)>();
-    else wait_vm<0>();
-    lds_barrier();
-    if (t + ST - 1 < cnt) {
-      load_pages(t + 2 * (ST - 1));
-      load_tile(t + ST - 1);
-    }
-    at = (t % ST) * 2 * F::TILE;
-    key0 = it.k0 + BN * t;
-    all_see = min(it.k1, lim_first) - key0;
-  };
-  // The block's products of queries and keys; what the scale makes -inf for keys that
-  // the row does not see.  (With a scale of 0 the queries were taken as zeros.)
+  // A block's products of queries and keys; what the scale makes -inf for keys that the
+  // row does not see.  (With a scale of 0 the queries were taken as zeros.)
   const float scale = a.scale == 0.f ? 1.f : a.scale, hide = scale < 0.f ? __builtin_inff() : -__builtin_inff();
-  auto products = [&](f32x16& s) {
+  const int every = min(it.k1, lim_first);  // keys that all rows of the wave see
+  auto products = [&](uint32_t at, int key0, f32x16& s) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[i] = 0.f;
 #pragma unroll
     for (int st = 0; st < NQ; ++st) s = mfma32(read16((ka + at) ^ (2 * st % SW * 16), 2 * st / SW * SW * 16), q[st], s);
-    if (all_see < 32) {
+    operands_ahead<NQ, 1, F::AHEAD_K>();
+    if (key0 + 32 > every) {
       const int see = min(it.k1, lim) - key0 - 4 * half;
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i] = 8 * (i / 4) + i % 4 < see ? s[i] : hide;
     }
   };
-  int left = cnt * XN;
-  if (left > 0) next_block();
-#pragma unroll 1
-  while (left > 0) {
-    // The reference is moved to the block's maximum: at the first block, and where the
-    // weights exceed their bound.  Outside the loop over the blocks, so that in it the
-    // result stays in its registers (scaled under a condition there, it was held, and
-    // copied, twice).
-    {
-      f32x16 s;
-      products(s);
-      float top = s[0] * scale, part = 0.f;
+  // A block with the reference as it is; false, and nothing changed, where its weights
+  // exceed their bound (which a block that is `sure` is not asked).
+  float ref = 0.f;
+  bool large = false, wide = false;
+  auto block = [&](uint32_t at, int key0, bool sure) {
+    f32x16 s;
+    products(at, key0, s);
+    if (!wide) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], scale, -ref));
+    } else {
+      // Of scores as large as this the product with the scale, in one step with the
+      // difference, may exceed the reference (which is rounded) by any amount: there
+      // the product is rounded as well.
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        top = fmaxf(top, s[i] * scale);
-        part += __builtin_amdgcn_exp2f(s[i] * scale - m);
+#pragma clang fp contract(off)
+        const float y = s[i] * scale, d = fmaf(s[i], scale, -ref);
+        s[i] = __builtin_amdgcn_exp2f(large ? y - ref : d);
       }
-      // (only of the rows that ask for it: a row's bits are its own, whatever lies beside it)
-      const bool need = (part > kMost) | (__shfl_xor(part, 32) > kMost) | (m == -__builtin_inff());
-      top = fmaxf(top, __shfl_xor(top, 32));
-      const float to = need ? fmaxf(top, m) : m, f = to == m ? 1.f : __builtin_amdgcn_exp2f(m - to);
-      m = to;
-      sum *= f;
-#pragma unroll
-      for (int d = 0; d < ND; ++d) o[d] *= f;
     }
-    const float ref = m == -__builtin_inff() ? 0.f : m;
-    const bool large = fabsf(ref) > 1048576.f, wide = __any(large);
-    bool fresh = true;  // (the block that the reference comes from is not tried twice, whatever it holds)
-    const bool again = __any(m == -__builtin_inff());  // a row that has seen no key yet: its first sets the reference
+    // (the sum before the weights are rounded: lse is the statistics' in 32 bits)
+    const float part = (((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]))) +
+                       (((s[8] + s[9]) + (s[10] + s[11])) + ((s[12] + s[13]) + (s[14] + s[15])));
+    if (!sure && __any(part > kMost)) return false;
+    sum += part;
+    bf16x8 p[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      p[j] = as_bf16x8(make_uint4(pack2_bf16(s[8 * j], s[8 * j + 1]), pack2_bf16(s[8 * j + 2], s[8 * j + 3]),
+                                  pack2_bf16(s[8 * j + 4], s[8 * j + 5]), pack2_bf16(s[8 * j + 6], s[8 * j + 7])));
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int off = 4 * d / SW * SW * 16 + 16 * j * PR * 16;
+        const uint2 v0 = read_tr((va[0] + at) ^ (4 * d % SW * 16), off), v1 = read_tr((va[1] + at) ^ (4 * d % SW * 16), off);
+        o[d] = mfma32(as_bf16x8(make_uint4(v0.x, v0.y, v1.x, v1.y)), p[j], o[d]);
+      }
+    operands_ahead<NQ, 2, F::AHEAD_V>();
+    return true;
+  };
+
+  if (cnt > 0) {
+    if (a.D != DC) {  // the places of channels that there are not
+      for (int i = threadIdx.x; i < 2 * F::TILE * ST / 16; i += 256) reinterpret_cast<uint4*>(lds)[i] = make_uint4(0, 0, 0, 0);
+      __syncthreads();
+    }
+    load_page(0);
+    wait_vm<0>();
+    load_tile(0);
+    load_page(1);
+    int t = -1, x = 0;
+    auto next_tile = [&]() {
+      ++t;
+      // this wave's part of tile t has come; behind the barrier everyone's has, and
+      // everyone is done with tile t - 1, whose place tile t + 1 takes
+      wait_vm<0>();
+      lds_barrier();
+      if (t + 1 < cnt) {
+        load_tile(t + 1);
+        load_page(t + 2);
+      }
+    };
+    next_tile();
 #pragma unroll 1
     while (true) {
-      f32x16 s;
-      products(s);
-      if (!wide) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], scale, -ref));
-      } else {
-        // Of scores as large as this the product with the scale, in one step with the
-        // difference, may exceed the reference (which is rounded) by any amount: there
-        // the product is rounded as well.
+      // The reference is moved to the block's maximum: at the first block, and where the
+      // weights exceed their bound.  Outside the loop over the tiles, so that in it the
+      // result stays in its registers (scaled under a condition there, or with a way
+      // round the products, it was held, and copied, twice).
+      bool again;
+      {
+        f32x16 s;
+        products((t % ST) * 2 * F::TILE + x * 32 * PR * 16, it.k0 + BN * t + 32 * x, s);
+        float top = s[0] * scale, part = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-#pragma clang fp contract(off)
-          const float y = s[i] * scale, d = fmaf(s[i], scale, -ref);
-          s[i] = __builtin_amdgcn_exp2f(large ? y - ref : d);
+          top = fmaxf(top, s[i] * scale);
+          part += __builtin_amdgcn_exp2f(s[i] * scale - m);
         }
+        // (only of the rows that ask for it: a row's bits are its own, whatever lies beside it)
+        const bool need = (part > kMost) | (__shfl_xor(part, 32) > kMost) | (m == -__builtin_inff());
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float to = need ? fmaxf(top, m) : m, f = to == m ? 1.f : __builtin_amdgcn_exp2f(m - to);
+        m = to;
+        sum *= f;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) o[d] *= f;
+        ref = m == -__builtin_inff() ? 0.f : m;
+        large = fabsf(ref) > 1048576.f;
+        wide = __any(large);
+        again = __any(m == -__builtin_inff());  // a row that has seen no key yet: its first sets the reference
       }
-      // (the sum before the weights are rounded: lse is the statistics' in 32 bits)
-      const float part = (((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]))) +
-                         (((s[8] + s[9]) + (s[10] + s[11])) + ((s[12] + s[13]) + (s[14] + s[15])));
-      if (!fresh && __any(part > kMost)) break;
-      fresh = false;
-      sum += part;
-      bf16x8 p[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        p[j] = as_bf16x8(make_uint4(pack2_bf16(s[8 * j], s[8 * j + 1]), pack2_bf16(s[8 * j + 2], s[8 * j + 3]),
-                                    pack2_bf16(s[8 * j + 4], s[8 * j + 5]), pack2_bf16(s[8 * j + 6], s[8 * j + 7])));
-#pragma unroll
-      for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int off = 4 * d / SW * SW * 16 + 16 * j * PR * 16;
-          const uint2 v0 = read_tr((va[0] + at) ^ (4 * d % SW * 16), off), v1 = read_tr((va[1] + at) ^ (4 * d % SW * 16), off);
-          o[d] = mfma32(as_bf16x8(make_uint4(v0.x, v0.y, v1.x, v1.y)), p[j], o[d]);
-        }
-      if (--left == 0) break;
-      next_block();
-      if (again) break;
+      // that block (which is not tried twice, whatever it holds), and the tile's others
+      bool ok = true, sure = true;
+#pragma unroll 1
+      do {
+        ok = block((t % ST) * 2 * F::TILE + x * 32 * PR * 16, it.k0 + BN * t + 32 * x, sure);
+        sure = false;
+        x += ok ? 1 : 0;
+      } while (ok && !again && x < XN);
+      if (x < XN) continue;
+      x = 0;
+      // whole tiles
+#pragma unroll 1
+      while (!again && ok && t + 1 < cnt) {
+        next_tile();
+        const uint32_t at = (t % ST) * 2 * F::TILE;
+        const int key0 = it.k0 + BN * t;
+        ok = block(at, key0, false);
+        if (XN == 1 || !ok) continue;
+        ok = block(at + 32 * PR * 16, key0 + 32, false);
+        x = ok ? 0 : 1;
+      }
+      if (ok) {
+        if (t + 1 >= cnt) break;
+        next_tile();  // (again)
+      }
     }
   }
 

@@ -36,9 +36,8 @@ Split split(int64_t items, int64_t len, const Cost& c, double part_us) {
 }  // namespace
 
 // Rows of an item.  The kernel for many rows from 65 on: 64 sequences' 512 rows and
-// 32768 keys of 2 heads of 256 take 67 us with it (128 rows), 167 us without.  256 rows
-// where a tile of them is full twice.  Few rows, 16 or 32 (the prefix's and own keys' in
-// one launch): what the cost says.
+// 32768 keys of 2 heads of 256 take 59 us with it, 167 us without.  Few rows, 16 or 32
+// (the prefix's and own keys' in one launch): what the cost says.
 void attn_plan(AttnArgs* a, bool bf, size_t* part, size_t* ml) {
   const int64_t own = static_cast<int64_t>(a->max_q) * a->G, all = static_cast<int64_t>(a->N) * a->G;
   const double part_us = static_cast<double>(a->N) * a->Hq * a->D * 8 / 4.0e6;  // written and read, at 4 TB/s

@@ -204,7 +204,7 @@ template <int LPH, bool INTER> struct Lane {
 // Queries and keys are normed (where they have weights) and turned; values are copied.
 // A batch of rows is on its way while the one before it is worked on (rows one by one
 // left the wave waiting for each: 8192 tokens of 32 + 8 heads of 128, bf16, 47 us
-// against 37).  find is called once, behind the first batch's loads: it gives the
+// against 38).  find is called once, behind the first batch's loads: it gives the
 // token's angles, and where each part's rows go (null: nowhere) and from one head to
 // the next, in bytes.
 template <typename T, int LPH, bool INTER, bool AXES, int PARTS, typename Args, typename Find>
