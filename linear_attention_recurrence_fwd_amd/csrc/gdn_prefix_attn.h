@@ -70,7 +70,7 @@ struct Item {
 // Items are numbered so that those which read the same keys of the prefix (row tiles
 // of one split and key head) run on the same XCD, one after the other: workgroups go
 // to the eight XCDs in turn.
-__device__ __forceinline__ Item find_item(const AttnArgs& a) {
+__device__ __forceinline__ Item item_of(const AttnArgs& a) {
   Item it{};
   int b = blockIdx.x;
   const int pairs = a.p_split * a.Hk, p_items = a.which & 1 ? (pairs + 7) / 8 * 8 * a.p_tiles : 0;
@@ -110,6 +110,20 @@ __device__ __forceinline__ Item find_item(const AttnArgs& a) {
   it.k0 = split * a.o_chunk;
   it.k1 = it.bad ? 0 : min(it.seen + last, it.k0 + a.o_chunk);
   it.empty = it.n <= 0 || (it.row0 >= it.n * a.G && !it.bad) || (!a.together && it.k1 <= it.k0);
+  return it;
+}
+
+// Every lane finds the same: in scalar registers, what follows from it is worked out once
+// for the wave.
+__device__ __forceinline__ Item find_item(const AttnArgs& a) {
+  Item it = item_of(a);
+  for (int* x : {&it.t0, &it.n, &it.row0, &it.hk, &it.slot, &it.k0, &it.k1, &it.seen}) *x = __builtin_amdgcn_readfirstlane(*x);
+  const uint64_t p = reinterpret_cast<uint64_t>(it.list);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(p));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(p >> 32));
+  it.list = reinterpret_cast<const int32_t*>(static_cast<uint64_t>(hi) << 32 | lo);
+  it.bad = __builtin_amdgcn_readfirstlane(it.bad);
+  it.empty = __builtin_amdgcn_readfirstlane(it.empty);
   return it;
 }
 

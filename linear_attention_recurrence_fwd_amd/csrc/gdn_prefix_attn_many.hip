@@ -13,10 +13,12 @@
 // quarters of the time beside the LDS.  What bounds the kernel is the issue of
 // instructions: two waves to a SIMD, each of which starts one in about four cycles, have
 // reads, exponentials, packing and waits to start beside each product.  Measured: 16
-// prompts of 20 to 290 tokens over 8192 shared keys, 32 heads of 128 on 8 key heads, 410
-// us of this kernel, 830 TFLOP/s (a large product of matrices reaches 1233 here); 64
-// single tokens over 32768 shared keys, 16 heads of 256 on 2, 59 us, 580 TFLOP/s.
+// prompts of 20 to 290 tokens over 8192 shared keys, 32 heads of 128 on 8 key heads, 398
+// us of this kernel, 860 TFLOP/s (a large product of matrices reaches 1233 here); 64
+// single tokens over 32768 shared keys, 16 heads of 256 on 2, 52 us, 660 TFLOP/s.
 #include "gdn_prefix_attn.h"
+
+#include <type_traits>
 
 namespace gdn {
 namespace attn {
@@ -118,7 +120,7 @@ template <int DC> __global__ void __launch_bounds__(256, 2) many_kernel(AttnArgs
   // with them held, 436 worked out).
   constexpr int RL = 64 / PR;  // whole rows of a load
   constexpr bool WHOLE = DC == 256;
-  const int place = ((l % PR) ^ swz(w * RW + l / PR)) * 16, first_at = l / PR * a.pool.ts;
+  const int place = ((l % PR) ^ swz(w * RW + l / PR)) * 16, first_at = l / PR * a.pool.ts, step = RL * a.pool.ts;
   uint32_t from_first[WHOLE ? 1 : NL];
   if constexpr (!WHOLE) {
 #pragma unroll
@@ -129,25 +131,29 @@ template <int DC> __global__ void __launch_bounds__(256, 2) many_kernel(AttnArgs
   }
   auto load_tile = [&](int t) {
     const int page = pages[l];
-    int place_ = place;
-    if constexpr (WHOLE) asm volatile("" : "+v"(place_));  // (not before the loop)
-    const uint32_t to = lds_at + (t % ST) * 2 * F::TILE + w * NL * 1024;
+    int place_ = place, first_ = first_at;
+    if constexpr (WHOLE) asm volatile("" : "+v"(place_), "+v"(first_));  // (not before the loop)
+    const uint32_t to = lds_at + (t & (ST - 1)) * 2 * F::TILE + w * NL * 1024;
     const int key_w = it.k0 + BN * t + w * RW, page_w = __builtin_amdgcn_readfirstlane(page);
     if (one_page && key_w + RW <= it.k1 && page_w >= 0 && page_w < a.pool.pages) {
       const int64_t off = page_w * a.pool.ps + static_cast<uint32_t>((key_w & in_page) * static_cast<uint32_t>(a.pool.ts));
       const char *kr = kb + off, *vr = vb + off;
+      auto rows = [&](auto whole) {
 #pragma unroll
-      for (int x = 0; x < 2 * NL; ++x) {
-        const int i = x % NL;
-        const uint32_t into = to + x / NL * F::TILE + i * 1024;
-        if constexpr (WHOLE) {
-          const int at = place_ ^ (swz(i * RL) * 16);
-          if (a.D == DC || at < a.D * 2) load_lds16((x < NL ? kr : vr) + i * RL * a.pool.ts, at + first_at, into);
-        } else {
-          const int piece = ((i * 64 + l) % PR) ^ swz(w * RW + (i * 64 + l) / PR);
-          if (a.D == DC || piece * 16 < a.D * 2) load_lds16(x < NL ? kr : vr, from_first[i], into);
+        for (int x = 0; x < 2 * NL; ++x) {
+          const int i = x % NL;
+          const uint32_t into = to + x / NL * F::TILE + i * 1024;
+          if constexpr (WHOLE) {
+            const int at = place_ ^ (swz(i * RL) * 16);
+            if (whole || at < a.D * 2) load_lds16(x < NL ? kr : vr, at + first_ + i * step, into);
+          } else {
+            const int piece = ((i * 64 + l) % PR) ^ swz(w * RW + (i * 64 + l) / PR);
+            if (whole || piece * 16 < a.D * 2) load_lds16(x < NL ? kr : vr, from_first[i], into);
+          }
         }
-      }
+      };
+      if (a.D == DC) rows(std::true_type{});
+      else rows(std::false_type{});
       return;
     }
     const int key = key_w + l % RW;
@@ -184,8 +190,10 @@ template <int DC> __global__ void __launch_bounds__(256, 2) many_kernel(AttnArgs
   auto products = [&](uint32_t at, int key0, f32x16& s) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[i] = 0.f;
+    uint32_t k_at = ka + at;
+    asm volatile("" : "+v"(k_at));  // (not taken apart: the constants would be held in registers)
 #pragma unroll
-    for (int st = 0; st < NQ; ++st) s = mfma32(read16((ka + at) ^ (2 * st % SW * 16), 2 * st / SW * SW * 16), q[st], s);
+    for (int st = 0; st < NQ; ++st) s = mfma32(read16(k_at ^ (2 * st % SW * 16), 2 * st / SW * SW * 16), q[st], s);
     operands_ahead<NQ, 1, F::AHEAD_K>();
     if (key0 + 32 > every) {
       const int see = min(it.k1, lim) - key0 - 4 * half;
@@ -224,12 +232,14 @@ template <int DC> __global__ void __launch_bounds__(256, 2) many_kernel(AttnArgs
     for (int j = 0; j < 2; ++j)
       p[j] = as_bf16x8(make_uint4(pack2_bf16(s[8 * j], s[8 * j + 1]), pack2_bf16(s[8 * j + 2], s[8 * j + 3]),
                                   pack2_bf16(s[8 * j + 4], s[8 * j + 5]), pack2_bf16(s[8 * j + 6], s[8 * j + 7])));
+    uint32_t v0_at = va[0] + at, v1_at = va[1] + at;
+    asm volatile("" : "+v"(v0_at), "+v"(v1_at));
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int off = 4 * d / SW * SW * 16 + 16 * j * PR * 16;
-        const uint2 v0 = read_tr((va[0] + at) ^ (4 * d % SW * 16), off), v1 = read_tr((va[1] + at) ^ (4 * d % SW * 16), off);
+        const uint2 v0 = read_tr(v0_at ^ (4 * d % SW * 16), off), v1 = read_tr(v1_at ^ (4 * d % SW * 16), off);
         o[d] = mfma32(as_bf16x8(make_uint4(v0.x, v0.y, v1.x, v1.y)), p[j], o[d]);
       }
     operands_ahead<NQ, 2, F::AHEAD_V>();
@@ -267,7 +277,7 @@ template <int DC> __global__ void __launch_bounds__(256, 2) many_kernel(AttnArgs
       bool again;
       {
         f32x16 s;
-        products((t % ST) * 2 * F::TILE + x * 32 * PR * 16, it.k0 + BN * t + 32 * x, s);
+        products((t & (ST - 1)) * 2 * F::TILE + x * 32 * PR * 16, it.k0 + BN * t + 32 * x, s);
         float top = s[0] * scale, part = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -291,7 +301,7 @@ template <int DC> __global__ void __launch_bounds__(256, 2) many_kernel(AttnArgs
       bool ok = true, sure = true;
 #pragma unroll 1
       do {
-        ok = block((t % ST) * 2 * F::TILE + x * 32 * PR * 16, it.k0 + BN * t + 32 * x, sure);
+        ok = block((t & (ST - 1)) * 2 * F::TILE + x * 32 * PR * 16, it.k0 + BN * t + 32 * x, sure);
         sure = false;
         x += ok ? 1 : 0;
       } while (ok && !again && x < XN);
@@ -301,7 +311,7 @@ template <int DC> __global__ void __launch_bounds__(256, 2) many_kernel(AttnArgs
 #pragma unroll 1
       while (!again && ok && t + 1 < cnt) {
         next_tile();
-        const uint32_t at = (t % ST) * 2 * F::TILE;
+        const uint32_t at = (t & (ST - 1)) * 2 * F::TILE;
         const int key0 = it.k0 + BN * t;
         ok = block(at, key0, false);
         if (XN == 1 || !ok) continue;

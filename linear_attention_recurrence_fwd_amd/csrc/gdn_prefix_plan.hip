@@ -36,7 +36,7 @@ Split split(int64_t items, int64_t len, const Cost& c, double part_us) {
 }  // namespace
 
 // Rows of an item.  The kernel for many rows from 65 on: 64 sequences' 512 rows and
-// 32768 keys of 2 heads of 256 take 59 us with it, 167 us without.  Few rows, 16 or 32
+// 32768 keys of 2 heads of 256 take 52 us with it, 167 us without.  Few rows, 16 or 32
 // (the prefix's and own keys' in one launch): what the cost says.
 void attn_plan(AttnArgs* a, bool bf, size_t* part, size_t* ml) {
   const int64_t own = static_cast<int64_t>(a->max_q) * a->G, all = static_cast<int64_t>(a->N) * a->G;
