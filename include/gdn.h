@@ -430,7 +430,7 @@ typedef struct gdn_paged_dims {
  * values into the pool as they are.
  *   cu   [S+1] int32: sequence s has the tokens cu[s] .. cu[s+1] - 1 (from 0 on,
  *        not decreasing); NULL = N / S tokens each.  Rows behind cu[S] (a padded
- *        batch) are neither read nor written.
+ *        batch) are not written, and nothing comes of what they hold.
  *   past [S] int32: tokens of each sequence that the cache holds already; the i-th
  *        new one goes to place past[s] + i.  A place behind the table's row, or on
  *        a page outside 0 .. pages-1, is not written (the queries are).  Every
