@@ -876,7 +876,11 @@ def norm_rope_axes_bwd(q, k, wq, wk, rope, axis, pos, dyq, dyk, *, eps=1e-6, w_o
 
 class NormRopeAxes(torch.autograd.Function):
     """Autograd wrapper of norm_rope_axes / norm_rope_axes_bwd: forward(q, k, wq, wk,
-    rope, axis, pos, eps, w_offset, interleaved) returns (q, k)."""
+    rope, axis, pos, eps, w_offset, interleaved) returns (q, k).  To capture a step into
+    a graph, drop what earlier eager steps of the same leaves returned first, and warm up
+    on the capture's stream: torch adds a leaf's gradient on the stream of the graph that
+    still holds it, which ends a capture on another one.  norm_rope_axes_bwd itself may
+    be captured anywhere."""
 
     @staticmethod
     def forward(ctx, q, k, wq=None, wk=None, rope=None, axis=None, pos=None, eps=1e-6, w_offset=0.0, interleaved=False):

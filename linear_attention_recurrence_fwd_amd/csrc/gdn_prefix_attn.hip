@@ -13,7 +13,7 @@
 // The kernel for few rows is bound by the keys and values that it reads once: the own
 // keys of 64 sequences, 100 to 2000 each, 2 heads of 256, bf16, 137 MB in 36 us, 3.8 TB/s
 // (a large copy: 5.15).  Eight single tokens over 1000 shared keys and a few hundred own
-// ones are latency: 10 us for the keys, 4 for the parts.
+// ones are latency: 9 us for the keys, 4 for the parts.
 #include "gdn_prefix_attn.h"
 namespace gdn {
 namespace attn {
