@@ -58,7 +58,10 @@ struct AttnArgs {
   int p_tiles, p_split, p_chunk;  // items of the prefix: row tiles, splits, keys of a split
   int o_tiles, o_split, o_chunk;  // of own keys, the tiles of each sequence
   float* part;              // [slots][N * Hq][D], not divided by the sums
-  float2* ml;               // [slots][N * Hq] maximum (base 2) and sum
+  float2* ml;               // [slots][N * Hq] reference m (base 2) and sum
+  // The weights are held as 2^(score - m - lift), so that all of a row's together stay
+  // under 1 and no sum of weighted values leaves fp32 while the values are in it.
+  float lift, unit, whole;  // unit: 2^-lift, whole: 2^lift
 };
 
 hipError_t launch_append(const AppendArgs& a, bool bf16, hipStream_t st);

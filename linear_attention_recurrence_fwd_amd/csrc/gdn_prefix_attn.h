@@ -8,11 +8,14 @@ namespace gdn {
 namespace attn {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// The statistics' reference maximum is moved when a score exceeds it by this (base 2):
-// the weights stay below 2^16 (whatever their size, they keep their relative precision),
-// and moving it, which scales the result's registers, is rare.
+// The statistics' reference m is moved when a score exceeds it by this (base 2), so that
+// moving it, which scales the result's registers, is rare.  The weights are held as
+// 2^(score - m - lift): with lift = 17 + log2(all keys of a row) their sum stays under a
+// half, and the sum of weighted values in fp32 for values up to its largest (relative to
+// m alone, 1600 equal scores over values of 1e37 gave Inf).  At the other end products
+// under 2^-126 lose bits: a factor of 2^17 earlier than with weights divided by their sum.
 constexpr float kSlack = 16.f;
-constexpr float kMost = 65536.f;  // and of a lane's weights of 32 keys together, where these are watched
+constexpr float kMost = 65536.f;  // and a lane's sixteen weights of a block by this together (times 2^-lift)
 
 // 16 bytes of zeros and of NaN (in either type): what the loads of keys behind the
 // end, and of keys on pages that do not exist, are pointed to.

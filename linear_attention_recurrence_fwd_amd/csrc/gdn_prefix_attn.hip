@@ -3,7 +3,8 @@
 //
 //   o_i = sum_j e^(s_ij - m_i) v_j / l_i,  s_ij = scale q_i . k_j,  l_i = sum_j e^(s_ij - m_i)
 //
-// in one pass over the keys with a running reference m and sum l; parts over
+// in one pass over the keys with a running reference m and sum l (all weights times
+// 2^-lift, gdn_prefix_attn.h); parts over
 // disjoint keys join by o = sum o_x e^(m_x - m), l = sum l_x e^(m_x - m).
 //
 // The rows of a key head's G query heads go together, and over the prefix those of
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) few_kernel(AttnArgs 
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         s[b][r] = key0 + 4 * lg + r < see ? s[b][r] * a.scale : -__builtin_inff();
-        move |= s[b][r] > m[b] + kSlack;
+        move |= s[b][r] - m[b] > kSlack;
       }
     }
     if (__any(move)) {
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) few_kernel(AttnArgs 
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
         // (only of the rows that ask for it: a row's bits are its own, whatever lies beside it)
-        const float to = top > m[b] + kSlack ? top : m[b], f = to == m[b] ? 1.f : __builtin_amdgcn_exp2f(m[b] - to);
+        const float to = top - m[b] > kSlack ? top : m[b], f = to == m[b] ? 1.f : __builtin_amdgcn_exp2f(m[b] - to);
         m[b] = to;
         sum[b] *= f;
 #pragma unroll
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) few_kernel(AttnArgs 
       const float ref = m[b] == -__builtin_inff() ? 0.f : m[b];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        p[b][r] = __builtin_amdgcn_exp2f(s[b][r] - ref);
+        p[b][r] = __builtin_amdgcn_exp2f(s[b][r] - ref) * a.unit;
         sum[b] += p[b][r];  // (bf16: before they are rounded, so that lse is exact to 32 bits)
       }
     }
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) few_kernel(AttnArgs 
       T* dst = static_cast<T*>(a.o) + row * a.D + c;
       if constexpr (BF) *reinterpret_cast<uint2*>(dst) = pack4_bf16(y.x * f, y.y * f, y.z * f, y.w * f);
       else *reinterpret_cast<float4*>(dst) = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
-      if (a.lse && c == 0) a.lse[row] = it.bad ? f : (top + log2f(t)) * kLn2;
+      if (a.lse && c == 0) a.lse[row] = it.bad ? f : (top + log2f(t * a.whole)) * kLn2;
     } else {
       const int64_t at = static_cast<int64_t>(it.slot) * a.N * a.Hq + row;
       *reinterpret_cast<float4*>(a.part + at * a.D + c) = y;
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(256) join_kernel(AttnArgs a) {
   T* dst = static_cast<T*>(a.o) + row * a.D + c;
   if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(dst) = pack4_bf16(y.x * f, y.y * f, y.z * f, y.w * f);
   else *reinterpret_cast<float4*>(dst) = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
-  if (a.lse && c == 0) a.lse[row] = bad ? f : (m + log2f(t)) * kLn2;
+  if (a.lse && c == 0) a.lse[row] = bad ? f : (m + log2f(t * a.whole)) * kLn2;
 }
 
 template <typename T, int LPR> hipError_t launch_join(const AttnArgs& a, hipStream_t st) {

@@ -26,6 +26,8 @@ namespace {
 
 typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16;
 
+constexpr float kLarge = 1048576.f;  // references beyond this do not hold the lift in fp32
+
 template <int DC> struct Many {
   static constexpr int W = 4, PR = DC / 8;                  // waves; pieces of 16 bytes of a row
   static constexpr int BN = DC <= 128 ? 64 : 32;            // keys of a tile
@@ -201,31 +203,37 @@ template <int DC> __global__ void __launch_bounds__(256, 2) many_kernel(AttnArgs
       for (int i = 0; i < 16; ++i) s[i] = 8 * (i / 4) + i % 4 < see ? s[i] : hide;
     }
   };
-  // A block with the reference as it is; false, and nothing changed, where its weights
-  // exceed their bound (which a block that is `sure` is not asked).
+  // A block's weights, in place, and their sum (before they are rounded: lse is the
+  // statistics' in 32 bits).  ref is m + lift, which m is chosen to have exactly.
   float ref = 0.f;
   bool large = false, wide = false;
-  auto block = [&](uint32_t at, int key0, bool sure) {
-    f32x16 s;
-    products(at, key0, s);
-    if (!wide) {
+  auto weights = [&](f32x16& s, bool all_small) {
+    if (all_small) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], scale, -ref));
     } else {
       // Of scores as large as this the product with the scale, in one step with the
       // difference, may exceed the reference (which is rounded) by any amount: there
-      // the product is rounded as well.
+      // the product is rounded as well, and the lift, which the reference cannot hold
+      // beside them, is a product of its own.
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
 #pragma clang fp contract(off)
         const float y = s[i] * scale, d = fmaf(s[i], scale, -ref);
-        s[i] = __builtin_amdgcn_exp2f(large ? y - ref : d);
+        s[i] = __builtin_amdgcn_exp2f(large ? y - ref : d) * (large ? a.unit : 1.f);
       }
     }
-    // (the sum before the weights are rounded: lse is the statistics' in 32 bits)
-    const float part = (((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]))) +
+    return (((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]))) +
                        (((s[8] + s[9]) + (s[10] + s[11])) + ((s[12] + s[13]) + (s[14] + s[15])));
-    if (!sure && __any(part > kMost)) return false;
+  };
+  // A block with the reference as it is; false, and nothing changed, where its weights
+  // exceed their bound (which a block that is `sure` is not asked).
+  const float most = kMost * a.unit;
+  auto block = [&](uint32_t at, int key0, bool sure) {
+    f32x16 s;
+    products(at, key0, s);
+    const float part = weights(s, !wide);
+    if (!sure && __any(part > most)) return false;
     sum += part;
     bf16x8 p[2];
 #pragma unroll
@@ -278,22 +286,22 @@ template <int DC> __global__ void __launch_bounds__(256, 2) many_kernel(AttnArgs
       {
         f32x16 s;
         products((t & (ST - 1)) * 2 * F::TILE + x * 32 * PR * 16, it.k0 + BN * t + 32 * x, s);
-        float top = s[0] * scale, part = 0.f;
+        float top = s[0] * scale;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          top = fmaxf(top, s[i] * scale);
-          part += __builtin_amdgcn_exp2f(s[i] * scale - m);
-        }
-        // (only of the rows that ask for it: a row's bits are its own, whatever lies beside it)
-        const bool need = (part > kMost) | (__shfl_xor(part, 32) > kMost) | (m == -__builtin_inff());
+        for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i] * scale);
+        // (only of the rows that ask for it, by the very sum that `block` asks for: a row's
+        // bits are its own, whatever lies beside it)
+        const float part = weights(s, false);  // (the same bits)
+        const bool need = (part > most) | (__shfl_xor(part, 32) > most) | (m == -__builtin_inff());
         top = fmaxf(top, __shfl_xor(top, 32));
+        if (fabsf(top) <= kLarge) top = (top + a.lift) - a.lift;
         const float to = need ? fmaxf(top, m) : m, f = to == m ? 1.f : __builtin_amdgcn_exp2f(m - to);
         m = to;
         sum *= f;
 #pragma unroll
         for (int d = 0; d < ND; ++d) o[d] *= f;
-        ref = m == -__builtin_inff() ? 0.f : m;
-        large = fabsf(ref) > 1048576.f;
+        large = fabsf(m) > kLarge && m != -__builtin_inff();
+        ref = m == -__builtin_inff() ? 0.f : large ? m : m + a.lift;
         wide = __any(large);
         again = __any(m == -__builtin_inff());  // a row that has seen no key yet: its first sets the reference
       }
@@ -332,7 +340,7 @@ template <int DC> __global__ void __launch_bounds__(256, 2) many_kernel(AttnArgs
   const bool first = half == 0 && row < nrows;
   const int64_t out_row = static_cast<int64_t>(it.t0 + row / G) * a.Hq + it.hk * G + row % G;
   if (a.together) {
-    if (first && a.lse) a.lse[out_row] = it.bad ? inv : (m + log2f(sum)) * kLn2;
+    if (first && a.lse) a.lse[out_row] = it.bad ? inv : (m + log2f(sum * a.whole)) * kLn2;
 #pragma unroll
     for (int d = 0; d < ND; ++d) o[d] *= inv;
   } else if (first) {

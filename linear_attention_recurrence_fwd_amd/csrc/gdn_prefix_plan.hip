@@ -46,6 +46,12 @@ Split split(int64_t items, int64_t len, const Cost& c, double part_us) {
 // 32768 keys of 2 heads of 256 take 52 us with it, 167 us without.  Few rows, 16 or 32
 // (the prefix's and own keys' in one launch): what the cost says.
 void attn_plan(AttnArgs* a, bool bf, size_t* part, size_t* ml) {
+  // (weights above the reference's: under 2^16 (gdn_prefix_attn.h), for each key)
+  int lift = 17;
+  while ((int64_t{1} << (lift - 17)) < static_cast<int64_t>(a->prefix) + a->max_len) ++lift;
+  a->lift = static_cast<float>(lift);
+  a->whole = static_cast<float>(int64_t{1} << lift);
+  a->unit = 1.f / a->whole;
   const int64_t own = static_cast<int64_t>(a->max_q) * a->G, all = static_cast<int64_t>(a->N) * a->G;
   const double part_us = static_cast<double>(a->N) * a->Hq * a->D * 8 / 4.0e6;  // written and read, at 4 TB/s
   auto many = [&](int64_t n) { return bf && n > 64; };
