@@ -486,9 +486,9 @@ int gdn_paged_append(const gdn_paged_dims* d, const gdn_turn* t, const void* q, 
  * statistics are fp32 (of weights that are not rounded); the weights p are rounded to
  * bf16 for the product with v (up to 2^-8 of each, at random: 1.7e-3 of the result in
  * 2-norm beside its own rounding's 1.7e-3).  fp32: fp32 products and sums throughout.
- * Values up to the type's largest are fine; products of weights (the largest of a row 2^-17
- * divided by the number of keys, or more) and values under 2^-126 lose bits, those of
- * values under 1e-33 times the number of keys.
+ * Values up to the type's largest are fine.  At the other end values under 3e-33 times
+ * the number of keys lose bits: a row's largest weight is held as 2^-18 / keys or more,
+ * and its products under 2^-126 are not normal numbers.
  * Deterministic: the keys are split by the sizes given on the host alone, and joined
  * in a fixed order; what else is in the batch does not reach a row's bits otherwise.
  */

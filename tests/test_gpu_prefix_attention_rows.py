@@ -103,3 +103,30 @@ def test_rows_behind_the_last_sequence(dtype, D):
     # (other tiles of rows and splits: the same up to roundings)
     close = 2 ** -7 if dtype == torch.bfloat16 else 1e-5
     assert (first[0].double() - ref[0].double()).abs().max() <= close * v.double().abs().max()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("prefix", [0, 330])
+def test_rows_of_nan_among_others(D, prefix):
+    """Queries of NaN in every wave of a causal prompt, whose first rows see few keys or (a
+    length smaller than the call's tokens) none: NaN there, the others' bits as without them."""
+    g = torch.Generator(device="cuda").manual_seed(D)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    new, lens = [150, 90], [120, 400]
+    pages = -(-prefix // 16)
+    k, v = rnd(pages + 60, 2, 16, D), rnd(pages + 60, 2, 16, D)
+    shared = torch.arange(pages, dtype=torch.int32, device="cuda") if prefix else None
+    table = torch.arange(pages, pages + 60, dtype=torch.int32, device="cuda").view(2, 30)
+    cu = torch.tensor([0, *new], device="cuda").cumsum(0).to(torch.int32)
+    length = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = 3 * rnd(sum(new), 4, D)
+    x = q.clone()
+    x[5::13, 1, 7] = math.nan
+    (a, la), (b, lb) = (B.prefix_attention(y, k, v, table, length, shared, prefix, cu, max_q=150, lse=True) for y in (q, x))
+    torch.cuda.synchronize()
+    bad = torch.isnan(x.float()).any(-1)
+    if not prefix:
+        bad[:30] = False  # (no key at all: zeros, whatever the query)
+        assert not b[:30].any() and (lb[:30] == -math.inf).all()
+    assert torch.isnan(b[bad].float()).all() and torch.isnan(lb[bad]).all()
+    assert torch.equal(a[~bad], b[~bad]) and torch.equal(la[~bad], lb[~bad])
