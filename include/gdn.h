@@ -469,7 +469,7 @@ int gdn_paged_append(const gdn_paged_dims* d, const gdn_turn* t, const void* q, 
  *   prefix       tokens of the prefix, up to 2^30; 0 without (prefix_pages NULL)
  *   prefix_pages [ceil(prefix / page)] int32
  *   max_q        no sequence has more tokens in the call than this (host; 1 .. N).
- *                With cu NULL it is N / S whatever is given.
+ *                With cu NULL the call takes N / S whatever is given.
  *   max_len      no lens[s] is larger than this (host; up to width * page, and 2^30;
  *                the size of the launch and of the workspace go by it)
  *   cu           as gdn_paged_append; rows behind cu[S] are left as they are
@@ -489,6 +489,10 @@ int gdn_paged_append(const gdn_paged_dims* d, const gdn_turn* t, const void* q, 
  * Values up to the type's largest are fine.  At the other end values under 3e-33 times
  * the number of keys lose bits: a row's largest weight is held as 2^-18 / keys or more,
  * and its products under 2^-126 are not normal numbers.
+ * Sizes: N Hq up to 2^26 - 64, and a launch holds 2^24 - 1 items: tiles of 16 or 32 rows
+ * (bf16 from max_q G = 65 on 128) of max_q G rows, for each key head and sequence, and for
+ * each split of their keys where these are few; the prefix's, of N G rows, besides
+ * (GDN_ERR_UNSUPPORTED beyond).  A max_q far above the longest sequence is what it costs.
  * Deterministic: the keys are split by the sizes given on the host alone, and joined
  * in a fixed order; what else is in the batch does not reach a row's bits otherwise.
  */

@@ -70,10 +70,10 @@ class Turn(ctypes.Structure):
 
 
 class GdnError(RuntimeError):
-    def __init__(self, fn, code):
+    def __init__(self, fn, code, hint=""):
         self.code = code
-        super().__init__("%s failed: %s (%s)" % (fn, STATUS.get(code, code),
-                                                 lib().gdn_status_string(code).decode()))
+        super().__init__("%s failed: %s (%s)%s" % (fn, STATUS.get(code, code),
+                                                   lib().gdn_status_string(code).decode(), hint))
 
 
 _lib = None
@@ -926,7 +926,8 @@ def _attention_ws(prefix, max_q, max_len, *dims):
     out = ctypes.c_size_t(0)
     rc = lib().gdn_prefix_attention_workspace_bytes(_paged_dims(*dims), prefix, max_q, max_len, ctypes.byref(out))
     if rc:
-        raise GdnError("gdn_prefix_attention_workspace_bytes", rc)
+        hint = "; the launch goes by max_q = %d for each of %d sequences: give the longest one's tokens" % (max_q, dims[1])
+        raise GdnError("gdn_prefix_attention_workspace_bytes", rc, hint if STATUS.get(rc) == "GDN_ERR_UNSUPPORTED" else "")
     return out.value
 
 
@@ -1016,7 +1017,8 @@ def prefix_attention(q, k_pages, v_pages, table, lens, prefix_pages=None, prefix
     last of its lens[s] own tokens in the pages table[s]; the prefix's first `prefix`
     tokens lie in prefix_pages.  cu as in paged_append.  max_q (N by default, with cu)
     and max_len (the room of a table's row) bound a sequence's tokens in the call and its
-    own length: the launch goes by them.  scale: D^-1/2 by default.  Returns o [N,Hq,D]
+    own length: the launch goes by them, and one of many sequences that are all taken to
+    be as long as the batch may be refused.  scale: D^-1/2 by default.  Returns o [N,Hq,D]
     (in out, if given), with lse=True (o, lse [N,Hq] fp32)."""
     if _calls is not None:
         y = _calls.prefix_attention(q, k_pages, v_pages, table, lens, prefix_pages, prefix, cu, max_q, max_len, scale, out,

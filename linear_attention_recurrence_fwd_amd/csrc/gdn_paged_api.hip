@@ -16,7 +16,7 @@ using gdn::overlaps;
 using gdn::Range;
 
 constexpr int64_t kMaxRows = (1 << 26) - 64;   // tokens by query heads of one call
-constexpr int64_t kMaxItems = (1 << 24) - 64;  // workgroups of the attention's launch
+constexpr int64_t kMaxItems = (1 << 24) - 1;   // workgroups of 256 threads of one launch
 constexpr int64_t kMaxKeys = 1 << 30;
 
 // Elements that rows of D at these strides span, in up to four directions; -1 where
@@ -111,8 +111,11 @@ int check_attn(const gdn_paged_dims* d, int64_t prefix, int64_t max_q, int64_t m
   a->max_len = static_cast<int>(max_len);
   *part = *ml = 0;
   if (d->N == 0) return GDN_OK;
-  if (static_cast<double>(max_q) * d->Hq * d->S / 16 + d->Hk * d->S > kMaxItems) return GDN_ERR_UNSUPPORTED;
   gdn::attn_plan(a, d->dtype == GDN_BF16, part, ml);
+  const int64_t prefix_items = gdn::prefix_items(*a), own_items = gdn::own_items(*a);
+  const bool one_launch = a->p_rows == a->o_rows;
+  if ((one_launch ? prefix_items + own_items : prefix_items > own_items ? prefix_items : own_items) > kMaxItems)
+    return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
 }
 

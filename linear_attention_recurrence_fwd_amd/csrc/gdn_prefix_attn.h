@@ -70,19 +70,13 @@ struct Item {
   bool bad, empty;
 };
 
-// Items are numbered so that those which read the same keys of the prefix (row tiles
-// of one split and key head) run on the same XCD, one after the other: workgroups go
-// to the eight XCDs in turn.
 __device__ __forceinline__ Item item_of(const AttnArgs& a) {
   Item it{};
   int b = blockIdx.x;
-  const int pairs = a.p_split * a.Hk, p_items = a.which & 1 ? (pairs + 7) / 8 * 8 * a.p_tiles : 0;
+  const int pairs = a.p_split * a.Hk, p_items = a.which & 1 ? pairs * a.p_tiles : 0;
   if (b < p_items) {
-    const int pair = b / (8 * a.p_tiles) * 8 + b % 8, tile = b / 8 % a.p_tiles;
-    if (pair >= pairs) {
-      it.empty = true;
-      return it;
-    }
+    const PairTile at = prefix_item(b, pairs, a.p_tiles);
+    const int pair = at.pair, tile = at.tile;
     it.slot = pair / a.Hk;
     it.hk = pair % a.Hk;
     it.n = a.N;

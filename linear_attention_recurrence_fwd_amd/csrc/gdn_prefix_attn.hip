@@ -404,8 +404,7 @@ template <typename T, int DC> hipError_t launch_qb(const AttnArgs& a, int rows, 
 // The items of a launch (which of them: a.which), all of the same number of rows.
 template <typename T> hipError_t launch_items(AttnArgs a, int which, hipStream_t st) {
   a.which = which;
-  const unsigned p_items = which & 1 ? (a.p_split * a.Hk + 7) / 8 * 8 * a.p_tiles : 0;
-  const unsigned items = p_items + (which & 2 ? static_cast<unsigned>(a.o_tiles) * a.Hk * a.S * a.o_split : 0);
+  const unsigned items = static_cast<unsigned>((which & 1 ? prefix_items(a) : 0) + (which & 2 ? own_items(a) : 0));
   const int rows = which & 2 ? a.o_rows : a.p_rows;
   if (items == 0) return hipSuccess;
   if (rows > 32) return launch_many(a, items, st);  // (bf16 only)
