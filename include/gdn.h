@@ -469,7 +469,8 @@ int gdn_paged_append(const gdn_paged_dims* d, const gdn_turn* t, const void* q, 
  *   prefix       tokens of the prefix, up to 2^30; 0 without (prefix_pages NULL)
  *   prefix_pages [ceil(prefix / page)] int32
  *   max_q        no sequence has more tokens in the call than this (host; 1 .. N).
- *                With cu NULL the call takes N / S whatever is given.
+ *                With cu NULL the call takes N / S whatever is given; the size query,
+ *                which does not know, has to be asked with N / S then.
  *   max_len      no lens[s] is larger than this (host; up to width * page, and 2^30;
  *                the size of the launch and of the workspace go by it)
  *   cu           as gdn_paged_append; rows behind cu[S] are left as they are
