@@ -898,6 +898,38 @@ class NormRopeAxes(torch.autograd.Function):
 
 # ---- keys and values in pages (gdn_paged_append, gdn_prefix_attention)
 
+class _NoBackward(torch.autograd.Function):
+    """Results of an operator that has no backward pass, from inputs that require a
+    gradient: whoever asks for one is told so.  forward(name, n, *n results, *inputs)."""
+
+    @staticmethod
+    def forward(ctx, name, n, *tensors):
+        ctx.name = name
+        ctx.mark_dirty(*tensors[:n])
+        return tensors[:n]
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise NotImplementedError("%s has no backward pass (it serves from a cache)" % ctx.name)
+
+
+def _wants_grad(tensors):
+    return torch.is_grad_enabled() and any(x is not None and x.requires_grad for x in tensors)
+
+
+def _without_backward(name, results, inputs):
+    """The results, behind a node that raises where any of the inputs requires a gradient."""
+    if not _wants_grad(inputs):
+        return results
+    return _NoBackward.apply(name, len(results), *results, *[x for x in inputs if x is not None])
+
+
+def _no_out(name, inputs):
+    if _wants_grad(inputs):
+        raise RuntimeError("%s: out= with arguments that require a gradient (it has no backward pass; call it under "
+                           "torch.no_grad())" % name)
+
+
 def _rows_stride(x, name, shape):
     """Elements between the rows of consecutive tokens of [N, H, D] (0: dense)."""
     if tuple(x.shape) != shape:
@@ -963,7 +995,8 @@ def paged_append(q, k, v, k_pages, v_pages, table, past, cu=None, *, wq=None, wk
     [pages,Hk,page,D] (any strides with contiguous rows, the same for both), to place
     past[s] + i of sequence s, whose pages are table[s].  Sequence s has the tokens
     cu[s] .. cu[s+1] - 1, or N / S tokens each.  q, k, v may be slices of a packed
-    projection; q may be None.  Returns the turned queries (in out, if given)."""
+    projection; q may be None.  Returns the turned queries (in out, if given).  There is no
+    backward pass: one that reaches the result raises, and the pools hold values alone."""
     if _calls is not None:
         y = _calls.paged_append(q, k, v, k_pages, v_pages, table, past, cu, wq, wk, rope, axis, pos, first, eps, w_offset,
                                 interleaved, out)
@@ -989,6 +1022,7 @@ def paged_append(q, k, v, k_pages, v_pages, table, past, cu=None, *, wq=None, wk
         P, R = rope.shape
         _check(rope, "rope", (P, R), torch.float32, dev)
     A = _axes_of(None, rope, axis, pos, (N,), dev)
+    given = False
     if q is None:
         qs = 0
         if out is not None:
@@ -999,6 +1033,8 @@ def paged_append(q, k, v, k_pages, v_pages, table, past, cu=None, *, wq=None, wk
             out = torch.empty((N, Hq, D), dtype=dt, device=dev)
         else:
             _check(out, "out", (N, Hq, D), dt, dev)
+            _no_out("paged_append", (q, k, v, k_pages, v_pages, wq, wk, out))
+            given = True
     turn = _turn_dims(P, R, qs, _rows_stride(k, "k", (N, Hk, D)), _rows_stride(v, "v", (N, Hk, D)), first, A,
                       1 if interleaved else 0, eps, w_offset)
     with _on_device(dev):
@@ -1007,7 +1043,9 @@ def paged_append(q, k, v, k_pages, v_pages, table, past, cu=None, *, wq=None, wk
                                     _raw_stream(dev.index))
     if rc:
         raise GdnError("gdn_paged_append", rc)
-    return out
+    if out is None or given:
+        return out
+    return _without_backward("paged_append", (out,), (q, k, v, k_pages, v_pages, wq, wk))[0]
 
 
 def prefix_attention(q, k_pages, v_pages, table, lens, prefix_pages=None, prefix=0, cu=None, *, max_q=None,
@@ -1019,7 +1057,8 @@ def prefix_attention(q, k_pages, v_pages, table, lens, prefix_pages=None, prefix
     and max_len (the room of a table's row) bound a sequence's tokens in the call and its
     own length: the launch goes by them, and one of many sequences that are all taken to
     be as long as the batch may be refused.  scale: D^-1/2 by default.  Returns o [N,Hq,D]
-    (in out, if given), with lse=True (o, lse [N,Hq] fp32)."""
+    (in out, if given), with lse=True (o, lse [N,Hq] fp32).  There is no backward pass: one
+    that reaches the result raises."""
     if _calls is not None:
         y = _calls.prefix_attention(q, k_pages, v_pages, table, lens, prefix_pages, prefix, cu, max_q, max_len, scale, out,
                                     lse)
@@ -1043,10 +1082,12 @@ def prefix_attention(q, k_pages, v_pages, table, lens, prefix_pages=None, prefix
         max_q = N // S
     elif max_q is None or max_q > N:
         max_q = N
-    if out is None:
-        out = torch.empty_like(q)
-    else:
+    given = out is not None
+    if given:
         _check(out, "out", q.shape, dt, dev)
+        _no_out("prefix_attention", (q, k_pages, v_pages, out))
+    else:
+        out = torch.empty_like(q)
     sums = torch.empty((N, Hq), dtype=torch.float32, device=dev) if lse else None
     wsb = _attention_ws(prefix, max_q, max_len, *dims)
     ws = torch.empty((wsb,), dtype=torch.uint8, device=dev) if wsb else None
@@ -1057,4 +1098,7 @@ def prefix_attention(q, k_pages, v_pages, table, lens, prefix_pages=None, prefix
                                         _raw_stream(dev.index))
     if rc:
         raise GdnError("gdn_prefix_attention", rc)
-    return (out, sums) if lse else out
+    results = (out, sums) if lse else (out,)
+    if not given:
+        results = _without_backward("prefix_attention", results, (q, k_pages, v_pages))
+    return results if lse else results[0]

@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/core/grad_mode.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -25,7 +26,8 @@ struct Args {
   PyObject* const* a;
   Py_ssize_t n, at = 0;
   bool ok = true;
-  int dev = -1;  // the first tensor's device, and the current one
+  bool no_graph = false;  // tensors that a graph would have to lead to do not fit
+  int dev = -1;           // the first tensor's device, and the current one
 
   PyObject* next() {
     if (at < n) return a[at++];
@@ -41,7 +43,7 @@ struct Args {
       return nullptr;
     }
     const Tensor& t = THPVariable_Unpack(o);
-    if (!t.is_cuda() || t.layout() != at::kStrided) {
+    if (!t.is_cuda() || t.layout() != at::kStrided || (no_graph && t.requires_grad() && at::GradMode::is_enabled())) {
       ok = false;
       return nullptr;
     }
@@ -262,6 +264,7 @@ bool pool_of(gdn_paged_dims* d, const Tensor& kp, const Tensor& vp, const Tensor
 
 PyObject* paged_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
   Args a{args, n};
+  a.no_graph = true;
   const Tensor* q = a.tensor();
   const Tensor &k = a.given(), &v = a.given(), &kp = a.given(), &vp = a.given(), &table = a.given(), &past = a.given();
   const Tensor *cu = a.tensor(), *wq = a.tensor(), *wk = a.tensor();
@@ -301,6 +304,7 @@ PyObject* paged_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 PyObject* prefix_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
   Args a{args, n};
+  a.no_graph = true;
   const Tensor &q = a.given(), &kp = a.given(), &vp = a.given(), &table = a.given(), &lens = a.given();
   const Tensor* pages = a.tensor();
   const int64_t prefix = a.integer();
