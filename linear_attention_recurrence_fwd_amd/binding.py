@@ -981,6 +981,8 @@ def _check_pool(k_pages, v_pages, table, cu, N, Hq, dt, dev):
         raise ValueError("k_pages and v_pages: expected the same strides, and contiguous rows")
     S, width = table.shape
     _check(table, "table", (S, width), torch.int32, dev)
+    if S < 1:
+        raise ValueError("table: expected a row for each sequence, got none")
     if cu is not None:
         _check(cu, "cu", (S + 1,), torch.int32, dev)
     return (N, S, Hq, Hk, D, pages, page, width, strides[0], strides[1], strides[2],
