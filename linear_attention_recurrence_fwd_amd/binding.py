@@ -855,7 +855,7 @@ def _norm_axes_dims(q, k, wq, wk, rope, axis, pos, eps, w_offset, interleaved):
 
 def norm_rope_axes_bwd(q, k, wq, wk, rope, axis, pos, dyq, dyk, *, eps=1e-6, w_offset=0.0, interleaved=False):
     """VJP of norm_rope_axes.  Returns dict(dq, dk, dwq, dwk), dq and dk dense, dwq and
-    dwk None without the norm."""
+    dwk None without the norm, where of q and k only the shapes are used."""
     if _calls is not None:
         out = _calls.norm_rope_axes_bwd(q, k, wq, wk, rope, axis, pos, eps, w_offset, interleaved, dyq, dyk)
         if out is not NotImplemented:
@@ -887,7 +887,8 @@ class NormRopeAxes(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, wq=None, wk=None, rope=None, axis=None, pos=None, eps=1e-6, w_offset=0.0, interleaved=False):
-        ctx.save_for_backward(q, k, wq, wk, rope, axis, pos)
+        # (without the norm the VJP reads neither q nor k)
+        ctx.save_for_backward(*((q, k) if wq is not None else (None, None)), wq, wk, rope, axis, pos)
         ctx.kw = dict(eps=eps, w_offset=w_offset, interleaved=interleaved)
         return norm_rope_axes(q, k, wq, wk, rope, axis, pos, **ctx.kw)
 
@@ -895,7 +896,10 @@ class NormRopeAxes(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dyq, dyk):
         q, k, wq, wk, rope, axis, pos = ctx.saved_tensors
-        g = norm_rope_axes_bwd(q, k, wq, wk, rope, axis, pos, _cotangent(dyq), _cotangent(dyk), **ctx.kw)
+        dyq, dyk = _cotangent(dyq), _cotangent(dyk)
+        if wq is None:
+            q, k = dyq, dyk  # for their shapes
+        g = norm_rope_axes_bwd(q, k, wq, wk, rope, axis, pos, dyq, dyk, **ctx.kw)
         return (g["dq"], g["dk"], g["dwq"], g["dwk"]) + (None,) * 6
 
 
