@@ -203,14 +203,20 @@ template <int LPH, bool INTER> struct Lane {
 // query heads, then the key heads', then (PARTS = 3) the value heads', from g0 to g1.
 // Queries and keys are normed (where they have weights) and turned; values are copied.
 // A batch of rows is on its way while the one before it is worked on (rows one by one
-// left the wave waiting for each: 8192 tokens of 32 + 8 heads of 128, bf16, 47 us
-// against 38).  find is called once, behind the first batch's loads: it gives the
-// token's angles, and where each part's rows go (null: nowhere) and from one head to
-// the next, in bytes.
+// left the wave waiting for each: 8192 tokens of 32 + 8 heads of 128, bf16, several
+// axes, 47 us against 38).  bf16 rows with one axis go one by one ahead, and the weights
+// are fetched where a part begins: that takes 76 registers and not 126, and twice as many
+// waves are there to wait for each other (4096 tokens of 16 + 2 heads of 256: 17.3 us, in
+// batches of four 20.1; 32 + 16 heads of 192, interleaved, 31.4 and 35.8).  With several
+// axes, whose angles are sixteen loads for each token, batches of four stay ahead (42 us
+// against 44).  find is called once, behind the first batch's loads: it gives the token's
+// angles, and where each part's rows go (null: nowhere) and from one head to the next, in
+// bytes.
 template <typename T, int LPH, bool INTER, bool AXES, int PARTS, typename Args, typename Find>
 __device__ __forceinline__ void turn_rows(const Args& a, const Lane<LPH, INTER>& ln, int64_t token, int g0, int g1,
                                           int gq, int gk, const T* const (&src)[PARTS], Find find) {
-  constexpr int RPW = 64 / LPH, U = sizeof(T) == 2 ? 4 : 2;
+  constexpr bool LEAN = sizeof(T) == 2 && !AXES;
+  constexpr int RPW = 64 / LPH, U = LEAN ? 1 : sizeof(T) == 2 ? 4 : 2;
   const int sub_row = (threadIdx.x & 63) / LPH;
   const int begin[4] = {0, gq, gq + gk, gq + 2 * gk};
   auto part_of = [&](int g) { return g < begin[1] ? 0 : PARTS == 2 || g < begin[2] ? 1 : 2; };
@@ -229,11 +235,14 @@ __device__ __forceinline__ void turn_rows(const Args& a, const Lane<LPH, INTER>&
   Raw<T> x[U];
   fetch(g0, x);
   Raw<float> raw[2];
-#pragma unroll
-  for (int part = 0; part < 2; ++part) {
+  auto fetch_w = [&](int part, Raw<float>& x) {
     const float* wp = part ? a.wk : a.wq;
-    raw[part].zero();
-    if (wp) raw[part].load(wp + (ln.on ? ln.c0 : 0));
+    x.zero();
+    if (wp) x.load(wp + (ln.on ? ln.c0 : 0));
+  };
+  if constexpr (!LEAN) {
+    fetch_w(0, raw[0]);
+    fetch_w(1, raw[1]);
   }
   Turn tn;
   char* dst[3];
@@ -250,6 +259,10 @@ __device__ __forceinline__ void turn_rows(const Args& a, const Lane<LPH, INTER>&
     const bool normed = !AXES || (part ? a.wk : a.wq) != nullptr;
     if (part != now && part < 2) {
       float w0[8], w1[8];
+      if constexpr (LEAN) {
+        fetch_w(part, raw[0]);
+        raw[1] = raw[0];
+      }
       raw[0].unpack(w0);
       raw[1].unpack(w1);
 #pragma unroll
