@@ -488,8 +488,8 @@ int gdn_paged_append(const gdn_paged_dims* d, const gdn_turn* t, const void* q, 
  * bf16 for the product with v (up to 2^-8 of each, at random: 1.7e-3 of the result in
  * 2-norm beside its own rounding's 1.7e-3).  fp32: fp32 products and sums throughout.
  * Values up to the type's largest are fine.  At the other end values under 3e-33 times
- * the number of keys lose bits: a row's largest weight is held as 2^-18 / keys or more,
- * and its products under 2^-126 are not normal numbers.
+ * (prefix + max_len) lose bits: a row's largest weight is held as 2^-18 / (prefix +
+ * max_len) or more, and its products under 2^-126 are not normal numbers.
  * Sizes: N Hq up to 2^26 - 64, and a launch holds 2^24 - 1 items: tiles of 16 or 32 rows
  * (bf16 from max_q G = 65 on 128) of max_q G rows, for each key head and sequence, and for
  * each split of their keys where these are few; the prefix's, of N G rows, besides

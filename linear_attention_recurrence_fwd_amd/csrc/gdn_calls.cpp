@@ -4,9 +4,10 @@
 //
 // Each function takes the arguments of its namesake in binding.py, by position, and
 // answers with its result, or with NotImplemented where anything is out of the ordinary
-// (a type, shape, stride or device that does not fit, another current device, a status
-// other than 0): nothing was enqueued then, and binding.py goes the long way, which says
-// what is wrong.
+// (a type, shape, stride or device that does not fit, another current device, a gradient
+// that would be asked for where there is none, a status other than 0): nothing was enqueued
+// then (but where a launch failed, of those before it what is made again), and binding.py
+// goes the long way, which says what is wrong.
 #include <Python.h>
 
 #include <ATen/ATen.h>

@@ -16,9 +16,9 @@
 // eight or more channels away in another lane of the row (or in the same lane
 // when interleaved) and comes by a lane move of the raw storage.
 //
-// Bound by memory: 4096 tokens, 32 + 16 heads of 128, bf16: forward 103 MB in 21.5 us,
-// 4.8 TB/s (a large copy: 5.1); backward 153 MB in 29.4 us, 5.2 TB/s, and 4 us for
-// dw's parts; fp32 201 MB in 41 us, 4.9 TB/s, and 302 MB in 51 us, 5.9 TB/s, a part of
+// Bound by memory: 4096 tokens, 32 + 16 heads of 128, bf16: forward 103 MB in 20.6 us,
+// 5.0 TB/s (a large copy: 5.1); backward 153 MB in 29.2 us, 5.2 TB/s, and 4 us for
+// dw's parts; fp32 201 MB in 36 us, 5.5 TB/s, and 302 MB in 56 us, 5.4 TB/s, a part of
 // it still cached.  64 tokens of 16 + 2 heads of 256, bf16 or fp32: 4 us, a launch and
 // a trip to memory.
 #include "gdn_decay.h"

@@ -12,7 +12,7 @@
 // of rows), not once for each sequence.
 //
 // The kernel for few rows is bound by the keys and values that it reads once: the own
-// keys of 64 sequences, 100 to 2000 each, 2 heads of 256, bf16, 137 MB in 36 us, 3.8 TB/s
+// keys of 64 sequences, 100 to 2000 each, 2 heads of 256, bf16, 137 MB in 38 us, 3.6 TB/s
 // (a large copy: 5.15).  Eight single tokens over 1000 shared keys and a few hundred own
 // ones are latency: 9 us for the keys, 4 for the parts.
 #include "gdn_prefix_attn.h"
@@ -107,7 +107,8 @@ __global__ void __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) few_kernel(AttnArgs 
   };
   // A full tile lies in one page where pages hold it: one address for the wave, and each
   // lane's constant distance from it.  (Row by row, the addresses cost as much as the
-  // tile's products.)
+  // tile's products.)  Heads of other sizes than 64, 128, 192 and 256 go row by row: the
+  // places of the channels that there are not have to be filled.
   const bool one_page = (1 << a.pool.shift) >= KT && a.D == DC && a.pool.ts < (1 << 26);
   uint32_t from_first[NL];
 #pragma unroll
@@ -223,6 +224,7 @@ __global__ void __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) few_kernel(AttnArgs 
       }
     }
     if constexpr (BF) {
+      // (the weights rounded to bf16: up to 2^-8 of each, as the products of bf16 take them)
       s16x4 pb[QB];
 #pragma unroll
       for (int b = 0; b < QB; ++b) pb[b] = __builtin_bit_cast(s16x4, pack4_bf16(p[b][0], p[b][1], p[b][2], p[b][3]));

@@ -9,13 +9,14 @@
 // values' transposing reads follow, so no weight changes its lane.
 //
 // A 32x32x16 product takes 32 cycles of a SIMD and one operand of 1 KB from LDS, 4
-// cycles of the compute unit's one LDS, so the products could keep the SIMDs busy three
-// quarters of the time beside the LDS.  What bounds the kernel is the issue of
+// cycles of the compute unit's one LDS: four SIMDs busy with products alone would keep
+// the LDS busy for half of the time.  What bounds the kernel is the issue of
 // instructions: two waves to a SIMD, each of which starts one in about four cycles, have
 // reads, exponentials, packing and waits to start beside each product.  Measured: 16
-// prompts of 20 to 290 tokens over 8192 shared keys, 32 heads of 128 on 8 key heads, 398
-// us of this kernel, 860 TFLOP/s (a large product of matrices reaches 1233 here); 64
-// single tokens over 32768 shared keys, 16 heads of 256 on 2, 52 us, 660 TFLOP/s.
+// prompts of 20 to 290 tokens over 8192 shared keys, 32 heads of 128 on 8 key heads, 404
+// us of this kernel, 850 TFLOP/s (a large product of matrices reaches 1233 here), the
+// matrix units busy 46% of the time and the LDS 25%; 64 single tokens over 32768 shared
+// keys, 16 heads of 256 on 2, 54 us, 640 TFLOP/s, 35% and 22%.
 #include "gdn_prefix_attn.h"
 
 #include <type_traits>
@@ -119,7 +120,7 @@ template <int DC> __global__ void __launch_bounds__(256, 2) many_kernel(AttnArgs
   // out each time from the first load's: held, some of them lay in scratch memory, and
   // reading one back waited for all loads under way (64 single tokens over 32768 shared
   // keys: 112 us, worked out 59; at 128 channels 16 prompts over 8192 keys take 410 us
-  // with them held, 436 worked out).
+  // with them held, 436 worked out).  76 bytes a lane lie there still at 256 channels.
   constexpr int RL = 64 / PR;  // whole rows of a load
   constexpr bool WHOLE = DC == 256;
   const int place = ((l % PR) ^ swz(w * RW + l / PR)) * 16, first_at = l / PR * a.pool.ts, step = RL * a.pool.ts;
@@ -235,6 +236,8 @@ template <int DC> __global__ void __launch_bounds__(256, 2) many_kernel(AttnArgs
     const float part = weights(s, !wide);
     if (!sure && __any(part > most)) return false;
     sum += part;
+    // (the weights rounded to bf16, for which the matrix cores take values of bf16 as they
+    // lie: up to 2^-8 of each weight, where fp32 products would take eight times as long)
     bf16x8 p[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j)

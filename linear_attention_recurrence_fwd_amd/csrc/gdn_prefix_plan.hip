@@ -5,12 +5,16 @@ namespace gdn {
 namespace {
 
 // What a launch's items cost, in us: each its keys and what it takes to begin and end,
-// `slots` of them at once; and the parts that are written and read back.  An item has at
-// least 128 keys, or `least` where that leaves half of the slots free.  Of few rows of 512
-// bytes and more, which two waves go through, 64: one token of 8 sequences over 1000 keys
-// of 256 channels, bf16, 12.7 us against 14.0; with the slots full, one token of 32 over
-// 2000 keys of 8 heads of 192, 25.8 against 20.6.  Of smaller rows (four waves) 128: one
-// token of 4 sequences over 4000 keys of 128 channels 13.3 us, with 64 keys 19.3.
+// `slots` of them at once; and the parts that are written and read back.  512 slots, two
+// workgroups to a compute unit, are taken for all kernels; by their LDS and registers the
+// compute units hold 256 of the one for few rows of fp32 beyond 128 channels, 768 of that
+// of bf16 of 129 to 192, 1024 of the one for many rows up to 64.  An item has at least 128
+// keys, or `least` where that leaves half of the slots free.  Of few rows of more than 256
+// bytes, which two waves go through, 64: one token of 8 sequences over 1000 keys of 256
+// channels, bf16, 12.7 us against 14.1, of 192 11.3 and 12.6, of 136 11.3 and 13.2, of 72
+// and 96, fp32, 12.8 and 16.9; with the slots full, one token of 32 over 2000 keys of 8
+// heads of 192, 25.8 against 20.6.  Of smaller rows (four waves) 128: one token of 4
+// sequences over 4000 keys of 128 channels 13.3 us, with 64 keys 19.3.
 struct Cost {
   double key, item;
   int slots, least;
